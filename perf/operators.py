@@ -352,8 +352,7 @@ def _run_own(op, s):
         return gla.layer_norm_fwd(s["x"], s["weight"], s["bias"], 1e-5,
                                   out_dtype=DTYPES[s["out"]])
     if op == "norm_bwd":
-        return gla.layer_norm_bwd(s["dy"], s["x"], s["weight"], s["mean"], s["rstd"],
-                                  out_dtype=DTYPES[s["out"]])
+        return gla.layer_norm_bwd(s["dy"], s["x"], s["weight"], s["mean"], s["rstd"])
     if op == "window_fwd":
         return gla.window_attn_fwd(s["q"], s["k"], s["v"], s["window"], s["sink"], s["lens"])
     if op == "window_bwd":
