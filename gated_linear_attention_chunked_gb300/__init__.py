@@ -12,6 +12,8 @@ Functions (same names as the C ABI, without the ``gla_`` prefix):
   decode_step(state, q, k, v, log_decay, aug_balance) -> o  (state updated in place)
   chunk_state_sum, chunk_adjoint_sum, state_link     (a sequence cut into slices across ranks;
                                                       seqshard.py runs the exchange)
+  gated_scan_fwd, _bwd, _decode_step, _decode_step_paged   (the operators around the mixer, bound
+  layer_norm_fwd, layer_norm_bwd                            in layer_ops.py)
   get_device_error(), set_wait_timeout_ns(ns), status_string(code)
 """
 from __future__ import annotations
@@ -119,10 +121,39 @@ def load(path: str | None = None):
             lib.gla_state_link.restype = _I
             lib.gla_chunk_bwd_noalloc.argtypes = [_P] * 3 + [_I] + [_P] * 11 + [_I] * 5 + [_P]
             lib.gla_chunk_bwd_noalloc.restype = _I
+            for name, (args, result) in _layer_calls().items():
+                f = getattr(lib, "gla_" + name)
+                f.argtypes, f.restype = args, result
             if path is not None:
                 return lib
             _lib = lib
     return _lib
+
+
+def _layer_calls():
+    """Argument and result types of the operators that layer_ops.py binds."""
+    _L, _F = ctypes.c_longlong, ctypes.c_float
+    return {
+        "gated_scan_fwd": ([_P, _P, _I] + [_P] * 4 + [_I] * 3 + [_P], _I),
+        "gated_scan_bwd": ([_P, _P, _I] + [_P] * 8 + [_I] * 3 + [_P], _I),
+        "gated_scan_decode_step": ([_P] * 3 + [_I, _P, _L, _I, _P], _I),
+        "gated_scan_decode_step_paged": ([_P, _P] + [_I] * 4 + [_P, _P, _I, _P] + [_I] * 2 + [_P],
+                                         _I),
+        "layer_norm_fwd": ([_P, _I, _P, _P, _F, _P, _I, _P, _P, _L, _I, _P], _I),
+        "layer_norm_bwd_workspace_size": ([_L, _I], _S),
+        "layer_norm_bwd": ([_P, _I, _P, _I] + [_P] * 7 + [_S, _L, _I, _P], _I),
+    }
+
+
+def __getattr__(name: str):
+    """The operators of layer_ops.py, on first use (that module needs torch, this one's import
+    does not)."""
+    if name.startswith(("gated_scan_", "layer_norm_", "window_")):
+        from . import layer_ops
+        if hasattr(layer_ops, name):
+            globals()[name] = f = getattr(layer_ops, name)
+            return f
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def status_string(code: int) -> str:

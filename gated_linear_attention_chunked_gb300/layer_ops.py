@@ -1,0 +1,203 @@
+"""Binding of the operators around the mixer: gated scan, layer norm, windowed attention.
+
+The functions are part of the package's namespace (``gla.gated_scan_fwd`` ...).  As there, this is
+argument marshalling only.  All tensors of a call lie on one CUDA device, which need not be the
+current one; outputs and workspaces are allocated there, on the stream of the call.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+CODES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+F32, I32 = torch.float32, torch.int32
+
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        from . import load
+        _lib = load()
+    return _lib
+
+
+def _check(call: str, rc: int) -> None:
+    if rc != 0:
+        from . import GlaError
+        raise GlaError(call, rc)
+
+
+def _code(t, name) -> int:
+    code = CODES.get(t)
+    if code is None:
+        raise TypeError(f"unsupported {name} dtype {t}")
+    return code
+
+
+def _ptr(t, name, dev, dtype, shape):
+    """Pointer of a contiguous tensor of the call's device, type and shape (None -> NULL)."""
+    if t is None:
+        return None
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _on(t, name, stream):
+    """Context of a call on tensor t's device and `stream` (None: that device's current one)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, {name} on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return _HERE
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _stream(dev) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _scratch(nbytes, dev, workspace):
+    """(pointer, bytes, tensor) of the caller's workspace or a new one."""
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {dev}")
+        if workspace.numel() * workspace.element_size() < nbytes:
+            raise ValueError("workspace too small")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+# ------------------------------------------------------------------------- gated scan
+def gated_scan_fwd(x, g, init_state=None, lens=None, *, want_final_state=True, out=None,
+                   stream=None):
+    """Gated scan h_t = f_t h_{t-1} + (1 - f_t) x_t, f = sigmoid(g) (gla_gated_scan_fwd).
+    x, g [B,T,D] (bf16/fp16/fp32), init_state [B,D] fp32, lens [B] int32: tokens of each sequence,
+    the rest is padding.  Returns (y fp32 [B,T,D], final_state fp32 [B,D] or None)."""
+    B, T, D = x.shape
+    dev, t = x.device, x.dtype
+    with _on(x, "x", stream):
+        y = torch.empty((B, T, D), dtype=F32, device=dev) if out is None else out
+        fin = torch.empty((B, D), dtype=F32, device=dev) if want_final_state else None
+        _check("gla_gated_scan_fwd", _library().gla_gated_scan_fwd(
+            _ptr(x, "x", dev, t, x.shape), _ptr(g, "g", dev, t, x.shape), _code(t, "input"),
+            _ptr(init_state, "init_state", dev, F32, (B, D)), _ptr(lens, "lens", dev, I32, (B,)),
+            _ptr(y, "out", dev, F32, x.shape), None if fin is None else fin.data_ptr(), B, T, D,
+            _stream(dev)))
+    return y, fin
+
+
+def gated_scan_bwd(x, g, y, dy, init_state=None, d_final_state=None, lens=None, *,
+                   want_d_init_state=True, stream=None):
+    """Gradient of gated_scan_fwd (gla_gated_scan_bwd); y: the forward's output, dy [B,T,D] fp32.
+    Returns (dx, dg, d_init_state or None), fp32."""
+    B, T, D = x.shape
+    dev, t = x.device, x.dtype
+    with _on(x, "x", stream):
+        dx = torch.empty((B, T, D), dtype=F32, device=dev)
+        dg = torch.empty((B, T, D), dtype=F32, device=dev)
+        dinit = torch.empty((B, D), dtype=F32, device=dev) if want_d_init_state else None
+        _check("gla_gated_scan_bwd", _library().gla_gated_scan_bwd(
+            _ptr(x, "x", dev, t, x.shape), _ptr(g, "g", dev, t, x.shape), _code(t, "input"),
+            _ptr(y, "y", dev, F32, x.shape), _ptr(dy, "dy", dev, F32, x.shape),
+            _ptr(init_state, "init_state", dev, F32, (B, D)),
+            _ptr(d_final_state, "d_final_state", dev, F32, (B, D)),
+            _ptr(lens, "lens", dev, I32, (B,)), dx.data_ptr(), dg.data_ptr(),
+            None if dinit is None else dinit.data_ptr(), B, T, D, _stream(dev)))
+    return dx, dg, dinit
+
+
+def gated_scan_decode_step(state, x, g, *, out=None, stream=None):
+    """One token of the gated scan (gla_gated_scan_decode_step): state [..., D] fp32 is updated in
+    place, x, g the same shape (bf16/fp16/fp32).  Returns y fp32 (the new state)."""
+    D = x.shape[-1]
+    dev, t = x.device, x.dtype
+    with _on(x, "x", stream):
+        y = torch.empty(x.shape, dtype=F32, device=dev) if out is None else out
+        _check("gla_gated_scan_decode_step", _library().gla_gated_scan_decode_step(
+            _ptr(state, "state", dev, F32, x.shape), _ptr(x, "x", dev, t, x.shape),
+            _ptr(g, "g", dev, t, x.shape), _code(t, "input"), _ptr(y, "out", dev, F32, x.shape),
+            x.numel() // max(D, 1), D, _stream(dev)))
+    return y
+
+
+def gated_scan_decode_step_paged(pool, page, x, g, *, layer0=0, out=None, stream=None):
+    """The same over a state pool (gla_gated_scan_decode_step_paged): pool [P,pool_layers,D] fp32 is
+    updated in place for pages page[n] (int32 [n_active], distinct) and layers layer0..layer0+L-1;
+    x, g [n_active,L,D].  Returns y fp32 [n_active,L,D]."""
+    n, L, D = x.shape
+    P, PL, _ = pool.shape
+    dev, t = x.device, x.dtype
+    with _on(x, "x", stream):
+        y = torch.empty(x.shape, dtype=F32, device=dev) if out is None else out
+        _check("gla_gated_scan_decode_step_paged", _library().gla_gated_scan_decode_step_paged(
+            _ptr(pool, "pool", dev, F32, (P, PL, D)), _ptr(page, "page", dev, I32, (n,)), n, P, PL,
+            layer0, _ptr(x, "x", dev, t, x.shape), _ptr(g, "g", dev, t, x.shape),
+            _code(t, "input"), _ptr(y, "out", dev, F32, x.shape), L, D, _stream(dev)))
+    return y
+
+
+# ------------------------------------------------------------------------- layer norm
+def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, out_dtype=None, want_stats=True,
+                   out=None, stream=None):
+    """Layer norm over the last axis (gla_layer_norm_fwd): x [..., D] (bf16/fp16/fp32), weight,
+    bias [D] fp32.  out_dtype: x's type (default) or fp32.  Returns (y, mean, rstd), the last two
+    fp32 [...] or None."""
+    D = x.shape[-1]
+    dev, t = x.device, x.dtype
+    with _on(x, "x", stream):
+        if out is None:
+            out = torch.empty(x.shape, dtype=out_dtype or t, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+        mean = torch.empty(x.shape[:-1], dtype=F32, device=dev) if want_stats else None
+        rstd = torch.empty(x.shape[:-1], dtype=F32, device=dev) if want_stats else None
+        _check("gla_layer_norm_fwd", _library().gla_layer_norm_fwd(
+            _ptr(x, "x", dev, t, x.shape), _code(t, "input"),
+            _ptr(weight, "weight", dev, F32, (D,)), _ptr(bias, "bias", dev, F32, (D,)), eps,
+            _ptr(out, "out", dev, out.dtype, x.shape), _code(out.dtype, "output"),
+            None if mean is None else mean.data_ptr(), None if rstd is None else rstd.data_ptr(),
+            x.numel() // max(D, 1), D, _stream(dev)))
+    return out, mean, rstd
+
+
+def layer_norm_bwd_workspace_size(n_tokens, D) -> int:
+    return _library().gla_layer_norm_bwd_workspace_size(n_tokens, D)
+
+
+def layer_norm_bwd(dy, x, weight, mean, rstd, *, workspace=None, stream=None):
+    """Gradient of layer_norm_fwd (gla_layer_norm_bwd): dy [..., D] of x's type or fp32, which is
+    also dx's type; mean, rstd as the forward returned them.  Returns (dx, d_weight, d_bias), the
+    last two fp32 [D]."""
+    D = x.shape[-1]
+    dev, t = x.device, x.dtype
+    n = x.numel() // max(D, 1)
+    with _on(x, "x", stream):
+        dx = torch.empty(x.shape, dtype=dy.dtype, device=dev)
+        dw = torch.empty((D,), dtype=F32, device=dev)
+        db = torch.empty((D,), dtype=F32, device=dev)
+        lib = _library()
+        wp, wb, hold = _scratch(lib.gla_layer_norm_bwd_workspace_size(n, D), dev, workspace)
+        _check("gla_layer_norm_bwd", lib.gla_layer_norm_bwd(
+            _ptr(dy, "dy", dev, dy.dtype, x.shape), _code(dy.dtype, "dy"),
+            _ptr(x, "x", dev, t, x.shape), _code(t, "input"),
+            _ptr(weight, "weight", dev, F32, (D,)),
+            _ptr(mean, "mean", dev, F32, x.shape[:-1]), _ptr(rstd, "rstd", dev, F32, x.shape[:-1]),
+            dx.data_ptr(), dw.data_ptr(), db.data_ptr(), wp, wb, n, D, _stream(dev)))
+    return dx, dw, db

@@ -474,6 +474,94 @@ GLA_API gla_status gla_conv_decode_step(float* state, const float* x, const floa
                                         const float* bias, float* y, long long N, int D,
                                         cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Gated scan: a linear recurrence whose forget gate depends on the data, per channel -- the
+ * mixers above with a decay that is an input instead of fixed, and a state of D floats per
+ * sequence:
+ *
+ *   f_t = sigmoid(g_t),  h_t = f_t h_{t-1} + (1 - f_t) x_t,  y_t = h_t  (h_0 = init_state)
+ *
+ *   x, g         [B,T,D] in_dtype (GLA_BF16, GLA_FP16 or GLA_FP32, both the same); any D.
+ *                g = +inf keeps the state (f = 1) and -inf resets it (f = 0), both exactly;
+ *                x must be finite where g = +inf
+ *   init_state   [B,D] fp32 or NULL (= zeros)
+ *   lens         [B] int32 (device) or NULL (= all T): tokens lens[b].. of sequence b are
+ *                padding: neither x nor g is read there, y is written as 0 and final_state is
+ *                the state after lens[b] tokens (0: init_state).  A length outside [0, T] is
+ *                read as the nearer end and sets the device error word to GLA_ERR_RANGE
+ *   y            [B,T,D] fp32 (written)      final_state [B,D] fp32 or NULL (written)
+ * All arithmetic is fp32; nothing is allocated; results repeat bit for bit.  May be captured
+ * into a CUDA graph, as the decode step and the gradient may.
+ */
+GLA_API gla_status gla_gated_scan_fwd(const void* x, const void* g, gla_dtype in_dtype,
+                                      const float* init_state, const int* lens, float* y,
+                                      float* final_state, int B, int T, int D,
+                                      cudaStream_t stream);
+
+/* Its gradient for the scalar loss sum(y . dy) + <d_final_state, final_state>, with
+ * G_t = dy_t + f_{t+1} G_{t+1} (G_T = dy_T + d_final_state):
+ *   dx_t = (1 - f_t) G_t,  dg_t = f_t (1 - f_t) (h_{t-1} - x_t) G_t,  d_init_state = f_1 G_1
+ *   y            [B,T,D] fp32: the forward's output for the same inputs (read)
+ *   dy           [B,T,D] fp32; not read on padding
+ *   d_final_state [B,D] fp32 or NULL (= zeros)
+ *   dx, dg       [B,T,D] fp32 (written; 0 on padding)
+ *   d_init_state [B,D] fp32 or NULL (written)
+ */
+GLA_API gla_status gla_gated_scan_bwd(const void* x, const void* g, gla_dtype in_dtype,
+                                      const float* y, const float* dy, const float* init_state,
+                                      const float* d_final_state, const int* lens, float* dx,
+                                      float* dg, float* d_init_state, int B, int T, int D,
+                                      cudaStream_t stream);
+
+/* One token of the gated scan: state [N,D] fp32 in place, x, g [N,D] in_dtype, y [N,D] fp32
+ * (written: the new state).  N == 0 returns GLA_OK without launching. */
+GLA_API gla_status gla_gated_scan_decode_step(float* state, const void* x, const void* g,
+                                              gla_dtype in_dtype, float* y, long long N, int D,
+                                              cudaStream_t stream);
+
+/* The same over a state pool, one page per sequence (see gla_decode_step_paged, whose rules for
+ * page, n_active and layer0 hold here): pool [n_pages,pool_layers,D] fp32, x, g, y
+ * [n_active,L,D]. */
+GLA_API gla_status gla_gated_scan_decode_step_paged(float* pool, const int* page, int n_active,
+                                                    int n_pages, int pool_layers, int layer0,
+                                                    const void* x, const void* g,
+                                                    gla_dtype in_dtype, float* y, int L, int D,
+                                                    cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Layer norm over the channels of each token, ahead of a layer's conv and of its FFN
+ * ("Normalization and convolution"):
+ *
+ *   m = mean_c x_c,  r = 1 / sqrt(mean_c (x_c - m)^2 + eps),  y_c = (x_c - m) r weight_c + bias_c
+ *
+ *   x            [n_tokens,D] x_dtype, 1 <= D <= 16384
+ *   weight, bias [D] fp32 or NULL (= ones, zeros)
+ *   y            [n_tokens,D] y_dtype: x_dtype or GLA_FP32 (written)
+ *   mean, rstd   [n_tokens] fp32 or NULL (written: m, r), which the gradient reads
+ * All fp32 arithmetic, one rounding to y_dtype; nothing allocated.  n_tokens == 0 returns GLA_OK.
+ */
+GLA_API gla_status gla_layer_norm_fwd(const void* x, gla_dtype x_dtype, const float* weight,
+                                      const float* bias, float eps, void* y, gla_dtype y_dtype,
+                                      float* mean, float* rstd, long long n_tokens, int D,
+                                      cudaStream_t stream);
+
+/* Its gradient for the scalar loss sum(y . dy), with n_c = (x_c - m) r and d_c = dy_c weight_c:
+ *   dx_c = r (d_c - mean(d) - n_c mean(d n))
+ *   d_weight_c = sum_tokens dy_c n_c,  d_bias_c = sum_tokens dy_c
+ *   dy, dx       [n_tokens,D] dy_dtype: x_dtype or GLA_FP32 (dx written)
+ *   mean, rstd   [n_tokens] fp32, as the forward wrote them
+ *   d_weight, d_bias [D] fp32 or NULL (written; summed in a fixed order: deterministic; zeros
+ *                if n_tokens == 0)
+ *   workspace    gla_layer_norm_bwd_workspace_size() bytes, 256-byte aligned (partial sums).
+ *                The size depends on the device current at the call.
+ */
+GLA_API size_t gla_layer_norm_bwd_workspace_size(long long n_tokens, int D);
+GLA_API gla_status gla_layer_norm_bwd(const void* dy, gla_dtype dy_dtype, const void* x,
+                                      gla_dtype x_dtype, const float* weight, const float* mean,
+                                      const float* rstd, void* dx, float* d_weight, float* d_bias,
+                                      void* workspace, size_t workspace_bytes, long long n_tokens,
+                                      int D, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
