@@ -14,6 +14,7 @@ Functions (same names as the C ABI, without the ``gla_`` prefix):
                                                       seqshard.py runs the exchange)
   gated_scan_fwd, _bwd, _decode_step, _decode_step_paged   (the operators around the mixer, bound
   layer_norm_fwd, layer_norm_bwd                            in layer_ops.py)
+  window_attn_fwd, _bwd, _decode_step, window_cache_fill
   get_device_error(), set_wait_timeout_ns(ns), status_string(code)
 """
 from __future__ import annotations
@@ -142,6 +143,14 @@ def _layer_calls():
         "layer_norm_fwd": ([_P, _I, _P, _P, _F, _P, _I, _P, _P, _L, _I, _P], _I),
         "layer_norm_bwd_workspace_size": ([_L, _I], _S),
         "layer_norm_bwd": ([_P, _I, _P, _I] + [_P] * 7 + [_S, _L, _I, _P], _I),
+        "window_attn_fwd": ([_P] * 3 + [_I, _P, _I, _I, _P, _I, _P] + [_I] * 6 + [_P], _I),
+        "window_attn_bwd_workspace_size": ([_I] * 6, _S),
+        "window_attn_bwd": ([_P] * 3 + [_I, _P, _I, _I, _P, _P, _I] + [_P] * 6 + [_S] + [_I] * 6 +
+                            [_P], _I),
+        "window_cache_fill": ([_P, _P, _I] + [_P] * 4 + [_I] * 10 + [_P], _I),
+        "window_attn_decode_workspace_size": ([_I] * 5, _S),
+        "window_attn_decode_step": ([_P, _P, _I, _P, _P] + [_I] * 6 + [_P] * 4 + [_I, _P, _S] +
+                                    [_I] * 4 + [_P], _I),
     }
 
 

@@ -21,9 +21,10 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libgla.so")
 
 SOURCES = ["api.cu", "decode.cu", "convert.cu", "chunk_fwd.cu", "chunk_bwd.cu", "noalloc.cu", "seg_scan.cu", "head_norm.cu", "conv.cu",
-           "api_layer.cu", "gated_scan.cu", "layer_norm.cu"]
+           "api_layer.cu", "gated_scan.cu", "layer_norm.cu",
+           "window_fwd.cu", "window_bwd.cu", "window_decode.cu"]
 HEADERS = ["ptx.cuh", "tmap.h", "kernels.h", "scan_common.cuh", "elem.cuh",
-           "gated_scan.h", "layer_norm.h"]
+           "gated_scan.h", "layer_norm.h", "window_attn.h", "mma.cuh", "window_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",

@@ -2,12 +2,14 @@
 // norm and windowed attention.  Argument checks, then the launches on the caller's stream.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "gated_scan.h"
 #include "gla.h"
 #include "kernels.h"
 #include "layer_norm.h"
+#include "window_attn.h"
 
 namespace {
 
@@ -39,6 +41,33 @@ gla_status check_scan_sizes(int B, int T, int D, gla_dtype t) {
   // the grid: one CTA per sequence and 32 channels, times a cluster of at most 8
   if (T > kMaxInt - 4096 || (long long)B * ((D + 31ll) / 32) > kMaxInt / 8 ||
       (long long)B * T > (1ll << 40) / D)
+    return GLA_ERR_UNSUPPORTED;
+  return GLA_OK;
+}
+
+// Sizes and types of the windowed attention; the tensors' element counts stay below 2^40.
+gla_status check_window(gla_dtype in, gla_dtype out, int window, int sink, int H, int KV, int dk,
+                        int dv) {
+  if (H <= 0 || KV <= 0 || H % KV != 0 || window <= 0 || sink < 0) return GLA_ERR_INVALID_ARG;
+  if (dk != gla::kDK || dv != gla::kDV || (in != GLA_BF16 && in != GLA_FP16) ||
+      (out != in && out != GLA_FP32))
+    return GLA_ERR_UNSUPPORTED;
+  return GLA_OK;
+}
+gla_status check_window_batch(int B, int T, int H) {
+  if (B <= 0 || T <= 0) return GLA_ERR_INVALID_ARG;
+  if (T > (1 << 30) || (long long)B * T > (1ll << 32) / H ||
+      (long long)B * ((T + 63ll) / 64) > kMaxInt / H)
+    return GLA_ERR_UNSUPPORTED;
+  return GLA_OK;
+}
+// Slots of a page and of the whole pool.
+gla_status check_window_pool(int n_pages, int pool_layers, int layer, int window, int sink,
+                             int KV) {
+  if (n_pages <= 0 || pool_layers <= 0 || layer < 0 || layer >= pool_layers)
+    return GLA_ERR_INVALID_ARG;
+  if (window > (1 << 30) - sink || KV > (1 << 16) ||
+      (long long)n_pages * pool_layers > (1ll << 40) / ((long long)(window + sink) * KV))
     return GLA_ERR_UNSUPPORTED;
   return GLA_OK;
 }
@@ -166,6 +195,122 @@ gla_status gla_layer_norm_bwd(const void* dy, gla_dtype dy_dtype, const void* x,
   a.part = static_cast<float*>(workspace);
   a.x_type = x_dtype; a.out_type = dy_dtype; a.n = n_tokens; a.D = D;
   return done(gla::launch_layer_norm_bwd(a, sm_count(), stream));
+}
+
+gla_status gla_window_attn_fwd(const void* q, const void* k, const void* v, gla_dtype in_dtype,
+                               const int* lens, int window, int sink, void* o,
+                               gla_dtype out_dtype, float* lse, int B, int T, int H, int KV,
+                               int dk, int dv, cudaStream_t stream) {
+  gla_status st = check_window(in_dtype, out_dtype, window, sink, H, KV, dk, dv);
+  if (st != GLA_OK || (st = check_window_batch(B, T, H)) != GLA_OK) return st;
+  if (!q || !k || !v || !o) return GLA_ERR_INVALID_ARG;
+  if (!aligned16(q, k, v, o) || !aligned4(lens, lse)) return GLA_ERR_ALIGNMENT;
+  gla::DevCtl ctl;
+  if (gla::current_device_ctl(&ctl) != cudaSuccess) return GLA_ERR_CUDA;
+  gla::WindowArgs a;
+  a.q = q; a.k = k; a.v = v; a.lens = lens; a.B = B; a.T = T; a.H = H; a.KV = KV;
+  a.window = std::min(window, T); a.sink = std::min(sink, T);
+  a.in_type = in_dtype; a.out_type = out_dtype; a.o = o; a.lse = lse;
+  return done(gla::launch_window_fwd(a, sm_count(), ctl, stream));
+}
+
+size_t gla_window_attn_bwd_workspace_size(int B, int T, int H, int KV, int window, int sink) {
+  if (check_window(GLA_BF16, GLA_BF16, window, sink, H, KV, gla::kDK, gla::kDV) != GLA_OK ||
+      check_window_batch(B, T, H) != GLA_OK)
+    return 0;
+  return gla::window_bwd_workspace_bytes(B, T, H, KV, std::min(window, T), std::min(sink, T));
+}
+
+gla_status gla_window_attn_bwd(const void* q, const void* k, const void* v, gla_dtype in_dtype,
+                               const int* lens, int window, int sink, const void* o,
+                               const long long* o_strides, gla_dtype out_dtype, const float* lse,
+                               const void* dO, void* dq, void* dk, void* dv, void* workspace,
+                               size_t workspace_bytes, int B, int T, int H, int KV, int dk_,
+                               int dv_, cudaStream_t stream) {
+  gla_status st = check_window(in_dtype, out_dtype, window, sink, H, KV, dk_, dv_);
+  if (st != GLA_OK || (st = check_window_batch(B, T, H)) != GLA_OK) return st;
+  if (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv) return GLA_ERR_INVALID_ARG;
+  if (!aligned16(q, k, v, o, dO, dq, dk, dv) || !aligned4(lens, lse)) return GLA_ERR_ALIGNMENT;
+  gla::WindowArgs a;
+  a.o_stride[0] = (long long)T * H * gla::kDV;
+  a.o_stride[1] = (long long)H * gla::kDV;
+  a.o_stride[2] = gla::kDV;
+  for (int i = 0; o_strides && i < 3; ++i) {
+    if (o_strides[i] < 0) return GLA_ERR_INVALID_ARG;
+    if (o_strides[i] % (out_dtype == GLA_FP32 ? 2 : 4)) return GLA_ERR_ALIGNMENT;
+    a.o_stride[i] = o_strides[i];
+  }
+  const size_t need = gla_window_attn_bwd_workspace_size(B, T, H, KV, window, sink);
+  if (!workspace || workspace_bytes < need) return GLA_ERR_WORKSPACE;
+  if (!aligned256(workspace)) return GLA_ERR_ALIGNMENT;
+  gla::DevCtl ctl;
+  if (gla::current_device_ctl(&ctl) != cudaSuccess) return GLA_ERR_CUDA;
+  a.q = q; a.k = k; a.v = v; a.lens = lens; a.B = B; a.T = T; a.H = H; a.KV = KV;
+  a.window = std::min(window, T); a.sink = std::min(sink, T);
+  a.in_type = in_dtype; a.out_type = out_dtype; a.o = const_cast<void*>(o);
+  a.lse = const_cast<float*>(lse); a.dO = dO; a.dq = dq; a.dk = dk; a.dv = dv;
+  a.workspace = workspace;
+  return done(gla::launch_window_bwd(a, sm_count(), ctl, stream));
+}
+
+gla_status gla_window_cache_fill(const void* k, const void* v, gla_dtype cache_dtype,
+                                 const int* lens, void* pool_k, void* pool_v, const int* page,
+                                 int n_pages, int pool_layers, int layer, int window, int sink,
+                                 int B, int T, int KV, int dk, int dv, cudaStream_t stream) {
+  gla_status st = check_window(cache_dtype, cache_dtype, window, sink, KV, KV, dk, dv);
+  if (st != GLA_OK || (st = check_window_batch(B, T, KV)) != GLA_OK ||
+      (st = check_window_pool(n_pages, pool_layers, layer, window, sink, KV)) != GLA_OK)
+    return st;
+  if (!k || !v || !pool_k || !pool_v || !page) return GLA_ERR_INVALID_ARG;
+  if (!aligned16(k, v, pool_k, pool_v) || !aligned4(lens, page)) return GLA_ERR_ALIGNMENT;
+  if ((long long)B * (window + sink) > 8 * kMaxInt) return GLA_ERR_UNSUPPORTED;
+  gla::DevCtl ctl;
+  if (gla::current_device_ctl(&ctl) != cudaSuccess) return GLA_ERR_CUDA;
+  gla::WindowCache c{pool_k, pool_v, page, B, n_pages, pool_layers, layer, KV, window, sink,
+                     cache_dtype};
+  return done(gla::launch_window_fill(c, k, v, lens, T, ctl, stream));
+}
+
+static gla_status check_window_active(int n_active, int H, int window, int sink) {
+  if (n_active < 0) return GLA_ERR_INVALID_ARG;
+  // CTAs: at most 64 parts of each (sequence, head)
+  if (window > (1 << 30) - sink || (long long)n_active * H > kMaxInt / 64)
+    return GLA_ERR_UNSUPPORTED;
+  return GLA_OK;
+}
+
+size_t gla_window_attn_decode_workspace_size(int n_active, int H, int KV, int window, int sink) {
+  if (check_window(GLA_BF16, GLA_BF16, window, sink, H, KV, gla::kDK, gla::kDV) != GLA_OK ||
+      check_window_active(n_active, H, window, sink) != GLA_OK)
+    return 0;
+  return gla::window_decode_workspace_bytes(n_active, KV, H, window + sink, sm_count());
+}
+
+gla_status gla_window_attn_decode_step(void* pool_k, void* pool_v, gla_dtype cache_dtype,
+                                       const int* page, const int* pos, int n_active, int n_pages,
+                                       int pool_layers, int layer, int window, int sink,
+                                       const void* q, const void* k, const void* v, void* o,
+                                       gla_dtype out_dtype, void* workspace,
+                                       size_t workspace_bytes, int H, int KV, int dk, int dv,
+                                       cudaStream_t stream) {
+  gla_status st = check_window(cache_dtype, out_dtype, window, sink, H, KV, dk, dv);
+  if (st != GLA_OK || (st = check_window_active(n_active, H, window, sink)) != GLA_OK ||
+      (st = check_window_pool(n_pages, pool_layers, layer, window, sink, KV)) != GLA_OK)
+    return st;
+  if (n_active == 0) return GLA_OK;
+  if (!pool_k || !pool_v || !page || !pos || !q || !k || !v || !o) return GLA_ERR_INVALID_ARG;
+  if (!aligned16(pool_k, pool_v, q, k, v, o) || !aligned4(page, pos)) return GLA_ERR_ALIGNMENT;
+  const size_t need = gla_window_attn_decode_workspace_size(n_active, H, KV, window, sink);
+  if (need && (!workspace || workspace_bytes < need)) return GLA_ERR_WORKSPACE;
+  if (need && !aligned256(workspace)) return GLA_ERR_ALIGNMENT;
+  gla::DevCtl ctl;
+  if (gla::current_device_ctl(&ctl) != cudaSuccess) return GLA_ERR_CUDA;
+  gla::WindowDecodeArgs a;
+  a.c = {pool_k, pool_v, page, n_active, n_pages, pool_layers, layer, KV, window, sink,
+         cache_dtype};
+  a.pos = pos; a.q = q; a.k = k; a.v = v; a.o = o; a.out_type = out_dtype; a.H = H;
+  a.workspace = workspace;
+  return done(gla::launch_window_decode(a, sm_count(), ctl, stream));
 }
 
 }  // extern "C"

@@ -7,6 +7,7 @@ current one; outputs and workspaces are allocated there, on the stream of the ca
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
 import torch
 
@@ -50,6 +51,17 @@ def _ptr(t, name, dev, dtype, shape):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _view(t, name, dev, shape):
+    """Pointer and strides (None: contiguous) of a tensor whose last axis is contiguous."""
+    if t.is_contiguous():
+        return _ptr(t, name, dev, t.dtype, shape), None
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.shape != shape or t.stride(-1) != 1:
+        raise ValueError(f"{name} must be {list(shape)} with its last axis contiguous")
+    return t.data_ptr(), (ctypes.c_longlong * (t.dim() - 1))(*t.stride()[:-1])
 
 
 def _on(t, name, stream):
@@ -201,3 +213,111 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, *, workspace=None, stream=None):
             _ptr(mean, "mean", dev, F32, x.shape[:-1]), _ptr(rstd, "rstd", dev, F32, x.shape[:-1]),
             dx.data_ptr(), dw.data_ptr(), db.data_ptr(), wp, wb, n, D, _stream(dev)))
     return dx, dw, db
+
+
+# ------------------------------------------------------------------ windowed attention
+def window_attn_fwd(q, k, v, window, sink=0, lens=None, *, out_dtype=None, want_lse=True,
+                    out=None, stream=None):
+    """Causal attention over the last `window` tokens and the first `sink` (gla_window_attn_fwd).
+    q [B,T,H,96], k [B,T,KV,96], v [B,T,KV,192] (bf16/fp16, q pre-scaled; KV divides H), lens [B]
+    int32: tokens of each sequence, the rest is padding.  out_dtype: q's type (default) or fp32.
+    Returns (o [B,T,H,192], lse fp32 [B,H,T] or None)."""
+    B, T, H, dk = q.shape
+    KV, dv = v.shape[2], v.shape[3]
+    dev, t = q.device, q.dtype
+    with _on(q, "q", stream):
+        if out is None:
+            out = torch.empty((B, T, H, dv), dtype=out_dtype or t, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+        lse = torch.empty((B, H, T), dtype=F32, device=dev) if want_lse else None
+        _check("gla_window_attn_fwd", _library().gla_window_attn_fwd(
+            _ptr(q, "q", dev, t, q.shape), _ptr(k, "k", dev, t, (B, T, KV, dk)),
+            _ptr(v, "v", dev, t, (B, T, KV, dv)), _code(t, "input"),
+            _ptr(lens, "lens", dev, I32, (B,)), window, sink,
+            _ptr(out, "out", dev, out.dtype, (B, T, H, dv)), _code(out.dtype, "output"),
+            None if lse is None else lse.data_ptr(), B, T, H, KV, dk, dv, _stream(dev)))
+    return out, lse
+
+
+def window_attn_bwd_workspace_size(B, T, H, KV, window, sink=0) -> int:
+    return _library().gla_window_attn_bwd_workspace_size(B, T, H, KV, window, sink)
+
+
+def window_attn_bwd(q, k, v, o, lse, dO, window, sink=0, lens=None, *, workspace=None,
+                    stream=None):
+    """Gradient of window_attn_fwd (gla_window_attn_bwd): o, lse as the forward returned them (o may
+    be a view of another layout whose channels are adjacent), dO of q's type.  Returns (dq, dk,
+    dv), of o's type."""
+    B, T, H, dk_ = q.shape
+    KV, dv_ = v.shape[2], v.shape[3]
+    dev, t = q.device, q.dtype
+    with _on(q, "q", stream):
+        dq = torch.empty(q.shape, dtype=o.dtype, device=dev)
+        dk = torch.empty(k.shape, dtype=o.dtype, device=dev)
+        dv = torch.empty(v.shape, dtype=o.dtype, device=dev)
+        lib = _library()
+        wp, wb, hold = _scratch(lib.gla_window_attn_bwd_workspace_size(B, T, H, KV, window, sink),
+                                dev, workspace)
+        _check("gla_window_attn_bwd", lib.gla_window_attn_bwd(
+            _ptr(q, "q", dev, t, q.shape), _ptr(k, "k", dev, t, (B, T, KV, dk_)),
+            _ptr(v, "v", dev, t, (B, T, KV, dv_)), _code(t, "input"),
+            _ptr(lens, "lens", dev, I32, (B,)), window, sink,
+            *_view(o, "o", dev, (B, T, H, dv_)), _code(o.dtype, "output"),
+            _ptr(lse, "lse", dev, F32, (B, H, T)), _ptr(dO, "dO", dev, t, (B, T, H, dv_)),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), wp, wb, B, T, H, KV, dk_, dv_,
+            _stream(dev)))
+    return dq, dk, dv
+
+
+def window_cache_fill(pool_k, pool_v, page, k, v, window, sink=0, lens=None, *, layer=0,
+                      stream=None):
+    """The keys and values of prompts into their pages (gla_window_cache_fill).  pool_k, pool_v
+    [P,pool_layers,sink+window,KV,96|192] (bf16/fp16) are updated in place in layer `layer` of
+    pages page[b] (int32 [B], distinct); k [B,T,KV,96], v [B,T,KV,192], lens [B] int32."""
+    B, T, KV, dk = k.shape
+    dv = v.shape[-1]
+    P, PL = pool_k.shape[:2]
+    dev, t = k.device, k.dtype
+    slots = window + sink
+    with _on(k, "k", stream):
+        _check("gla_window_cache_fill", _library().gla_window_cache_fill(
+            _ptr(k, "k", dev, t, k.shape), _ptr(v, "v", dev, t, (B, T, KV, dv)),
+            _code(t, "input"), _ptr(lens, "lens", dev, I32, (B,)),
+            _ptr(pool_k, "pool_k", dev, t, (P, PL, slots, KV, dk)),
+            _ptr(pool_v, "pool_v", dev, t, (P, PL, slots, KV, dv)),
+            _ptr(page, "page", dev, I32, (B,)), P, PL, layer, window, sink, B, T, KV, dk, dv,
+            _stream(dev)))
+
+
+def window_attn_decode_workspace_size(n_active, H, KV, window, sink=0) -> int:
+    return _library().gla_window_attn_decode_workspace_size(n_active, H, KV, window, sink)
+
+
+def window_attn_decode_step(pool_k, pool_v, page, pos, q, k, v, window, sink=0, *, layer=0,
+                            out_dtype=None, out=None, workspace=None, stream=None):
+    """One token of the windowed attention over its caches (gla_window_attn_decode_step).  pool_k,
+    pool_v as in window_cache_fill get the token's key and value in place; page, pos int32
+    [n_active]: its page and its position from 0; q [n_active,H,96], k [n_active,KV,96], v
+    [n_active,KV,192].  out_dtype: q's type (default) or fp32.  Returns o [n_active,H,192]."""
+    n, H, dk = q.shape
+    KV, dv = v.shape[1], v.shape[2]
+    P, PL = pool_k.shape[:2]
+    dev, t = q.device, q.dtype
+    slots = window + sink
+    with _on(q, "q", stream):
+        if out is None:
+            out = torch.empty((n, H, dv), dtype=out_dtype or t, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+        lib = _library()
+        wp, wb, hold = _scratch(lib.gla_window_attn_decode_workspace_size(n, H, KV, window, sink),
+                                dev, workspace)
+        _check("gla_window_attn_decode_step", lib.gla_window_attn_decode_step(
+            _ptr(pool_k, "pool_k", dev, t, (P, PL, slots, KV, dk)),
+            _ptr(pool_v, "pool_v", dev, t, (P, PL, slots, KV, dv)), _code(t, "input"),
+            _ptr(page, "page", dev, I32, (n,)), _ptr(pos, "pos", dev, I32, (n,)), n, P, PL, layer,
+            window, sink, _ptr(q, "q", dev, t, q.shape), _ptr(k, "k", dev, t, (n, KV, dk)),
+            _ptr(v, "v", dev, t, (n, KV, dv)), _ptr(out, "out", dev, out.dtype, (n, H, dv)),
+            _code(out.dtype, "output"), wp, wb, H, KV, dk, dv, _stream(dev)))
+    return out

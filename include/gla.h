@@ -562,6 +562,97 @@ GLA_API gla_status gla_layer_norm_bwd(const void* dy, gla_dtype dy_dtype, const 
                                       void* workspace, size_t workspace_bytes, long long n_tokens,
                                       int D, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Windowed attention: causal softmax attention over the last `window` tokens and the first `sink`
+ * ones, with the mixer's head sizes, so that a layer takes either from the same projection --
+ * the other kind of mixer whose state a serving engine keeps in one fixed page per sequence:
+ *
+ *   z_ts = q_t . k_s  over the s <= t with t - s < window or s < sink
+ *   lse_t = ln sum_s exp(z_ts),   o_t = sum_s exp(z_ts - lse_t) v_s
+ *
+ *   q            [B,T,H,96] in_dtype (GLA_BF16 or GLA_FP16; GLA_FP32 -> GLA_ERR_UNSUPPORTED)
+ *   k            [B,T,KV,96], v [B,T,KV,192] in_dtype; KV divides H: query head h reads key head
+ *                h / (H / KV).  No internal scaling: callers pre-scale q
+ *   lens         [B] int32 (device) or NULL (= all T): tokens lens[b].. of sequence b are padding,
+ *                neither read nor seen; there o is written as 0 and lse as -inf.  A length outside
+ *                [0, T] is read as the nearer end and sets the device error word to GLA_ERR_RANGE
+ *   window >= 1, sink >= 0 (values past T mean all of T)
+ *   o            [B,T,H,192] out_dtype: in_dtype or GLA_FP32 (written)
+ *   lse          [B,H,T] fp32 or NULL (written; the gradient reads it; 4-byte aligned)
+ * Scores, softmax statistics and sums are fp32; the softmax weights round once to in_dtype for
+ * the product with v, which the tensor cores take in one type.  T <= 2^30.  May be captured into
+ * a CUDA graph, as the gradient and the decode step may.
+ */
+GLA_API gla_status gla_window_attn_fwd(const void* q, const void* k, const void* v,
+                                       gla_dtype in_dtype, const int* lens, int window, int sink,
+                                       void* o, gla_dtype out_dtype, float* lse, int B, int T,
+                                       int H, int KV, int dk, int dv, cudaStream_t stream);
+
+/* Its gradient for the scalar loss sum(o . dO), with p_ts = exp(z_ts - lse_t):
+ *   dz_ts = p_ts (dO_t . v_s - dO_t . o_t)
+ *   dq_t = sum_s dz_ts k_s,  dk_s = sum_t dz_ts q_t,  dv_s = sum_t p_ts dO_t
+ * (dk, dv summed over the query heads of a key head).
+ *   o, lse       as the forward wrote them for the same inputs (o of out_dtype).  o is read row
+ *                by row only, so it may be a view: o_strides, a HOST array of three element
+ *                strides (sequence, token, head; non-negative, the channels adjacent, every row
+ *                8-byte aligned), or NULL for the layout of the forward
+ *   dO           [B,T,H,192] in_dtype; not read on padding
+ *   dq, dk, dv   the shapes of q, k, v, of out_dtype (written; 0 on padding)
+ *   workspace    gla_window_attn_bwd_workspace_size() bytes, 256-byte aligned.  The size depends
+ *                on the device current at the call.
+ * p and dz round once to in_dtype for their products; fp16 callers scale their loss so that dz
+ * stays in that type's range.  All sums run in a fixed order: results repeat bit for bit.
+ */
+GLA_API size_t gla_window_attn_bwd_workspace_size(int B, int T, int H, int KV, int window,
+                                                  int sink);
+GLA_API gla_status gla_window_attn_bwd(const void* q, const void* k, const void* v,
+                                       gla_dtype in_dtype, const int* lens, int window, int sink,
+                                       const void* o, const long long* o_strides,
+                                       gla_dtype out_dtype, const float* lse, const void* dO,
+                                       void* dq, void* dk, void* dv,
+                                       void* workspace, size_t workspace_bytes, int B, int T,
+                                       int H, int KV, int dk_, int dv_, cudaStream_t stream);
+
+/* The windowed attention's caches: one page per sequence, of a size that does not depend on its
+ * length -- the first `sink` tokens in slots 0 .. sink-1, the last `window` others in a ring
+ * behind them (token t >= sink in slot sink + (t - sink) % window):
+ *   pool_k       [n_pages,pool_layers,sink + window,KV,96]   pool_v [..,192]   cache_dtype
+ *                (GLA_BF16 or GLA_FP16); a call uses layer `layer` of its pages
+ *   page         [n] int32 (device), distinct: sequences that share a page race.  A page outside
+ *                [0, n_pages) leaves its sequence untouched and sets the device error word to
+ *                GLA_ERR_RANGE
+ *
+ * gla_window_cache_fill: the keys and values of prompts (k [B,T,KV,96], v [B,T,KV,192], tokens
+ * 0 .. lens[b]-1 of each; lens as in gla_window_attn_fwd) go into their pages: each slot gets the
+ * last token that belongs there, slots that none does stay as they are.
+ */
+GLA_API gla_status gla_window_cache_fill(const void* k, const void* v, gla_dtype cache_dtype,
+                                         const int* lens, void* pool_k, void* pool_v,
+                                         const int* page, int n_pages, int pool_layers, int layer,
+                                         int window, int sink, int B, int T, int KV, int dk,
+                                         int dv, cudaStream_t stream);
+
+/* gla_window_attn_decode_step: token pos[n] (its position, from 0) of each active sequence: its
+ * key and value go into the page, and o[n] is the attention over all that it sees.  The page
+ * must hold the tokens before it (by gla_window_cache_fill or earlier steps).
+ *   pos          [n_active] int32 (device).  A negative position leaves its sequence untouched
+ *                and sets the device error word to GLA_ERR_RANGE
+ *   q            [n_active,H,96]   k [n_active,KV,96]   v [n_active,KV,192]   cache_dtype
+ *   o            [n_active,H,192] out_dtype: cache_dtype or GLA_FP32 (written)
+ *   workspace    gla_window_attn_decode_workspace_size() bytes, 256-byte aligned (0: not needed).
+ *                The size depends on the device current at the call.
+ * n_active == 0 returns GLA_OK without launching.
+ */
+GLA_API size_t gla_window_attn_decode_workspace_size(int n_active, int H, int KV, int window,
+                                                     int sink);
+GLA_API gla_status gla_window_attn_decode_step(void* pool_k, void* pool_v, gla_dtype cache_dtype,
+                                               const int* page, const int* pos, int n_active,
+                                               int n_pages, int pool_layers, int layer, int window,
+                                               int sink, const void* q, const void* k,
+                                               const void* v, void* o, gla_dtype out_dtype,
+                                               void* workspace, size_t workspace_bytes, int H,
+                                               int KV, int dk, int dv, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

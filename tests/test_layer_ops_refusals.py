@@ -1,5 +1,7 @@
 """The operators around the mixer refuse bad calls before they touch a device: status codes of
 the C ABI (fake addresses that nothing reads) and the binding's checks.  CPU only."""
+import ctypes
+
 import pytest
 
 import gated_linear_attention_chunked_gb300 as gla
@@ -70,12 +72,67 @@ def test_layer_norm(lib):
     assert lib.gla_layer_norm_bwd_workspace_size(0, 9) == 0
 
 
+def test_window_attn(lib):
+    def fwd(q=A, dt=0, lens=None, window=8, sink=0, o=A, ot=0, lse=None, B=1, T=9, H=4, KV=2,
+            dk=96, dv=192):
+        return lib.gla_window_attn_fwd(q, A, A, dt, lens, window, sink, o, ot, lse, B, T, H, KV,
+                                       dk, dv, None)
+    assert fwd(B=0) == INVALID and fwd(T=0) == INVALID and fwd(H=0) == INVALID
+    assert fwd(KV=3) == INVALID and fwd(KV=0) == INVALID and fwd(KV=-2) == INVALID
+    assert fwd(window=0) == INVALID and fwd(sink=-1) == INVALID
+    assert fwd(dk=64) == UNSUPPORTED and fwd(dv=96) == UNSUPPORTED
+    assert fwd(dt=1) == UNSUPPORTED and fwd(dt=0, ot=2) == UNSUPPORTED and fwd(dt=5, ot=5) == UNSUPPORTED
+    assert fwd(T=(1 << 30) + 1) == UNSUPPORTED and fwd(B=1 << 20, T=1 << 12) == UNSUPPORTED
+    assert fwd(B=1 << 28, T=1, H=16) == UNSUPPORTED
+    assert fwd(q=None) == INVALID and fwd(o=None) == INVALID
+    assert fwd(q=A + 8) == ALIGN and fwd(lens=A + 2) == ALIGN and fwd(lse=A + 2) == ALIGN
+
+    def bwd(lse=A, dO=A, dq=A, dk=A, dv=A, ws=A, wb=1 << 30, H=4, KV=2, dt=0, ot=0, st=None):
+        strides = None if st is None else (ctypes.c_longlong * 3)(*st)
+        return lib.gla_window_attn_bwd(A, A, A, dt, None, 8, 0, A, strides, ot, lse, dO, dq, dk, dv, ws, wb,
+                                       1, 9, H, KV, 96, 192, None)
+    assert bwd(KV=3) == INVALID and bwd(dt=1) == UNSUPPORTED and bwd(ot=2) == UNSUPPORTED
+    assert bwd(lse=None) == INVALID and bwd(dO=None) == INVALID and bwd(dv=None) == INVALID
+    assert bwd(st=(-192, 192, 192)) == INVALID and bwd(st=(192, 192, 194)) == ALIGN
+    need = lib.gla_window_attn_bwd_workspace_size(1, 9, 4, 2, 8, 0)
+    assert need > 0 and bwd(ws=None) == WORKSPACE and bwd(wb=need - 1) == WORKSPACE
+    assert bwd(ws=A + 16, wb=need) == ALIGN and bwd(dk=A + 8) == ALIGN
+    assert lib.gla_window_attn_bwd_workspace_size(1, 9, 4, 3, 8, 0) == 0
+
+
+def test_window_cache(lib):
+    def fill(pk=A, page=A, dt=0, P=3, PL=2, layer=0, window=8, sink=1, B=2, T=9, KV=2, lens=None):
+        return lib.gla_window_cache_fill(A, A, dt, lens, pk, A, page, P, PL, layer, window, sink,
+                                         B, T, KV, 96, 192, None)
+    assert fill(layer=2) == INVALID and fill(layer=-1) == INVALID and fill(P=0) == INVALID
+    assert fill(T=0) == INVALID and fill(window=0) == INVALID and fill(dt=1) == UNSUPPORTED
+    assert fill(window=(1 << 30) + 1) == UNSUPPORTED and fill(P=1 << 30, window=1 << 12) == UNSUPPORTED
+    assert fill(pk=None) == INVALID and fill(page=None) == INVALID
+    assert fill(pk=A + 8) == ALIGN and fill(page=A + 2) == ALIGN and fill(lens=A + 1) == ALIGN
+
+    def dec(pk=A, dt=0, page=A, pos=A, n=2, P=3, PL=2, layer=0, window=8, sink=1, o=A, ot=0,
+            ws=None, wb=0, H=4, KV=2, dk=96):
+        return lib.gla_window_attn_decode_step(pk, A, dt, page, pos, n, P, PL, layer, window, sink,
+                                               A, A, A, o, ot, ws, wb, H, KV, dk, 192, None)
+    assert dec(n=0) == 0 and dec(n=-1) == INVALID and dec(KV=3) == INVALID
+    assert dec(layer=2) == INVALID and dec(PL=0) == INVALID and dec(window=-1) == INVALID
+    assert dec(dk=64) == UNSUPPORTED and dec(dt=1) == UNSUPPORTED and dec(ot=2) == UNSUPPORTED
+    assert dec(n=1 << 29, H=16) == UNSUPPORTED
+    assert dec(window=1 << 30, sink=1) == UNSUPPORTED
+    assert dec(pos=None) == INVALID and dec(o=None) == INVALID
+    assert dec(pos=A + 2) == ALIGN and dec(pk=A + 8) == ALIGN
+    assert lib.gla_window_attn_decode_workspace_size(2, 4, 3, 8, 1) == 0
+
+
 def test_the_binding_refuses_host_tensors_and_misfits():
     torch = pytest.importorskip("torch")
     x = torch.zeros(2, 3, 4)
     for call in (lambda: gla.gated_scan_fwd(x, x), lambda: gla.layer_norm_fwd(x),
                  lambda: gla.gated_scan_decode_step(x, x, x),
-                 lambda: gla.gated_scan_decode_step_paged(x, x, x, x)):
+                 lambda: gla.gated_scan_decode_step_paged(x, x, x, x),
+                 lambda: gla.window_attn_fwd(x[None], x[None], x[None], 4),
+                 lambda: gla.window_attn_decode_step(x, x, x, x, x, x, x, 4),
+                 lambda: gla.window_cache_fill(x, x, x, x[None], x[None], 4)):
         with pytest.raises(ValueError, match="must be a CUDA tensor"):
             call()
     with pytest.raises(AttributeError):
