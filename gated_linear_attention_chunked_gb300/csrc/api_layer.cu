@@ -57,7 +57,7 @@ gla_status check_window(gla_dtype in, gla_dtype out, int window, int sink, int H
 gla_status check_window_batch(int B, int T, int H) {
   if (B <= 0 || T <= 0) return GLA_ERR_INVALID_ARG;
   if (T > (1 << 30) || (long long)B * T > (1ll << 32) / H ||
-      (long long)B * ((T + 63ll) / 64) > kMaxInt / H)
+      (long long)B * ((T + 63ll) / 64) > kMaxInt / 4 / H)
     return GLA_ERR_UNSUPPORTED;
   return GLA_OK;
 }
@@ -237,7 +237,7 @@ gla_status gla_window_attn_bwd(const void* q, const void* k, const void* v, gla_
   a.o_stride[2] = gla::kDV;
   for (int i = 0; o_strides && i < 3; ++i) {
     if (o_strides[i] < 0) return GLA_ERR_INVALID_ARG;
-    if (o_strides[i] % (out_dtype == GLA_FP32 ? 2 : 4)) return GLA_ERR_ALIGNMENT;
+    if (o_strides[i] % (out_dtype == GLA_FP32 ? 4 : 8)) return GLA_ERR_ALIGNMENT;
     a.o_stride[i] = o_strides[i];
   }
   const size_t need = gla_window_attn_bwd_workspace_size(B, T, H, KV, window, sink);

@@ -5,384 +5,676 @@
 //   dq_t = sum_s dz_ts k_s,   dk_s = sum_t dz_ts q_t,   dv_s = sum_t p_ts dO_t
 // where dk and dv also sum over the query heads that share the key head.
 //
-// Three kernels and no atomics, so that results repeat bit for bit: delta (a row sum); dk and dv
-// with a key tile held and the queries that see it walked in order, head after head; dq with a
-// query tile held and its keys walked.  Both recompute the scores.
+// window_delta_kernel takes delta (bound by HBM); window_bwd_kernel does the rest on tcgen05.  It
+// runs two kinds of items, each with a tile of 128 rows held and tiles of 64 rows streamed by:
+//   KEYS     keys held (k, v), the queries that see them streamed (q, dO), head after head:
+//              S = K Q^T, D = V dO^T, dv += P dO, dk += Z Q
+//   QUERIES  queries held (q, dO), the keys they see streamed (k, v):
+//              S = Q K^T, D = dO V^T, dq += Z K
+// with P and Z (dz) written back to tensor memory in 16 bits as the left operand.  Both recompute
+// the scores: seven products where five would do, but no sum crosses a CTA, so there are no
+// atomics on results and they repeat bit for bit.
+//   warp 8       takes items from a counter (longest kind first) and issues the TMA loads: the
+//                held tile, and a ring of four streamed tiles
+//   warp 9       lse and delta of the streamed queries, into shared memory (KEYS)
+//   warp 10      tcgen05 issuer and TMEM owner; the scores run one tile ahead of the sums
+//   warps 0..7   two per row quadrant (thread = row), each with 32 of the 64 columns: mask, P, Z;
+//                after the last tile the item's output rows
+// Keys that hold sinks are seen by every query behind them.  Those far queries are items of their
+// own, at least as long as an ordinary one and at most 16 of a key tile, whose sums go to the
+// workspace as fp32 and are added in order by window_sink_kernel.  Past four tiles of sinks the
+// items of a tile are many enough as they are, and one item takes all queries of its keys.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
+#include "scan_common.cuh"
+#include "tmap.h"
 #include "window_common.cuh"
 
 namespace gla {
 namespace {
 
-// ---- delta[b,h,t] = dO . o, one warp per (token, head); 0 past a sequence's end
+using scan::Cta;
+using scan::DRAIN_NS;
+using scan::wait;
+using scan::wait_warp;
+
+constexpr int BH = 128, BS = 64, STAGES = 4;  // rows held, rows streamed
+constexpr int kSums = kDK + kDV;              // dk and dv of a key
+constexpr uint32_t HX_BOX = 8192, HY_BOX = 16384, SX_BOX = 4096, SY_BOX = 8192;
+constexpr uint32_t H_BYTES = 3 * (HX_BOX + HY_BOX), S_BYTES = 3 * (SX_BOX + SY_BOX);
+constexpr uint32_t OFF_HX = 0, OFF_HY = 3 * HX_BOX, OFF_S = H_BYTES;
+constexpr uint32_t OFF_STAT = OFF_S + STAGES * S_BYTES;  // float [STAGES][2][64]: lse, delta
+constexpr uint32_t OFF_BAR = OFF_STAT + STAGES * 512;
+enum Bar : uint32_t {
+  FULL = 0,        // +stage
+  EMPTY = 4,       // +stage
+  STAT_FULL = 8,   // +stage
+  STAT_EMPTY = 12, // +stage
+  HELD_FULL = 16,
+  HELD_EMPTY = 17,
+  ITEM_FULL = 18,  // +slot
+  ITEM_EMPTY = 20, // +slot
+  S_FULL = 22,     // S and D are in tensor memory
+  S_READ = 23,     // ... and have been read
+  P_READY = 24,    // P and Z have been written
+  SUM_DONE = 25,   // ... and added
+  SUM_FREE = 26,   // the item's sums have been read
+  DRAIN = 27,
+  NBAR = 28
+};
+constexpr uint32_t OFF_ITEM = OFF_BAR + NBAR * 8;  // int item[2]
+constexpr uint32_t OFF_TMEM = OFF_ITEM + 8, OFF_ABORT = OFF_TMEM + 4;
+constexpr uint32_t SMEM_USED = OFF_ABORT + 4, SMEM_BYTES = SMEM_USED + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+// tensor memory columns: dv (192), dk or dq (96), S and D (64 each), P and Z (32 each)
+constexpr uint32_t TM_Y = 0, TM_X = 192, TM_S = 288, TM_D = 352, TM_P = 416, TM_Z = 448;
+
+constexpr int EW = 8, LOAD_WARP = 8, STAT_WARP = 9, MMA_WARP = 10, THREADS = 11 * 32;
+
+// How the work is cut into items, the same for every part of the call.
+struct BwdPlan {
+  int tiles;       // of 128 rows, of a sequence
+  int steps;       // streamed query tiles of an ordinary KEYS item, per head
+  int far_steps;   // ... of a far one
+  int sink_tiles;  // key tiles that hold sinks and have far queries
+  int far_parts;   // most far items of one of them
+  long long keys, far, queries;  // items
+  __host__ __device__ long long total() const { return keys + far + queries; }
+  // First streamed tile past the window's of key tile j.
+  __host__ __device__ int far_begin(int j) const { return j * (BH / BS) + steps; }
+  // Far items of key tile j of a sequence of `len` tokens.
+  __host__ __device__ int far_of(int j, int len) const {
+    const int n = (len + BS - 1) / BS - far_begin(j);
+    return n > 0 ? (n + far_steps - 1) / far_steps : 0;
+  }
+};
+BwdPlan make_plan(int B, int T, int H, int KV, int window, int sink) {
+  BwdPlan p;
+  p.tiles = (T + BH - 1) / BH;
+  p.steps = (int)(((long long)BH - 1 + window + BS - 1) / BS);
+  p.far_steps = std::max(p.steps, ((T + BS - 1) / BS + 15) / 16);
+  p.sink_tiles = 0;
+  p.far_parts = p.far_of(0, T);
+  while (sink <= 4 * BH && p.sink_tiles * BH < sink && p.sink_tiles < p.tiles && p.far_of(p.sink_tiles, T) > 0)
+    ++p.sink_tiles;
+  if (!p.sink_tiles) p.far_parts = 0;
+  p.keys = (long long)B * KV * p.tiles;
+  p.far = (long long)B * KV * p.sink_tiles * p.far_parts;
+  p.queries = (long long)B * H * p.tiles;
+  return p;
+}
+// fp32 sums of sink rows: [B][KV][sink rows][1 + far_parts][kSums].
+__host__ __device__ inline int sink_rows(const BwdPlan& p, int sink) {
+  return p.sink_tiles * BH < sink ? p.sink_tiles * BH : sink;
+}
+
+// ---- delta[b,h,t] = dO . o, eight lanes per (token, head); 0 past a sequence's end
 template <class T, class TO>
 __global__ void __launch_bounds__(256)
-window_delta_kernel(WindowArgs a, float* __restrict__ delta, DevCtl ctl) {
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);  // (b T + t) H + h
-  const int lane = threadIdx.x & 31;
-  if (row >= (long long)a.B * a.T * a.H) return;
-  const int h = (int)(row % a.H);
-  const long long bt = row / a.H;
-  const int b = (int)(bt / a.T), t = (int)(bt % a.T);
-  const int len = window_length(a.lens, b, a.T, ctl);
+window_delta_kernel(WindowArgs a, float* __restrict__ delta, int* __restrict__ counter, DevCtl ctl) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
+  const long long rows = (long long)a.B * a.T * a.H;
+  const long long row = (long long)blockIdx.x * 32 + (threadIdx.x >> 3);  // (b T + t) H + h
+  const int l = threadIdx.x & 7;
   float s = 0.f;
-  if (t < len) {
-    const T* g = static_cast<const T*>(a.dO) + row * kDV;
-    const TO* o = static_cast<const TO*>(a.o) + b * a.o_stride[0] + t * a.o_stride[1] +
-                  h * a.o_stride[2];
+  int h = 0, b = 0, t = 0;
+  if (row < rows) {
+    h = (int)(row % a.H);
+    const long long bt = row / a.H;
+    b = (int)(bt / a.T);
+    t = (int)(bt - (long long)b * a.T);
+    int len = a.T;
+    if (a.lens) {
+      len = __ldg(a.lens + b);
+      if ((len < 0 || len > a.T) && t == 0 && h == 0) record_error(ctl, DEV_RANGE);
+    }
+    if (t < len) {
+      const T* g = static_cast<const T*>(a.dO) + row * kDV;
+      const TO* o = static_cast<const TO*>(a.o) + b * a.o_stride[0] + t * a.o_stride[1] +
+                    h * a.o_stride[2];
+      Pack<T, 8> x[3];
+      Pack<TO, 8> y[3];
 #pragma unroll
-    for (int i = 0; i < kDV / 64; ++i) {
-      const int c = i * 64 + lane * 2;
-      float g0, g1, o0, o1;
-      if constexpr (__is_same(T, __half)) {
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(g + c));
-        g0 = x.x; g1 = x.y;
-      } else {
-        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(g + c));
-        g0 = x.x; g1 = x.y;
+      for (int i = 0; i < 3; ++i) {
+        x[i].template load<false>(g + (i * 8 + l) * 8);  // read again by the kernel behind
+        y[i].load(o + (i * 8 + l) * 8);
       }
-      if constexpr (sizeof(TO) == 4) {
-        const float2 x = *reinterpret_cast<const float2*>(o + c);
-        o0 = x.x; o1 = x.y;
-      } else if constexpr (__is_same(TO, __half)) {
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(o + c));
-        o0 = x.x; o1 = x.y;
-      } else {
-        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(o + c));
-        o0 = x.x; o1 = x.y;
-      }
-      s = fmaf(g0, o0, fmaf(g1, o1, s));
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = fmaf(x[i].get(j), y[i].get(j), s);
     }
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  if (lane == 0) delta[((long long)b * a.H + h) * a.T + t] = s;
+  for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (row < rows && l == 0) delta[((long long)b * a.H + h) * a.T + t] = s;
 }
 
-// ---- dk, dv: a tile of 64 keys per CTA, 16 per warp; queries in tiles of 32
-constexpr int KB = 64, QB = 32, THREADS = 128;
-constexpr int KV_Q = QB * kDK * 2, KV_G = QB * kDV * 2, KV_STAGE = KV_Q + KV_G + QB * 8;
-constexpr int KV_HELD = KB * (kDK + kDV) * 2, KV_SMEM = KV_HELD + 2 * KV_STAGE;
-
-template <class T, class TO>
-__global__ void __launch_bounds__(THREADS)
-window_dkv_kernel(WindowArgs a, const float* __restrict__ delta, DevCtl ctl) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t sm = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int tiles = (a.T + KB - 1) / KB, G = a.H / a.KV;
-  const int kv = blockIdx.x % a.KV;
-  const long long bt = blockIdx.x / a.KV;
-  const int b = (int)(bt / tiles), s0 = (int)(bt % tiles) * KB;
-  const int len = window_length(a.lens, b, a.T, ctl);
-  const int g = lane >> 2, t2 = (lane & 3) * 2;
-
-  float dk[kDK / 8][4], dv[kDV / 8][4];
-#pragma unroll
-  for (int n = 0; n < kDK / 8; ++n)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dk[n][j] = 0.f;
-#pragma unroll
-  for (int n = 0; n < kDV / 8; ++n)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dv[n][j] = 0.f;
-
-  if (s0 < len) {
-    const long long ktok = ((long long)b * a.T * a.KV + kv);
-    const T* k = static_cast<const T*>(a.k) + ktok * kDK;
-    const T* v = static_cast<const T*>(a.v) + ktok * kDV;
-    const uint32_t vs = sm + KB * kDK * 2;
-    copy_rows<kCK>(sm, k, (long long)a.KV * kDK, s0, KB, len, tid, THREADS);
-    copy_rows<kCV>(vs, v, (long long)a.KV * kDV, s0, KB, len, tid, THREADS);
-    copy_commit();
-
-    // the queries that see a key of the tile: from its first key to the end of its last key's
-    // window, or of the sequence where it holds a sink
-    const int qend = s0 < a.sink ? len : (int)min((long long)len, (long long)s0 + KB - 1 + a.window);
-    const int q_first = s0 / QB, per_head = (qend + QB - 1) / QB - q_first, n_it = per_head * G;
-    auto fetch = [&](int i) {
-      const uint32_t st = sm + KV_HELD + (i & 1) * KV_STAGE;
-      const int h = kv * G + i / per_head, t0 = (q_first + i % per_head) * QB;
-      const long long qtok = (long long)b * a.T * a.H + h;
-      copy_rows<kCK>(st, static_cast<const T*>(a.q) + qtok * kDK, (long long)a.H * kDK, t0, QB,
-                     len, tid, THREADS);
-      copy_rows<kCV>(st + KV_Q, static_cast<const T*>(a.dO) + qtok * kDV, (long long)a.H * kDV, t0,
-                     QB, len, tid, THREADS);
-      if (tid < 2 * QB) {  // lse in base 2, then delta
-        const int t = t0 + tid % QB;
-        const long long at = ((long long)b * a.H + h) * a.T + t;
-        float x = 0.f;
-        if (t < len) x = tid < QB ? a.lse[at] * kLog2e : delta[at];
-        reinterpret_cast<float*>(smem + KV_HELD + (i & 1) * KV_STAGE + KV_Q + KV_G)[tid] = x;
+// One item, as every role of a CTA sees it.
+struct Item {
+  bool keys;              // KEYS or QUERIES
+  int b, head, row0;      // sequence, key (KEYS) or query head, first held row
+  int len;                // tokens of the sequence
+  int part;               // far part, or -1
+  int first, per_head;    // KEYS: first streamed tile and tiles per head
+  int n;                  // streamed tiles in all
+  KeyTiles kt;            // QUERIES: the key tiles
+  __device__ Item() : kt(0, 1, BS, 1, 0) {}
+  __device__ void set(long long i, const WindowArgs& a, const BwdPlan& p) {
+    long long r = i;
+    keys = i < p.keys + p.far;
+    part = -1;
+    if (i < p.keys) {
+      head = (int)(r % a.KV);
+      r /= a.KV;
+      row0 = (int)(r % p.tiles) * BH;
+      b = (int)(r / p.tiles);
+    } else if (keys) {
+      r -= p.keys;
+      head = (int)(r % a.KV);
+      r /= a.KV;
+      part = (int)(r % p.far_parts);
+      r /= p.far_parts;
+      row0 = (int)(r % p.sink_tiles) * BH;
+      b = (int)(r / p.sink_tiles);
+    } else {
+      r -= p.keys + p.far;
+      head = (int)(r % a.H);
+      r /= a.H;
+      row0 = (int)(r % p.tiles) * BH;
+      b = (int)(r / p.tiles);
+    }
+    len = a.T;
+    if (a.lens) len = min(max(__ldg(a.lens + b), 0), a.T);
+    n = 0;
+    if (row0 >= len) return;
+    if (keys) {
+      const int all = (len + BS - 1) / BS;  // streamed tiles of the sequence
+      first = row0 / BS;
+      int last = row0 < a.sink && row0 / BH >= p.sink_tiles ? all : first + p.steps;
+      if (part >= 0) {
+        first = p.far_begin(row0 / BH) + part * p.far_steps;
+        last = first + p.far_steps;
       }
-      copy_commit();
-    };
-    fetch(0);
-    for (int i = 0; i < n_it; ++i) {
-      if (i + 1 < n_it) {
-        fetch(i + 1);
-        copy_wait<1>();
-      } else {
-        copy_wait<0>();
-      }
-      __syncthreads();
-      const uint32_t qs = sm + KV_HELD + (i & 1) * KV_STAGE, gs = qs + KV_Q;
-      const float* stat =
-          reinterpret_cast<const float*>(smem + KV_HELD + (i & 1) * KV_STAGE + KV_Q + KV_G);
-      const int t0 = (q_first + i % per_head) * QB;
-      float z[QB / 8][4], dp[QB / 8][4];  // [keys, queries]
-#pragma unroll
-      for (int n = 0; n < QB / 8; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) z[n][j] = dp[n][j] = 0.f;
-#pragma unroll
-      for (int c = 0; c < kDK / 16; ++c) {
-        uint32_t af[4];
-        load_a<kCK>(af, sm, w * 16, 2 * c);
-#pragma unroll
-        for (int n = 0; n < QB / 8; n += 2) {
-          uint32_t bf[4];
-          load_b<kCK>(bf, qs, n * 8, 2 * c);
-          mma16816<T>(z[n], af, bf[0], bf[1]);
-          mma16816<T>(z[n + 1], af, bf[2], bf[3]);
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < kDV / 16; ++c) {
-        uint32_t af[4];
-        load_a<kCV>(af, vs, w * 16, 2 * c);
-#pragma unroll
-        for (int n = 0; n < QB / 8; n += 2) {
-          uint32_t bf[4];
-          load_b<kCV>(bf, gs, n * 8, 2 * c);
-          mma16816<T>(dp[n], af, bf[0], bf[1]);
-          mma16816<T>(dp[n + 1], af, bf[2], bf[3]);
-        }
-      }
-      const bool whole = s0 + KB - 1 <= t0 && t0 + QB <= len &&
-                         (t0 + QB - 1 - s0 < a.window || s0 + KB <= a.sink);
-#pragma unroll
-      for (int n = 0; n < QB / 8; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = n * 8 + t2 + (j & 1), t = t0 + c, s = s0 + w * 16 + g + (j >> 1) * 8;
-          float p = ex2(fmaf(z[n][j], kLog2e, -stat[c]));
-          if (!whole && (t >= len || !window_sees(t, s, a.window, a.sink))) p = 0.f;
-          z[n][j] = p;
-          dp[n][j] = p == 0.f ? 0.f : p * (dp[n][j] - stat[QB + c]);
-        }
-#pragma unroll
-      for (int c = 0; c < QB / 16; ++c) {
-        const uint32_t pf[4] = {pack2<T>(z[2 * c][0], z[2 * c][1]),
-                                pack2<T>(z[2 * c][2], z[2 * c][3]),
-                                pack2<T>(z[2 * c + 1][0], z[2 * c + 1][1]),
-                                pack2<T>(z[2 * c + 1][2], z[2 * c + 1][3])};
-        const uint32_t df[4] = {pack2<T>(dp[2 * c][0], dp[2 * c][1]),
-                                pack2<T>(dp[2 * c][2], dp[2 * c][3]),
-                                pack2<T>(dp[2 * c + 1][0], dp[2 * c + 1][1]),
-                                pack2<T>(dp[2 * c + 1][2], dp[2 * c + 1][3])};
-#pragma unroll
-        for (int n = 0; n < kDV / 8; n += 2) {
-          uint32_t bf[4];
-          load_bt<kCV>(bf, gs, c * 16, n);
-          mma16816<T>(dv[n], pf, bf[0], bf[1]);
-          mma16816<T>(dv[n + 1], pf, bf[2], bf[3]);
-        }
-#pragma unroll
-        for (int n = 0; n < kDK / 8; n += 2) {
-          uint32_t bf[4];
-          load_bt<kCK>(bf, qs, c * 16, n);
-          mma16816<T>(dk[n], df, bf[0], bf[1]);
-          mma16816<T>(dk[n + 1], df, bf[2], bf[3]);
-        }
-      }
-      __syncthreads();
+      per_head = max(0, min(last, all) - first);
+      n = per_head * (a.H / a.KV);
+    } else {
+      kt = KeyTiles(row0, min(row0 + BH, len), BS, a.window, a.sink);
+      n = kt.n;
     }
   }
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int s = s0 + w * 16 + g + 8 * r;
-    if (s >= a.T) continue;
-    const long long row = ((long long)b * a.T + s) * a.KV + kv;  // padding: the zeros it began with
-    TO* ok = static_cast<TO*>(a.dk) + row * kDK;
-    TO* ov = static_cast<TO*>(a.dv) + row * kDV;
-    const bool live = s < len;
-#pragma unroll
-    for (int n = 0; n < kDK / 8; ++n)
-      store2(ok + n * 8 + t2, live ? dk[n][2 * r] : 0.f, live ? dk[n][2 * r + 1] : 0.f);
-#pragma unroll
-    for (int n = 0; n < kDV / 8; ++n)
-      store2(ov + n * 8 + t2, live ? dv[n][2 * r] : 0.f, live ? dv[n][2 * r + 1] : 0.f);
+  // first row and head of streamed tile i
+  __device__ int tile_row(int i) const { return (keys ? first + i % per_head : kt.tile(i)) * BS; }
+  __device__ int tile_head(int i, int G) const { return keys ? head * G + i / per_head : head / G; }
+  // columns of streamed tile i that count: fewer in the sinks' tiles in front of the window
+  __device__ int cols(int i, int sink) const {
+    return !keys && i < kt.far ? min(BS, (sink - kt.tile(i) * BS + 15) & ~15) : BS;
   }
+};
+
+// Bits 0 .. n of a 32-bit word (none for n < 0).
+__device__ __forceinline__ uint32_t bits_to(int n) {
+  return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1;
 }
 
-// ---- dq: a tile of 64 queries per CTA, 16 per warp; keys in tiles of 64
-constexpr int DQ_HELD = KB * (kDK + kDV) * 2, DQ_STAGE = KB * (kDK + kDV) * 2;
-constexpr int DQ_SMEM = DQ_HELD + 2 * DQ_STAGE;
-
-template <class T, class TO>
-__global__ void __launch_bounds__(THREADS)
-window_dq_kernel(WindowArgs a, const float* __restrict__ delta, DevCtl ctl) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t sm = smem_u32(smem), gs = sm + KB * kDK * 2;
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int tiles = (a.T + KB - 1) / KB;
-  const int h = blockIdx.x % a.H;
-  const long long bt = blockIdx.x / a.H;
-  const int b = (int)(bt / tiles), q0 = (int)(bt % tiles) * KB;
-  const int len = window_length(a.lens, b, a.T, ctl);
-  const int g = lane >> 2, t2 = (lane & 3) * 2;
-  const int r0 = q0 + w * 16 + g;
-
-  float dq[kDK / 8][4];
+// 32 bytes of outputs from fp32 values (16-byte aligned).
+template <class TO>
+__device__ __forceinline__ void store32(TO* p, const uint32_t* r, bool live) {
+  uint32_t w[8];
 #pragma unroll
-  for (int n = 0; n < kDK / 8; ++n)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dq[n][j] = 0.f;
-
-  if (q0 < len) {
-    const long long qtok = (long long)b * a.T * a.H + h;
-    const int kv = h / (a.H / a.KV);
-    const T* k = static_cast<const T*>(a.k) + ((long long)b * a.T * a.KV + kv) * kDK;
-    const T* v = static_cast<const T*>(a.v) + ((long long)b * a.T * a.KV + kv) * kDV;
-    copy_rows<kCK>(sm, static_cast<const T*>(a.q) + qtok * kDK, (long long)a.H * kDK, q0, KB, len,
-                   tid, THREADS);
-    copy_rows<kCV>(gs, static_cast<const T*>(a.dO) + qtok * kDV, (long long)a.H * kDV, q0, KB, len,
-                   tid, THREADS);
-    copy_commit();
-    float lse[2], del[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int t = r0 + 8 * r;
-      const long long at = ((long long)b * a.H + h) * a.T + t;
-      lse[r] = t < len ? a.lse[at] * kLog2e : 0.f;
-      del[r] = t < len ? delta[at] : 0.f;
-    }
-    const KeyTiles kt(q0, min(q0 + KB, len), KB, a.window, a.sink);
-    auto fetch = [&](int i) {
-      const uint32_t s = sm + DQ_HELD + (i & 1) * DQ_STAGE;
-      const int s0 = kt.tile(i) * KB;
-      copy_rows<kCK>(s, k, (long long)a.KV * kDK, s0, KB, len, tid, THREADS);
-      copy_rows<kCV>(s + KB * kDK * 2, v, (long long)a.KV * kDV, s0, KB, len, tid, THREADS);
-      copy_commit();
-    };
-    fetch(0);
-    for (int i = 0; i < kt.n; ++i) {
-      if (i + 1 < kt.n) {
-        fetch(i + 1);
-        copy_wait<1>();
-      } else {
-        copy_wait<0>();
-      }
-      __syncthreads();
-      const uint32_t ks = sm + DQ_HELD + (i & 1) * DQ_STAGE, vs = ks + KB * kDK * 2;
-      const int s0 = kt.tile(i) * KB;
-      float z[KB / 8][4], dp[KB / 8][4];
-#pragma unroll
-      for (int n = 0; n < KB / 8; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) z[n][j] = dp[n][j] = 0.f;
-#pragma unroll
-      for (int c = 0; c < kDK / 16; ++c) {
-        uint32_t af[4];
-        load_a<kCK>(af, sm, w * 16, 2 * c);
-#pragma unroll
-        for (int n = 0; n < KB / 8; n += 2) {
-          uint32_t bf[4];
-          load_b<kCK>(bf, ks, n * 8, 2 * c);
-          mma16816<T>(z[n], af, bf[0], bf[1]);
-          mma16816<T>(z[n + 1], af, bf[2], bf[3]);
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < kDV / 16; ++c) {
-        uint32_t af[4];
-        load_a<kCV>(af, gs, w * 16, 2 * c);
-#pragma unroll
-        for (int n = 0; n < KB / 8; n += 2) {
-          uint32_t bf[4];
-          load_b<kCV>(bf, vs, n * 8, 2 * c);
-          mma16816<T>(dp[n], af, bf[0], bf[1]);
-          mma16816<T>(dp[n + 1], af, bf[2], bf[3]);
-        }
-      }
-      const bool whole = s0 + KB - 1 <= q0 && s0 + KB <= len &&
-                         (q0 + KB - 1 - s0 < a.window || s0 + KB <= a.sink);
-#pragma unroll
-      for (int n = 0; n < KB / 8; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = r0 + (j >> 1) * 8, s = s0 + n * 8 + t2 + (j & 1);
-          float p = ex2(fmaf(z[n][j], kLog2e, -lse[j >> 1]));
-          if (t >= len || (!whole && (s >= len || !window_sees(t, s, a.window, a.sink)))) p = 0.f;
-          dp[n][j] = p == 0.f ? 0.f : p * (dp[n][j] - del[j >> 1]);
-        }
-#pragma unroll
-      for (int c = 0; c < KB / 16; ++c) {
-        const uint32_t df[4] = {pack2<T>(dp[2 * c][0], dp[2 * c][1]),
-                                pack2<T>(dp[2 * c][2], dp[2 * c][3]),
-                                pack2<T>(dp[2 * c + 1][0], dp[2 * c + 1][1]),
-                                pack2<T>(dp[2 * c + 1][2], dp[2 * c + 1][3])};
-#pragma unroll
-        for (int n = 0; n < kDK / 8; n += 2) {
-          uint32_t bf[4];
-          load_bt<kCK>(bf, ks, c * 16, n);
-          mma16816<T>(dq[n], df, bf[0], bf[1]);
-          mma16816<T>(dq[n + 1], df, bf[2], bf[3]);
-        }
-      }
-      __syncthreads();
-    }
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(TO) == 4) w[i] = live ? r[i] : 0u;
+    else w[i] = live ? pack2<TO>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])) : 0u;
   }
-  TO* out = static_cast<TO*>(a.dq) + ((long long)b * a.T * a.H + h) * kDK;
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int t = r0 + 8 * r;
-    if (t >= a.T) continue;
-#pragma unroll
-    for (int n = 0; n < kDK / 8; ++n)  // past the sequence: the zeros it began with
-      store2(out + (long long)t * a.H * kDK + n * 8 + t2, dq[n][2 * r], dq[n][2 * r + 1]);
-  }
+  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 template <class T, class TO>
-cudaError_t run(const WindowArgs& a, DevCtl ctl, cudaStream_t stream) {
-  float* delta = static_cast<float*>(a.workspace);
-  const long long rows = (long long)a.B * a.T * a.H, tiles = (a.T + KB - 1) / KB;
-  window_delta_kernel<T, TO><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(a, delta, ctl);
+__global__ void __launch_bounds__(THREADS, 1)
+window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
+                  const __grid_constant__ CUtensorMap held_k,
+                  const __grid_constant__ CUtensorMap held_v,
+                  const __grid_constant__ CUtensorMap held_g,
+                  const __grid_constant__ CUtensorMap str_q,
+                  const __grid_constant__ CUtensorMap str_k,
+                  const __grid_constant__ CUtensorMap str_v,
+                  const __grid_constant__ CUtensorMap str_g, WindowArgs a, BwdPlan plan,
+                  const float* __restrict__ delta, int* __restrict__ counter,
+                  float* __restrict__ sink_sums, DevCtl ctl) {
+  constexpr bool BF16 = !__is_same(T, __half);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Cta cta;
+  cta.base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  cta.sb = smem_u32(cta.base);
+  cta.bar_off = OFF_BAR;
+  cta.abort_off = OFF_ABORT;
+  uint8_t* const base = cta.base;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t* tmem_slot = (uint32_t*)(base + OFF_TMEM);
+  volatile int* items = (volatile int*)(base + OFF_ITEM);
+  if (warp == MMA_WARP) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (tid == LOAD_WARP * 32) {
+    for (uint32_t s = 0; s < STAGES; ++s) {
+      mbar_init(cta.bar(FULL + s), 1);
+      mbar_init(cta.bar(EMPTY + s), 1);
+      mbar_init(cta.bar(STAT_FULL + s), 32);
+      mbar_init(cta.bar(STAT_EMPTY + s), EW * 32);
+    }
+    mbar_init(cta.bar(HELD_FULL), 1);
+    mbar_init(cta.bar(HELD_EMPTY), 1);
+    for (uint32_t s = 0; s < 2; ++s) {
+      mbar_init(cta.bar(ITEM_FULL + s), 1);
+      mbar_init(cta.bar(ITEM_EMPTY + s), EW + 2);
+    }
+    mbar_init(cta.bar(S_FULL), 1);
+    mbar_init(cta.bar(S_READ), EW * 32);
+    mbar_init(cta.bar(P_READY), EW * 32);
+    mbar_init(cta.bar(SUM_DONE), 1);
+    mbar_init(cta.bar(SUM_FREE), EW * 32);
+    mbar_init(cta.bar(DRAIN), 1);
+    *cta.abort_flag() = 0;
+    fence_barrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int G = a.H / a.KV;
+
+  // The next item as a consumer sees it (slot m & 1): false at the end or after a give-up.  Called
+  // by whole warps, or by the single MMA thread.
+  auto next_item = [&](Item& it, int m, bool whole_warp) -> bool {
+    const uint32_t s = m & 1;
+    if (whole_warp ? !wait_warp(cta, cta.bar(ITEM_FULL + s), (m >> 1) & 1, ctl)
+                   : !wait(cta, cta.bar(ITEM_FULL + s), (m >> 1) & 1, ctl))
+      return false;
+    const int i = items[s];
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) mbar_arrive(cta.bar(ITEM_EMPTY + s));
+    if (i < 0) return false;
+    it.set(i, a, plan);
+    return true;
+  };
+
+  if (warp == LOAD_WARP) {
+    // ------------------------------------------------------------ items and TMA loads
+    if (lane == 0) {
+      Item it;
+      int n = 0, held = 0;
+      bool ok = true;
+      int ticket = atomicAdd(counter, 1);
+      for (int m = 0; ok; ++m) {
+        const uint32_t slot = m & 1;
+        if (m >= 2 && !wait(cta, cta.bar(ITEM_EMPTY + slot), ((m >> 1) - 1) & 1, ctl)) break;
+        const bool end = ticket >= plan.total();
+        items[slot] = end ? -1 : ticket;
+        mbar_arrive(cta.bar(ITEM_FULL + slot));
+        if (end) break;
+        it.set(ticket, a, plan);
+        ticket = atomicAdd(counter, 1);
+        if (it.n == 0) continue;
+        if (held > 0 && !wait(cta, cta.bar(HELD_EMPTY), (held - 1) & 1, ctl)) break;
+        ++held;
+        mbar_arrive_expect_tx(cta.bar(HELD_FULL), H_BYTES);
+        for (int j = 0; j < 3; ++j) {
+          tma_load_4d(cta.sb + OFF_HX + j * HX_BOX, it.keys ? &held_k : &held_q,
+                      cta.bar(HELD_FULL), 32 * j, it.head, it.row0, it.b);
+          tma_load_4d(cta.sb + OFF_HY + j * HY_BOX, it.keys ? &held_v : &held_g,
+                      cta.bar(HELD_FULL), 64 * j, it.head, it.row0, it.b);
+        }
+        for (int i = 0; i < it.n; ++i, ++n) {
+          const uint32_t s = n % STAGES, st = cta.sb + OFF_S + s * S_BYTES;
+          if (n >= STAGES && !(ok = wait(cta, cta.bar(EMPTY + s), (n / STAGES - 1) & 1, ctl)))
+            break;
+          const int r = it.tile_row(i), h = it.tile_head(i, G);
+          mbar_arrive_expect_tx(cta.bar(FULL + s), S_BYTES);
+          for (int j = 0; j < 3; ++j) {
+            tma_load_4d(st + j * SX_BOX, it.keys ? &str_q : &str_k, cta.bar(FULL + s), 32 * j, h,
+                        r, it.b);
+            tma_load_4d(st + 3 * SX_BOX + j * SY_BOX, it.keys ? &str_g : &str_v,
+                        cta.bar(FULL + s), 64 * j, h, r, it.b);
+          }
+        }
+      }
+      // every armed load has landed before the CTA may exit
+      for (int s = 0; s < STAGES; ++s)
+        if (n > s) mbar_wait(cta.bar(FULL + s), ((n - 1 - s) / STAGES) & 1, ctl, DRAIN_NS);
+      if (held) mbar_wait(cta.bar(HELD_FULL), (held - 1) & 1, ctl, DRAIN_NS);
+    }
+  } else if (warp == STAT_WARP) {
+    // ------------------------------------------------------------ lse and delta of the queries
+    Item it;
+    bool ok = true;
+    for (int m = 0, n = 0; ok && next_item(it, m, true); ++m) {
+      if (!it.keys) continue;
+      for (int i = 0; i < it.n; ++i, ++n) {
+        const uint32_t s = n % STAGES;
+        const int t0 = it.tile_row(i);
+        const long long at = ((long long)it.b * a.H + it.tile_head(i, G)) * a.T + t0;
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int c = lane + 32 * j;
+          x[j] = t0 + c < it.len ? __ldg(a.lse + at + c) * kLog2e : 0.f;
+          x[2 + j] = t0 + c < it.len ? __ldg(delta + at + c) : 0.f;
+        }
+        if (n >= STAGES && !(ok = wait_warp(cta, cta.bar(STAT_EMPTY + s), (n / STAGES - 1) & 1,
+                                            ctl)))
+          break;
+        float* st = (float*)(base + OFF_STAT + s * 512);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st[lane + 32 * j] = x[j];
+        mbar_arrive(cta.bar(STAT_FULL + s));
+      }
+    }
+  } else if (warp == MMA_WARP) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t ID_S = idesc_f16(128, 0, BF16, BF16, false, false);
+      constexpr uint32_t ID_Y = idesc_f16(128, kDV, BF16, BF16, false, true);
+      constexpr uint32_t ID_X = idesc_f16(128, kDK, BF16, BF16, false, true);
+      Item it;
+      int n = 0, held = 0;  // streamed tiles and items with work so far
+      bool ok = true;
+      auto scores = [&](int i, int at) -> bool {  // S, D of the item's tile i, tile `at` in all
+        const uint32_t s = at % STAGES, st = cta.sb + OFF_S + s * S_BYTES;
+        if (i == 0 && !wait(cta, cta.bar(HELD_FULL), (held - 1) & 1, ctl)) return false;
+        if (!wait(cta, cta.bar(FULL + s), (at / STAGES) & 1, ctl)) return false;
+        if (at > 0 && !wait(cta, cta.bar(S_READ), (at - 1) & 1, ctl)) return false;
+        tc_fence_after();
+        const uint32_t id = ID_S | ((uint32_t)(it.cols(i, a.sink) >> 3) << 17);
+#pragma unroll
+        for (int c = 0; c < 6; ++c)
+          mma_f16_ss(tmem + TM_S,
+                     smem_desc(cta.sb + OFF_HX + (c >> 1) * HX_BOX + (c & 1) * 32, 16, 512, SW_64),
+                     smem_desc(st + (c >> 1) * SX_BOX + (c & 1) * 32, 16, 512, SW_64), id, c > 0);
+#pragma unroll
+        for (int c = 0; c < 12; ++c)
+          mma_f16_ss(tmem + TM_D,
+                     smem_desc(cta.sb + OFF_HY + (c >> 2) * HY_BOX + (c & 3) * 32, 16, 1024, SW_128),
+                     smem_desc(st + 3 * SX_BOX + (c >> 2) * SY_BOX + (c & 3) * 32, 16, 1024, SW_128),
+                     id, c > 0);
+        mma_commit(cta.bar(S_FULL));
+        if (i == it.n - 1) mma_commit(cta.bar(HELD_EMPTY));
+        return true;
+      };
+      for (int m = 0; ok && next_item(it, m, false); ++m) {
+        if (it.n == 0) continue;
+        ++held;
+        if (!(ok = scores(0, n))) break;
+        for (int i = 0; i < it.n; ++i, ++n) {
+          const uint32_t s = n % STAGES, st = cta.sb + OFF_S + s * S_BYTES;
+          if (n == ctl.stall_step) {  // the give-up path's diagnostic (see chunk_fwd.cu)
+            wait(cta, cta.bar(DRAIN), 0, ctl);
+            ok = false;
+            break;
+          }
+          if (i + 1 < it.n && !(ok = scores(i + 1, n + 1))) break;
+          if (i == 0 && held > 1 && !(ok = wait(cta, cta.bar(SUM_FREE), (held - 2) & 1, ctl)))
+            break;
+          if (!(ok = wait(cta, cta.bar(P_READY), n & 1, ctl))) break;
+          tc_fence_after();
+          const int steps = it.cols(i, a.sink) >> 4;
+          if (it.keys) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              mma_f16_ts(tmem + TM_Y, tmem + TM_P + 8 * c,
+                         smem_desc(st + 3 * SX_BOX + c * 2048, SY_BOX, 1024, SW_128), ID_Y,
+                         i > 0 || c > 0);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c < steps)
+              mma_f16_ts(tmem + TM_X, tmem + TM_Z + 8 * c,
+                         smem_desc(st + c * 1024, SX_BOX, 512, SW_64), ID_X, i > 0 || c > 0);
+          mma_commit(cta.bar(SUM_DONE));
+          mma_commit(cta.bar(EMPTY + s));
+        }
+      }
+      mma_commit(cta.bar(DRAIN));
+      mbar_wait(cta.bar(DRAIN), 0, ctl, DRAIN_NS);
+    }
+  } else {
+    // ------------------------------------------------------------ P, Z and the output rows
+    const int q4 = warp & 3, hv = warp >> 2, row = 32 * q4 + lane;
+    const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
+    Item it;
+    int n = 0, ks = 0;  // streamed tiles; those of KEYS items
+    bool ok = true;
+    for (int m = 0; ok && next_item(it, m, true); ++m) {
+      const int r = it.row0 + row, len = it.len;  // this thread's key (KEYS) or query
+      float lse = 0.f, del = 0.f;
+      if (!it.keys && r < len) {
+        const long long at = ((long long)it.b * a.H + it.head) * a.T + r;
+        lse = __ldg(a.lse + at) * kLog2e;
+        del = __ldg(delta + at);
+      }
+      for (int i = 0; i < it.n; ++i, ++n) {
+        const uint32_t st = n % STAGES;
+        const int x0 = it.tile_row(i), c0 = x0 + 32 * hv;
+        // the columns of this half that the row sees, or is seen by
+        uint32_t see = ~0u;
+        if (it.keys) {
+          if (!(it.row0 + BH - 1 <= x0 && x0 + BS <= len &&
+                (x0 + BS - 1 - it.row0 < a.window || it.row0 + BH <= a.sink))) {
+            const int end = r < a.sink ? len - 1 : (int)min((long long)len, (long long)r + a.window) - 1;
+            see = bits_to(end - c0) & ~bits_to(r - 1 - c0);
+          }
+          if (!(ok = wait_warp(cta, cta.bar(STAT_FULL + ks % STAGES), (ks / STAGES) & 1, ctl)))
+            break;
+        } else if (!(x0 + BS - 1 <= it.row0 && x0 + BS <= len &&
+                     (it.row0 + BH - 1 - x0 < a.window || x0 + BS <= a.sink))) {
+          see = bits_to(min(r, len - 1) - c0) &
+                (~bits_to(r - a.window - c0) | bits_to(a.sink - 1 - c0));
+        }
+        if (!(ok = wait_warp(cta, cta.bar(S_FULL), n & 1, ctl))) break;
+        tc_fence_after();
+        uint32_t z[32], d[32];
+        tmem_ld32(trow + TM_S + 32 * hv, z);
+        tmem_ld32(trow + TM_D + 32 * hv, d);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(cta.bar(S_READ));
+        uint32_t pk[16], zk[16];
+        const float* stat = (const float*)(base + OFF_STAT + (ks % STAGES) * 512) + 32 * hv;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float4 l4 = make_float4(lse, lse, lse, lse), d4 = make_float4(del, del, del, del);
+          if (it.keys) {
+            l4 = *reinterpret_cast<const float4*>(stat + 4 * c);
+            d4 = *reinterpret_cast<const float4*>(stat + 64 + 4 * c);
+          }
+          const float lc[4] = {l4.x, l4.y, l4.z, l4.w}, dc[4] = {d4.x, d4.y, d4.z, d4.w};
+          float p[4], w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int x = 4 * c + e;
+            const bool v = (see >> x) & 1;
+            p[e] = ex2(fmaf(__uint_as_float(z[x]), kLog2e, -lc[e]));
+            w[e] = p[e] * (__uint_as_float(d[x]) - dc[e]);
+            p[e] = v ? p[e] : 0.f;  // selected, not multiplied: padding may hold anything
+            w[e] = v ? w[e] : 0.f;
+          }
+          pk[2 * c] = pack2<T>(p[0], p[1]);
+          pk[2 * c + 1] = pack2<T>(p[2], p[3]);
+          zk[2 * c] = pack2<T>(w[0], w[1]);
+          zk[2 * c + 1] = pack2<T>(w[2], w[3]);
+        }
+        if (it.keys) mbar_arrive(cta.bar(STAT_EMPTY + ks++ % STAGES));
+        // P's and Z's columns are free once the tile before has been added
+        if (n > 0 && !(ok = wait_warp(cta, cta.bar(SUM_DONE), (n - 1) & 1, ctl))) break;
+        tc_fence_after();
+        if (it.keys) tmem_st16(trow + TM_P + 16 * hv, pk);
+        tmem_st16(trow + TM_Z + 16 * hv, zk);
+        if (x0 + BS > len && len < a.T) {
+          // rows of padding may hold anything, and 0 x NaN is NaN: zero them (the scores, which
+          // also read them, are done)
+          const int r0 = len - x0, cnt = (BS - r0) * 36;  // 12 + 24 chunks of 16 bytes a row
+          uint8_t* const tile = base + OFF_S + st * S_BYTES;
+          for (int x = tid; x < cnt; x += EW * 32) {
+            const int rr = r0 + x / 36, c = x % 36;
+            uint8_t* p = c < 12 ? tile + (c >> 2) * SX_BOX + rr * 64 + (c & 3) * 16
+                                : tile + 3 * SX_BOX + ((c - 12) >> 3) * SY_BOX + rr * 128 +
+                                      ((c - 12) & 7) * 16;
+            *(uint4*)p = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(cta.bar(P_READY));
+      }
+      if (!ok) break;
+      if (it.n > 0) {
+        if (!(ok = wait_warp(cta, cta.bar(SUM_DONE), (n - 1) & 1, ctl))) break;
+        tc_fence_after();
+      }
+      // output rows: dv (KEYS) and dk or dq, each half of the channels
+      const bool live = r < len && it.n > 0;
+      constexpr int E = 32 / (int)sizeof(TO);  // values of 32 bytes
+      const bool sums = it.keys && r < sink_rows(plan, a.sink);  // fp32, added up later
+      float* ss = nullptr;
+      if (sums)
+        ss = sink_sums + ((((long long)it.b * a.KV + it.head) * sink_rows(plan, a.sink) + r) *
+                              (1 + plan.far_parts) + 1 + it.part) * kSums;
+      if (it.keys) {
+        TO* dv = static_cast<TO*>(a.dv) + (((long long)it.b * a.T + r) * a.KV + it.head) * kDV;
+        TO* dk = static_cast<TO*>(a.dk) + (((long long)it.b * a.T + r) * a.KV + it.head) * kDK;
+        const bool direct = !sums && it.part < 0 && r < a.T;
+#pragma unroll 1
+        for (int c = 0; c < 9; ++c) {  // 16 channels at a time: 6 of dv, 3 of dk
+          const int ch = c < 6 ? 96 * hv + 16 * c : 48 * hv + 16 * (c - 6);
+          uint32_t x[16];
+          if (it.n > 0) {
+            tmem_ld16(trow + (c < 6 ? TM_Y : TM_X) + ch, x);
+            tmem_wait_ld();
+          }
+          if (sums) {
+            store32(ss + (c < 6 ? 0 : kDV) + ch, x, live);
+            store32(ss + (c < 6 ? 0 : kDV) + ch + 8, x + 8, live);
+          } else if (direct) {
+            TO* p = (c < 6 ? dv : dk) + ch;
+#pragma unroll
+            for (int e = 0; e < 16 / E; ++e) store32(p + E * e, x + E * e, live);
+          }
+        }
+      } else {
+        TO* dq = static_cast<TO*>(a.dq) + (((long long)it.b * a.T + r) * a.H + it.head) * kDK;
+#pragma unroll 1
+        for (int c = 0; c < 3; ++c) {
+          const int ch = 48 * hv + 16 * c;
+          uint32_t x[16];
+          if (it.n > 0) {
+            tmem_ld16(trow + TM_X + ch, x);
+            tmem_wait_ld();
+          }
+          if (r < a.T)
+#pragma unroll
+            for (int e = 0; e < 16 / E; ++e) store32(dq + ch + E * e, x + E * e, live);
+        }
+      }
+      if (it.n > 0) {
+        tc_fence_before();
+        mbar_arrive(cta.bar(SUM_FREE));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dk, dv of the sinks' keys: the window's sums and the far parts', in order.
+template <class TO>
+__global__ void __launch_bounds__(kSums / 2)
+window_sink_kernel(WindowArgs a, BwdPlan plan, const float* __restrict__ sums) {
+  const int rows = sink_rows(plan, a.sink);
+  const int s = blockIdx.x % rows;
+  const long long bk = blockIdx.x / rows;
+  const int b = (int)(bk / a.KV), kv = (int)(bk % a.KV), c = threadIdx.x * 2;
+  int len = a.T;
+  if (a.lens) len = min(max(__ldg(a.lens + b), 0), a.T);
+  float x = 0.f, y = 0.f;
+  if (s < len) {
+    const float* p = sums + (bk * rows + s) * (1 + plan.far_parts) * kSums + c;
+    const int parts = 1 + plan.far_of(s / BH, len);
+    for (int k = 0; k < parts; ++k) {
+      const float2 v = *reinterpret_cast<const float2*>(p + (long long)k * kSums);
+      x += v.x;
+      y += v.y;
+    }
+  }
+  const long long row = ((long long)b * a.T + s) * a.KV + kv;
+  if (c < kDV) store2(static_cast<TO*>(a.dv) + row * kDV + c, x, y);
+  else store2(static_cast<TO*>(a.dk) + row * kDK + c - kDV, x, y);
+}
+
+// Workspace: the item counter, delta, the sinks' sums.
+size_t delta_bytes(int B, int T, int H) { return ((size_t)B * T * H * 4 + 255) & ~(size_t)255; }
+size_t sink_bytes(const BwdPlan& p, int B, int KV, int sink) {
+  return p.sink_tiles ? (size_t)B * KV * sink_rows(p, sink) * (1 + p.far_parts) * kSums * 4 : 0;
+}
+
+template <class T, class TO>
+cudaError_t run(const WindowArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream) {
+  constexpr bool bf16 = !__is_same(T, __half);
+  const BwdPlan plan = make_plan(a.B, a.T, a.H, a.KV, a.window, a.sink);
+  int* counter = static_cast<int*>(a.workspace);
+  float* delta = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + 256);
+  float* sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(delta) +
+                                         delta_bytes(a.B, a.T, a.H));
+  const long long rows = (long long)a.B * a.T * a.H;
+  window_delta_kernel<T, TO><<<(unsigned)((rows + 31) / 32), 256, 0, stream>>>(a, delta, counter,
+                                                                              ctl);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  auto dkv = window_dkv_kernel<T, TO>;
-  if ((e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, KV_SMEM)) !=
+  CUtensorMap hq, hk, hv, hg, sq, sk, sv, sg;
+  auto x = [&](CUtensorMap* m, const void* p, int heads, int rows_) {
+    return make_tmap_seq_16bit(m, p, kDK, heads, a.T, a.B, 32, rows_, CU_TENSOR_MAP_SWIZZLE_64B, bf16);
+  };
+  auto y = [&](CUtensorMap* m, const void* p, int heads, int rows_) {
+    return make_tmap_seq_16bit(m, p, kDV, heads, a.T, a.B, 64, rows_, CU_TENSOR_MAP_SWIZZLE_128B, bf16);
+  };
+  if (!x(&hq, a.q, a.H, BH) || !x(&hk, a.k, a.KV, BH) || !y(&hv, a.v, a.KV, BH) ||
+      !y(&hg, a.dO, a.H, BH) || !x(&sq, a.q, a.H, BS) || !x(&sk, a.k, a.KV, BS) ||
+      !y(&sv, a.v, a.KV, BS) || !y(&sg, a.dO, a.H, BS))
+    return cudaErrorInvalidValue;
+  auto kern = window_bwd_kernel<T, TO>;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)) !=
       cudaSuccess)
     return e;
-  dkv<<<(unsigned)(a.B * tiles * a.KV), THREADS, KV_SMEM, stream>>>(a, delta, ctl);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  auto dq = window_dq_kernel<T, TO>;
-  if ((e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, DQ_SMEM)) !=
-      cudaSuccess)
-    return e;
-  dq<<<(unsigned)(a.B * tiles * a.H), THREADS, DQ_SMEM, stream>>>(a, delta, ctl);
+  kern<<<(unsigned)std::min<long long>(plan.total(), n_sm), THREADS, SMEM_BYTES, stream>>>(
+      hq, hk, hv, hg, sq, sk, sv, sg, a, plan, delta, counter, sums, ctl);
+  if ((e = cudaGetLastError()) != cudaSuccess || !plan.sink_tiles) return e;
+  window_sink_kernel<TO><<<(unsigned)((long long)a.B * a.KV * sink_rows(plan, a.sink)), kSums / 2, 0,
+                           stream>>>(a, plan, sums);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t window_bwd_workspace_bytes(int B, int T, int H, int KV, int window, int sink) {
-  (void)KV; (void)window; (void)sink;
-  return (size_t)B * T * H * sizeof(float);
+  return 256 + delta_bytes(B, T, H) +
+         sink_bytes(make_plan(B, T, H, KV, window, sink), B, KV, sink);
 }
 
 cudaError_t launch_window_bwd(const WindowArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream) {
-  (void)n_sm;
   const bool wide = a.out_type == GLA_FP32;
   if (a.in_type == GLA_BF16)
-    return wide ? run<__nv_bfloat16, float>(a, ctl, stream)
-                : run<__nv_bfloat16, __nv_bfloat16>(a, ctl, stream);
-  return wide ? run<__half, float>(a, ctl, stream) : run<__half, __half>(a, ctl, stream);
+    return wide ? run<__nv_bfloat16, float>(a, n_sm, ctl, stream)
+                : run<__nv_bfloat16, __nv_bfloat16>(a, n_sm, ctl, stream);
+  return wide ? run<__half, float>(a, n_sm, ctl, stream) : run<__half, __half>(a, n_sm, ctl, stream);
 }
 
 }  // namespace gla

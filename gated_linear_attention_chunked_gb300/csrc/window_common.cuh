@@ -1,5 +1,6 @@
 // window_common.cuh -- which keys a query of the windowed attention sees, shared by its kernels.
 #pragma once
+#include "elem.cuh"
 #include "mma.cuh"
 #include "window_attn.h"
 
@@ -10,18 +11,6 @@ constexpr int kCK = kDK / 8, kCV = kDV / 8;  // 16-byte chunks of a key and a va
 // Query t sees key s: itself, the window - 1 tokens before it, and the first `sink` tokens.
 __device__ __forceinline__ bool window_sees(int t, int s, int window, int sink) {
   return s <= t && (t - s < window || s < sink);
-}
-
-// Tokens of sequence b: lens[b], or all T.  A length outside [0, T] is an error; it is recorded
-// and read as the nearer end.
-__device__ __forceinline__ int window_length(const int* lens, int b, int T, const DevCtl& ctl) {
-  if (!lens) return T;
-  const int n = __ldg(lens + b);
-  if (n < 0 || n > T) {
-    if (threadIdx.x == 0) record_error(ctl, DEV_RANGE);
-    return n < 0 ? 0 : T;
-  }
-  return n;
 }
 
 // The key tiles (of BN keys) that the queries [q0, q1) see: those of the window, lo .. hi, and

@@ -275,7 +275,8 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     bool ok = true;
     while (ok && it.next()) {
       const int t = it.q0 + row, len = it.len;
-      if (a.lens && it.q0 == 0 && it.h == 0 && tid == 0) window_length(a.lens, it.b, a.T, ctl);
+      if (a.lens && it.q0 == 0 && it.h == 0 && tid == 0 && __ldg(a.lens + it.b) != len)
+        record_error(ctl, DEV_RANGE);  // outside [0, T]: read as the nearer end
       const bool live_item = it.q0 < len;
       float ref = -INFINITY, sum = 0.f;
       if (live_item) {

@@ -595,7 +595,7 @@ GLA_API gla_status gla_window_attn_fwd(const void* q, const void* k, const void*
  *   o, lse       as the forward wrote them for the same inputs (o of out_dtype).  o is read row
  *                by row only, so it may be a view: o_strides, a HOST array of three element
  *                strides (sequence, token, head; non-negative, the channels adjacent, every row
- *                8-byte aligned), or NULL for the layout of the forward
+ *                16-byte aligned), or NULL for the layout of the forward
  *   dO           [B,T,H,192] in_dtype; not read on padding
  *   dq, dk, dv   the shapes of q, k, v, of out_dtype (written; 0 on padding)
  *   workspace    gla_window_attn_bwd_workspace_size() bytes, 256-byte aligned.  The size depends

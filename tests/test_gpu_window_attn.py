@@ -5,7 +5,9 @@ Bounds, with u half a step of the 16-bit type and p the softmax weights: the ker
 (relative u) for the product with v, and the output once, so |do| <= u (sum p |v| + |o|).  dv has
 the same form.  The gradient's delta takes the rounded o, off by sum |dO| |do|, and dz = p (dp -
 delta) rounds once, so dq is off by u (sum |dz| |k| + |dq|) + sum p ddelta |k|, dk alike.  Sums
-and scores in fp32 add less than 1024 roundings of 2^-24 of the sums of magnitudes."""
+and scores in fp32 add less than 1024 roundings of 2^-24 of the sums of magnitudes.  Below 2^-14
+fp16 has steps of 2^-24, so there a rounding is off by up to 2^-25 whatever the value: each p and
+dz (for o: each exp(z - m), divided by a sum of at least 1) adds TINY times what it multiplies."""
 import numpy as np
 import pytest
 
@@ -15,6 +17,7 @@ from oracle import layer_ops as ref
 pytestmark = pytest.mark.gpu
 U = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
 F = 1024 * 2.0 ** -24
+TINY = {"bf16": 0.0, "fp16": 2.0 ** -25}
 
 
 @pytest.fixture(scope="module")
@@ -60,6 +63,8 @@ CASES = [  # B, T, H, KV, window, sink, type, output type, lengths
     (1, 200, 2, 2, 7, 1000, "bf16", "bf16", None),      # every token a sink
     (3, 150, 6, 2, 64, 16, "bf16", "fp32", [64, 128, 150]),
     (1, 700, 1, 1, 129, 1, "fp16", "fp16", None),
+    (1, 700, 2, 1, 20, 600, "bf16", "bf16", [650]),     # more tiles of sinks than are cut up
+    (2, 900, 2, 2, 1, 140, "fp16", "fp32", [900, 333]), # far queries in many parts
 ]
 
 
@@ -100,14 +105,14 @@ def test_matches_the_definition(env, B, T, H, KV, window, sink, dt, out, lens):
             p = _weights(q, k, b, h, G, window, sink, n)
             K, V, D = (np.abs(x.astype(np.float64)) for x in (k[b, :n, h // G], v[b, :n, h // G],
                                                             dO[b, :n, h]))
-            do[b, :n, h] += (u + F) * (p @ V)
+            do[b, :n, h] += (u + F) * (p @ V) + TINY[dt] * ((p > 0) @ V)
             dd = (D * do[b, :n, h]).sum(1)[:, None] + F * (D * (p @ V)).sum(1)[:, None]
             dp = dO[b, :n, h].astype(np.float64) @ v[b, :n, h // G].astype(np.float64).T
             dz = np.abs(p * (dp - (p * dp).sum(1)[:, None]))
-            ez = (u + F) * dz + p * dd + F * p * (D @ V.T)
+            ez = (u + F) * dz + p * dd + F * p * (D @ V.T) + TINY[dt] * (p > 0)
             slack[0][b, :n, h] += ez @ K
             slack[1][b, :n, h // G] += ez.T @ np.abs(q[b, :n, h].astype(np.float64))
-            slack[2][b, :n, h // G] += (u + F) * (p.T @ D)
+            slack[2][b, :n, h // G] += (u + F) * (p.T @ D) + TINY[dt] * ((p > 0).T @ D)
     assert np.all(np.abs(_npy(o) - o_r) <= do + 2.0 ** -25)
     live = np.isfinite(lse_r)
     lg = _npy(lse)
@@ -177,7 +182,8 @@ def test_decode_matches_the_definition(env, N, P, PL, H, KV, window, sink, dt, o
             z = pk_r[page[n], layer, :m, h // G] @ q[n, h].astype(np.float64)
             p = np.exp(z - z.max())
             p /= p.sum()
-            slack = (u + F) * (p @ np.abs(pv_r[page[n], layer, :m, h // G])) + uo * np.abs(o_r[n, h])
+            V = np.abs(pv_r[page[n], layer, :m, h // G])
+            slack = (u + F) * (p @ V) + TINY[dt] * V.sum(0) + uo * np.abs(o_r[n, h])
             assert np.all(np.abs(_npy(o[n, h]) - o_r[n, h]) <= slack + 2.0 ** -25)
 
 
