@@ -11,17 +11,19 @@
 // A persistent grid of one CTA per SM; an item is 128 queries of one head, walked in tiles of 128
 // keys: first the ones that hold sinks (only as many columns as there are sinks, rounded to 16),
 // then the window's.
-//   warps 0..7   softmax, two per row quadrant of 32 queries, each with 64 of the 128 columns of
-//                a tile of scores (thread = row): mask, maximum (joined by the two through shared
-//                memory), exp2, weights as 16-bit pairs into tensor memory; after the item's last
-//                tile the output rows, TMA-stored
+//   warps 0..7   softmax, two groups of four warps that take the tiles in turn (thread = row, one
+//                warp per 32 queries): mask, maximum, exp2, weights as 16-bit pairs into tensor
+//                memory.  The reference goes from group to group as soon as a tile's maximum is
+//                known, so that the two work on two tiles at once
 //   warp 8       TMA loads of queries and keys (3 boxes of 32 channels, 64-byte swizzle)
 //   warp 9       TMA loads of values (3 boxes of 64 channels, 128-byte swizzle)
 //   warp 10      tcgen05 issuer and TMEM owner: S = Q K^T into one of two score buffers, O += P V
 //                with P from tensor memory
+//   warps 11..14 the output rows of an item, while the softmax is on the next one
 // The scores run two tiles ahead of the values (and across items), so that the tensor cores go
 // from P V of a tile to the scores of the next but one while the softmax works on the tile
-// between; P has columns of its own, so neither waits for the other's reads.
+// between; P has columns of its own, so neither waits for the other's reads.  A tile's scores
+// and sums are each one commit, which also frees the key and value buffers.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -43,11 +45,21 @@ constexpr int BM = 128, BN = 128;
 constexpr uint32_t K_BOX = 8192, V_BOX = 16384;  // 128 rows x 64 B, x 128 B
 constexpr uint32_t K_BYTES = 3 * K_BOX, V_BYTES = 3 * V_BOX;
 constexpr uint32_t OFF_Q = 0, OFF_K = 2 * K_BYTES, OFF_V = 4 * K_BYTES;
-constexpr uint32_t OFF_STG = OFF_V + 2 * V_BYTES;  // output staging, 2 KB per softmax warp
-constexpr uint32_t OFF_EX = OFF_STG + 8 * 2048;    // float ex[2][2][128]: halves' row maxima
-constexpr uint32_t OFF_EL = OFF_EX + 2048;         // float el[2][128]: halves' row sums
-constexpr uint32_t OFF_BAR = OFF_EL + 1024;
-constexpr uint32_t NBAR = 27;
+constexpr uint32_t OFF_STG = OFF_V + 2 * V_BYTES;  // output staging, 4 KB per output warp
+constexpr uint32_t OFF_REF = OFF_STG + 4 * 4096;   // float ref[2][128]: each group's reference
+constexpr uint32_t OFF_SUM = OFF_REF + 1024;       // float2 sum[2][2][128]: (sum, ref), by item
+constexpr uint32_t OFF_BAR = OFF_SUM + 4096;
+enum Bar : uint32_t {  // +stage (+4 group + quadrant, + quadrant) where there are several
+  Q_FULL = 0, K_FULL = 2, V_FULL = 4,
+  S_FULL = 6,    // a tile's scores are in tensor memory (and its keys have been read)
+  O_DONE = 8,    // O += P V has run: P, V and O are free to touch
+  P_READY = 10,  // a group has written P (and read S)
+  O_FREE = 11,   // the output rows have been read
+  DRAIN = 12,
+  REF = 13,      // a group's references of a tile are known
+  SUM = 21,      // both groups' sums of an item are known
+  NBAR = 25
+};
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
 constexpr uint32_t SMEM_USED = OFF_ABORT + 4, SMEM_BYTES = SMEM_USED + 1024;
@@ -55,36 +67,26 @@ static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_P = 448;  // columns: S 2 x 128, O 192, P 64
 
-enum Bar : uint32_t {  // +stage where two
-  Q_FULL = 0, Q_EMPTY = 2, K_FULL = 4, K_EMPTY = 6, V_FULL = 8, V_EMPTY = 10, S_FULL = 12,
-  P_READY = 14,  // the softmax group has written P (and read S)
-  O_DONE = 15,   // O += P V has run (P, V and O are free to touch)
-  O_FREE = 16,   // the output rows have been read
-  DRAIN = 17,
-  PX = 18,       // 18..21: quadrant's two warps have their row maxima
-  PL = 22,       // 22..25: ... their row sums
-};
-constexpr int SM_WARPS = 8, K_WARP = 8, V_WARP = 9, MMA_WARP = 10, THREADS = 11 * 32;
+constexpr int GROUP = 128, K_WARP = 8, V_WARP = 9, MMA_WARP = 10, OUT_WARP = 11;
+constexpr int THREADS = 15 * 32;
 
 // The items of a CTA, blockIdx.x, + gridDim.x, ...: heads fastest, then tiles of a sequence.
 struct Items {
   const WindowArgs& a;
-  const DevCtl& ctl;
-  long long at, total;
-  int tiles;
+  unsigned at, total, tiles;  // the host keeps the count of items below 2^30
   int b, h, q0, len;
-  __device__ Items(const WindowArgs& a_, const DevCtl& c) : a(a_), ctl(c) {
+  __device__ Items(const WindowArgs& a_) : a(a_) {
     tiles = (a.T + BM - 1) / BM;
-    total = (long long)a.B * tiles * a.H;
-    at = (long long)blockIdx.x - gridDim.x;
+    total = (unsigned)a.B * tiles * a.H;
+    at = blockIdx.x - gridDim.x;
   }
   __device__ bool next() {
     at += gridDim.x;
     if (at >= total) return false;
-    h = (int)(at % a.H);
-    const long long r = at / a.H;
+    const unsigned r = at / (unsigned)a.H;
+    h = (int)(at - r * a.H);
     b = (int)(r / tiles);
-    q0 = (int)(r % tiles) * BM;
+    q0 = (int)(r - b * tiles) * BM;
     len = a.T;
     if (a.lens) len = min(max(__ldg(a.lens + b), 0), a.T);
     return true;
@@ -101,17 +103,38 @@ struct Items {
 __device__ __forceinline__ int tile_cols(const KeyTiles& kt, int i, int sink) {
   return i < kt.far ? min(BN, (sink - kt.tile(i) * BN + 15) & ~15) : BN;
 }
-// Bits 0 .. n of a 64-bit word (none for n < 0).
-__device__ __forceinline__ uint64_t bits_to(int n) {
-  return n < 0 ? 0ull : n >= 63 ? ~0ull : (2ull << n) - 1;
+// Bits 0 .. n of a 32-bit word (none for n < 0).
+__device__ __forceinline__ uint32_t bits_to(int n) {
+  return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1;
+}
+// (a0, a1) * b + c and (a0, a1) + (b0, b1): two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
 }
 
-template <bool BF16, bool WIDE>
+template <class T, class TO>
 __global__ void __launch_bounds__(THREADS, 1)
 window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
                   const __grid_constant__ CUtensorMap map_k,
-                  const __grid_constant__ CUtensorMap map_v,
-                  const __grid_constant__ CUtensorMap map_o, WindowArgs a, DevCtl ctl) {
+                  const __grid_constant__ CUtensorMap map_v, WindowArgs a, DevCtl ctl) {
+  constexpr bool BF16 = !__is_same(T, __half), WIDE = sizeof(TO) == 4;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Cta cta;
   cta.base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -127,20 +150,16 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   }
   if (tid == K_WARP * 32) {
     for (uint32_t i = 0; i < P_READY; ++i) mbar_init(cta.bar(i), 1);
-    mbar_init(cta.bar(P_READY), SM_WARPS * 32);
-    mbar_init(cta.bar(O_DONE), 1);
-    mbar_init(cta.bar(O_FREE), SM_WARPS * 32);
+    mbar_init(cta.bar(P_READY), GROUP);
+    mbar_init(cta.bar(O_FREE), GROUP);
     mbar_init(cta.bar(DRAIN), 1);
-    for (uint32_t q = 0; q < 4; ++q) {
-      mbar_init(cta.bar(PX + q), 64);
-      mbar_init(cta.bar(PL + q), 64);
-    }
+    for (uint32_t q = REF; q < SUM; ++q) mbar_init(cta.bar(q), 32);
+    for (uint32_t q = SUM; q < NBAR; ++q) mbar_init(cta.bar(q), 64);
     *cta.abort_flag() = 0;
     fence_barrier_init();
     prefetch_tensormap(&map_q);
     prefetch_tensormap(&map_k);
     prefetch_tensormap(&map_v);
-    prefetch_tensormap(&map_o);
   }
   tc_fence_before();
   __syncthreads();
@@ -151,20 +170,24 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   if (warp == K_WARP) {
     // ------------------------------------------------------------ TMA: queries and keys
     if (lane == 0) {
-      Items it(a, ctl);
-      int n = 0, m = 0;  // key tiles and items so far
+      Items it(a);
+      int n = 0, m = 0, q_armed = 0;  // key tiles and items so far
       bool ok = true;
       for (; ok && it.next_live(); ++m) {
         const uint32_t qs = m & 1;
-        if (m >= 2 && !wait(cta, cta.bar(Q_EMPTY + qs), ((m >> 1) - 1) & 1, ctl)) break;
-        mbar_arrive_expect_tx(cta.bar(Q_FULL + qs), K_BYTES);
-        for (int j = 0; j < 3; ++j)
-          tma_load_4d(cta.sb + OFF_Q + qs * K_BYTES + j * K_BOX, &map_q, cta.bar(Q_FULL + qs),
-                      32 * j, it.h, it.q0, it.b);
         const KeyTiles kt = it.keys();
         for (int i = 0; i < kt.n; ++i, ++n) {
           const uint32_t s = n & 1;
-          if (n >= 2 && !(ok = wait(cta, cta.bar(K_EMPTY + s), ((n >> 1) - 1) & 1, ctl))) break;
+          if (n >= 2 && !(ok = wait(cta, cta.bar(S_FULL + s), ((n >> 1) - 1) & 1, ctl))) break;
+          // with an item between, the scores of two tiles ago are past the item before it: its
+          // queries' buffer is free
+          if (i == 0) {
+            ++q_armed;
+            mbar_arrive_expect_tx(cta.bar(Q_FULL + qs), K_BYTES);
+            for (int j = 0; j < 3; ++j)
+              tma_load_4d(cta.sb + OFF_Q + qs * K_BYTES + j * K_BOX, &map_q, cta.bar(Q_FULL + qs),
+                          32 * j, it.h, it.q0, it.b);
+          }
           mbar_arrive_expect_tx(cta.bar(K_FULL + s), K_BYTES);
           for (int j = 0; j < 3; ++j)
             tma_load_4d(cta.sb + OFF_K + s * K_BYTES + j * K_BOX, &map_k, cta.bar(K_FULL + s),
@@ -174,20 +197,20 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       // every armed load has landed before the CTA may exit
       for (int s = 0; s < 2; ++s) {
         if (n > s) mbar_wait(cta.bar(K_FULL + s), ((n - 1 - s) >> 1) & 1, ctl, DRAIN_NS);
-        if (m > s) mbar_wait(cta.bar(Q_FULL + s), ((m - 1 - s) >> 1) & 1, ctl, DRAIN_NS);
+        if (q_armed > s) mbar_wait(cta.bar(Q_FULL + s), ((q_armed - 1 - s) >> 1) & 1, ctl, DRAIN_NS);
       }
     }
   } else if (warp == V_WARP) {
     // ------------------------------------------------------------ TMA: values
     if (lane == 0) {
-      Items it(a, ctl);
+      Items it(a);
       int n = 0;
       bool ok = true;
       while (ok && it.next_live()) {
         const KeyTiles kt = it.keys();
         for (int i = 0; i < kt.n; ++i, ++n) {
           const uint32_t s = n & 1;
-          if (n >= 2 && !(ok = wait(cta, cta.bar(V_EMPTY + s), ((n >> 1) - 1) & 1, ctl))) break;
+          if (n >= 2 && !(ok = wait(cta, cta.bar(O_DONE + s), ((n >> 1) - 1) & 1, ctl))) break;
           mbar_arrive_expect_tx(cta.bar(V_FULL + s), V_BYTES);
           for (int j = 0; j < 3; ++j)
             tma_load_4d(cta.sb + OFF_V + s * V_BYTES + j * V_BOX, &map_v, cta.bar(V_FULL + s),
@@ -202,7 +225,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     if (lane == 0) {
       constexpr uint32_t ID_PV = idesc_f16(128, 192, BF16, BF16, false, true);
       // the scores' walk (two tiles ahead) and the values'
-      Items si(a, ctl), vi(a, ctl);
+      Items si(a), vi(a);
       KeyTiles sk(0, 1, BN, 1, 0), vk(0, 1, BN, 1, 0);
       int sn = 0, sm = -1, s_at = 0, vn = 0, vm = -1, v_at = 0;
       bool s_live = si.next_live();
@@ -222,10 +245,8 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
                      smem_desc(k + off, 16, 512, SW_64), id | cols, c > 0);
         }
         mma_commit(cta.bar(S_FULL + s));
-        mma_commit(cta.bar(K_EMPTY + s));
         ++sn;
         if (++s_at == sk.n) {
-          mma_commit(cta.bar(Q_EMPTY + qs));
           s_at = 0;
           if ((s_live = si.next_live())) { sk = si.keys(); ++sm; }
         }
@@ -255,172 +276,252 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
             if (c < steps)
               mma_f16_ts(tmem + TM_O, tmem + TM_P + 8 * c,
                          smem_desc(v + c * 2048, V_BOX, 1024, SW_128), ID_PV, v_at > 0 || c > 0);
-          mma_commit(cta.bar(O_DONE));
-          mma_commit(cta.bar(V_EMPTY + s));
+          mma_commit(cta.bar(O_DONE + s));
           if (s_live && !(ok = scores())) break;
         }
       }
       mma_commit(cta.bar(DRAIN));
       mbar_wait(cta.bar(DRAIN), 0, ctl, DRAIN_NS);
     }
-  } else {
-    // ------------------------------------------------------------ softmax and output
-    const int q4 = warp & 3, hv = warp >> 2, row = 32 * q4 + lane;
+  } else if (warp < K_WARP) {
+    // ------------------------------------------------------------ softmax
+    // Group g takes the CTA's tiles of parity g, whose scores are in buffer g.  ref and the sums
+    // are in base 2.
+    const int q4 = warp & 3, g = warp >> 2, row = 32 * q4 + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
-    float* ex = (float*)(base + OFF_EX);
-    float* el = (float*)(base + OFF_EL);
-    uint8_t* const stg = base + OFF_STG + warp * 2048;
-    Items it(a, ctl);
-    int n = 0, m = 0;
+    float* refs = (float*)(base + OFF_REF);
+    float2* sums = (float2*)(base + OFF_SUM);
+    Items it(a);
+    int n0 = 0;  // tiles before this item
     bool ok = true;
-    while (ok && it.next()) {
+    for (int m = 0; ok && it.next_live(); ++m) {
       const int t = it.q0 + row, len = it.len;
-      if (a.lens && it.q0 == 0 && it.h == 0 && tid == 0 && __ldg(a.lens + it.b) != len)
-        record_error(ctl, DEV_RANGE);  // outside [0, T]: read as the nearer end
-      const bool live_item = it.q0 < len;
-      float ref = -INFINITY, sum = 0.f;
-      if (live_item) {
-        const KeyTiles kt = it.keys();
-        for (int i = 0; i < kt.n; ++i, ++n) {
-          const uint32_t s = n & 1;
-          const int s0 = kt.tile(i) * BN;
-          if (!(ok = wait_warp(cta, cta.bar(S_FULL + s), (n >> 1) & 1, ctl))) break;
-          tc_fence_after();
-          uint32_t z[2][32];
-          tmem_ld32(trow + TM_S + 128 * s + 64 * hv, z[0]);
-          tmem_ld32(trow + TM_S + 128 * s + 64 * hv + 32, z[1]);
-          tmem_wait_ld();
-          const bool whole = s0 + BN - 1 <= it.q0 && s0 + BN <= len &&
-                             (it.q0 + BM - 1 - s0 < a.window || s0 + BN <= a.sink);
-          if (!whole) {
-            const int c0 = s0 + 64 * hv;
-            const uint64_t see = bits_to(min(t, len - 1) - c0) &
-                                 (~bits_to(t - a.window - c0) | bits_to(a.sink - 1 - c0));
-            const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
+      float ref = -INFINITY, sum = 0.f;  // this row's, as of the group's last tile
+      const KeyTiles kt = it.keys();
+      for (int i = (n0 ^ g) & 1; i < kt.n; i += 2) {
+        const int n = n0 + i, s0 = kt.tile(i) * BN;
+        const bool whole = s0 + BN - 1 <= it.q0 && s0 + BN <= len &&
+                           (it.q0 + BM - 1 - s0 < a.window || s0 + BN <= a.sink);
+        // the columns 32 c .. of the tile that this row sees
+        auto sees = [&](int c) -> uint32_t {
+          const int c0 = s0 + 32 * c;
+          return bits_to(min(t, len - 1) - c0) &
+                 (~bits_to(t - a.window - c0) | bits_to(a.sink - 1 - c0));
+        };
+        if (!(ok = wait_warp(cta, cta.bar(S_FULL + g), (n >> 1) & 1, ctl))) break;
+        tc_fence_after();
+        const uint32_t ts = trow + TM_S + 128 * g;
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto maxima = [&](const uint32_t (&z)[32]) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if (!((lo >> c) & 1)) z[0][c] = 0xFF800000u;  // -inf
-              if (!((hi >> c) & 1)) z[1][c] = 0xFF800000u;
-            }
-          }
-          float t4[4];
+          for (int j = 0; j < 16; ++j)
+            m4[j & 3] = max3(m4[j & 3], __uint_as_float(z[2 * j]), __uint_as_float(z[2 * j + 1]));
+        };
+        if (whole) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            t4[j] = fmaxf(__uint_as_float(z[j & 1][j]), __uint_as_float(z[j & 1][j + 4]));
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            t4[c & 3] = fmaxf(t4[c & 3], __uint_as_float(z[0][c]));
-            t4[(c + 2) & 3] = fmaxf(t4[(c + 2) & 3], __uint_as_float(z[1][c]));
+          for (int c = 0; c < 4; ++c) {
+            uint32_t z[32];
+            tmem_ld32(ts + 32 * c, z);
+            tmem_wait_ld();
+            maxima(z);
           }
-          float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-          ex[(n & 1) * 256 + hv * 128 + row] = top;
-          mbar_arrive(cta.bar(PX + q4));
-          if (!(ok = wait_warp(cta, cta.bar(PX + q4), n & 1, ctl))) break;
-          top = fmaxf(top, ex[(n & 1) * 256 + (hv ^ 1) * 128 + row]) * kLog2e;
-          // ref, sum: in base 2; a row that has seen nothing yet has o = 0 and takes any scale
-          float scale = 1.f;
-          if (top > ref + 8.f) {
-            if (ref != -INFINITY) scale = ex2(ref - top);
-            ref = top;
-          }
-          const float sub = ref == -INFINITY ? 0.f : ref;
-          sum *= scale;
-          uint32_t p[32];
-          float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float x = ex2(fmaf(__uint_as_float(z[c >> 4][(2 * c) & 31]), kLog2e, -sub));
-            const float y = ex2(fmaf(__uint_as_float(z[c >> 4][(2 * c + 1) & 31]), kLog2e, -sub));
-            s4[c & 1] += x;
-            s4[2 + (c & 1)] += y;
-            p[c] = BF16 ? pack2<__nv_bfloat16>(x, y) : pack2<__half>(x, y);
-          }
-          sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-          // P's columns and, for the rescaling, O are free once the tile before has been added
-          if (n > 0 && !(ok = wait_warp(cta, cta.bar(O_DONE), (n - 1) & 1, ctl))) break;
-          tc_fence_after();
-          if (i > 0 && __any_sync(0xffffffffu, scale != 1.f)) {
+        } else {
 #pragma unroll 1
-            for (int c = 0; c < 3; ++c) {
-              uint32_t o[32];
-              tmem_ld32(trow + TM_O + 96 * hv + 32 * c, o);
-              tmem_wait_ld();
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t see = sees(c);
+            if (!__any_sync(0xffffffffu, see != 0u)) continue;
+            uint32_t z[32];
+            tmem_ld32(ts + 32 * c, z);
+            tmem_wait_ld();
+            if (!__all_sync(0xffffffffu, see == ~0u))
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * scale);
-              tmem_st32(trow + TM_O + 96 * hv + 32 * c, o);
+              for (int j = 0; j < 32; ++j)
+                if (!((see >> j) & 1)) z[j] = 0xFF800000u;  // -inf
+            maxima(z);
+          }
+        }
+        const float top = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * kLog2e;
+        // the other group's reference of the tile before (and, as the item begins, no more
+        // than its word that it is past that tile)
+        if (n > 0 &&
+            !(ok = wait_warp(cta, cta.bar(REF + 4 * (g ^ 1) + q4), ((n - 1) >> 1) & 1, ctl)))
+          break;
+        const float before = i > 0 ? refs[(g ^ 1) * 128 + row] : -INFINITY;
+        // a row that has seen nothing yet has o = 0 and takes any scale
+        const float now = top > before + 8.f ? top : before;
+        refs[g * 128 + row] = now;
+        mbar_arrive(cta.bar(REF + 4 * g + q4));
+        const float scale = now == before || before == -INFINITY ? 1.f : ex2(before - now);
+        if (now != ref) sum = ref == -INFINITY ? 0.f : sum * ex2(ref - now);
+        ref = now;
+        const float sub = ref == -INFINITY ? 0.f : -ref;
+        const float2 sub2 = make_float2(sub, sub), l2e = make_float2(kLog2e, kLog2e);
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // weights of 32 columns from their scores, as pairs, and their sum
+        auto weights = [&](const uint32_t (&z)[32], uint32_t (&p)[16], uint32_t see, bool masked) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float2 x = fma2(make_float2(__uint_as_float(z[2 * j]), __uint_as_float(z[2 * j + 1])),
+                            l2e, sub2);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            if (masked) {
+              x.x = (see >> (2 * j)) & 1 ? x.x : 0.f;
+              x.y = (see >> (2 * j + 1)) & 1 ? x.y : 0.f;
             }
+            acc[j & 1] = add2(acc[j & 1], x);
+            p[j] = pack2<T>(x.x, x.y);
           }
-          tmem_st32(trow + TM_P + 32 * hv, p);
-          if (s0 + BN > len && len < a.T) {
-            // values of padding may be anything, and 0 x NaN is NaN: zero their rows
-            if (!(ok = wait_warp(cta, cta.bar(V_FULL + s), (n >> 1) & 1, ctl))) break;
-            const int r0 = len - s0, cnt = (BN - r0) * 24;
-            for (int x = tid; x < cnt; x += SM_WARPS * 32)
-              *(uint4*)(base + OFF_V + s * V_BYTES + (x % 24 / 8) * V_BOX + (r0 + x / 24) * 128 +
-                        (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async();
+        };
+        // P's columns and, for the rescaling, O are free once the tile before has been added
+        auto free_p = [&]() -> bool {
+          if (n > 0 &&
+              !(ok = wait_warp(cta, cta.bar(O_DONE + (g ^ 1)), ((n - 1) >> 1) & 1, ctl)))
+            return false;
+          tc_fence_after();
+          return true;
+        };
+        if (whole) {  // all weights first: once P is free they only have to be written
+          uint32_t p[4][16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t z[32];
+            tmem_ld32(ts + 32 * c, z);
+            tmem_wait_ld();
+            weights(z, p[c], 0u, false);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(cta.bar(P_READY));
+          if (!free_p()) break;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_st16(trow + TM_P + 16 * c, p[c]);
+        } else if (free_p()) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t see = sees(c);
+            uint32_t p[16];
+            if (__any_sync(0xffffffffu, see != 0u)) {
+              uint32_t z[32];
+              tmem_ld32(ts + 32 * c, z);
+              tmem_wait_ld();
+              if (__all_sync(0xffffffffu, see == ~0u)) weights(z, p, 0u, false);
+              else weights(z, p, see, true);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) p[j] = 0u;
+            }
+            tmem_st16(trow + TM_P + 16 * c, p);
+          }
         }
         if (!ok) break;
-        // the row's sum: both halves'
-        el[hv * 128 + row] = sum;
-        mbar_arrive(cta.bar(PL + q4));
-        if (!(ok = wait_warp(cta, cta.bar(PL + q4), m & 1, ctl))) break;
-        sum += el[(hv ^ 1) * 128 + row];
-        if (!(ok = wait_warp(cta, cta.bar(O_DONE), (n - 1) & 1, ctl))) break;
+        acc[0] = add2(acc[0], acc[1]);
+        sum += acc[0].x + acc[0].y;
+        if (i > 0 && __any_sync(0xffffffffu, scale != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < 6; ++c) {
+            uint32_t o[32];
+            tmem_ld32(trow + TM_O + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * scale);
+            tmem_st32(trow + TM_O + 32 * c, o);
+          }
+        }
+        if (s0 + BN > len && len < a.T) {
+          // values of padding may be anything, and 0 x NaN is NaN: zero their rows
+          if (!(ok = wait_warp(cta, cta.bar(V_FULL + g), (n >> 1) & 1, ctl))) break;
+          const int r0 = len - s0, cnt = (BN - r0) * 24;
+          for (int x = row; x < cnt; x += GROUP)
+            *(uint4*)(base + OFF_V + g * V_BYTES + (x % 24 / 8) * V_BOX + (r0 + x / 24) * 128 +
+                      (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(cta.bar(P_READY));
+      }
+      if (!ok) break;
+      n0 += kt.n;
+      // one item at a time: the output warps have taken the sums of the item before
+      if (m > 0 && !(ok = wait_warp(cta, cta.bar(O_FREE), (m - 1) & 1, ctl))) break;
+      sums[(m & 1) * 256 + g * 128 + row] = make_float2(sum, ref);
+      mbar_arrive(cta.bar(SUM + q4));
+    }
+  } else {
+    // ------------------------------------------------------------ output rows
+    const int q4 = warp & 3, row = 32 * q4 + lane;  // the quadrant that the warp may read
+    const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
+    const float2* sums = (const float2*)(base + OFF_SUM);
+    uint8_t* const stg = base + OFF_STG + q4 * 4096;
+    constexpr int CB = WIDE ? 16 : 32;  // channels of 64 bytes
+    Items it(a);
+    int n0 = 0, m = 0;
+    while (it.next()) {
+      const int t = it.q0 + row;
+      const bool live_item = it.q0 < it.len, live = t < it.len;
+      if (a.lens && it.q0 == 0 && it.h == 0 && tid == OUT_WARP * 32 &&
+          __ldg(a.lens + it.b) != it.len)
+        record_error(ctl, DEV_RANGE);  // outside [0, T]: read as the nearer end
+      float ref = -INFINITY, sum = 0.f;
+      if (live_item) {
+        n0 += it.keys().n;
+        if (!wait_warp(cta, cta.bar(SUM + q4), m & 1, ctl)) break;
+        const float2 s0 = sums[(m & 1) * 256 + row], s1 = sums[(m & 1) * 256 + 128 + row];
+        ref = fmaxf(s0.y, s1.y);
+        if (s0.y != -INFINITY) sum = s0.x * ex2(s0.y - ref);
+        if (s1.y != -INFINITY) sum = fmaf(s1.x, ex2(s1.y - ref), sum);
+        // the tile before the last has been added (its softmax waited for that): this is the
+        // last one's phase
+        if (!wait_warp(cta, cta.bar(O_DONE + ((n0 - 1) & 1)), ((n0 - 1) >> 1) & 1, ctl)) break;
         tc_fence_after();
         ++m;
       }
-      const bool live = t < len;
       const float inv = live ? 1.f / sum : 0.f;
-      const int t0 = it.q0 + 32 * q4;
-      constexpr int CB = WIDE ? 16 : 32;  // channels of a 64-byte staged row
+      TO* const out =
+          static_cast<TO*>(a.o) + (((long long)it.b * a.T + it.q0 + 32 * q4) * a.H + it.h) * kDV;
+      // 32 rows of 128 bytes at a time go through shared memory, so that eight lanes write a row
 #pragma unroll 1
-      for (int k = 0; k < 96 / CB; ++k) {
-        uint32_t o[CB];
-        if (live_item) {
-          if constexpr (WIDE) tmem_ld16(trow + TM_O + 96 * hv + CB * k, o);
-          else tmem_ld32(trow + TM_O + 96 * hv + CB * k, o);
-          tmem_wait_ld();
-        }
-        if (lane == 0) bulk_wait_read<0>();  // the store before has read the staging
+      for (int k = 0; k < kDV / (2 * CB); ++k) {
         __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint4 u;
-          uint32_t* w = &u.x;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (WIDE) {
-              w[e] = live ? __float_as_uint(__uint_as_float(o[4 * c + e]) * inv) : 0u;
-            } else {
-              const float x = __uint_as_float(o[8 * c + 2 * e]) * inv;
-              const float y = __uint_as_float(o[8 * c + 2 * e + 1]) * inv;
-              w[e] = !live ? 0u : BF16 ? pack2<__nv_bfloat16>(x, y) : pack2<__half>(x, y);
-            }
+        for (int e = 0; e < 2; ++e) {
+          uint32_t o[CB];
+          if (live_item) {
+            if constexpr (WIDE) tmem_ld16(trow + TM_O + CB * (2 * k + e), o);
+            else tmem_ld32(trow + TM_O + CB * (2 * k + e), o);
+            tmem_wait_ld();
           }
-          *(uint4*)(stg + swz_off(lane, c, 64)) = u;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if constexpr (WIDE) {
+                w[j] = live ? __float_as_uint(__uint_as_float(o[4 * c + j]) * inv) : 0u;
+              } else {
+                const float lo = __uint_as_float(o[8 * c + 2 * j]) * inv;
+                const float hi = __uint_as_float(o[8 * c + 2 * j + 1]) * inv;
+                w[j] = live ? pack2<TO>(lo, hi) : 0u;
+              }
+            }
+            *(uint4*)(stg + swz_off(lane, 4 * e + c, 128)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
-        fence_proxy_async();
+        if (k == kDV / (2 * CB) - 1 && live_item) {
+          tc_fence_before();
+          mbar_arrive(cta.bar(O_FREE));
+        }
         __syncwarp();
-        if (lane == 0 && t0 < a.T) {
-          tma_store_4d(&map_o, smem_u32(stg), 96 * hv + CB * k, it.h, t0, it.b);
-          bulk_commit();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int r = 4 * c + (lane >> 3);
+          const uint4 x = *(const uint4*)(stg + swz_off(r, lane & 7, 128));
+          if (it.q0 + 32 * q4 + r < a.T)
+            reinterpret_cast<uint4*>(out + (long long)r * a.H * kDV + 2 * CB * k)[lane & 7] = x;
         }
       }
-      if (live_item) {
-        tc_fence_before();
-        mbar_arrive(cta.bar(O_FREE));
-      }
-      if (a.lse && hv == 0 && t < a.T)
+      if (a.lse && t < a.T)
         a.lse[((long long)it.b * a.H + it.h) * a.T + t] =
             live ? (ref + log2f(sum)) * kLn2 : -INFINITY;
     }
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
   }
 
   tc_fence_before();
@@ -431,26 +532,31 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   }
 }
 
-}  // namespace
-
-cudaError_t launch_window_fwd(const WindowArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream) {
-  const bool bf16 = a.in_type == GLA_BF16, wide = a.out_type == GLA_FP32;
-  CUtensorMap mq, mk, mv, mo;
+template <class T, class TO>
+cudaError_t run(const WindowArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream) {
+  constexpr bool bf16 = !__is_same(T, __half);
+  CUtensorMap mq, mk, mv;
   if (!make_tmap_seq_16bit(&mq, a.q, kDK, a.H, a.T, a.B, 32, BM, CU_TENSOR_MAP_SWIZZLE_64B, bf16) ||
       !make_tmap_seq_16bit(&mk, a.k, kDK, a.KV, a.T, a.B, 32, BN, CU_TENSOR_MAP_SWIZZLE_64B, bf16) ||
-      !make_tmap_seq_16bit(&mv, a.v, kDV, a.KV, a.T, a.B, 64, BN, CU_TENSOR_MAP_SWIZZLE_128B, bf16) ||
-      !(wide ? make_tmap_seq_out_f32(&mo, a.o, kDV, a.H, a.T, a.B)
-             : make_tmap_seq_16bit(&mo, a.o, kDV, a.H, a.T, a.B, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
-                                   bf16)))
+      !make_tmap_seq_16bit(&mv, a.v, kDV, a.KV, a.T, a.B, 64, BN, CU_TENSOR_MAP_SWIZZLE_128B, bf16))
     return cudaErrorInvalidValue;
-  auto kern = bf16 ? (wide ? window_fwd_kernel<true, true> : window_fwd_kernel<true, false>)
-                   : (wide ? window_fwd_kernel<false, true> : window_fwd_kernel<false, false>);
+  auto kern = window_fwd_kernel<T, TO>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const long long items = (long long)a.B * a.H * ((a.T + BM - 1) / BM);
-  kern<<<(unsigned)std::min<long long>(items, n_sm), THREADS, SMEM_BYTES, stream>>>(mq, mk, mv, mo,
-                                                                                   a, ctl);
+  kern<<<(unsigned)std::min<long long>(items, n_sm), THREADS, SMEM_BYTES, stream>>>(
+      mq, mk, mv, a, ctl);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_fwd(const WindowArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream) {
+  const bool wide = a.out_type == GLA_FP32;
+  if (a.in_type == GLA_BF16)
+    return wide ? run<__nv_bfloat16, float>(a, n_sm, ctl, stream)
+                : run<__nv_bfloat16, __nv_bfloat16>(a, n_sm, ctl, stream);
+  return wide ? run<__half, float>(a, n_sm, ctl, stream) : run<__half, __half>(a, n_sm, ctl, stream);
 }
 
 }  // namespace gla
