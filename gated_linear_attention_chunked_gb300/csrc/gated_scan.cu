@@ -12,15 +12,18 @@
 // arithmetic and the carried state are fp32.
 //
 // Bound by HBM: a token and channel cost 8 bytes forward (bf16 x, g in, fp32 y out) and 20
-// backward (x, g, y, dy in, dx, dg out), against ~20 and ~30 instructions.  The split keeps
-// one pass over memory: a CTA owns one sequence and a slab of channels (32 lanes x VEC
-// channels: whole 128-byte lines of 16-bit inputs) and walks the tokens in tiles, each of its
-// WARPS warps holding S consecutive tokens of the tile in registers.  A warp composes its
-// tokens' pairs, the warps' pairs meet in shared memory, and each thread then runs its tokens
-// from the state entering them.  Where sequences x slabs leave SMs idle, a cluster of up to 8
-// CTAs takes consecutive tiles of the same slab and exchanges its CTAs' pairs through
-// distributed shared memory, one cluster barrier per round; no flag in global memory, no
-// workspace, and the order of composition is fixed by the sizes, so results repeat bit for bit.
+// backward (x, g, y, dy in, dx, dg out), against ~20 and ~30 instructions.  One pass over memory:
+// a CTA owns one sequence and 64 channels (whole 128-byte lines of 16-bit inputs; 56 so that the
+// CTAs fill the last round of SMs cost 57 us where 64 took 47) and walks the tokens in tiles that
+// TMA brings into a ring of three, each of its warps taking consecutive tokens of the tile.  A
+// warp composes its tokens' pairs, the warps' pairs meet in shared memory, and each thread then
+// runs its tokens from the state entering them.  Where sequences x slabs leave SMs idle, a
+// cluster of up to 8 CTAs takes consecutive tiles of the same slab and sends its CTAs' pairs
+// around through distributed shared memory, counted on barriers there (a cluster barrier in
+// their place also waited for the output stores: 272 us against 216 at B=2 T=50021 D=1536); no
+// flag in global memory, no workspace, and the order of composition is fixed by the sizes, so
+// results repeat bit for bit.  Measured (bf16, against the copy rate): forward B=8 T=2048 D=2048
+// 47.3 us (84 %), gradient B=8 T=2047 105.6 us (94 %).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -28,20 +31,23 @@
 
 #include "elem.cuh"
 #include "gated_scan.h"
+#include "tmap.h"
 
 namespace gla {
 namespace {
 namespace cg = cooperative_groups;
 
-constexpr int WARPS = 8, THREADS = 32 * WARPS;
-constexpr int FWD_S = 8, BWD_S = 4;  // tokens per warp and round
+constexpr int FWD_W = 4, BWD_W = 8;   // warps of a CTA
+constexpr int FWD_S = 16, BWD_S = 8;  // tokens per warp and round
+constexpr int FWD_STAGES = 3, BWD_STAGES = 3;  // rounds in flight (TMA)
 
-// sigmoid(g) and sigmoid(-g) from e = exp(-|g|); g = +inf gives exactly (1, 0), -inf (0, 1).
+// sigmoid(g) and sigmoid(-g) from e = exp(-g): f = 1 / (1 + e), and 1 - f as e f where it is the
+// smaller of the two.  g = +inf gives exactly (1, 0), -inf (0, 1).
 __device__ __forceinline__ void gates(float g, float& f, float& u) {
-  const float e = __expf(-fabsf(g));
-  const float r = __fdividef(1.f, 1.f + e), s = e * r;
-  f = g >= 0.f ? r : s;
-  u = g >= 0.f ? s : r;
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(1.f + e));
+  u = g >= 0.f ? e * f : 1.f - f;
 }
 
 template <int VEC>
@@ -49,24 +55,73 @@ struct alignas(8 * VEC) Pair {
   float a[VEC], b[VEC];
 };
 
-template <int VEC, int CL>
+template <int VEC, int CL, int WARPS>
 struct Exchange {
   Pair<VEC> warp[2][WARPS][32];
   Pair<VEC> cta[CL > 1 ? 2 : 1][CL > 1 ? CL : 1][32];
+  alignas(8) uint64_t bar[2];  // a round's pairs of all CTAs have arrived
+
+  // Before the first round.  A cluster's CTAs write into each other's memory: every one has to
+  // be running, with its barriers set up.
+  __device__ __forceinline__ void init() {
+    if constexpr (CL > 1) {
+      if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&bar[0]), 1);
+        mbar_init(smem_u32(&bar[1]), 1);
+        fence_barrier_init();
+      }
+      cg::this_cluster().sync();
+    }
+  }
+  // After the last round: no CTA leaves while another may still write into it (which only
+  // happens after a wait that gave up).  Orders no memory, so it waits for no store.
+  __device__ __forceinline__ void done() {
+    if constexpr (CL > 1) {
+      __syncwarp();
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    }
+  }
 };
 
-// The state entering this warp's tokens, from the round's pair of every warp (and CTA of the
-// cluster) and the state `carry` entering the round, which becomes the one leaving it.
-template <int VEC, int CL>
-__device__ __forceinline__ void enter(Exchange<VEC, CL>& ex, int buf, const Pair<VEC>& own,
-                                      float (&carry)[VEC], float (&in)[VEC]) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+// A pair into CTA `to`'s copy of *p; its bytes count on that CTA's copy of the barrier.  (A
+// cluster barrier in its place would wait for the round's output stores as well.)
+template <int VEC>
+__device__ __forceinline__ void send(const Pair<VEC>& v, const Pair<VEC>* p, const uint64_t* bar,
+                                     int to) {
+  uint32_t rp, rb;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rp) : "r"(smem_u32(p)), "r"(to));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rb) : "r"(smem_u32(bar)), "r"(to));
+  if constexpr (VEC == 2)
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+        ::"r"(rp), "r"(__float_as_uint(v.a[0])), "r"(__float_as_uint(v.a[1])),
+          "r"(__float_as_uint(v.b[0])), "r"(__float_as_uint(v.b[1])), "r"(rb)
+        : "memory");
+  else
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(rp),
+        "r"(__float_as_uint(v.a[0])), "r"(__float_as_uint(v.b[0])), "r"(rb)
+        : "memory");
+}
+
+// The state entering this warp's tokens, from round r's pair of every warp (and CTA of the
+// cluster) and the state `carry` entering the round, which becomes the one leaving it.  `ok`
+// turns false where a CTA of the cluster did not answer in time.
+template <int VEC, int CL, int WARPS>
+__device__ __forceinline__ void enter(Exchange<VEC, CL, WARPS>& ex, int r, const Pair<VEC>& own,
+                                      float (&carry)[VEC], float (&in)[VEC], const DevCtl& ctl,
+                                      bool& ok) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, buf = r & 1;
   ex.warp[buf][w][lane] = own;
+  // The buffers alternate: a CTA sends round r + 2 only after it has this one's pairs of round
+  // r + 1, which go out behind a barrier that every thread reaches after it has read round r's.
   __syncthreads();
   if constexpr (CL > 1) {
-    cg::cluster_group cl = cg::this_cluster();
-    const int rank = (int)cl.block_rank();
-    if (w < CL) {  // warp w hands the CTA's pair to CTA w of the cluster
+    const int rank = (int)cg::this_cluster().block_rank();
+    if (threadIdx.x == 0)
+      mbar_arrive_expect_tx(smem_u32(&ex.bar[buf]), CL * 32 * (int)sizeof(Pair<VEC>));
+    if (w < CL) {
       Pair<VEC> p = ex.warp[buf][0][lane];
 #pragma unroll
       for (int k = 1; k < WARPS; ++k) {
@@ -77,9 +132,10 @@ __device__ __forceinline__ void enter(Exchange<VEC, CL>& ex, int buf, const Pair
           p.a[j] *= n.a[j];
         }
       }
-      *cl.map_shared_rank(&ex.cta[buf][rank][lane], w) = p;
+      for (int to = w; to < CL; to += WARPS)  // each warp hands the CTA's pair to some of them
+        send(p, &ex.cta[buf][rank][lane], &ex.bar[buf], to);
     }
-    cl.sync();
+    ok = ok && mbar_wait(smem_u32(&ex.bar[buf]), (r >> 1) & 1, ctl);
 #pragma unroll
     for (int k = 0; k < CL; ++k) {
       const Pair<VEC> p = ex.cta[buf][k][lane];
@@ -122,12 +178,12 @@ __device__ __forceinline__ int length_of(const int* lens, int b, int T, const De
 }
 
 template <class T, int VEC, int CL>
-__global__ void __launch_bounds__(THREADS, 3)
+__global__ void __launch_bounds__(32 * FWD_W, 4)
 scan_fwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* __restrict__ init,
                 const int* __restrict__ lens, float* __restrict__ y, float* __restrict__ fin,
                 int T_, int D, int slabs, DevCtl ctl) {
-  constexpr int S = FWD_S, TILE = WARPS * S;
-  __shared__ Exchange<VEC, CL> ex;
+  constexpr int S = FWD_S, WARPS = FWD_W, TILE = WARPS * S;
+  __shared__ Exchange<VEC, CL, FWD_W> ex;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int rank = CL > 1 ? blockIdx.x % CL : 0, unit = blockIdx.x / CL;
   const int b = unit / slabs, ch = (unit % slabs) * 32 * VEC + lane * VEC;
@@ -141,6 +197,16 @@ scan_fwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
 
   Pack<T, VEC> xr[S], gr[S];
   auto fetch = [&](int t0) {
+    if (t0 + S <= len && live) {
+      const T* xp = x + base + (long long)t0 * D;
+      const T* gp = g + base + (long long)t0 * D;
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        xr[i].load(xp + i * D);
+        gr[i].load(gp + i * D);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       const int t = t0 + i;
@@ -156,7 +222,9 @@ scan_fwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
   const int step = TILE * CL;
   int t0 = rank * TILE + w * S;
   fetch(t0);
-  for (int at = 0, buf = 0; at < T_; at += step, t0 += step, buf ^= 1) {
+  ex.init();
+  bool ok = true;
+  for (int at = 0, r = 0; at < T_; at += step, t0 += step, ++r) {
     float f[S][VEC], a[S][VEC];
     Pair<VEC> own;
 #pragma unroll
@@ -173,33 +241,35 @@ scan_fwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
       }
     if (at + step < T_) fetch(t0 + step);
     float h[VEC];
-    enter<VEC, CL>(ex, buf, own, carry, h);
+    enter(ex, r, own, carry, h, ctl, ok);
+    const bool whole = t0 + S <= len;
+    float* yp = y + base + (long long)t0 * D;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      const int t = t0 + i;
       Pack<float, VEC> out;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         h[j] = fmaf(f[i][j], h[j], a[i][j]);
-        out.set(j, t < len ? h[j] : 0.f);
+        out.set(j, whole || t0 + i < len ? h[j] : 0.f);
       }
-      if (live && t < T_) out.store(y + base + (long long)t * D);
+      if (live && (whole || t0 + i < T_)) out.store(yp + i * D);
     }
   }
   if (fin && live && rank == 0 && w == 0)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) fin[(long long)b * D + ch + j] = carry[j];
+  ex.done();
 }
 
 template <class T, int VEC, int CL>
-__global__ void __launch_bounds__(THREADS, 3)
+__global__ void __launch_bounds__(32 * BWD_W, 2)
 scan_bwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* __restrict__ y,
                 const float* __restrict__ dy, const float* __restrict__ init,
                 const float* __restrict__ dfin, const int* __restrict__ lens,
                 float* __restrict__ dx, float* __restrict__ dg, float* __restrict__ dinit, int T_,
                 int D, int slabs, DevCtl ctl) {
-  constexpr int S = BWD_S, TILE = WARPS * S;
-  __shared__ Exchange<VEC, CL> ex;
+  constexpr int S = BWD_S, WARPS = BWD_W, TILE = WARPS * S;
+  __shared__ Exchange<VEC, CL, BWD_W> ex;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int rank = CL > 1 ? blockIdx.x % CL : 0, unit = blockIdx.x / CL;
   const int b = unit / slabs, ch = (unit % slabs) * 32 * VEC + lane * VEC;
@@ -212,7 +282,9 @@ scan_bwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
   for (int j = 0; j < VEC; ++j) carry[j] = live && dfin ? dfin[edge + j] : 0.f;
 
   const int step = TILE * CL;
-  for (int at = 0, buf = 0; at < T_; at += step, buf ^= 1) {
+  ex.init();
+  bool ok = true;
+  for (int at = 0, r = 0; at < T_; at += step, ++r) {
     const int last = T_ - 1 - (at + rank * TILE + w * S);  // this warp's tokens, from the last
     Pack<T, VEC> xr[S], gr[S];
     Pack<float, VEC> dr[S], hr[S];
@@ -247,7 +319,7 @@ scan_bwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
         own.a[j] *= f[i][j];
       }
     float c[VEC];
-    enter<VEC, CL>(ex, buf, own, carry, c);
+    enter(ex, r, own, carry, c, ctl, ok);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       const int t = last - i;
@@ -268,6 +340,243 @@ scan_bwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
   if (dinit && live && rank == 0 && w == 0)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dinit[edge + j] = carry[j];
+  ex.done();
+}
+
+// ---- the same with tiles brought in by TMA, where rows start on 16 bytes
+//
+// A ring of STAGES tiles of 64 channels in shared memory takes the place of the registers that
+// held the next round's inputs: more rounds in flight, no address arithmetic.  The barrier of
+// enter() also frees the tile just read.  Tokens past a sequence's end may hold anything: their
+// tiles are read, and the values not used.
+constexpr int SLAB = 64;  // channels of a CTA: whole 128-byte lines of 16-bit inputs
+
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                          int ch, int t, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(ch), "r"(t), "r"(b), "r"(bar)
+      : "memory");
+}
+// Two adjacent values of a row in shared memory.
+template <class T>
+__device__ __forceinline__ float2 tile_pair(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const float2*>(p);
+  } else {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    if constexpr (__is_same(T, __half)) return __half22float2(reinterpret_cast<const __half2&>(w));
+    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+}
+
+template <class T, int CL, int STAGES>
+__global__ void __launch_bounds__(32 * FWD_W)
+scan_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
+                    const __grid_constant__ CUtensorMap map_g, const float* __restrict__ init,
+                    const int* __restrict__ lens, float* __restrict__ y, float* __restrict__ fin,
+                    int T_, int D, int slabs, DevCtl ctl) {
+  constexpr int S = FWD_S, WARPS = FWD_W, TILE = WARPS * S, BYTES = TILE * SLAB * (int)sizeof(T);
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Exchange<2, CL, FWD_W> ex;
+  __shared__ alignas(8) uint64_t full[STAGES];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int rank = CL > 1 ? blockIdx.x % CL : 0, unit = blockIdx.x / CL;
+  const int b = unit / slabs, ch0 = (unit % slabs) * SLAB, ch = ch0 + 2 * lane;
+  const bool live = ch < D;
+  const int len = length_of(lens, b, T_, ctl);
+  const int step = TILE * CL, rounds = (int)(((long long)len + step - 1) / step);
+  auto fetch = [&](int r) {  // one thread
+    const int s = r % STAGES;
+    const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(smem) + s * 2 * BYTES;
+    const int t = r * step + rank * TILE;
+    mbar_arrive_expect_tx(bar, 2 * BYTES);
+    load_tile(dst, &map_x, bar, ch0, t, b);
+    load_tile(dst + BYTES, &map_g, bar, ch0, t, b);
+  };
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&full[s]), 1);
+    fence_barrier_init();
+    fence_proxy_async();
+    for (int r = 0; r < STAGES && r < rounds; ++r) fetch(r);
+  }
+  float carry[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) carry[j] = live && init ? init[(long long)b * D + ch + j] : 0.f;
+  ex.init();
+  __syncthreads();
+  float* const yb = y + (long long)b * T_ * D + ch;
+
+  bool ok = true;
+  for (int r = 0; r < rounds; ++r) {
+    const int s = r % STAGES;
+    const T* xt = reinterpret_cast<const T*>(smem + s * 2 * BYTES) + w * S * SLAB + 2 * lane;
+    const T* gt = xt + TILE * SLAB;
+    const int t0 = r * step + rank * TILE + w * S;
+    const bool whole = t0 + S <= len;
+    ok = ok && mbar_wait(smem_u32(&full[s]), (r / STAGES) & 1, ctl);
+    float f[S][2], a[S][2];
+    Pair<2> own;
+    own.a[0] = own.a[1] = 1.f;
+    own.b[0] = own.b[1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const float2 xv = tile_pair(xt + i * SLAB), gv = tile_pair(gt + i * SLAB);
+      const float xs[2] = {xv.x, xv.y}, gs[2] = {gv.x, gv.y};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float u;
+        gates(gs[j], f[i][j], u);
+        a[i][j] = u * xs[j];
+        if (!whole && t0 + i >= len) {  // past the sequence: the identity
+          f[i][j] = 1.f;
+          a[i][j] = 0.f;
+        }
+        own.b[j] = fmaf(f[i][j], own.b[j], a[i][j]);
+        own.a[j] *= f[i][j];
+      }
+    }
+    float h[2];
+    enter(ex, r, own, carry, h, ctl, ok);
+    if (tid == 0 && r + STAGES < rounds) fetch(r + STAGES);
+    float* yp = yb + (long long)t0 * D;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) h[j] = fmaf(f[i][j], h[j], a[i][j]);
+      if (live && (whole || t0 + i < T_))
+        __stcs(reinterpret_cast<float2*>(yp + (long long)i * D),
+               whole || t0 + i < len ? make_float2(h[0], h[1]) : make_float2(0.f, 0.f));
+    }
+  }
+  // after a wait that gave up: the copies in flight land before the CTA's memory is given back
+  if (!ok && tid == 0)
+    for (int r = max(0, rounds - STAGES); r < rounds; ++r)
+      mbar_wait(smem_u32(&full[r % STAGES]), (r / STAGES) & 1, ctl, 4000000000ull);
+  // the padding that no round has reached
+  for (int t = rounds * step + rank * WARPS + w; t < T_; t += WARPS * CL)
+    if (live) __stcs(reinterpret_cast<float2*>(yb + (long long)t * D), make_float2(0.f, 0.f));
+  if (fin && live && rank == 0 && w == 0)
+    *reinterpret_cast<float2*>(fin + (long long)b * D + ch) = make_float2(carry[0], carry[1]);
+  ex.done();
+}
+
+template <class T, int CL, int STAGES>
+__global__ void __launch_bounds__(32 * BWD_W)
+scan_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
+                    const __grid_constant__ CUtensorMap map_g,
+                    const __grid_constant__ CUtensorMap map_y,
+                    const __grid_constant__ CUtensorMap map_dy, const float* __restrict__ init,
+                    const float* __restrict__ dfin, const int* __restrict__ lens,
+                    float* __restrict__ dx, float* __restrict__ dg, float* __restrict__ dinit,
+                    int T_, int D, int slabs, DevCtl ctl) {
+  constexpr int S = BWD_S, WARPS = BWD_W, TILE = WARPS * S, BX = TILE * SLAB * (int)sizeof(T);
+  constexpr int BY = TILE * SLAB * 4, STAGE = 2 * BX + 2 * BY;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Exchange<2, CL, BWD_W> ex;
+  __shared__ alignas(8) uint64_t full[STAGES];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int rank = CL > 1 ? blockIdx.x % CL : 0, unit = blockIdx.x / CL;
+  const int b = unit / slabs, ch0 = (unit % slabs) * SLAB, ch = ch0 + 2 * lane;
+  const bool live = ch < D;
+  const int len = length_of(lens, b, T_, ctl);
+  const long long edge = (long long)b * D + ch;
+  const int step = TILE * CL, rounds = (int)(((long long)len + step - 1) / step);
+  // round r, from the sequence's last token: this CTA's tile starts at token
+  auto tile_at = [&](int r) { return len - (r * step + rank * TILE) - TILE; };
+  auto fetch = [&](int r) {  // one thread; a tile may begin before the sequence: zeros there
+    const int s = r % STAGES, t = tile_at(r);
+    const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(smem) + s * STAGE;
+    mbar_arrive_expect_tx(bar, STAGE);
+    load_tile(dst, &map_x, bar, ch0, t, b);
+    load_tile(dst + BX, &map_g, bar, ch0, t, b);
+    load_tile(dst + 2 * BX, &map_y, bar, ch0, t - 1, b);
+    load_tile(dst + 2 * BX + BY, &map_dy, bar, ch0, t, b);
+  };
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&full[s]), 1);
+    fence_barrier_init();
+    fence_proxy_async();
+    for (int r = 0; r < STAGES && r < rounds; ++r) fetch(r);
+  }
+  float carry[2], first[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    carry[j] = live && dfin ? dfin[edge + j] : 0.f;
+    first[j] = live && init ? init[edge + j] : 0.f;
+  }
+  ex.init();
+  __syncthreads();
+  float* const xb = dx + (long long)b * T_ * D + ch;
+  float* const gb = dg + (long long)b * T_ * D + ch;
+
+  bool ok = true;
+  for (int r = 0; r < rounds; ++r) {
+    const int s = r % STAGES;
+    const int row = TILE - 1 - w * S, last = tile_at(r) + row;  // this warp's last token
+    const T* xt = reinterpret_cast<const T*>(smem + s * STAGE) + row * SLAB + 2 * lane;
+    const T* gt = xt + TILE * SLAB;
+    const float* yt =
+        reinterpret_cast<const float*>(smem + s * STAGE + 2 * BX) + row * SLAB + 2 * lane;
+    const float* dt = yt + TILE * SLAB;
+    const bool whole = last - S >= 0;  // past its first token too
+    ok = ok && mbar_wait(smem_u32(&full[s]), (r / STAGES) & 1, ctl);
+    float f[S][2], v[S][2], d[S][2], k[S][2];  // f, 1 - f, dy, f (1 - f) (h_{t-1} - x)
+    Pair<2> own;
+    own.a[0] = own.a[1] = 1.f;
+    own.b[0] = own.b[1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const float2 x2 = tile_pair(xt - i * SLAB), g2 = tile_pair(gt - i * SLAB);
+      const float2 y2 = tile_pair(yt - i * SLAB), d2 = tile_pair(dt - i * SLAB);
+      const float xs[2] = {x2.x, x2.y}, gs[2] = {g2.x, g2.y};
+      float ys[2] = {y2.x, y2.y};
+      d[i][0] = d2.x;
+      d[i][1] = d2.y;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        gates(gs[j], f[i][j], v[i][j]);
+        if (!whole && last - i == 0) ys[j] = first[j];
+        k[i][j] = f[i][j] * v[i][j] * (ys[j] - xs[j]);
+        if (!whole && last - i < 0) {  // before the sequence: the identity
+          f[i][j] = 1.f;
+          v[i][j] = d[i][j] = k[i][j] = 0.f;
+        }
+        own.b[j] = f[i][j] * (own.b[j] + d[i][j]);
+        own.a[j] *= f[i][j];
+      }
+    }
+    float c[2];
+    enter(ex, r, own, carry, c, ctl, ok);
+    if (tid == 0 && r + STAGES < rounds) fetch(r + STAGES);
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      float G[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        G[j] = d[i][j] + c[j];
+        c[j] = f[i][j] * G[j];
+      }
+      if (live && (whole || last - i >= 0)) {
+        const long long p = (long long)(last - i) * D;
+        __stcs(reinterpret_cast<float2*>(xb + p), make_float2(v[i][0] * G[0], v[i][1] * G[1]));
+        __stcs(reinterpret_cast<float2*>(gb + p), make_float2(k[i][0] * G[0], k[i][1] * G[1]));
+      }
+    }
+  }
+  // after a wait that gave up: the copies in flight land before the CTA's memory is given back
+  if (!ok && tid == 0)
+    for (int r = max(0, rounds - STAGES); r < rounds; ++r)
+      mbar_wait(smem_u32(&full[r % STAGES]), (r / STAGES) & 1, ctl, 4000000000ull);
+  for (int t = len + rank * WARPS + w; t < T_; t += WARPS * CL)  // padding
+    if (live) {
+      __stcs(reinterpret_cast<float2*>(xb + (long long)t * D), make_float2(0.f, 0.f));
+      __stcs(reinterpret_cast<float2*>(gb + (long long)t * D), make_float2(0.f, 0.f));
+    }
+  if (dinit && live && rank == 0 && w == 0)
+    *reinterpret_cast<float2*>(dinit + edge) = make_float2(carry[0], carry[1]);
+  ex.done();
 }
 
 // One token: state [.., D] in place.  Pure streaming, one thread per VEC channels; with a page
@@ -308,20 +617,26 @@ scan_decode_kernel(float* __restrict__ state, const int* __restrict__ page, int 
   h.store(y + at);
 }
 
-// CTAs of a cluster along the tokens: the fewest (1, 2, 4, 8) that give every SM two CTAs, and
-// no more than there are tiles.
+// CTAs of a cluster along the tokens: the fewest (1, 2, 4, 8) that give the SMs one and a half
+// CTAs each, and no more than there are tiles.
 int pick_cluster(long long units, int T, int tile, int n_sm) {
   const int tiles = (T + tile - 1) / tile;
   int cl = 1;
-  while (cl < 8 && units * cl < 2ll * n_sm && cl * 2 <= tiles) cl *= 2;
+  while (cl < 8 && units * cl * 2 < 3ll * n_sm && cl * 2 <= tiles) cl *= 2;
   return cl;
 }
 
 template <class K, class... A>
-cudaError_t launch(K kernel, int cl, long long units, cudaStream_t stream, A... args) {
+cudaError_t launch(K kernel, int cl, int warps, long long units, int smem, cudaStream_t stream, A... args) {
+  if (smem > 0) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(units * cl));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -331,49 +646,109 @@ cudaError_t launch(K kernel, int cl, long long units, cudaStream_t stream, A... 
   cfg.numAttrs = cl > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+// f.go<CL>() for the cluster size at hand.
+template <class F>
+cudaError_t with_cluster(int cl, const F& f) {
+  return cl == 1 ? f.template go<1>() : cl == 2 ? f.template go<2>()
+         : cl == 4 ? f.template go<4>() : f.template go<8>();
+}
 
-template <class T, int VEC>
-cudaError_t fwd_cl(const ScanArgs& a, int cl, long long units, int slabs, DevCtl ctl,
-                   cudaStream_t stream) {
-  auto go = [&](auto k) {
-    return launch(k, cl, units, stream, (const T*)a.x, (const T*)a.g, a.init, a.lens, a.y, a.fin,
+// [B, T, D] as {D, T, B}, in boxes of SLAB channels and `rows` tokens.
+template <class T>
+bool scan_map(CUtensorMap* m, const void* p, const ScanArgs& a, int rows) {
+  const unsigned long long dims[3] = {(unsigned long long)a.D, (unsigned long long)a.T,
+                                      (unsigned long long)a.B};
+  const unsigned long long strides[2] = {a.D * sizeof(T), a.D * sizeof(T) * a.T};
+  const unsigned box[3] = {(unsigned)SLAB, (unsigned)rows, 1};
+  const CUtensorMapDataType t = sizeof(T) == 4          ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : __is_same(T, __half) ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return make_tmap_3d(m, p, t, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+template <class T>
+struct FwdTma {
+  const ScanArgs& a;
+  long long units;
+  int slabs;
+  DevCtl ctl;
+  cudaStream_t stream;
+  template <int CL>
+  cudaError_t go() const {
+    constexpr int ST = FWD_STAGES, TILE = FWD_W * FWD_S;
+    CUtensorMap x, g;
+    if (!scan_map<T>(&x, a.x, a, TILE) || !scan_map<T>(&g, a.g, a, TILE))
+      return cudaErrorInvalidValue;
+    return launch(scan_fwd_tma_kernel<T, CL, ST>, CL, FWD_W, units,
+                  ST * 2 * TILE * SLAB * (int)sizeof(T), stream, x, g, a.init, a.lens, a.y, a.fin,
                   a.T, a.D, slabs, ctl);
-  };
-  switch (cl) {
-    case 1: return go(scan_fwd_kernel<T, VEC, 1>);
-    case 2: return go(scan_fwd_kernel<T, VEC, 2>);
-    case 4: return go(scan_fwd_kernel<T, VEC, 4>);
-    default: return go(scan_fwd_kernel<T, VEC, 8>);
   }
-}
+};
+template <class T>
+struct BwdTma {
+  const ScanArgs& a;
+  long long units;
+  int slabs;
+  DevCtl ctl;
+  cudaStream_t stream;
+  template <int CL>
+  cudaError_t go() const {
+    constexpr int ST = BWD_STAGES, TILE = BWD_W * BWD_S;
+    CUtensorMap x, g, y, dy;
+    if (!scan_map<T>(&x, a.x, a, TILE) || !scan_map<T>(&g, a.g, a, TILE) ||
+        !scan_map<float>(&y, a.y, a, TILE) || !scan_map<float>(&dy, a.dy, a, TILE))
+      return cudaErrorInvalidValue;
+    return launch(scan_bwd_tma_kernel<T, CL, ST>, CL, BWD_W, units,
+                  ST * 2 * TILE * SLAB * ((int)sizeof(T) + 4), stream, x, g, y, dy, a.init, a.dfin,
+                  a.lens, a.dx, a.dg, a.dinit, a.T, a.D, slabs, ctl);
+  }
+};
 template <class T, int VEC>
-cudaError_t bwd_cl(const ScanArgs& a, int cl, long long units, int slabs, DevCtl ctl,
-                   cudaStream_t stream) {
-  auto go = [&](auto k) {
-    return launch(k, cl, units, stream, (const T*)a.x, (const T*)a.g, (const float*)a.y, a.dy,
-                  a.init, a.dfin, a.lens, a.dx, a.dg, a.dinit, a.T, a.D, slabs, ctl);
-  };
-  switch (cl) {
-    case 1: return go(scan_bwd_kernel<T, VEC, 1>);
-    case 2: return go(scan_bwd_kernel<T, VEC, 2>);
-    case 4: return go(scan_bwd_kernel<T, VEC, 4>);
-    default: return go(scan_bwd_kernel<T, VEC, 8>);
+struct FwdReg {
+  const ScanArgs& a;
+  long long units;
+  int slabs;
+  DevCtl ctl;
+  cudaStream_t stream;
+  template <int CL>
+  cudaError_t go() const {
+    return launch(scan_fwd_kernel<T, VEC, CL>, CL, FWD_W, units, 0, stream, (const T*)a.x,
+                  (const T*)a.g, a.init, a.lens, a.y, a.fin, a.T, a.D, slabs, ctl);
   }
-}
+};
+template <class T, int VEC>
+struct BwdReg {
+  const ScanArgs& a;
+  long long units;
+  int slabs;
+  DevCtl ctl;
+  cudaStream_t stream;
+  template <int CL>
+  cudaError_t go() const {
+    return launch(scan_bwd_kernel<T, VEC, CL>, CL, BWD_W, units, 0, stream, (const T*)a.x,
+                  (const T*)a.g, (const float*)a.y, a.dy, a.init, a.dfin, a.lens, a.dx, a.dg,
+                  a.dinit, a.T, a.D, slabs, ctl);
+  }
+};
 
 template <class T>
 cudaError_t scan_typed(const ScanArgs& a, bool backward, int n_sm, DevCtl ctl,
                        cudaStream_t stream) {
-  // two channels per lane where every row starts on a pair (D even), else one
+  // TMA where rows of the inputs start on 16 bytes, two channels per lane where they start on a
+  // pair (D even), else one
+  const bool tma = a.D % (16 / (int)sizeof(T)) == 0;
   const int vec = a.D % 2 == 0 ? 2 : 1;
   const int slabs = (a.D + 32 * vec - 1) / (32 * vec);
   const long long units = (long long)a.B * slabs;
-  const int cl = pick_cluster(units, a.T, WARPS * (backward ? BWD_S : FWD_S), n_sm);
+  const int cl = pick_cluster(units, a.T, backward ? BWD_W * BWD_S : FWD_W * FWD_S, n_sm);
+  if (tma)
+    return backward ? with_cluster(cl, BwdTma<T>{a, units, slabs, ctl, stream})
+                    : with_cluster(cl, FwdTma<T>{a, units, slabs, ctl, stream});
   if (vec == 2)
-    return backward ? bwd_cl<T, 2>(a, cl, units, slabs, ctl, stream)
-                    : fwd_cl<T, 2>(a, cl, units, slabs, ctl, stream);
-  return backward ? bwd_cl<T, 1>(a, cl, units, slabs, ctl, stream)
-                  : fwd_cl<T, 1>(a, cl, units, slabs, ctl, stream);
+    return backward ? with_cluster(cl, BwdReg<T, 2>{a, units, slabs, ctl, stream})
+                    : with_cluster(cl, FwdReg<T, 2>{a, units, slabs, ctl, stream});
+  return backward ? with_cluster(cl, BwdReg<T, 1>{a, units, slabs, ctl, stream})
+                  : with_cluster(cl, FwdReg<T, 1>{a, units, slabs, ctl, stream});
 }
 
 template <class T>
