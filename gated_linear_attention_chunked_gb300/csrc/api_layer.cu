@@ -169,7 +169,9 @@ gla_status gla_layer_norm_fwd(const void* x, gla_dtype x_dtype, const float* wei
   gla::LayerNormArgs a;
   a.x = x; a.weight = weight; a.bias = bias; a.y = y; a.mean = mean; a.rstd = rstd;
   a.x_type = x_dtype; a.out_type = y_dtype; a.eps = eps; a.n = n_tokens; a.D = D;
-  return done(gla::launch_layer_norm_fwd(a, sm_count(), stream));
+  gla::DevCtl ctl;
+  if (gla::current_device_ctl(&ctl) != cudaSuccess) return GLA_ERR_CUDA;
+  return done(gla::launch_layer_norm_fwd(a, sm_count(), ctl, stream));
 }
 
 size_t gla_layer_norm_bwd_workspace_size(long long n_tokens, int D) {
@@ -194,7 +196,9 @@ gla_status gla_layer_norm_bwd(const void* dy, gla_dtype dy_dtype, const void* x,
   a.rstd = const_cast<float*>(rstd); a.dx = dx; a.dw = d_weight; a.db = d_bias;
   a.part = static_cast<float*>(workspace);
   a.x_type = x_dtype; a.out_type = dy_dtype; a.n = n_tokens; a.D = D;
-  return done(gla::launch_layer_norm_bwd(a, sm_count(), stream));
+  gla::DevCtl ctl;
+  if (gla::current_device_ctl(&ctl) != cudaSuccess) return GLA_ERR_CUDA;
+  return done(gla::launch_layer_norm_bwd(a, sm_count(), ctl, stream));
 }
 
 gla_status gla_window_attn_fwd(const void* q, const void* k, const void* v, gla_dtype in_dtype,

@@ -77,6 +77,31 @@ struct Pack {
       else return __uint_as_float(h << 16);
     }
   }
+  // elements 2 i and 2 i + 1
+  __device__ __forceinline__ float2 get2(int i) const {
+    if constexpr (sizeof(T) == 4) return make_float2(get(2 * i), get(2 * i + 1));
+    else if constexpr (__is_same(T, __half)) return __half22float2(reinterpret_cast<const __half2&>(w[i]));
+    else return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ void set2(int i, float2 x) {
+    if constexpr (sizeof(T) == 4) {
+      set(2 * i, x.x);
+      set(2 * i + 1, x.y);
+    } else if constexpr (__is_same(T, __half)) {
+      reinterpret_cast<__half2&>(w[i]) = __floats2half2_rn(x.x, x.y);
+    } else {
+      reinterpret_cast<__nv_bfloat162&>(w[i]) = __floats2bfloat162_rn(x.x, x.y);
+    }
+  }
+  // from shared memory
+  __device__ __forceinline__ void load_shared(const T* p) {
+    static_assert(BYTES >= 16, "whole 16-byte pieces");
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+    }
+  }
   __device__ __forceinline__ void set(int i, float x) {
     if constexpr (sizeof(T) == 4) {
       w[i] = __float_as_uint(x);
@@ -89,5 +114,29 @@ struct Pack {
     }
   }
 };
+
+// Two fp32 operations in one instruction: a * b + c, a + b, a * b.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
 
 }  // namespace gla

