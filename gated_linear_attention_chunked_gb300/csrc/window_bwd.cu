@@ -17,9 +17,10 @@
 //   warp 8       takes items from a counter (longest kind first) and issues the TMA loads: the
 //                held tile, and a ring of four streamed tiles
 //   warp 9       lse and delta of the streamed queries, into shared memory (KEYS)
-//   warp 10      tcgen05 issuer and TMEM owner; the scores run one tile ahead of the sums
-//   warps 0..7   two per row quadrant (thread = row), each with 32 of the 64 columns: mask, P, Z;
-//                after the last tile the item's output rows
+//   warp 10      tcgen05 issuer and TMEM owner; the scores run ahead of the sums, one tile for
+//                KEYS, two for QUERIES (which have the columns of dv for a second buffer)
+//   warps 0..7   two per row quadrant (thread = row), each with 32 of the 64 columns: mask, P, Z
+//   warps 11..14 the output rows of an item, while the others are on the next one
 // Keys that hold sinks are seen by every query behind them.  Those far queries are items of their
 // own, at least as long as an ordinary one and at most 16 of a key tile, whose sums go to the
 // workspace as fp32 and are added in order by window_sink_kernel.  Past four tiles of sinks the
@@ -47,32 +48,39 @@ constexpr uint32_t HX_BOX = 8192, HY_BOX = 16384, SX_BOX = 4096, SY_BOX = 8192;
 constexpr uint32_t H_BYTES = 3 * (HX_BOX + HY_BOX), S_BYTES = 3 * (SX_BOX + SY_BOX);
 constexpr uint32_t OFF_HX = 0, OFF_HY = 3 * HX_BOX, OFF_S = H_BYTES;
 constexpr uint32_t OFF_STAT = OFF_S + STAGES * S_BYTES;  // float [STAGES][2][64]: lse, delta
-constexpr uint32_t OFF_BAR = OFF_STAT + STAGES * 512;
+constexpr uint32_t OFF_STG = OFF_STAT + STAGES * 512;  // output staging, 2 KB per output warp
+constexpr uint32_t OFF_BAR = OFF_STG + 4 * 2048;
 enum Bar : uint32_t {
   FULL = 0,        // +stage
-  EMPTY = 4,       // +stage
+  EMPTY = 4,       // +stage: the tile's P and Z have been added (and it and they are free)
   STAT_FULL = 8,   // +stage
   STAT_EMPTY = 12, // +stage
   HELD_FULL = 16,
   HELD_EMPTY = 17,
   ITEM_FULL = 18,  // +slot
   ITEM_EMPTY = 20, // +slot
-  S_FULL = 22,     // S and D are in tensor memory
-  S_READ = 23,     // ... and have been read
-  P_READY = 24,    // P and Z have been written
-  SUM_DONE = 25,   // ... and added
-  SUM_FREE = 26,   // the item's sums have been read
-  DRAIN = 27,
-  NBAR = 28
+  S_FULL = 22,     // +buffer: S and D are in tensor memory
+  S_READ = 24,     // ... and have been read (KEYS)
+  P_READY = 25,    // P and Z have been written
+  SUM_DONE = 26,   // an item's sums are complete
+  SUM_FREE = 27,   // ... and have been read
+  DRAIN = 28,
+  NBAR = 29
 };
 constexpr uint32_t OFF_ITEM = OFF_BAR + NBAR * 8;  // int item[2]
 constexpr uint32_t OFF_TMEM = OFF_ITEM + 8, OFF_ABORT = OFF_TMEM + 4;
-constexpr uint32_t SMEM_USED = OFF_ABORT + 4, SMEM_BYTES = SMEM_USED + 1024;
-static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-// tensor memory columns: dv (192), dk or dq (96), S and D (64 each), P and Z (32 each)
+// The opt-in maximum; the kernel aligns its base to 1024 bytes and does not run (GLA_ERR_LAYOUT)
+// if the padding that takes would not fit.  Dynamic shared memory normally starts aligned.
+constexpr uint32_t SMEM_USED = OFF_ABORT + 4, SMEM_BYTES = 232448;
+static_assert(SMEM_USED <= SMEM_BYTES, "shared memory budget");
+// tensor memory columns: dv (192), dk or dq (96), S and D (64 each), P and Z (32 each); the second
+// S and D of QUERIES in dv's
 constexpr uint32_t TM_Y = 0, TM_X = 192, TM_S = 288, TM_D = 352, TM_P = 416, TM_Z = 448;
+__device__ __forceinline__ uint32_t s_at(int buf) { return buf ? 0u : TM_S; }
+__device__ __forceinline__ uint32_t d_at(int buf) { return buf ? 64u : TM_D; }
 
-constexpr int EW = 8, LOAD_WARP = 8, STAT_WARP = 9, MMA_WARP = 10, THREADS = 11 * 32;
+constexpr int EW = 8, LOAD_WARP = 8, STAT_WARP = 9, MMA_WARP = 10, OUT_WARP = 11;
+constexpr int THREADS = 15 * 32;
 
 // How the work is cut into items, the same for every part of the call.
 struct BwdPlan {
@@ -163,30 +171,30 @@ struct Item {
   int n;                  // streamed tiles in all
   KeyTiles kt;            // QUERIES: the key tiles
   __device__ Item() : kt(0, 1, BS, 1, 0) {}
-  __device__ void set(long long i, const WindowArgs& a, const BwdPlan& p) {
-    long long r = i;
-    keys = i < p.keys + p.far;
+  __device__ void set(int i, const WindowArgs& a, const BwdPlan& p) {
+    const int keys_end = (int)p.keys, far_end = keys_end + (int)p.far;
+    unsigned r = i;
+    auto take = [&](unsigned m) {  // r mod m, then r / m
+      const unsigned q = r / m, x = r - q * m;
+      r = q;
+      return (int)x;
+    };
+    keys = i < far_end;
     part = -1;
-    if (i < p.keys) {
-      head = (int)(r % a.KV);
-      r /= a.KV;
-      row0 = (int)(r % p.tiles) * BH;
-      b = (int)(r / p.tiles);
+    if (i < keys_end) {
+      head = take(a.KV);
+      row0 = take(p.tiles) * BH;
     } else if (keys) {
-      r -= p.keys;
-      head = (int)(r % a.KV);
-      r /= a.KV;
-      part = (int)(r % p.far_parts);
-      r /= p.far_parts;
-      row0 = (int)(r % p.sink_tiles) * BH;
-      b = (int)(r / p.sink_tiles);
+      r -= keys_end;
+      head = take(a.KV);
+      part = take(p.far_parts);
+      row0 = take(p.sink_tiles) * BH;
     } else {
-      r -= p.keys + p.far;
-      head = (int)(r % a.H);
-      r /= a.H;
-      row0 = (int)(r % p.tiles) * BH;
-      b = (int)(r / p.tiles);
+      r -= far_end;
+      head = take(a.H);
+      row0 = take(p.tiles) * BH;
     }
+    b = (int)r;
     len = a.T;
     if (a.lens) len = min(max(__ldg(a.lens + b), 0), a.T);
     n = 0;
@@ -206,31 +214,29 @@ struct Item {
       n = kt.n;
     }
   }
-  // first row and head of streamed tile i
-  __device__ int tile_row(int i) const { return (keys ? first + i % per_head : kt.tile(i)) * BS; }
-  __device__ int tile_head(int i, int G) const { return keys ? head * G + i / per_head : head / G; }
   // columns of streamed tile i that count: fewer in the sinks' tiles in front of the window
   __device__ int cols(int i, int sink) const {
     return !keys && i < kt.far ? min(BS, (sink - kt.tile(i) * BS + 15) & ~15) : BS;
   }
 };
 
+// The streamed tiles of an item in order: first row, and the head they are of.
+struct Walk {
+  int i = 0, x = 0, head;  // tile, tile within the head (KEYS), head
+  __device__ Walk(const Item& it, int G) : head(it.keys ? it.head * G : it.head / G) {}
+  __device__ int row(const Item& it) const { return (it.keys ? it.first + x : it.kt.tile(i)) * BS; }
+  __device__ void next(const Item& it) {
+    ++i;
+    if (it.keys && ++x == it.per_head) {
+      x = 0;
+      ++head;
+    }
+  }
+};
+
 // Bits 0 .. n of a 32-bit word (none for n < 0).
 __device__ __forceinline__ uint32_t bits_to(int n) {
   return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1;
-}
-
-// 32 bytes of outputs from fp32 values (16-byte aligned).
-template <class TO>
-__device__ __forceinline__ void store32(TO* p, const uint32_t* r, bool live) {
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if constexpr (sizeof(TO) == 4) w[i] = live ? r[i] : 0u;
-    else w[i] = live ? pack2<TO>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])) : 0u;
-  }
-  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 template <class T, class TO>
@@ -249,6 +255,10 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Cta cta;
   cta.base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  if ((uint32_t)(cta.base - smem_raw) + SMEM_USED > SMEM_BYTES) {
+    if (threadIdx.x == 0) record_error(ctl, DEV_LAYOUT);
+    return;
+  }
   cta.sb = smem_u32(cta.base);
   cta.bar_off = OFF_BAR;
   cta.abort_off = OFF_ABORT;
@@ -271,13 +281,13 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
     mbar_init(cta.bar(HELD_EMPTY), 1);
     for (uint32_t s = 0; s < 2; ++s) {
       mbar_init(cta.bar(ITEM_FULL + s), 1);
-      mbar_init(cta.bar(ITEM_EMPTY + s), EW + 2);
+      mbar_init(cta.bar(ITEM_EMPTY + s), EW + 2 + 4);
+      mbar_init(cta.bar(S_FULL + s), 1);
     }
-    mbar_init(cta.bar(S_FULL), 1);
     mbar_init(cta.bar(S_READ), EW * 32);
     mbar_init(cta.bar(P_READY), EW * 32);
     mbar_init(cta.bar(SUM_DONE), 1);
-    mbar_init(cta.bar(SUM_FREE), EW * 32);
+    mbar_init(cta.bar(SUM_FREE), 128);
     mbar_init(cta.bar(DRAIN), 1);
     *cta.abort_flag() = 0;
     fence_barrier_init();
@@ -329,11 +339,11 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
           tma_load_4d(cta.sb + OFF_HY + j * HY_BOX, it.keys ? &held_v : &held_g,
                       cta.bar(HELD_FULL), 64 * j, it.head, it.row0, it.b);
         }
-        for (int i = 0; i < it.n; ++i, ++n) {
+        for (Walk k(it, G); k.i < it.n; k.next(it), ++n) {
           const uint32_t s = n % STAGES, st = cta.sb + OFF_S + s * S_BYTES;
           if (n >= STAGES && !(ok = wait(cta, cta.bar(EMPTY + s), (n / STAGES - 1) & 1, ctl)))
             break;
-          const int r = it.tile_row(i), h = it.tile_head(i, G);
+          const int r = k.row(it), h = k.head;
           mbar_arrive_expect_tx(cta.bar(FULL + s), S_BYTES);
           for (int j = 0; j < 3; ++j) {
             tma_load_4d(st + j * SX_BOX, it.keys ? &str_q : &str_k, cta.bar(FULL + s), 32 * j, h,
@@ -354,10 +364,10 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
     bool ok = true;
     for (int m = 0, n = 0; ok && next_item(it, m, true); ++m) {
       if (!it.keys) continue;
-      for (int i = 0; i < it.n; ++i, ++n) {
+      for (Walk k(it, G); k.i < it.n; k.next(it), ++n) {
         const uint32_t s = n % STAGES;
-        const int t0 = it.tile_row(i);
-        const long long at = ((long long)it.b * a.H + it.tile_head(i, G)) * a.T + t0;
+        const int t0 = k.row(it);
+        const long long at = ((long long)it.b * a.H + k.head) * a.T + t0;
         float x[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -381,34 +391,46 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
       constexpr uint32_t ID_Y = idesc_f16(128, kDV, BF16, BF16, false, true);
       constexpr uint32_t ID_X = idesc_f16(128, kDK, BF16, BF16, false, true);
       Item it;
-      int n = 0, held = 0;  // streamed tiles and items with work so far
-      bool ok = true;
+      // streamed tiles, those of KEYS items whose scores are out, and items with work, so far
+      int n = 0, keyed = 0, held = 0;
+      bool ok = true, was_keys = false;
+      const uint64_t hx = smem_desc(cta.sb + OFF_HX, 16, 512, SW_64);
+      const uint64_t hy = smem_desc(cta.sb + OFF_HY, 16, 1024, SW_128);
       auto scores = [&](int i, int at) -> bool {  // S, D of the item's tile i, tile `at` in all
         const uint32_t s = at % STAGES, st = cta.sb + OFF_S + s * S_BYTES;
+        const int buf = it.keys ? 0 : i & 1;
         if (i == 0 && !wait(cta, cta.bar(HELD_FULL), (held - 1) & 1, ctl)) return false;
         if (!wait(cta, cta.bar(FULL + s), (at / STAGES) & 1, ctl)) return false;
-        if (at > 0 && !wait(cta, cta.bar(S_READ), (at - 1) & 1, ctl)) return false;
+        if (it.keys) {
+          if (keyed > 0 && !wait(cta, cta.bar(S_READ), (keyed - 1) & 1, ctl)) return false;
+          ++keyed;
+        }
         tc_fence_after();
         const uint32_t id = ID_S | ((uint32_t)(it.cols(i, a.sink) >> 3) << 17);
+        const uint64_t sx = smem_desc(st, 16, 512, SW_64);
+        const uint64_t sy = smem_desc(st + 3 * SX_BOX, 16, 1024, SW_128);
 #pragma unroll
-        for (int c = 0; c < 6; ++c)
-          mma_f16_ss(tmem + TM_S,
-                     smem_desc(cta.sb + OFF_HX + (c >> 1) * HX_BOX + (c & 1) * 32, 16, 512, SW_64),
-                     smem_desc(st + (c >> 1) * SX_BOX + (c & 1) * 32, 16, 512, SW_64), id, c > 0);
+        for (int c = 0; c < 6; ++c)  // (the descriptors count in 16 bytes)
+          mma_f16_ss(tmem + s_at(buf), hx + (((c >> 1) * HX_BOX + (c & 1) * 32) >> 4),
+                     sx + (((c >> 1) * SX_BOX + (c & 1) * 32) >> 4), id, c > 0);
 #pragma unroll
         for (int c = 0; c < 12; ++c)
-          mma_f16_ss(tmem + TM_D,
-                     smem_desc(cta.sb + OFF_HY + (c >> 2) * HY_BOX + (c & 3) * 32, 16, 1024, SW_128),
-                     smem_desc(st + 3 * SX_BOX + (c >> 2) * SY_BOX + (c & 3) * 32, 16, 1024, SW_128),
-                     id, c > 0);
-        mma_commit(cta.bar(S_FULL));
+          mma_f16_ss(tmem + d_at(buf), hy + (((c >> 2) * HY_BOX + (c & 3) * 32) >> 4),
+                     sy + (((c >> 2) * SY_BOX + (c & 3) * 32) >> 4), id, c > 0);
+        mma_commit(cta.bar(S_FULL + buf));
         if (i == it.n - 1) mma_commit(cta.bar(HELD_EMPTY));
         return true;
       };
       for (int m = 0; ok && next_item(it, m, false); ++m) {
         if (it.n == 0) continue;
         ++held;
+        // the second score buffer lies in the sums of a KEYS item
+        if (!it.keys && was_keys &&
+            !(ok = wait(cta, cta.bar(SUM_FREE), (held - 2) & 1, ctl)))
+          break;
+        was_keys = it.keys;
         if (!(ok = scores(0, n))) break;
+        if (!it.keys && it.n > 1 && !(ok = scores(1, n + 1))) break;
         for (int i = 0; i < it.n; ++i, ++n) {
           const uint32_t s = n % STAGES, st = cta.sb + OFF_S + s * S_BYTES;
           if (n == ctl.stall_step) {  // the give-up path's diagnostic (see chunk_fwd.cu)
@@ -416,37 +438,41 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
             ok = false;
             break;
           }
-          if (i + 1 < it.n && !(ok = scores(i + 1, n + 1))) break;
+          if (it.keys && i + 1 < it.n && !(ok = scores(i + 1, n + 1))) break;
           if (i == 0 && held > 1 && !(ok = wait(cta, cta.bar(SUM_FREE), (held - 2) & 1, ctl)))
             break;
           if (!(ok = wait(cta, cta.bar(P_READY), n & 1, ctl))) break;
           tc_fence_after();
-          const int steps = it.cols(i, a.sink) >> 4;
+          const uint64_t sx = smem_desc(st, SX_BOX, 512, SW_64);
           if (it.keys) {
+            const uint64_t sy = smem_desc(st + 3 * SX_BOX, SY_BOX, 1024, SW_128);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              mma_f16_ts(tmem + TM_Y, tmem + TM_P + 8 * c,
-                         smem_desc(st + 3 * SX_BOX + c * 2048, SY_BOX, 1024, SW_128), ID_Y,
+              mma_f16_ts(tmem + TM_Y, tmem + TM_P + 8 * c, sy + (c * 2048 >> 4), ID_Y,
                          i > 0 || c > 0);
           }
+          const int steps = it.cols(i, a.sink) >> 4;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             if (c < steps)
-              mma_f16_ts(tmem + TM_X, tmem + TM_Z + 8 * c,
-                         smem_desc(st + c * 1024, SX_BOX, 512, SW_64), ID_X, i > 0 || c > 0);
-          mma_commit(cta.bar(SUM_DONE));
+              mma_f16_ts(tmem + TM_X, tmem + TM_Z + 8 * c, sx + (c * 1024 >> 4), ID_X,
+                         i > 0 || c > 0);
           mma_commit(cta.bar(EMPTY + s));
+          if (i == it.n - 1) mma_commit(cta.bar(SUM_DONE));
+          // its scores' buffer was read before P and Z were written
+          if (!it.keys && i + 2 < it.n && !(ok = scores(i + 2, n + 2))) break;
         }
       }
       mma_commit(cta.bar(DRAIN));
       mbar_wait(cta.bar(DRAIN), 0, ctl, DRAIN_NS);
     }
-  } else {
-    // ------------------------------------------------------------ P, Z and the output rows
+  } else if (warp < EW) {
+    // ------------------------------------------------------------ P and Z
     const int q4 = warp & 3, hv = warp >> 2, row = 32 * q4 + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
     Item it;
     int n = 0, ks = 0;  // streamed tiles; those of KEYS items
+    uint32_t phase[2] = {0, 0};  // of the score buffers
     bool ok = true;
     for (int m = 0; ok && next_item(it, m, true); ++m) {
       const int r = it.row0 + row, len = it.len;  // this thread's key (KEYS) or query
@@ -456,68 +482,86 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
         lse = __ldg(a.lse + at) * kLog2e;
         del = __ldg(delta + at);
       }
-      for (int i = 0; i < it.n; ++i, ++n) {
-        const uint32_t st = n % STAGES;
-        const int x0 = it.tile_row(i), c0 = x0 + 32 * hv;
+      for (Walk k(it, G); k.i < it.n; k.next(it), ++n) {
+        const int x0 = k.row(it), c0 = x0 + 32 * hv, buf = it.keys ? 0 : k.i & 1;
         // the columns of this half that the row sees, or is seen by
         uint32_t see = ~0u;
+        bool whole;
         if (it.keys) {
-          if (!(it.row0 + BH - 1 <= x0 && x0 + BS <= len &&
-                (x0 + BS - 1 - it.row0 < a.window || it.row0 + BH <= a.sink))) {
+          whole = it.row0 + BH - 1 <= x0 && x0 + BS <= len &&
+                  (x0 + BS - 1 - it.row0 < a.window || it.row0 + BH <= a.sink);
+          if (!whole) {
             const int end = r < a.sink ? len - 1 : (int)min((long long)len, (long long)r + a.window) - 1;
             see = bits_to(end - c0) & ~bits_to(r - 1 - c0);
           }
           if (!(ok = wait_warp(cta, cta.bar(STAT_FULL + ks % STAGES), (ks / STAGES) & 1, ctl)))
             break;
-        } else if (!(x0 + BS - 1 <= it.row0 && x0 + BS <= len &&
-                     (it.row0 + BH - 1 - x0 < a.window || x0 + BS <= a.sink))) {
-          see = bits_to(min(r, len - 1) - c0) &
-                (~bits_to(r - a.window - c0) | bits_to(a.sink - 1 - c0));
+        } else {
+          whole = x0 + BS - 1 <= it.row0 && x0 + BS <= len &&
+                  (it.row0 + BH - 1 - x0 < a.window || x0 + BS <= a.sink);
+          if (!whole)
+            see = bits_to(min(r, len - 1) - c0) &
+                  (~bits_to(r - a.window - c0) | bits_to(a.sink - 1 - c0));
         }
-        if (!(ok = wait_warp(cta, cta.bar(S_FULL), n & 1, ctl))) break;
+        if (!(ok = wait_warp(cta, cta.bar(S_FULL + buf), phase[buf] & 1, ctl))) break;
+        ++phase[buf];
         tc_fence_after();
         uint32_t z[32], d[32];
-        tmem_ld32(trow + TM_S + 32 * hv, z);
-        tmem_ld32(trow + TM_D + 32 * hv, d);
+        tmem_ld32(trow + s_at(buf) + 32 * hv, z);
+        tmem_ld32(trow + d_at(buf) + 32 * hv, d);
         tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(cta.bar(S_READ));
-        uint32_t pk[16], zk[16];
-        const float* stat = (const float*)(base + OFF_STAT + (ks % STAGES) * 512) + 32 * hv;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          float4 l4 = make_float4(lse, lse, lse, lse), d4 = make_float4(del, del, del, del);
-          if (it.keys) {
-            l4 = *reinterpret_cast<const float4*>(stat + 4 * c);
-            d4 = *reinterpret_cast<const float4*>(stat + 64 + 4 * c);
-          }
-          const float lc[4] = {l4.x, l4.y, l4.z, l4.w}, dc[4] = {d4.x, d4.y, d4.z, d4.w};
-          float p[4], w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int x = 4 * c + e;
-            const bool v = (see >> x) & 1;
-            p[e] = ex2(fmaf(__uint_as_float(z[x]), kLog2e, -lc[e]));
-            w[e] = p[e] * (__uint_as_float(d[x]) - dc[e]);
-            p[e] = v ? p[e] : 0.f;  // selected, not multiplied: padding may hold anything
-            w[e] = v ? w[e] : 0.f;
-          }
-          pk[2 * c] = pack2<T>(p[0], p[1]);
-          pk[2 * c + 1] = pack2<T>(p[2], p[3]);
-          zk[2 * c] = pack2<T>(w[0], w[1]);
-          zk[2 * c + 1] = pack2<T>(w[2], w[3]);
+        if (it.keys) {
+          tc_fence_before();
+          mbar_arrive(cta.bar(S_READ));
         }
+        // P = exp2(S log2(e) - lse), Z = P (D - delta), as pairs in place of S and D
+        const float* stat = (const float*)(base + OFF_STAT + (ks % STAGES) * 512) + 32 * hv;
+        const float2 l2e = make_float2(kLog2e, kLog2e);
+        auto pair = [&](int c, float2 l, float2 e, bool masked) {  // columns 2 c, 2 c + 1
+          float2 p = fma2(make_float2(__uint_as_float(z[2 * c]), __uint_as_float(z[2 * c + 1])), l2e,
+                          make_float2(-l.x, -l.y));
+          p.x = ex2(p.x);
+          p.y = ex2(p.y);
+          float2 w = mul2(p, add2(make_float2(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1])),
+                                  make_float2(-e.x, -e.y)));
+          if (masked) {  // selected, not multiplied: padding may hold anything
+            const bool v0 = (see >> (2 * c)) & 1, v1 = (see >> (2 * c + 1)) & 1;
+            p = make_float2(v0 ? p.x : 0.f, v1 ? p.y : 0.f);
+            w = make_float2(v0 ? w.x : 0.f, v1 ? w.y : 0.f);
+          }
+          z[c] = pack2<T>(p.x, p.y);
+          d[c] = pack2<T>(w.x, w.y);
+        };
+        auto all = [&](bool masked) {
+          if (it.keys) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float4 l = *reinterpret_cast<const float4*>(stat + 4 * c);
+              const float4 e = *reinterpret_cast<const float4*>(stat + 64 + 4 * c);
+              pair(2 * c, make_float2(l.x, l.y), make_float2(e.x, e.y), masked);
+              pair(2 * c + 1, make_float2(l.z, l.w), make_float2(e.z, e.w), masked);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              pair(c, make_float2(lse, lse), make_float2(del, del), masked);
+          }
+        };
+        if (whole) all(false);
+        else all(true);
         if (it.keys) mbar_arrive(cta.bar(STAT_EMPTY + ks++ % STAGES));
         // P's and Z's columns are free once the tile before has been added
-        if (n > 0 && !(ok = wait_warp(cta, cta.bar(SUM_DONE), (n - 1) & 1, ctl))) break;
+        if (n > 0 && !(ok = wait_warp(cta, cta.bar(EMPTY + (n - 1) % STAGES),
+                                      ((n - 1) / STAGES) & 1, ctl)))
+          break;
         tc_fence_after();
-        if (it.keys) tmem_st16(trow + TM_P + 16 * hv, pk);
-        tmem_st16(trow + TM_Z + 16 * hv, zk);
+        if (it.keys) tmem_st16(trow + TM_P + 16 * hv, reinterpret_cast<uint32_t(&)[16]>(z));
+        tmem_st16(trow + TM_Z + 16 * hv, reinterpret_cast<uint32_t(&)[16]>(d));
         if (x0 + BS > len && len < a.T) {
           // rows of padding may hold anything, and 0 x NaN is NaN: zero them (the scores, which
           // also read them, are done)
           const int r0 = len - x0, cnt = (BS - r0) * 36;  // 12 + 24 chunks of 16 bytes a row
-          uint8_t* const tile = base + OFF_S + st * S_BYTES;
+          uint8_t* const tile = base + OFF_S + (n % STAGES) * S_BYTES;
           for (int x = tid; x < cnt; x += EW * 32) {
             const int rr = r0 + x / 36, c = x % 36;
             uint8_t* p = c < 12 ? tile + (c >> 2) * SX_BOX + rr * 64 + (c & 3) * 16
@@ -531,54 +575,76 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
         tc_fence_before();
         mbar_arrive(cta.bar(P_READY));
       }
-      if (!ok) break;
+    }
+  } else {
+    // ------------------------------------------------------------ output rows
+    const int q4 = warp & 3, row = 32 * q4 + lane;  // the quadrant that the warp may read
+    const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
+    uint8_t* const stg = base + OFF_STG + q4 * 2048;
+    constexpr int CB = 64 / (int)sizeof(TO);  // channels of 64 bytes
+    const int held_sinks = sink_rows(plan, a.sink);
+    Item it;
+    int done = 0;  // items with work so far
+    for (int m = 0; next_item(it, m, true); ++m) {
+      const int r = it.row0 + row;
+      const bool live = r < it.len && it.n > 0;
+      // rows whose sums are added up later, as fp32 (KEYS); the others go out here
+      const bool sums = it.keys && r < held_sinks;
+      float* const ss = sink_sums + ((((long long)it.b * a.KV + it.head) * held_sinks + (sums ? r : 0)) *
+                                         (1 + plan.far_parts) + 1 + it.part) * kSums;
+      const int from = it.keys ? held_sinks : 0, to = it.part < 0 ? a.T : 0;
       if (it.n > 0) {
-        if (!(ok = wait_warp(cta, cta.bar(SUM_DONE), (n - 1) & 1, ctl))) break;
+        if (!wait_warp(cta, cta.bar(SUM_DONE), done & 1, ctl)) break;
+        ++done;
         tc_fence_after();
       }
-      // output rows: dv (KEYS) and dk or dq, each half of the channels
-      const bool live = r < len && it.n > 0;
-      constexpr int E = 32 / (int)sizeof(TO);  // values of 32 bytes
-      const bool sums = it.keys && r < sink_rows(plan, a.sink);  // fp32, added up later
-      float* ss = nullptr;
-      if (sums)
-        ss = sink_sums + ((((long long)it.b * a.KV + it.head) * sink_rows(plan, a.sink) + r) *
-                              (1 + plan.far_parts) + 1 + it.part) * kSums;
+      // `count` channels from tensor memory column col, to rows of `heads` heads of d channels
+      auto emit = [&](uint32_t col, int count, TO* out, int heads, int d, float* sum_at) {
+        TO* const p = out + (((long long)it.b * a.T + it.row0 + 32 * q4) * heads + it.head) * d;
+#pragma unroll 1
+        for (int k = 0; k < count; k += CB) {
+          uint32_t x[CB];
+          if (it.n > 0) {
+            if constexpr (CB == 16) tmem_ld16(trow + col + k, x);
+            else tmem_ld32(trow + col + k, x);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int c = 0; c < CB; ++c) x[c] = live ? x[c] : 0u;
+          if (sums)
+#pragma unroll
+            for (int c = 0; c < CB / 4; ++c)
+              reinterpret_cast<uint4*>(sum_at + k)[c] =
+                  make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint4 u;
+            if constexpr (CB == 16) {
+              u = make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+            } else {
+              u.x = pack2<TO>(__uint_as_float(x[8 * c]), __uint_as_float(x[8 * c + 1]));
+              u.y = pack2<TO>(__uint_as_float(x[8 * c + 2]), __uint_as_float(x[8 * c + 3]));
+              u.z = pack2<TO>(__uint_as_float(x[8 * c + 4]), __uint_as_float(x[8 * c + 5]));
+              u.w = pack2<TO>(__uint_as_float(x[8 * c + 6]), __uint_as_float(x[8 * c + 7]));
+            }
+            *(uint4*)(stg + swz_off(lane, c, 64)) = u;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {  // four lanes write the 64 bytes of a row
+            const int o = 8 * c + (lane >> 2), t = it.row0 + 32 * q4 + o;
+            const uint4 u = *(const uint4*)(stg + swz_off(o, lane & 3, 64));
+            if (t >= from && t < to)
+              reinterpret_cast<uint4*>(p + (long long)o * heads * d + k)[lane & 3] = u;
+          }
+        }
+      };
       if (it.keys) {
-        TO* dv = static_cast<TO*>(a.dv) + (((long long)it.b * a.T + r) * a.KV + it.head) * kDV;
-        TO* dk = static_cast<TO*>(a.dk) + (((long long)it.b * a.T + r) * a.KV + it.head) * kDK;
-        const bool direct = !sums && it.part < 0 && r < a.T;
-#pragma unroll 1
-        for (int c = 0; c < 9; ++c) {  // 16 channels at a time: 6 of dv, 3 of dk
-          const int ch = c < 6 ? 96 * hv + 16 * c : 48 * hv + 16 * (c - 6);
-          uint32_t x[16];
-          if (it.n > 0) {
-            tmem_ld16(trow + (c < 6 ? TM_Y : TM_X) + ch, x);
-            tmem_wait_ld();
-          }
-          if (sums) {
-            store32(ss + (c < 6 ? 0 : kDV) + ch, x, live);
-            store32(ss + (c < 6 ? 0 : kDV) + ch + 8, x + 8, live);
-          } else if (direct) {
-            TO* p = (c < 6 ? dv : dk) + ch;
-#pragma unroll
-            for (int e = 0; e < 16 / E; ++e) store32(p + E * e, x + E * e, live);
-          }
-        }
+        emit(TM_Y, kDV, static_cast<TO*>(a.dv), a.KV, kDV, ss);
+        emit(TM_X, kDK, static_cast<TO*>(a.dk), a.KV, kDK, ss + kDV);
       } else {
-        TO* dq = static_cast<TO*>(a.dq) + (((long long)it.b * a.T + r) * a.H + it.head) * kDK;
-#pragma unroll 1
-        for (int c = 0; c < 3; ++c) {
-          const int ch = 48 * hv + 16 * c;
-          uint32_t x[16];
-          if (it.n > 0) {
-            tmem_ld16(trow + TM_X + ch, x);
-            tmem_wait_ld();
-          }
-          if (r < a.T)
-#pragma unroll
-            for (int e = 0; e < 16 / E; ++e) store32(dq + ch + E * e, x + E * e, live);
-        }
+        emit(TM_X, kDK, static_cast<TO*>(a.dq), a.H, kDK, ss);
       }
       if (it.n > 0) {
         tc_fence_before();

@@ -6,7 +6,6 @@ current one; outputs and workspaces are allocated there, on the stream of the ca
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -14,6 +13,11 @@ import torch
 CODES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 F32, I32 = torch.float32, torch.int32
 
+_empty = torch.empty
+_getdev = torch._C._cuda_getDevice
+# the handle of a device's current stream; torch.cuda.current_stream(dev).cuda_stream costs 6 us a
+# call, a third of a small call's time
+_stream = torch._C._cuda_getCurrentRawStream
 _lib = None
 
 
@@ -25,10 +29,9 @@ def _library():
     return _lib
 
 
-def _check(call: str, rc: int) -> None:
-    if rc != 0:
-        from . import GlaError
-        raise GlaError(call, rc)
+def _fail(call: str, rc: int):
+    from . import GlaError
+    raise GlaError(call, rc)
 
 
 def _code(t, name) -> int:
@@ -42,60 +45,59 @@ def _ptr(t, name, dev, dtype, shape):
     """Pointer of a contiguous tensor of the call's device, type and shape (None -> NULL)."""
     if t is None:
         return None
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _view(t, name, dev, shape):
     """Pointer and strides (None: contiguous) of a tensor whose last axis is contiguous."""
     if t.is_contiguous():
         return _ptr(t, name, dev, t.dtype, shape), None
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if t.shape != shape or t.stride(-1) != 1:
         raise ValueError(f"{name} must be {list(shape)} with its last axis contiguous")
     return t.data_ptr(), (ctypes.c_longlong * (t.dim() - 1))(*t.stride()[:-1])
 
 
-def _on(t, name, stream):
-    """Context of a call on tensor t's device and `stream` (None: that device's current one)."""
-    if not t.is_cuda:
+def _begin(t, name, stream):
+    """(device index, context to leave or None) of a call on tensor t's device and `stream` (None:
+    that device's current one): what the call allocates and launches goes there."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"stream is on {stream.device}, {name} on {t.device}")
-        return torch.cuda.stream(stream)
-    if t.device.index != torch._C._cuda_getDevice():
-        return torch.cuda.device(t.device)
-    return _HERE
+    if stream is None and dev == _getdev():
+        return dev, None
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, {name} on {t.device}")
+    ctx = torch.cuda.device(t.device) if stream is None else torch.cuda.stream(stream)
+    ctx.__enter__()
+    return dev, ctx
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _stream(dev) -> int:
-    # the handle alone: torch.cuda.current_stream(dev).cuda_stream costs 6 us a call, a third of a
-    # small call's time
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+def _end(ctx):
+    if ctx is not None:
+        ctx.__exit__(None, None, None)
 
 
 def _scratch(nbytes, dev, workspace):
     """(pointer, bytes, tensor) of the caller's workspace or a new one."""
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    else:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {dev}")
-        if workspace.numel() * workspace.element_size() < nbytes:
-            raise ValueError("workspace too small")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+        workspace = _empty(nbytes, dtype=torch.uint8, device=dev)
+        return workspace.data_ptr(), nbytes, workspace
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{dev}")
+    have = workspace.numel() * workspace.element_size()
+    if have < nbytes:
+        raise ValueError("workspace too small")
+    return workspace.data_ptr(), have, workspace
 
 
 # ------------------------------------------------------------------------- gated scan
@@ -105,15 +107,20 @@ def gated_scan_fwd(x, g, init_state=None, lens=None, *, want_final_state=True, o
     x, g [B,T,D] (bf16/fp16/fp32), init_state [B,D] fp32, lens [B] int32: tokens of each sequence,
     the rest is padding.  Returns (y fp32 [B,T,D], final_state fp32 [B,D] or None)."""
     B, T, D = x.shape
-    dev, t = x.device, x.dtype
-    with _on(x, "x", stream):
-        y = torch.empty((B, T, D), dtype=F32, device=dev) if out is None else out
-        fin = torch.empty((B, D), dtype=F32, device=dev) if want_final_state else None
-        _check("gla_gated_scan_fwd", _library().gla_gated_scan_fwd(
+    t = x.dtype
+    dev, ctx = _begin(x, "x", stream)
+    try:
+        y = _empty((B, T, D), dtype=F32, device=dev) if out is None else out
+        fin = _empty((B, D), dtype=F32, device=dev) if want_final_state else None
+        rc = _library().gla_gated_scan_fwd(
             _ptr(x, "x", dev, t, x.shape), _ptr(g, "g", dev, t, x.shape), _code(t, "input"),
             _ptr(init_state, "init_state", dev, F32, (B, D)), _ptr(lens, "lens", dev, I32, (B,)),
             _ptr(y, "out", dev, F32, x.shape), None if fin is None else fin.data_ptr(), B, T, D,
-            _stream(dev)))
+            _stream(dev))
+        if rc:
+            _fail("gla_gated_scan_fwd", rc)
+    finally:
+        _end(ctx)
     return y, fin
 
 
@@ -122,18 +129,23 @@ def gated_scan_bwd(x, g, y, dy, init_state=None, d_final_state=None, lens=None, 
     """Gradient of gated_scan_fwd (gla_gated_scan_bwd); y: the forward's output, dy [B,T,D] fp32.
     Returns (dx, dg, d_init_state or None), fp32."""
     B, T, D = x.shape
-    dev, t = x.device, x.dtype
-    with _on(x, "x", stream):
-        dx = torch.empty((B, T, D), dtype=F32, device=dev)
-        dg = torch.empty((B, T, D), dtype=F32, device=dev)
-        dinit = torch.empty((B, D), dtype=F32, device=dev) if want_d_init_state else None
-        _check("gla_gated_scan_bwd", _library().gla_gated_scan_bwd(
+    t = x.dtype
+    dev, ctx = _begin(x, "x", stream)
+    try:
+        dx = _empty((B, T, D), dtype=F32, device=dev)
+        dg = _empty((B, T, D), dtype=F32, device=dev)
+        dinit = _empty((B, D), dtype=F32, device=dev) if want_d_init_state else None
+        rc = _library().gla_gated_scan_bwd(
             _ptr(x, "x", dev, t, x.shape), _ptr(g, "g", dev, t, x.shape), _code(t, "input"),
             _ptr(y, "y", dev, F32, x.shape), _ptr(dy, "dy", dev, F32, x.shape),
             _ptr(init_state, "init_state", dev, F32, (B, D)),
             _ptr(d_final_state, "d_final_state", dev, F32, (B, D)),
             _ptr(lens, "lens", dev, I32, (B,)), dx.data_ptr(), dg.data_ptr(),
-            None if dinit is None else dinit.data_ptr(), B, T, D, _stream(dev)))
+            None if dinit is None else dinit.data_ptr(), B, T, D, _stream(dev))
+        if rc:
+            _fail("gla_gated_scan_bwd", rc)
+    finally:
+        _end(ctx)
     return dx, dg, dinit
 
 
@@ -141,13 +153,18 @@ def gated_scan_decode_step(state, x, g, *, out=None, stream=None):
     """One token of the gated scan (gla_gated_scan_decode_step): state [..., D] fp32 is updated in
     place, x, g the same shape (bf16/fp16/fp32).  Returns y fp32 (the new state)."""
     D = x.shape[-1]
-    dev, t = x.device, x.dtype
-    with _on(x, "x", stream):
-        y = torch.empty(x.shape, dtype=F32, device=dev) if out is None else out
-        _check("gla_gated_scan_decode_step", _library().gla_gated_scan_decode_step(
+    t = x.dtype
+    dev, ctx = _begin(x, "x", stream)
+    try:
+        y = _empty(x.shape, dtype=F32, device=dev) if out is None else out
+        rc = _library().gla_gated_scan_decode_step(
             _ptr(state, "state", dev, F32, x.shape), _ptr(x, "x", dev, t, x.shape),
             _ptr(g, "g", dev, t, x.shape), _code(t, "input"), _ptr(y, "out", dev, F32, x.shape),
-            x.numel() // max(D, 1), D, _stream(dev)))
+            x.numel() // max(D, 1), D, _stream(dev))
+        if rc:
+            _fail("gla_gated_scan_decode_step", rc)
+    finally:
+        _end(ctx)
     return y
 
 
@@ -157,13 +174,18 @@ def gated_scan_decode_step_paged(pool, page, x, g, *, layer0=0, out=None, stream
     x, g [n_active,L,D].  Returns y fp32 [n_active,L,D]."""
     n, L, D = x.shape
     P, PL, _ = pool.shape
-    dev, t = x.device, x.dtype
-    with _on(x, "x", stream):
-        y = torch.empty(x.shape, dtype=F32, device=dev) if out is None else out
-        _check("gla_gated_scan_decode_step_paged", _library().gla_gated_scan_decode_step_paged(
+    t = x.dtype
+    dev, ctx = _begin(x, "x", stream)
+    try:
+        y = _empty(x.shape, dtype=F32, device=dev) if out is None else out
+        rc = _library().gla_gated_scan_decode_step_paged(
             _ptr(pool, "pool", dev, F32, (P, PL, D)), _ptr(page, "page", dev, I32, (n,)), n, P, PL,
             layer0, _ptr(x, "x", dev, t, x.shape), _ptr(g, "g", dev, t, x.shape),
-            _code(t, "input"), _ptr(y, "out", dev, F32, x.shape), L, D, _stream(dev)))
+            _code(t, "input"), _ptr(y, "out", dev, F32, x.shape), L, D, _stream(dev))
+        if rc:
+            _fail("gla_gated_scan_decode_step_paged", rc)
+    finally:
+        _end(ctx)
     return y
 
 
@@ -174,20 +196,25 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, out_dtype=None, want_
     bias [D] fp32.  out_dtype: x's type (default) or fp32.  Returns (y, mean, rstd), the last two
     fp32 [...] or None."""
     D = x.shape[-1]
-    dev, t = x.device, x.dtype
-    with _on(x, "x", stream):
+    t = x.dtype
+    dev, ctx = _begin(x, "x", stream)
+    try:
         if out is None:
-            out = torch.empty(x.shape, dtype=out_dtype or t, device=dev)
+            out = _empty(x.shape, dtype=out_dtype or t, device=dev)
         elif out_dtype is not None and out.dtype != out_dtype:
             raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
-        mean = torch.empty(x.shape[:-1], dtype=F32, device=dev) if want_stats else None
-        rstd = torch.empty(x.shape[:-1], dtype=F32, device=dev) if want_stats else None
-        _check("gla_layer_norm_fwd", _library().gla_layer_norm_fwd(
+        mean = _empty(x.shape[:-1], dtype=F32, device=dev) if want_stats else None
+        rstd = _empty(x.shape[:-1], dtype=F32, device=dev) if want_stats else None
+        rc = _library().gla_layer_norm_fwd(
             _ptr(x, "x", dev, t, x.shape), _code(t, "input"),
             _ptr(weight, "weight", dev, F32, (D,)), _ptr(bias, "bias", dev, F32, (D,)), eps,
             _ptr(out, "out", dev, out.dtype, x.shape), _code(out.dtype, "output"),
             None if mean is None else mean.data_ptr(), None if rstd is None else rstd.data_ptr(),
-            x.numel() // max(D, 1), D, _stream(dev)))
+            x.numel() // max(D, 1), D, _stream(dev))
+        if rc:
+            _fail("gla_layer_norm_fwd", rc)
+    finally:
+        _end(ctx)
     return out, mean, rstd
 
 
@@ -200,20 +227,25 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, *, workspace=None, stream=None):
     also dx's type; mean, rstd as the forward returned them.  Returns (dx, d_weight, d_bias), the
     last two fp32 [D]."""
     D = x.shape[-1]
-    dev, t = x.device, x.dtype
+    t = x.dtype
     n = x.numel() // max(D, 1)
-    with _on(x, "x", stream):
-        dx = torch.empty(x.shape, dtype=dy.dtype, device=dev)
-        dw = torch.empty((D,), dtype=F32, device=dev)
-        db = torch.empty((D,), dtype=F32, device=dev)
+    dev, ctx = _begin(x, "x", stream)
+    try:
+        dx = _empty(x.shape, dtype=dy.dtype, device=dev)
+        dw = _empty((D,), dtype=F32, device=dev)
+        db = _empty((D,), dtype=F32, device=dev)
         lib = _library()
         wp, wb, hold = _scratch(lib.gla_layer_norm_bwd_workspace_size(n, D), dev, workspace)
-        _check("gla_layer_norm_bwd", lib.gla_layer_norm_bwd(
+        rc = lib.gla_layer_norm_bwd(
             _ptr(dy, "dy", dev, dy.dtype, x.shape), _code(dy.dtype, "dy"),
             _ptr(x, "x", dev, t, x.shape), _code(t, "input"),
             _ptr(weight, "weight", dev, F32, (D,)),
             _ptr(mean, "mean", dev, F32, x.shape[:-1]), _ptr(rstd, "rstd", dev, F32, x.shape[:-1]),
-            dx.data_ptr(), dw.data_ptr(), db.data_ptr(), wp, wb, n, D, _stream(dev)))
+            dx.data_ptr(), dw.data_ptr(), db.data_ptr(), wp, wb, n, D, _stream(dev))
+        if rc:
+            _fail("gla_layer_norm_bwd", rc)
+    finally:
+        _end(ctx)
     return dx, dw, db
 
 
@@ -226,19 +258,24 @@ def window_attn_fwd(q, k, v, window, sink=0, lens=None, *, out_dtype=None, want_
     Returns (o [B,T,H,192], lse fp32 [B,H,T] or None)."""
     B, T, H, dk = q.shape
     KV, dv = v.shape[2], v.shape[3]
-    dev, t = q.device, q.dtype
-    with _on(q, "q", stream):
+    t = q.dtype
+    dev, ctx = _begin(q, "q", stream)
+    try:
         if out is None:
-            out = torch.empty((B, T, H, dv), dtype=out_dtype or t, device=dev)
+            out = _empty((B, T, H, dv), dtype=out_dtype or t, device=dev)
         elif out_dtype is not None and out.dtype != out_dtype:
             raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
-        lse = torch.empty((B, H, T), dtype=F32, device=dev) if want_lse else None
-        _check("gla_window_attn_fwd", _library().gla_window_attn_fwd(
+        lse = _empty((B, H, T), dtype=F32, device=dev) if want_lse else None
+        rc = _library().gla_window_attn_fwd(
             _ptr(q, "q", dev, t, q.shape), _ptr(k, "k", dev, t, (B, T, KV, dk)),
             _ptr(v, "v", dev, t, (B, T, KV, dv)), _code(t, "input"),
             _ptr(lens, "lens", dev, I32, (B,)), window, sink,
             _ptr(out, "out", dev, out.dtype, (B, T, H, dv)), _code(out.dtype, "output"),
-            None if lse is None else lse.data_ptr(), B, T, H, KV, dk, dv, _stream(dev)))
+            None if lse is None else lse.data_ptr(), B, T, H, KV, dk, dv, _stream(dev))
+        if rc:
+            _fail("gla_window_attn_fwd", rc)
+    finally:
+        _end(ctx)
     return out, lse
 
 
@@ -253,22 +290,27 @@ def window_attn_bwd(q, k, v, o, lse, dO, window, sink=0, lens=None, *, workspace
     dv), of o's type."""
     B, T, H, dk_ = q.shape
     KV, dv_ = v.shape[2], v.shape[3]
-    dev, t = q.device, q.dtype
-    with _on(q, "q", stream):
-        dq = torch.empty(q.shape, dtype=o.dtype, device=dev)
-        dk = torch.empty(k.shape, dtype=o.dtype, device=dev)
-        dv = torch.empty(v.shape, dtype=o.dtype, device=dev)
+    t = q.dtype
+    dev, ctx = _begin(q, "q", stream)
+    try:
+        dq = _empty(q.shape, dtype=o.dtype, device=dev)
+        dk = _empty(k.shape, dtype=o.dtype, device=dev)
+        dv = _empty(v.shape, dtype=o.dtype, device=dev)
         lib = _library()
         wp, wb, hold = _scratch(lib.gla_window_attn_bwd_workspace_size(B, T, H, KV, window, sink),
                                 dev, workspace)
-        _check("gla_window_attn_bwd", lib.gla_window_attn_bwd(
+        rc = lib.gla_window_attn_bwd(
             _ptr(q, "q", dev, t, q.shape), _ptr(k, "k", dev, t, (B, T, KV, dk_)),
             _ptr(v, "v", dev, t, (B, T, KV, dv_)), _code(t, "input"),
             _ptr(lens, "lens", dev, I32, (B,)), window, sink,
             *_view(o, "o", dev, (B, T, H, dv_)), _code(o.dtype, "output"),
             _ptr(lse, "lse", dev, F32, (B, H, T)), _ptr(dO, "dO", dev, t, (B, T, H, dv_)),
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), wp, wb, B, T, H, KV, dk_, dv_,
-            _stream(dev)))
+            _stream(dev))
+        if rc:
+            _fail("gla_window_attn_bwd", rc)
+    finally:
+        _end(ctx)
     return dq, dk, dv
 
 
@@ -280,18 +322,21 @@ def window_cache_fill(pool_k, pool_v, page, k, v, window, sink=0, lens=None, *, 
     B, T, KV, dk = k.shape
     dv = v.shape[-1]
     P, PL = pool_k.shape[:2]
-    dev, t = k.device, k.dtype
+    t = k.dtype
     slots = window + sink
-    with _on(k, "k", stream):
-        _check("gla_window_cache_fill", _library().gla_window_cache_fill(
+    dev, ctx = _begin(k, "k", stream)
+    try:
+        rc = _library().gla_window_cache_fill(
             _ptr(k, "k", dev, t, k.shape), _ptr(v, "v", dev, t, (B, T, KV, dv)),
             _code(t, "input"), _ptr(lens, "lens", dev, I32, (B,)),
             _ptr(pool_k, "pool_k", dev, t, (P, PL, slots, KV, dk)),
             _ptr(pool_v, "pool_v", dev, t, (P, PL, slots, KV, dv)),
             _ptr(page, "page", dev, I32, (B,)), P, PL, layer, window, sink, B, T, KV, dk, dv,
-            _stream(dev)))
-
-
+            _stream(dev))
+        if rc:
+            _fail("gla_window_cache_fill", rc)
+    finally:
+        _end(ctx)
 def window_attn_decode_workspace_size(n_active, H, KV, window, sink=0) -> int:
     return _library().gla_window_attn_decode_workspace_size(n_active, H, KV, window, sink)
 
@@ -305,21 +350,26 @@ def window_attn_decode_step(pool_k, pool_v, page, pos, q, k, v, window, sink=0, 
     n, H, dk = q.shape
     KV, dv = v.shape[1], v.shape[2]
     P, PL = pool_k.shape[:2]
-    dev, t = q.device, q.dtype
+    t = q.dtype
     slots = window + sink
-    with _on(q, "q", stream):
+    dev, ctx = _begin(q, "q", stream)
+    try:
         if out is None:
-            out = torch.empty((n, H, dv), dtype=out_dtype or t, device=dev)
+            out = _empty((n, H, dv), dtype=out_dtype or t, device=dev)
         elif out_dtype is not None and out.dtype != out_dtype:
             raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
         lib = _library()
         wp, wb, hold = _scratch(lib.gla_window_attn_decode_workspace_size(n, H, KV, window, sink),
                                 dev, workspace)
-        _check("gla_window_attn_decode_step", lib.gla_window_attn_decode_step(
+        rc = lib.gla_window_attn_decode_step(
             _ptr(pool_k, "pool_k", dev, t, (P, PL, slots, KV, dk)),
             _ptr(pool_v, "pool_v", dev, t, (P, PL, slots, KV, dv)), _code(t, "input"),
             _ptr(page, "page", dev, I32, (n,)), _ptr(pos, "pos", dev, I32, (n,)), n, P, PL, layer,
             window, sink, _ptr(q, "q", dev, t, q.shape), _ptr(k, "k", dev, t, (n, KV, dk)),
             _ptr(v, "v", dev, t, (n, KV, dv)), _ptr(out, "out", dev, out.dtype, (n, H, dv)),
-            _code(out.dtype, "output"), wp, wb, H, KV, dk, dv, _stream(dev)))
+            _code(out.dtype, "output"), wp, wb, H, KV, dk, dv, _stream(dev))
+        if rc:
+            _fail("gla_window_attn_decode_step", rc)
+    finally:
+        _end(ctx)
     return out
