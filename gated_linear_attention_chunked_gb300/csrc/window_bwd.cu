@@ -5,21 +5,26 @@
 //   dq_t = sum_s dz_ts k_s,   dk_s = sum_t dz_ts q_t,   dv_s = sum_t p_ts dO_t
 // where dk and dv also sum over the query heads that share the key head.
 //
-// window_delta_kernel takes delta (bound by HBM); window_bwd_kernel does the rest on tcgen05.  It
-// runs two kinds of items, each with a tile of 128 rows held and tiles of 64 rows streamed by:
-//   KEYS     keys held (k, v), the queries that see them streamed (q, dO), head after head:
-//              S = K Q^T, D = V dO^T, dv += P dO, dk += Z Q
+// window_delta_kernel takes delta (bound by HBM); window_bwd_kernel does the rest on tcgen05, in
+// three kinds, each with a tile of 128 rows held and tiles of 64 rows streamed by:
+//   VALUES   keys held (k), the queries that see them streamed (q, dO), head after head:
+//              S = K Q^T, dv += P dO
+//   KEYS     the same with k, v held:  S = K Q^T, D = V dO^T, dk += Z Q
 //   QUERIES  queries held (q, dO), the keys they see streamed (k, v):
 //              S = Q K^T, D = dO V^T, dq += Z K
-// with P and Z (dz) written back to tensor memory in 16 bits as the left operand.  Both recompute
-// the scores: seven products where five would do, but no sum crosses a CTA, so there are no
-// atomics on results and they repeat bit for bit.
-//   warp 8       takes items from a counter (longest kind first) and issues the TMA loads: the
-//                held tile, and a ring of four streamed tiles
-//   warp 9       lse and delta of the streamed queries, into shared memory (KEYS)
-//   warp 10      tcgen05 issuer and TMEM owner; the scores run ahead of the sums, one tile for
-//                KEYS, two for QUERIES (which have the columns of dv for a second buffer)
-//   warps 0..7   two per row quadrant (thread = row), each with 32 of the 64 columns: mask, P, Z
+// with P and Z (dz) written back to tensor memory in 16 bits as the left operand.  All three
+// recompute the scores: eight products where five would do, but no sum crosses a CTA, so there are
+// no atomics on results and they repeat bit for bit; and apart the kinds have the tensor memory
+// for two tiles of scores each, and for the held operand of the longer product (k, or v or dO):
+// an operand of 128 x 16 from shared memory next to one of 64 x 16 takes 1.5 times as long to read
+// as the product takes.  The three grids are programmatic dependents of one another and wait for
+// nothing, so that a CTA of the next kind starts where one of the last has no item left.
+//   warp 8       takes items from a counter and issues the TMA loads: the held tile, and a ring of
+//                four streamed tiles
+//   warp 9       lse and delta of the streamed queries, into shared memory (VALUES, KEYS)
+//   warp 10      tcgen05 issuer and TMEM owner; the scores run two tiles ahead of the sums
+//   warps 0..7   two groups that take an item's tiles in turn (thread = row): mask, P, Z; between
+//                items they bring the held operand into tensor memory
 //   warps 11..14 the output rows of an item, while the others are on the next one
 // Keys that hold sinks are seen by every query behind them.  Those far queries are items of their
 // own, at least as long as an ordinary one and at most 16 of a key tile, whose sums go to the
@@ -52,20 +57,20 @@ constexpr uint32_t OFF_STG = OFF_STAT + STAGES * 512;  // output staging, 2 KB p
 constexpr uint32_t OFF_BAR = OFF_STG + 4 * 2048;
 enum Bar : uint32_t {
   FULL = 0,        // +stage
-  EMPTY = 4,       // +stage: the tile's P and Z have been added (and it and they are free)
+  EMPTY = 4,       // +stage: the tile has been added
   STAT_FULL = 8,   // +stage
   STAT_EMPTY = 12, // +stage
   HELD_FULL = 16,
-  HELD_EMPTY = 17,
-  ITEM_FULL = 18,  // +slot
-  ITEM_EMPTY = 20, // +slot
-  S_FULL = 22,     // +buffer: S and D are in tensor memory
-  S_READ = 24,     // ... and have been read (KEYS)
-  P_READY = 25,    // P and Z have been written
-  SUM_DONE = 26,   // an item's sums are complete
-  SUM_FREE = 27,   // ... and have been read
-  DRAIN = 28,
-  NBAR = 29
+  HELD_EMPTY = 17, // the item's scores are complete
+  HELD_READY = 18, // the held operand is in tensor memory
+  ITEM_FULL = 19,  // +slot
+  ITEM_EMPTY = 21, // +slot
+  S_FULL = 23,     // +group: its S and D are in tensor memory
+  P_READY = 25,    // +group: ... and have been read, and P or Z written
+  SUM_DONE = 27,   // an item's sums are complete
+  SUM_FREE = 28,   // ... and have been read
+  DRAIN = 29,
+  NBAR = 30
 };
 constexpr uint32_t OFF_ITEM = OFF_BAR + NBAR * 8;  // int item[2]
 constexpr uint32_t OFF_TMEM = OFF_ITEM + 8, OFF_ABORT = OFF_TMEM + 4;
@@ -73,24 +78,30 @@ constexpr uint32_t OFF_TMEM = OFF_ITEM + 8, OFF_ABORT = OFF_TMEM + 4;
 // if the padding that takes would not fit.  Dynamic shared memory normally starts aligned.
 constexpr uint32_t SMEM_USED = OFF_ABORT + 4, SMEM_BYTES = 232448;
 static_assert(SMEM_USED <= SMEM_BYTES, "shared memory budget");
-// tensor memory columns: dv (192), dk or dq (96), S and D (64 each), P and Z (32 each); the second
-// S and D of QUERIES in dv's
-constexpr uint32_t TM_Y = 0, TM_X = 192, TM_S = 288, TM_D = 352, TM_P = 416, TM_Z = 448;
-__device__ __forceinline__ uint32_t s_at(int buf) { return buf ? 0u : TM_S; }
-__device__ __forceinline__ uint32_t d_at(int buf) { return buf ? 64u : TM_D; }
+enum Kind : int { VALUES = 0, KEYS = 1, QUERIES = 2 };
+// Tensor memory columns.  VALUES: dv 192, S twice 64, P twice 32, k 48; the others: v or dO 96, dk
+// or dq 96, S and D twice 64, Z twice 32.
+template <int KIND>
+struct Tm {
+  static constexpr bool V = KIND == VALUES;
+  static constexpr uint32_t SUM = V ? 0 : 96, HELD = V ? 384 : 0;
+  __device__ static uint32_t s(int g) { return V ? 192 + 64 * g : 192 + 128 * g; }
+  __device__ static uint32_t d(int g) { return 256 + 128 * g; }
+  __device__ static uint32_t p(int g) { return (V ? 320 : 448) + 32 * g; }
+};
 
-constexpr int EW = 8, LOAD_WARP = 8, STAT_WARP = 9, MMA_WARP = 10, OUT_WARP = 11;
+constexpr int EW = 8, LOAD_WARP = 8, STAT_WARP = 9, MMA_WARP = 10, GROUP = 128;
 constexpr int THREADS = 15 * 32;
 
 // How the work is cut into items, the same for every part of the call.
 struct BwdPlan {
   int tiles;       // of 128 rows, of a sequence
-  int steps;       // streamed query tiles of an ordinary KEYS item, per head
+  int steps;       // streamed query tiles of an ordinary item of held keys, per head
   int far_steps;   // ... of a far one
   int sink_tiles;  // key tiles that hold sinks and have far queries
   int far_parts;   // most far items of one of them
-  long long keys, far, queries;  // items
-  __host__ __device__ long long total() const { return keys + far + queries; }
+  long long keys, far, queries;  // items: ordinary and far ones of held keys, of held queries
+  __host__ __device__ int total(int kind) const { return (int)(kind == QUERIES ? queries : keys + far); }
   // First streamed tile past the window's of key tile j.
   __host__ __device__ int far_begin(int j) const { return j * (BH / BS) + steps; }
   // Far items of key tile j of a sequence of `len` tokens.
@@ -123,7 +134,7 @@ __host__ __device__ inline int sink_rows(const BwdPlan& p, int sink) {
 template <class T, class TO>
 __global__ void __launch_bounds__(256)
 window_delta_kernel(WindowArgs a, float* __restrict__ delta, int* __restrict__ counter, DevCtl ctl) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
+  if (blockIdx.x == 0 && threadIdx.x < 3) counter[threadIdx.x] = 0;  // one a kind
   const long long rows = (long long)a.B * a.T * a.H;
   const long long row = (long long)blockIdx.x * 32 + (threadIdx.x >> 3);  // (b T + t) H + h
   const int l = threadIdx.x & 7;
@@ -162,48 +173,39 @@ window_delta_kernel(WindowArgs a, float* __restrict__ delta, int* __restrict__ c
 }
 
 // One item, as every role of a CTA sees it.
+template <int KIND>
 struct Item {
-  bool keys;              // KEYS or QUERIES
-  int b, head, row0;      // sequence, key (KEYS) or query head, first held row
+  static constexpr bool HELD_KEYS = KIND != QUERIES;
+  int b, head, row0;      // sequence, key or (QUERIES) query head, first held row
   int len;                // tokens of the sequence
   int part;               // far part, or -1
-  int first, per_head;    // KEYS: first streamed tile and tiles per head
+  int first, per_head;    // held keys: first streamed tile and tiles per head
   int n;                  // streamed tiles in all
   KeyTiles kt;            // QUERIES: the key tiles
   __device__ Item() : kt(0, 1, BS, 1, 0) {}
   __device__ void set(int i, const WindowArgs& a, const BwdPlan& p) {
-    const int keys_end = (int)p.keys, far_end = keys_end + (int)p.far;
     unsigned r = i;
     auto take = [&](unsigned m) {  // r mod m, then r / m
       const unsigned q = r / m, x = r - q * m;
       r = q;
       return (int)x;
     };
-    keys = i < far_end;
     part = -1;
-    if (i < keys_end) {
-      head = take(a.KV);
-      row0 = take(p.tiles) * BH;
-    } else if (keys) {
-      r -= keys_end;
-      head = take(a.KV);
-      part = take(p.far_parts);
-      row0 = take(p.sink_tiles) * BH;
-    } else {
-      r -= far_end;
-      head = take(a.H);
-      row0 = take(p.tiles) * BH;
-    }
+    const bool far = HELD_KEYS && i >= (int)p.keys;
+    if (far) r -= (unsigned)p.keys;
+    head = take(HELD_KEYS ? a.KV : a.H);
+    if (far) part = take(p.far_parts);
+    row0 = take(far ? p.sink_tiles : p.tiles) * BH;
     b = (int)r;
     len = a.T;
     if (a.lens) len = min(max(__ldg(a.lens + b), 0), a.T);
     n = 0;
     if (row0 >= len) return;
-    if (keys) {
+    if (HELD_KEYS) {
       const int all = (len + BS - 1) / BS;  // streamed tiles of the sequence
       first = row0 / BS;
       int last = row0 < a.sink && row0 / BH >= p.sink_tiles ? all : first + p.steps;
-      if (part >= 0) {
+      if (far) {
         first = p.far_begin(row0 / BH) + part * p.far_steps;
         last = first + p.far_steps;
       }
@@ -216,18 +218,21 @@ struct Item {
   }
   // columns of streamed tile i that count: fewer in the sinks' tiles in front of the window
   __device__ int cols(int i, int sink) const {
-    return !keys && i < kt.far ? min(BS, (sink - kt.tile(i) * BS + 15) & ~15) : BS;
+    return !HELD_KEYS && i < kt.far ? min(BS, (sink - kt.tile(i) * BS + 15) & ~15) : BS;
   }
 };
 
 // The streamed tiles of an item in order: first row, and the head they are of.
+template <int KIND>
 struct Walk {
-  int i = 0, x = 0, head;  // tile, tile within the head (KEYS), head
-  __device__ Walk(const Item& it, int G) : head(it.keys ? it.head * G : it.head / G) {}
-  __device__ int row(const Item& it) const { return (it.keys ? it.first + x : it.kt.tile(i)) * BS; }
-  __device__ void next(const Item& it) {
+  const Item<KIND>& it;
+  int i = 0, x = 0, head;  // tile, tile within the head (held keys), head
+  __device__ Walk(const Item<KIND>& it_, int G)
+      : it(it_), head(KIND != QUERIES ? it_.head * G : it_.head / G) {}
+  __device__ int row() const { return (KIND != QUERIES ? it.first + x : it.kt.tile(i)) * BS; }
+  __device__ void next() {
     ++i;
-    if (it.keys && ++x == it.per_head) {
+    if (KIND != QUERIES && ++x == it.per_head) {
       x = 0;
       ++head;
     }
@@ -239,19 +244,17 @@ __device__ __forceinline__ uint32_t bits_to(int n) {
   return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1;
 }
 
-template <class T, class TO>
+template <class T, class TO, int KIND>
 __global__ void __launch_bounds__(THREADS, 1)
-window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
-                  const __grid_constant__ CUtensorMap held_k,
-                  const __grid_constant__ CUtensorMap held_v,
-                  const __grid_constant__ CUtensorMap held_g,
-                  const __grid_constant__ CUtensorMap str_q,
-                  const __grid_constant__ CUtensorMap str_k,
-                  const __grid_constant__ CUtensorMap str_v,
-                  const __grid_constant__ CUtensorMap str_g, WindowArgs a, BwdPlan plan,
+window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
+                  const __grid_constant__ CUtensorMap held_y,
+                  const __grid_constant__ CUtensorMap str_x,
+                  const __grid_constant__ CUtensorMap str_y, WindowArgs a, BwdPlan plan,
                   const float* __restrict__ delta, int* __restrict__ counter,
                   float* __restrict__ sink_sums, DevCtl ctl) {
-  constexpr bool BF16 = !__is_same(T, __half);
+  constexpr bool BF16 = !__is_same(T, __half), STATS = KIND != QUERIES;
+  using M = Tm<KIND>;
+  griddep_launch_dependents();  // the next kind needs SMs, and nothing of this one
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Cta cta;
   cta.base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -275,17 +278,17 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
       mbar_init(cta.bar(FULL + s), 1);
       mbar_init(cta.bar(EMPTY + s), 1);
       mbar_init(cta.bar(STAT_FULL + s), 32);
-      mbar_init(cta.bar(STAT_EMPTY + s), EW * 32);
+      mbar_init(cta.bar(STAT_EMPTY + s), GROUP);
     }
     mbar_init(cta.bar(HELD_FULL), 1);
     mbar_init(cta.bar(HELD_EMPTY), 1);
+    mbar_init(cta.bar(HELD_READY), EW * 32);
     for (uint32_t s = 0; s < 2; ++s) {
       mbar_init(cta.bar(ITEM_FULL + s), 1);
-      mbar_init(cta.bar(ITEM_EMPTY + s), EW + 2 + 4);
+      mbar_init(cta.bar(ITEM_EMPTY + s), EW + 4 + (STATS ? 2 : 1));
       mbar_init(cta.bar(S_FULL + s), 1);
+      mbar_init(cta.bar(P_READY + s), GROUP);
     }
-    mbar_init(cta.bar(S_READ), EW * 32);
-    mbar_init(cta.bar(P_READY), EW * 32);
     mbar_init(cta.bar(SUM_DONE), 1);
     mbar_init(cta.bar(SUM_FREE), 128);
     mbar_init(cta.bar(DRAIN), 1);
@@ -300,7 +303,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
 
   // The next item as a consumer sees it (slot m & 1): false at the end or after a give-up.  Called
   // by whole warps, or by the single MMA thread.
-  auto next_item = [&](Item& it, int m, bool whole_warp) -> bool {
+  auto next_item = [&](Item<KIND>& it, int m, bool whole_warp) -> bool {
     const uint32_t s = m & 1;
     if (whole_warp ? !wait_warp(cta, cta.bar(ITEM_FULL + s), (m >> 1) & 1, ctl)
                    : !wait(cta, cta.bar(ITEM_FULL + s), (m >> 1) & 1, ctl))
@@ -316,40 +319,40 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
   if (warp == LOAD_WARP) {
     // ------------------------------------------------------------ items and TMA loads
     if (lane == 0) {
-      Item it;
+      Item<KIND> it;
       int n = 0, held = 0;
       bool ok = true;
-      int ticket = atomicAdd(counter, 1);
+      int ticket = atomicAdd(counter + KIND, 1);
       for (int m = 0; ok; ++m) {
         const uint32_t slot = m & 1;
         if (m >= 2 && !wait(cta, cta.bar(ITEM_EMPTY + slot), ((m >> 1) - 1) & 1, ctl)) break;
-        const bool end = ticket >= plan.total();
+        const bool end = ticket >= plan.total(KIND);
         items[slot] = end ? -1 : ticket;
         mbar_arrive(cta.bar(ITEM_FULL + slot));
         if (end) break;
         it.set(ticket, a, plan);
-        ticket = atomicAdd(counter, 1);
+        ticket = atomicAdd(counter + KIND, 1);
         if (it.n == 0) continue;
         if (held > 0 && !wait(cta, cta.bar(HELD_EMPTY), (held - 1) & 1, ctl)) break;
         ++held;
-        mbar_arrive_expect_tx(cta.bar(HELD_FULL), H_BYTES);
+        mbar_arrive_expect_tx(cta.bar(HELD_FULL), KIND == VALUES ? 3 * HX_BOX : H_BYTES);
         for (int j = 0; j < 3; ++j) {
-          tma_load_4d(cta.sb + OFF_HX + j * HX_BOX, it.keys ? &held_k : &held_q,
-                      cta.bar(HELD_FULL), 32 * j, it.head, it.row0, it.b);
-          tma_load_4d(cta.sb + OFF_HY + j * HY_BOX, it.keys ? &held_v : &held_g,
-                      cta.bar(HELD_FULL), 64 * j, it.head, it.row0, it.b);
+          tma_load_4d(cta.sb + OFF_HX + j * HX_BOX, &held_x, cta.bar(HELD_FULL), 32 * j, it.head,
+                      it.row0, it.b);
+          if (KIND != VALUES)
+            tma_load_4d(cta.sb + OFF_HY + j * HY_BOX, &held_y, cta.bar(HELD_FULL), 64 * j, it.head,
+                        it.row0, it.b);
         }
-        for (Walk k(it, G); k.i < it.n; k.next(it), ++n) {
+        for (Walk<KIND> k(it, G); k.i < it.n; k.next(), ++n) {
           const uint32_t s = n % STAGES, st = cta.sb + OFF_S + s * S_BYTES;
           if (n >= STAGES && !(ok = wait(cta, cta.bar(EMPTY + s), (n / STAGES - 1) & 1, ctl)))
             break;
-          const int r = k.row(it), h = k.head;
+          const int r = k.row();
           mbar_arrive_expect_tx(cta.bar(FULL + s), S_BYTES);
           for (int j = 0; j < 3; ++j) {
-            tma_load_4d(st + j * SX_BOX, it.keys ? &str_q : &str_k, cta.bar(FULL + s), 32 * j, h,
-                        r, it.b);
-            tma_load_4d(st + 3 * SX_BOX + j * SY_BOX, it.keys ? &str_g : &str_v,
-                        cta.bar(FULL + s), 64 * j, h, r, it.b);
+            tma_load_4d(st + j * SX_BOX, &str_x, cta.bar(FULL + s), 32 * j, k.head, r, it.b);
+            tma_load_4d(st + 3 * SX_BOX + j * SY_BOX, &str_y, cta.bar(FULL + s), 64 * j, k.head, r,
+                        it.b);
           }
         }
       }
@@ -360,107 +363,106 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
     }
   } else if (warp == STAT_WARP) {
     // ------------------------------------------------------------ lse and delta of the queries
-    Item it;
-    bool ok = true;
-    for (int m = 0, n = 0; ok && next_item(it, m, true); ++m) {
-      if (!it.keys) continue;
-      for (Walk k(it, G); k.i < it.n; k.next(it), ++n) {
-        const uint32_t s = n % STAGES;
-        const int t0 = k.row(it);
-        const long long at = ((long long)it.b * a.H + k.head) * a.T + t0;
-        float x[4];
+    if constexpr (STATS) {
+      Item<KIND> it;
+      bool ok = true;
+      for (int m = 0, n = 0; ok && next_item(it, m, true); ++m) {
+        for (Walk<KIND> k(it, G); k.i < it.n; k.next(), ++n) {
+          const uint32_t s = n % STAGES;
+          const int t0 = k.row();
+          const long long at = ((long long)it.b * a.H + k.head) * a.T + t0;
+          float x[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int c = lane + 32 * j;
-          x[j] = t0 + c < it.len ? __ldg(a.lse + at + c) * kLog2e : 0.f;
-          x[2 + j] = t0 + c < it.len ? __ldg(delta + at + c) : 0.f;
+          for (int j = 0; j < 2; ++j) {
+            const int c = lane + 32 * j;
+            x[j] = t0 + c < it.len ? -__ldg(a.lse + at + c) * kLog2e : 0.f;
+            x[2 + j] = t0 + c < it.len ? -__ldg(delta + at + c) : 0.f;
+          }
+          if (n >= STAGES && !(ok = wait_warp(cta, cta.bar(STAT_EMPTY + s), (n / STAGES - 1) & 1,
+                                              ctl)))
+            break;
+          float* st = (float*)(base + OFF_STAT + s * 512);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) st[lane + 32 * j] = x[j];
+          mbar_arrive(cta.bar(STAT_FULL + s));
         }
-        if (n >= STAGES && !(ok = wait_warp(cta, cta.bar(STAT_EMPTY + s), (n / STAGES - 1) & 1,
-                                            ctl)))
-          break;
-        float* st = (float*)(base + OFF_STAT + s * 512);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) st[lane + 32 * j] = x[j];
-        mbar_arrive(cta.bar(STAT_FULL + s));
       }
     }
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t ID_S = idesc_f16(128, 0, BF16, BF16, false, false);
-      constexpr uint32_t ID_Y = idesc_f16(128, kDV, BF16, BF16, false, true);
-      constexpr uint32_t ID_X = idesc_f16(128, kDK, BF16, BF16, false, true);
-      Item it;
-      // streamed tiles, those of KEYS items whose scores are out, and items with work, so far
-      int n = 0, keyed = 0, held = 0;
-      bool ok = true, was_keys = false;
+      constexpr uint32_t ID_SUM = idesc_f16(128, KIND == VALUES ? kDV : kDK, BF16, BF16, false, true);
+      Item<KIND> it;
+      int n = 0, held = 0;       // streamed tiles and items with work so far
+      uint32_t ready[2] = {0, 0};  // tiles of each group so far
+      bool ok = true;
       const uint64_t hx = smem_desc(cta.sb + OFF_HX, 16, 512, SW_64);
-      const uint64_t hy = smem_desc(cta.sb + OFF_HY, 16, 1024, SW_128);
       auto scores = [&](int i, int at) -> bool {  // S, D of the item's tile i, tile `at` in all
         const uint32_t s = at % STAGES, st = cta.sb + OFF_S + s * S_BYTES;
-        const int buf = it.keys ? 0 : i & 1;
-        if (i == 0 && !wait(cta, cta.bar(HELD_FULL), (held - 1) & 1, ctl)) return false;
+        const int g = i & 1;
         if (!wait(cta, cta.bar(FULL + s), (at / STAGES) & 1, ctl)) return false;
-        if (it.keys) {
-          if (keyed > 0 && !wait(cta, cta.bar(S_READ), (keyed - 1) & 1, ctl)) return false;
-          ++keyed;
-        }
         tc_fence_after();
         const uint32_t id = ID_S | ((uint32_t)(it.cols(i, a.sink) >> 3) << 17);
         const uint64_t sx = smem_desc(st, 16, 512, SW_64);
         const uint64_t sy = smem_desc(st + 3 * SX_BOX, 16, 1024, SW_128);
 #pragma unroll
-        for (int c = 0; c < 6; ++c)  // (the descriptors count in 16 bytes)
-          mma_f16_ss(tmem + s_at(buf), hx + (((c >> 1) * HX_BOX + (c & 1) * 32) >> 4),
-                     sx + (((c >> 1) * SX_BOX + (c & 1) * 32) >> 4), id, c > 0);
+        for (int c = 0; c < 6; ++c) {  // (the descriptors count in 16 bytes)
+          const uint64_t b = sx + (((c >> 1) * SX_BOX + (c & 1) * 32) >> 4);
+          if constexpr (KIND == VALUES)
+            mma_f16_ts(tmem + M::s(g), tmem + M::HELD + 8 * c, b, id, c > 0);
+          else
+            mma_f16_ss(tmem + M::s(g), hx + (((c >> 1) * HX_BOX + (c & 1) * 32) >> 4), b, id, c > 0);
+        }
+        if constexpr (KIND != VALUES) {
 #pragma unroll
-        for (int c = 0; c < 12; ++c)
-          mma_f16_ss(tmem + d_at(buf), hy + (((c >> 2) * HY_BOX + (c & 3) * 32) >> 4),
-                     sy + (((c >> 2) * SY_BOX + (c & 3) * 32) >> 4), id, c > 0);
-        mma_commit(cta.bar(S_FULL + buf));
+          for (int c = 0; c < 12; ++c)
+            mma_f16_ts(tmem + M::d(g), tmem + M::HELD + 8 * c,
+                       sy + (((c >> 2) * SY_BOX + (c & 3) * 32) >> 4), id, c > 0);
+        }
+        mma_commit(cta.bar(S_FULL + g));
         if (i == it.n - 1) mma_commit(cta.bar(HELD_EMPTY));
         return true;
       };
       for (int m = 0; ok && next_item(it, m, false); ++m) {
         if (it.n == 0) continue;
         ++held;
-        // the second score buffer lies in the sums of a KEYS item
-        if (!it.keys && was_keys &&
-            !(ok = wait(cta, cta.bar(SUM_FREE), (held - 2) & 1, ctl)))
-          break;
-        was_keys = it.keys;
+        if (!(ok = wait(cta, cta.bar(HELD_FULL), (held - 1) & 1, ctl))) break;
+        if (!(ok = wait(cta, cta.bar(HELD_READY), (held - 1) & 1, ctl))) break;
         if (!(ok = scores(0, n))) break;
-        if (!it.keys && it.n > 1 && !(ok = scores(1, n + 1))) break;
+        if (it.n > 1 && !(ok = scores(1, n + 1))) break;
         for (int i = 0; i < it.n; ++i, ++n) {
           const uint32_t s = n % STAGES, st = cta.sb + OFF_S + s * S_BYTES;
+          const int g = i & 1;
           if (n == ctl.stall_step) {  // the give-up path's diagnostic (see chunk_fwd.cu)
             wait(cta, cta.bar(DRAIN), 0, ctl);
             ok = false;
             break;
           }
-          if (it.keys && i + 1 < it.n && !(ok = scores(i + 1, n + 1))) break;
           if (i == 0 && held > 1 && !(ok = wait(cta, cta.bar(SUM_FREE), (held - 2) & 1, ctl)))
             break;
-          if (!(ok = wait(cta, cta.bar(P_READY), n & 1, ctl))) break;
+          if (!(ok = wait(cta, cta.bar(P_READY + g), ready[g]++ & 1, ctl))) break;
           tc_fence_after();
-          const uint64_t sx = smem_desc(st, SX_BOX, 512, SW_64);
-          if (it.keys) {
+          if constexpr (KIND == VALUES) {
             const uint64_t sy = smem_desc(st + 3 * SX_BOX, SY_BOX, 1024, SW_128);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              mma_f16_ts(tmem + TM_Y, tmem + TM_P + 8 * c, sy + (c * 2048 >> 4), ID_Y,
+              mma_f16_ts(tmem + M::SUM, tmem + M::p(g) + 8 * c, sy + (c * 2048 >> 4), ID_SUM,
                          i > 0 || c > 0);
-          }
-          const int steps = it.cols(i, a.sink) >> 4;
+          } else {
+            const uint64_t sx = smem_desc(st, SX_BOX, 512, SW_64);
+            const int steps = it.cols(i, a.sink) >> 4;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c < steps)
-              mma_f16_ts(tmem + TM_X, tmem + TM_Z + 8 * c, sx + (c * 1024 >> 4), ID_X,
-                         i > 0 || c > 0);
+            for (int c = 0; c < 4; ++c)
+              if (c < steps)
+                mma_f16_ts(tmem + M::SUM, tmem + M::p(g) + 8 * c, sx + (c * 1024 >> 4), ID_SUM,
+                           i > 0 || c > 0);
+          }
           mma_commit(cta.bar(EMPTY + s));
           if (i == it.n - 1) mma_commit(cta.bar(SUM_DONE));
-          // its scores' buffer was read before P and Z were written
-          if (!it.keys && i + 2 < it.n && !(ok = scores(i + 2, n + 2))) break;
+          // the group has read its scores, and the commit behind the new ones also says that the
+          // sum above is done: P or Z may be written again
+          if (i + 2 < it.n && !(ok = scores(i + 2, n + 2))) break;
         }
       }
       mma_commit(cta.bar(DRAIN));
@@ -468,101 +470,122 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
     }
   } else if (warp < EW) {
     // ------------------------------------------------------------ P and Z
-    const int q4 = warp & 3, hv = warp >> 2, row = 32 * q4 + lane;
+    const int q4 = warp & 3, g = warp >> 2, row = 32 * q4 + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
-    Item it;
-    int n = 0, ks = 0;  // streamed tiles; those of KEYS items
-    uint32_t phase[2] = {0, 0};  // of the score buffers
+    Item<KIND> it;
+    int n0 = 0, held = 0;  // streamed tiles and items with work before this item
+    uint32_t used = 0;     // tiles of this group so far
     bool ok = true;
     for (int m = 0; ok && next_item(it, m, true); ++m) {
-      const int r = it.row0 + row, len = it.len;  // this thread's key (KEYS) or query
-      float lse = 0.f, del = 0.f;
-      if (!it.keys && r < len) {
+      if (it.n == 0) continue;
+      const int r = it.row0 + row, len = it.len;  // this thread's key or query
+      float lse = 0.f, del = 0.f;                 // negated, lse in base 2
+      if (!STATS && r < len) {
         const long long at = ((long long)it.b * a.H + it.head) * a.T + r;
-        lse = __ldg(a.lse + at) * kLog2e;
-        del = __ldg(delta + at);
+        lse = -__ldg(a.lse + at) * kLog2e;
+        del = -__ldg(delta + at);
       }
-      for (Walk k(it, G); k.i < it.n; k.next(it), ++n) {
-        const int x0 = k.row(it), c0 = x0 + 32 * hv, buf = it.keys ? 0 : k.i & 1;
-        // the columns of this half that the row sees, or is seen by
-        uint32_t see = ~0u;
-        bool whole;
-        if (it.keys) {
-          whole = it.row0 + BH - 1 <= x0 && x0 + BS <= len &&
-                  (x0 + BS - 1 - it.row0 < a.window || it.row0 + BH <= a.sink);
-          if (!whole) {
+      // the held operand into tensor memory, half a row per group, once the item before has no
+      // more scores to take with it
+      if (held > 0 && !(ok = wait_warp(cta, cta.bar(HELD_EMPTY), (held - 1) & 1, ctl))) break;
+      if (!(ok = wait_warp(cta, cta.bar(HELD_FULL), held & 1, ctl))) break;
+      ++held;
+      tc_fence_after();
+      constexpr int CH = KIND == VALUES ? 6 : 12;  // 16-byte chunks of half a row
+#pragma unroll
+      for (int c = 0; c < CH; c += 2) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int ch = CH * g + c + e;
+          const uint4 u = *(const uint4*)(
+              KIND == VALUES ? base + OFF_HX + (ch >> 2) * HX_BOX + swz_off(row, ch & 3, 64)
+                             : base + OFF_HY + (ch >> 3) * HY_BOX + swz_off(row, ch & 7, 128));
+          w[4 * e] = u.x; w[4 * e + 1] = u.y; w[4 * e + 2] = u.z; w[4 * e + 3] = u.w;
+        }
+        tmem_st8(trow + M::HELD + 4 * (CH * g + c), w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(cta.bar(HELD_READY));
+
+      Walk<KIND> k(it, G);
+      if (g && it.n > 1) k.next();
+      for (int i = g; i < it.n; i += 2) {
+        const int n = n0 + i, x0 = k.row();
+        // the 32 columns from c that the row sees, or is seen by
+        auto sees = [&](int c) -> uint32_t {
+          const int c0 = x0 + c;
+          if (STATS) {
             const int end = r < a.sink ? len - 1 : (int)min((long long)len, (long long)r + a.window) - 1;
-            see = bits_to(end - c0) & ~bits_to(r - 1 - c0);
+            return bits_to(end - c0) & ~bits_to(r - 1 - c0);
           }
-          if (!(ok = wait_warp(cta, cta.bar(STAT_FULL + ks % STAGES), (ks / STAGES) & 1, ctl)))
-            break;
-        } else {
-          whole = x0 + BS - 1 <= it.row0 && x0 + BS <= len &&
-                  (it.row0 + BH - 1 - x0 < a.window || x0 + BS <= a.sink);
-          if (!whole)
-            see = bits_to(min(r, len - 1) - c0) &
-                  (~bits_to(r - a.window - c0) | bits_to(a.sink - 1 - c0));
-        }
-        if (!(ok = wait_warp(cta, cta.bar(S_FULL + buf), phase[buf] & 1, ctl))) break;
-        ++phase[buf];
-        tc_fence_after();
-        uint32_t z[32], d[32];
-        tmem_ld32(trow + s_at(buf) + 32 * hv, z);
-        tmem_ld32(trow + d_at(buf) + 32 * hv, d);
-        tmem_wait_ld();
-        if (it.keys) {
-          tc_fence_before();
-          mbar_arrive(cta.bar(S_READ));
-        }
-        // P = exp2(S log2(e) - lse), Z = P (D - delta), as pairs in place of S and D
-        const float* stat = (const float*)(base + OFF_STAT + (ks % STAGES) * 512) + 32 * hv;
-        const float2 l2e = make_float2(kLog2e, kLog2e);
-        auto pair = [&](int c, float2 l, float2 e, bool masked) {  // columns 2 c, 2 c + 1
-          float2 p = fma2(make_float2(__uint_as_float(z[2 * c]), __uint_as_float(z[2 * c + 1])), l2e,
-                          make_float2(-l.x, -l.y));
-          p.x = ex2(p.x);
-          p.y = ex2(p.y);
-          float2 w = mul2(p, add2(make_float2(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1])),
-                                  make_float2(-e.x, -e.y)));
-          if (masked) {  // selected, not multiplied: padding may hold anything
-            const bool v0 = (see >> (2 * c)) & 1, v1 = (see >> (2 * c + 1)) & 1;
-            p = make_float2(v0 ? p.x : 0.f, v1 ? p.y : 0.f);
-            w = make_float2(v0 ? w.x : 0.f, v1 ? w.y : 0.f);
-          }
-          z[c] = pack2<T>(p.x, p.y);
-          d[c] = pack2<T>(w.x, w.y);
+          return bits_to(min(r, len - 1) - c0) &
+                 (~bits_to(r - a.window - c0) | bits_to(a.sink - 1 - c0));
         };
-        auto all = [&](bool masked) {
-          if (it.keys) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const float4 l = *reinterpret_cast<const float4*>(stat + 4 * c);
-              const float4 e = *reinterpret_cast<const float4*>(stat + 64 + 4 * c);
-              pair(2 * c, make_float2(l.x, l.y), make_float2(e.x, e.y), masked);
-              pair(2 * c + 1, make_float2(l.z, l.w), make_float2(e.z, e.w), masked);
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              pair(c, make_float2(lse, lse), make_float2(del, del), masked);
-          }
-        };
-        if (whole) all(false);
-        else all(true);
-        if (it.keys) mbar_arrive(cta.bar(STAT_EMPTY + ks++ % STAGES));
-        // P's and Z's columns are free once the tile before has been added
-        if (n > 0 && !(ok = wait_warp(cta, cta.bar(EMPTY + (n - 1) % STAGES),
-                                      ((n - 1) / STAGES) & 1, ctl)))
+        const bool whole = STATS ? it.row0 + BH - 1 <= x0 && x0 + BS <= len &&
+                                       (x0 + BS - 1 - it.row0 < a.window || it.row0 + BH <= a.sink)
+                                 : x0 + BS - 1 <= it.row0 && x0 + BS <= len &&
+                                       (it.row0 + BH - 1 - x0 < a.window || x0 + BS <= a.sink);
+        if (!(ok = wait_warp(cta, cta.bar(S_FULL + g), used++ & 1, ctl))) break;
+        // (behind the scores' wait: every earlier tile of the stage has been through here)
+        if (STATS &&
+            !(ok = wait_warp(cta, cta.bar(STAT_FULL + n % STAGES), (n / STAGES) & 1, ctl)))
           break;
         tc_fence_after();
-        if (it.keys) tmem_st16(trow + TM_P + 16 * hv, reinterpret_cast<uint32_t(&)[16]>(z));
-        tmem_st16(trow + TM_Z + 16 * hv, reinterpret_cast<uint32_t(&)[16]>(d));
+        const float* stat = (const float*)(base + OFF_STAT + (n % STAGES) * 512);
+        const float2 l2e = make_float2(kLog2e, kLog2e);
+        // 32 columns: P = exp2(S log2(e) - lse) or Z = P (D - delta) as pairs
+        auto half = [&](int c, uint32_t see, bool masked) {
+          uint32_t z[32], d[32], out[16];
+          tmem_ld32(trow + M::s(g) + c, z);
+          if constexpr (KIND != VALUES) tmem_ld32(trow + M::d(g) + c, d);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float2 l = make_float2(lse, lse), e = make_float2(del, del);
+            if constexpr (STATS) {
+              l = *reinterpret_cast<const float2*>(stat + c + 2 * j);
+              if constexpr (KIND != VALUES)
+                e = *reinterpret_cast<const float2*>(stat + 64 + c + 2 * j);
+            }
+            float2 p = fma2(make_float2(__uint_as_float(z[2 * j]), __uint_as_float(z[2 * j + 1])),
+                            l2e, l);
+            p.x = ex2(p.x);
+            p.y = ex2(p.y);
+            if constexpr (KIND != VALUES)
+              p = mul2(p, add2(make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])),
+                               e));
+            if (masked) {  // selected, not multiplied: padding may hold anything
+              p.x = (see >> (2 * j)) & 1 ? p.x : 0.f;
+              p.y = (see >> (2 * j + 1)) & 1 ? p.y : 0.f;
+            }
+            out[j] = pack2<T>(p.x, p.y);
+          }
+          tmem_st16(trow + M::p(g) + c / 2, out);
+        };
+        if (whole) {
+          half(0, 0u, false);
+          half(32, 0u, false);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < BS; c += 32) {
+            const uint32_t see = sees(c);
+            if (__any_sync(0xffffffffu, see != 0u)) {
+              half(c, see, true);
+            } else {
+              const uint32_t none[16] = {};
+              tmem_st16(trow + M::p(g) + c / 2, none);
+            }
+          }
+        }
+        if (STATS) mbar_arrive(cta.bar(STAT_EMPTY + n % STAGES));
         if (x0 + BS > len && len < a.T) {
           // rows of padding may hold anything, and 0 x NaN is NaN: zero them (the scores, which
           // also read them, are done)
           const int r0 = len - x0, cnt = (BS - r0) * 36;  // 12 + 24 chunks of 16 bytes a row
           uint8_t* const tile = base + OFF_S + (n % STAGES) * S_BYTES;
-          for (int x = tid; x < cnt; x += EW * 32) {
+          for (int x = row; x < cnt; x += GROUP) {
             const int rr = r0 + x / 36, c = x % 36;
             uint8_t* p = c < 12 ? tile + (c >> 2) * SX_BOX + rr * 64 + (c & 3) * 16
                                 : tile + 3 * SX_BOX + ((c - 12) >> 3) * SY_BOX + rr * 128 +
@@ -573,8 +596,11 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(cta.bar(P_READY));
+        mbar_arrive(cta.bar(P_READY + g));
+        k.next();
+        k.next();
       }
+      n0 += it.n;
     }
   } else {
     // ------------------------------------------------------------ output rows
@@ -582,73 +608,67 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
     uint8_t* const stg = base + OFF_STG + q4 * 2048;
     constexpr int CB = 64 / (int)sizeof(TO);  // channels of 64 bytes
-    const int held_sinks = sink_rows(plan, a.sink);
-    Item it;
+    constexpr int D = KIND == VALUES ? kDV : kDK;
+    const int held_sinks = sink_rows(plan, a.sink), heads = STATS ? a.KV : a.H;
+    TO* const dst = static_cast<TO*>(KIND == VALUES ? a.dv : KIND == KEYS ? a.dk : a.dq);
+    Item<KIND> it;
     int done = 0;  // items with work so far
     for (int m = 0; next_item(it, m, true); ++m) {
       const int r = it.row0 + row;
       const bool live = r < it.len && it.n > 0;
-      // rows whose sums are added up later, as fp32 (KEYS); the others go out here
-      const bool sums = it.keys && r < held_sinks;
+      // rows whose sums are added up later, as fp32 (held keys); the others go out here
+      const bool sums = STATS && r < held_sinks;
       float* const ss = sink_sums + ((((long long)it.b * a.KV + it.head) * held_sinks + (sums ? r : 0)) *
-                                         (1 + plan.far_parts) + 1 + it.part) * kSums;
-      const int from = it.keys ? held_sinks : 0, to = it.part < 0 ? a.T : 0;
+                                         (1 + plan.far_parts) + 1 + it.part) * kSums +
+                        (KIND == VALUES ? 0 : kDV);
+      const int from = STATS ? held_sinks : 0, to = it.part < 0 ? a.T : 0;
       if (it.n > 0) {
         if (!wait_warp(cta, cta.bar(SUM_DONE), done & 1, ctl)) break;
         ++done;
         tc_fence_after();
       }
-      // `count` channels from tensor memory column col, to rows of `heads` heads of d channels
-      auto emit = [&](uint32_t col, int count, TO* out, int heads, int d, float* sum_at) {
-        TO* const p = out + (((long long)it.b * a.T + it.row0 + 32 * q4) * heads + it.head) * d;
+      TO* const p = dst + (((long long)it.b * a.T + it.row0 + 32 * q4) * heads + it.head) * D;
 #pragma unroll 1
-        for (int k = 0; k < count; k += CB) {
-          uint32_t x[CB];
-          if (it.n > 0) {
-            if constexpr (CB == 16) tmem_ld16(trow + col + k, x);
-            else tmem_ld32(trow + col + k, x);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int c = 0; c < CB; ++c) x[c] = live ? x[c] : 0u;
-          if (sums)
-#pragma unroll
-            for (int c = 0; c < CB / 4; ++c)
-              reinterpret_cast<uint4*>(sum_at + k)[c] =
-                  make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint4 u;
-            if constexpr (CB == 16) {
-              u = make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-            } else {
-              u.x = pack2<TO>(__uint_as_float(x[8 * c]), __uint_as_float(x[8 * c + 1]));
-              u.y = pack2<TO>(__uint_as_float(x[8 * c + 2]), __uint_as_float(x[8 * c + 3]));
-              u.z = pack2<TO>(__uint_as_float(x[8 * c + 4]), __uint_as_float(x[8 * c + 5]));
-              u.w = pack2<TO>(__uint_as_float(x[8 * c + 6]), __uint_as_float(x[8 * c + 7]));
-            }
-            *(uint4*)(stg + swz_off(lane, c, 64)) = u;
-          }
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {  // four lanes write the 64 bytes of a row
-            const int o = 8 * c + (lane >> 2), t = it.row0 + 32 * q4 + o;
-            const uint4 u = *(const uint4*)(stg + swz_off(o, lane & 3, 64));
-            if (t >= from && t < to)
-              reinterpret_cast<uint4*>(p + (long long)o * heads * d + k)[lane & 3] = u;
-          }
+      for (int k = 0; k < D; k += CB) {
+        uint32_t x[CB];
+        if (it.n > 0) {
+          if constexpr (CB == 16) tmem_ld16(trow + M::SUM + k, x);
+          else tmem_ld32(trow + M::SUM + k, x);
+          tmem_wait_ld();
         }
-      };
-      if (it.keys) {
-        emit(TM_Y, kDV, static_cast<TO*>(a.dv), a.KV, kDV, ss);
-        emit(TM_X, kDK, static_cast<TO*>(a.dk), a.KV, kDK, ss + kDV);
-      } else {
-        emit(TM_X, kDK, static_cast<TO*>(a.dq), a.H, kDK, ss);
-      }
-      if (it.n > 0) {
-        tc_fence_before();
-        mbar_arrive(cta.bar(SUM_FREE));
+#pragma unroll
+        for (int c = 0; c < CB; ++c) x[c] = live ? x[c] : 0u;
+        if (sums)
+#pragma unroll
+          for (int c = 0; c < CB / 4; ++c)
+            reinterpret_cast<uint4*>(ss + k)[c] =
+                make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+        if (k + CB == D && it.n > 0) {
+          tc_fence_before();
+          mbar_arrive(cta.bar(SUM_FREE));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint4 u;
+          if constexpr (CB == 16) {
+            u = make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+          } else {
+            u.x = pack2<TO>(__uint_as_float(x[8 * c]), __uint_as_float(x[8 * c + 1]));
+            u.y = pack2<TO>(__uint_as_float(x[8 * c + 2]), __uint_as_float(x[8 * c + 3]));
+            u.z = pack2<TO>(__uint_as_float(x[8 * c + 4]), __uint_as_float(x[8 * c + 5]));
+            u.w = pack2<TO>(__uint_as_float(x[8 * c + 6]), __uint_as_float(x[8 * c + 7]));
+          }
+          *(uint4*)(stg + swz_off(lane, c, 64)) = u;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // four lanes write the 64 bytes of a row
+          const int o = 8 * c + (lane >> 2), t = it.row0 + 32 * q4 + o;
+          const uint4 u = *(const uint4*)(stg + swz_off(o, lane & 3, 64));
+          if (t >= from && t < to)
+            reinterpret_cast<uint4*>(p + (long long)o * heads * D + k)[lane & 3] = u;
+        }
       }
     }
   }
@@ -659,6 +679,9 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_q,
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // this grid is complete only after the one ahead of it: what follows on the stream waits for
+  // both by waiting for this one
+  griddep_wait();
 }
 
 // dk, dv of the sinks' keys: the window's sums and the far parts', in order.
@@ -716,13 +739,22 @@ cudaError_t run(const WindowArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream) 
       !y(&hg, a.dO, a.H, BH) || !x(&sq, a.q, a.H, BS) || !x(&sk, a.k, a.KV, BS) ||
       !y(&sv, a.v, a.KV, BS) || !y(&sg, a.dO, a.H, BS))
     return cudaErrorInvalidValue;
-  auto kern = window_bwd_kernel<T, TO>;
-  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)) !=
-      cudaSuccess)
+  auto kind = [&](auto kern, int k, const CUtensorMap& hx, const CUtensorMap& hy,
+                  const CUtensorMap& sx, const CUtensorMap& sy, bool dependent) -> cudaError_t {
+    const cudaError_t f =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (f != cudaSuccess) return f;
+    PdlLaunch l(dim3((unsigned)std::min(plan.total(k), n_sm)), dim3(THREADS), SMEM_BYTES, stream,
+                dependent);
+    return cudaLaunchKernelEx(&l.cfg, kern, hx, hy, sx, sy, a, plan, (const float*)delta, counter,
+                              sums, ctl);
+  };
+  // the kind of the longest items first; the first waits for delta as a plain launch does
+  if ((e = kind(window_bwd_kernel<T, TO, KEYS>, KEYS, hk, hv, sq, sg, false)) != cudaSuccess ||
+      (e = kind(window_bwd_kernel<T, TO, VALUES>, VALUES, hk, hv, sq, sg, true)) != cudaSuccess ||
+      (e = kind(window_bwd_kernel<T, TO, QUERIES>, QUERIES, hq, hg, sk, sv, true)) != cudaSuccess)
     return e;
-  kern<<<(unsigned)std::min<long long>(plan.total(), n_sm), THREADS, SMEM_BYTES, stream>>>(
-      hq, hk, hv, hg, sq, sk, sv, sg, a, plan, delta, counter, sums, ctl);
-  if ((e = cudaGetLastError()) != cudaSuccess || !plan.sink_tiles) return e;
+  if (!plan.sink_tiles) return cudaSuccess;
   window_sink_kernel<TO><<<(unsigned)((long long)a.B * a.KV * sink_rows(plan, a.sink)), kSums / 2, 0,
                            stream>>>(a, plan, sums);
   return cudaGetLastError();

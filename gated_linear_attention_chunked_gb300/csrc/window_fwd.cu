@@ -205,7 +205,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     }
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t ID_PV = idesc_f16(128, 192, BF16, BF16, false, true);
       // the scores' walk (two tiles ahead) and the values'
       Items si(a), vi(a);
