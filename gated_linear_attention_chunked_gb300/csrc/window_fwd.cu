@@ -206,7 +206,11 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ MMA issuer
     if (elect_one()) {
+      constexpr uint32_t ID_S = idesc_f16(128, 0, BF16, BF16, false, false);
       constexpr uint32_t ID_PV = idesc_f16(128, 192, BF16, BF16, false, true);
+      const uint64_t q_desc = smem_desc(cta.sb + OFF_Q, 16, 512, SW_64);
+      const uint64_t k_desc = smem_desc(cta.sb + OFF_K, 16, 512, SW_64);
+      const uint64_t v_desc = smem_desc(cta.sb + OFF_V, V_BOX, 1024, SW_128);
       // the scores' walk (two tiles ahead) and the values'
       Items si(a), vi(a);
       KeyTiles sk(0, 1, BN, 1, 0), vk(0, 1, BN, 1, 0);
@@ -218,14 +222,12 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         if (s_at == 0 && !wait(cta, cta.bar(Q_FULL + qs), (sm >> 1) & 1, ctl)) return false;
         if (!wait(cta, cta.bar(K_FULL + s), (sn >> 1) & 1, ctl)) return false;
         tc_fence_after();
-        const uint32_t id = idesc_f16(128, 128, BF16, BF16, false, false) & ~(0x3Fu << 17);
-        const uint32_t cols = (uint32_t)(tile_cols(sk, s_at, a.sink) >> 3) << 17;
-        const uint32_t q = cta.sb + OFF_Q + qs * K_BYTES, k = cta.sb + OFF_K + s * K_BYTES;
+        const uint32_t id = ID_S | ((uint32_t)(tile_cols(sk, s_at, a.sink) >> 3) << 17);
+        const uint64_t q = q_desc + (qs * K_BYTES >> 4), k = k_desc + (s * K_BYTES >> 4);
 #pragma unroll
-        for (int c = 0; c < 6; ++c) {
-          const uint32_t off = (c >> 1) * K_BOX + (c & 1) * 32;
-          mma_f16_ss(tmem + TM_S + 128 * s, smem_desc(q + off, 16, 512, SW_64),
-                     smem_desc(k + off, 16, 512, SW_64), id | cols, c > 0);
+        for (int c = 0; c < 6; ++c) {  // (the descriptors count in 16 bytes)
+          const uint32_t off = ((c >> 1) * K_BOX + (c & 1) * 32) >> 4;
+          mma_f16_ss(tmem + TM_S + 128 * s, q + off, k + off, id, c > 0);
         }
         mma_commit(cta.bar(S_FULL + s));
         ++sn;
@@ -252,13 +254,13 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
               !(ok = wait(cta, cta.bar(O_FREE), (vm - 1) & 1, ctl))) break;
           if (!(ok = wait(cta, cta.bar(P_READY), vn & 1, ctl))) break;
           tc_fence_after();
-          const uint32_t v = cta.sb + OFF_V + s * V_BYTES;
+          const uint64_t v = v_desc + (s * V_BYTES >> 4);
           const int steps = tile_cols(vk, v_at, a.sink) >> 4;
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             if (c < steps)
-              mma_f16_ts(tmem + TM_O, tmem + TM_P + 8 * c,
-                         smem_desc(v + c * 2048, V_BOX, 1024, SW_128), ID_PV, v_at > 0 || c > 0);
+              mma_f16_ts(tmem + TM_O, tmem + TM_P + 8 * c, v + (c * 2048 >> 4), ID_PV,
+                         v_at > 0 || c > 0);
           mma_commit(cta.bar(O_DONE + s));
           if (s_live && !(ok = scores())) break;
         }
