@@ -119,7 +119,7 @@ __device__ __forceinline__ void enter(Exchange<VEC, CL, WARPS>& ex, int r, const
   __syncthreads();
   if constexpr (CL > 1) {
     const int rank = (int)cg::this_cluster().block_rank();
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0 && ok)  // (a phase that never completed is not armed again)
       mbar_arrive_expect_tx(smem_u32(&ex.bar[buf]), CL * 32 * (int)sizeof(Pair<VEC>));
     if (w < CL) {
       Pair<VEC> p = ex.warp[buf][0][lane];
@@ -178,7 +178,7 @@ __device__ __forceinline__ int length_of(const int* lens, int b, int T, const De
 }
 
 template <class T, int VEC, int CL>
-__global__ void __launch_bounds__(32 * FWD_W, 4)
+__global__ void __launch_bounds__(32 * FWD_W, 3)
 scan_fwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* __restrict__ init,
                 const int* __restrict__ lens, float* __restrict__ y, float* __restrict__ fin,
                 int T_, int D, int slabs, DevCtl ctl) {
@@ -201,9 +201,9 @@ scan_fwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
       const T* xp = x + base + (long long)t0 * D;
       const T* gp = g + base + (long long)t0 * D;
 #pragma unroll
-      for (int i = 0; i < S; ++i) {
-        xr[i].load(xp + i * D);
-        gr[i].load(gp + i * D);
+      for (int i = 0; i < S; ++i, xp += D, gp += D) {
+        xr[i].load(xp);
+        gr[i].load(gp);
       }
       return;
     }
@@ -245,14 +245,14 @@ scan_fwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
     const bool whole = t0 + S <= len;
     float* yp = y + base + (long long)t0 * D;
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
+    for (int i = 0; i < S; ++i, yp += D) {
       Pack<float, VEC> out;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         h[j] = fmaf(f[i][j], h[j], a[i][j]);
         out.set(j, whole || t0 + i < len ? h[j] : 0.f);
       }
-      if (live && (whole || t0 + i < T_)) out.store(yp + i * D);
+      if (live && (whole || t0 + i < T_)) out.store(yp);
     }
   }
   if (fin && live && rank == 0 && w == 0)
@@ -387,7 +387,9 @@ scan_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
   const bool live = ch < D;
   const int len = length_of(lens, b, T_, ctl);
   const int step = TILE * CL, rounds = (int)(((long long)len + step - 1) / step);
+  int armed = 0;  // rounds fetched so far
   auto fetch = [&](int r) {  // one thread
+    armed = r + 1;
     const int s = r % STAGES;
     const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(smem) + s * 2 * BYTES;
     const int t = r * step + rank * TILE;
@@ -439,7 +441,7 @@ scan_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
     }
     float h[2];
     enter(ex, r, own, carry, h, ctl, ok);
-    if (tid == 0 && r + STAGES < rounds) fetch(r + STAGES);
+    if (tid == 0 && ok && r + STAGES < rounds) fetch(r + STAGES);
     float* yp = yb + (long long)t0 * D;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
@@ -450,9 +452,10 @@ scan_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
                whole || t0 + i < len ? make_float2(h[0], h[1]) : make_float2(0.f, 0.f));
     }
   }
-  // after a wait that gave up: the copies in flight land before the CTA's memory is given back
+  // after a wait that gave up nothing is fetched any more; the copies in flight land before the
+  // CTA's memory is given back
   if (!ok && tid == 0)
-    for (int r = max(0, rounds - STAGES); r < rounds; ++r)
+    for (int r = max(0, armed - STAGES); r < armed; ++r)
       mbar_wait(smem_u32(&full[r % STAGES]), (r / STAGES) & 1, ctl, 4000000000ull);
   // the padding that no round has reached
   for (int t = rounds * step + rank * WARPS + w; t < T_; t += WARPS * CL)
@@ -485,7 +488,9 @@ scan_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
   const int step = TILE * CL, rounds = (int)(((long long)len + step - 1) / step);
   // round r, from the sequence's last token: this CTA's tile starts at token
   auto tile_at = [&](int r) { return len - (r * step + rank * TILE) - TILE; };
+  int armed = 0;  // rounds fetched so far
   auto fetch = [&](int r) {  // one thread; a tile may begin before the sequence: zeros there
+    armed = r + 1;
     const int s = r % STAGES, t = tile_at(r);
     const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(smem) + s * STAGE;
     mbar_arrive_expect_tx(bar, STAGE);
@@ -549,7 +554,7 @@ scan_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
     }
     float c[2];
     enter(ex, r, own, carry, c, ctl, ok);
-    if (tid == 0 && r + STAGES < rounds) fetch(r + STAGES);
+    if (tid == 0 && ok && r + STAGES < rounds) fetch(r + STAGES);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       float G[2];
@@ -565,9 +570,10 @@ scan_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
       }
     }
   }
-  // after a wait that gave up: the copies in flight land before the CTA's memory is given back
+  // after a wait that gave up nothing is fetched any more; the copies in flight land before the
+  // CTA's memory is given back
   if (!ok && tid == 0)
-    for (int r = max(0, rounds - STAGES); r < rounds; ++r)
+    for (int r = max(0, armed - STAGES); r < armed; ++r)
       mbar_wait(smem_u32(&full[r % STAGES]), (r / STAGES) & 1, ctl, 4000000000ull);
   for (int t = len + rank * WARPS + w; t < T_; t += WARPS * CL)  // padding
     if (live) {

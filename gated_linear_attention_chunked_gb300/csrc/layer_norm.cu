@@ -260,7 +260,9 @@ layer_norm_fwd_ring_kernel(const TX* __restrict__ x, const float* __restrict__ w
   uint8_t* const ring = smem + w * stages * row_bytes;
   const long long first = (long long)blockIdx.x * warps + w, step = (long long)gridDim.x * warps;
   const int mine = first < n ? (int)((n - first + step - 1) / step) : 0;  // rows of this warp
+  int armed = 0;  // rows fetched so far
   auto fetch = [&](int k) {  // one lane
+    armed = k + 1;
     const uint32_t bar = smem_u32(&full[w][k % stages]);
     mbar_arrive_expect_tx(bar, row_bytes);
     bulk_load(smem_u32(ring) + (k % stages) * row_bytes, x + (first + k * step) * D, row_bytes, bar);
@@ -293,7 +295,7 @@ layer_norm_fwd_ring_kernel(const TX* __restrict__ x, const float* __restrict__ w
       else in[i].fill(0.f);
     }
     __syncwarp();
-    if (lane == 0 && k + stages < mine) fetch(k + stages);
+    if (lane == 0 && ok && k + stages < mine) fetch(k + stages);
     float2 a = make_float2(0.f, 0.f), b = a;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -342,8 +344,10 @@ layer_norm_fwd_ring_kernel(const TX* __restrict__ x, const float* __restrict__ w
       if (rstd) rstd[row] = rs;
     }
   }
-  if (!ok && lane == 0)  // the copies in flight land before the CTA's memory is given back
-    for (int k = max(0, mine - stages); k < mine; ++k)
+  // after a wait that gave up nothing is fetched any more; the copies in flight land before the
+  // CTA's memory is given back
+  if (!ok && lane == 0)
+    for (int k = max(0, armed - stages); k < armed; ++k)
       mbar_wait(smem_u32(&full[w][k % stages]), (k / stages) & 1, ctl, 4000000000ull);
 }
 
@@ -368,7 +372,9 @@ layer_norm_bwd_ring_kernel(const TY* __restrict__ dy, const TX* __restrict__ x,
   const int x_bytes = R * D * (int)sizeof(TX), stage = x_bytes + R * D * (int)sizeof(TY);
   const long long groups = (n + R - 1) / R;
   const int mine = (int)((groups - blockIdx.x + gridDim.x - 1) / gridDim.x);  // groups of this CTA
+  int armed = 0;  // groups fetched so far
   auto fetch = [&](int k) {  // one thread
+    armed = k + 1;
     const long long row0 = (blockIdx.x + (long long)k * gridDim.x) * R;
     const int rows = (int)min((long long)R, n - row0);
     const uint32_t bar = smem_u32(&full[k % RING_STAGES]);
@@ -464,7 +470,7 @@ layer_norm_bwd_ring_kernel(const TY* __restrict__ dy, const TX* __restrict__ x,
     q += __shfl_xor_sync(0xffffffffu, q, 1);
     if ((lane & 7) == 0) reinterpret_cast<float*>(&stat[k & 1][w])[lane >> 3] = q;
     __syncthreads();  // also frees the ring's stage
-    if (t == 0 && k + RING_STAGES < mine) fetch(k + RING_STAGES);
+    if (t == 0 && ok && k + RING_STAGES < mine) fetch(k + RING_STAGES);
     // lane l: value l % 4 of warps l / 4 and l / 4 + 8
     const float* st = reinterpret_cast<const float*>(stat[k & 1]);
     q = lane < 4 * warps ? st[lane] : 0.f;
@@ -495,8 +501,10 @@ layer_norm_bwd_ring_kernel(const TY* __restrict__ dy, const TX* __restrict__ x,
       rs[r] = rs_next[r];
     }
   }
-  if (!ok && t == 0)  // the copies in flight land before the CTA's memory is given back
-    for (int k = max(0, mine - RING_STAGES); k < mine; ++k)
+  // after a wait that gave up nothing is fetched any more; the copies in flight land before the
+  // CTA's memory is given back
+  if (!ok && t == 0)
+    for (int k = max(0, armed - RING_STAGES); k < armed; ++k)
       mbar_wait(smem_u32(&full[k % RING_STAGES]), (k / RING_STAGES) & 1, ctl, 4000000000ull);
   float* p = part + (long long)blockIdx.x * 2 * D;
 #pragma unroll

@@ -64,7 +64,8 @@ def _view(t, name, dev, shape):
         raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if t.shape != shape or t.stride(-1) != 1:
         raise ValueError(f"{name} must be {list(shape)} with its last axis contiguous")
-    return t.data_ptr(), (ctypes.c_longlong * (t.dim() - 1))(*t.stride()[:-1])
+    strides = [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], shape)]
+    return t.data_ptr(), (ctypes.c_longlong * len(strides))(*strides)
 
 
 def _begin(t, name, stream):
@@ -337,6 +338,8 @@ def window_cache_fill(pool_k, pool_v, page, k, v, window, sink=0, lens=None, *, 
             _fail("gla_window_cache_fill", rc)
     finally:
         _end(ctx)
+
+
 def window_attn_decode_workspace_size(n_active, H, KV, window, sink=0) -> int:
     return _library().gla_window_attn_decode_workspace_size(n_active, H, KV, window, sink)
 

@@ -22,10 +22,12 @@
  *    pointers unless a comment says "host".  The library allocates no device
  *    memory; scratch comes from the caller's `workspace`.
  *  - Streams: calls enqueue work on `stream` (NULL = legacy default stream)
- *    and return without synchronising.  gla_chunk_fwd, gla_chunk_bwd and
- *    gla_decode_step can be captured into a CUDA graph (stream capture) once
- *    the device has run them eagerly: a replay gives exactly the results of
- *    the same calls made then on the captured buffers' contents.
+ *    and return without synchronising.  gla_chunk_fwd, gla_chunk_bwd,
+ *    gla_decode_step and the gated scan, layer norm and windowed attention
+ *    calls can be captured into a CUDA graph (stream capture) once the device
+ *    has run them eagerly: a replay gives exactly the results of the same
+ *    calls made then on the captured buffers' contents.  A workspace serves
+ *    one call at a time: graphs or streams that share one must not overlap.
  *  - Errors: argument errors are returned before anything is launched, as
  *    GLA_ERR_INVALID_ARG / GLA_ERR_UNSUPPORTED / GLA_ERR_ALIGNMENT /
  *    GLA_ERR_WORKSPACE.  A failed launch returns GLA_ERR_CUDA.  Errors found
@@ -106,8 +108,8 @@ GLA_API gla_status gla_wait_probe(cudaStream_t stream);
 
 /* Diagnostic of the chunk kernels' give-up path (no counterpart in the article).  For calls
  * made after it returns (process-wide), the tensor-core issuer of every CTA of the chunked
- * forward, backward and segment-pass kernels, on reaching chunk step `step` of its loop,
- * waits on a barrier whose phase completes only after that loop.  The bounded wait gives up
+ * forward, backward and segment-pass kernels, and of the windowed attention's forward and
+ * gradient, on reaching chunk step (streamed tile) `step` of its loop, waits on a barrier whose phase completes only after that loop.  The bounded wait gives up
  * after the limit of gla_set_wait_timeout_ns, records GLA_ERR_TIMEOUT and raises the CTA's
  * abort flag; every role then leaves its loop (one path per warp), drains its copies and
  * tensor-core work, frees its tensor memory and exits.  The call's outputs are then
@@ -490,8 +492,7 @@ GLA_API gla_status gla_conv_decode_step(float* state, const float* x, const floa
  *                the state after lens[b] tokens (0: init_state).  A length outside [0, T] is
  *                read as the nearer end and sets the device error word to GLA_ERR_RANGE
  *   y            [B,T,D] fp32 (written)      final_state [B,D] fp32 or NULL (written)
- * All arithmetic is fp32; nothing is allocated; results repeat bit for bit.  May be captured
- * into a CUDA graph, as the decode step and the gradient may.
+ * All arithmetic is fp32; nothing is allocated; results repeat bit for bit.
  */
 GLA_API gla_status gla_gated_scan_fwd(const void* x, const void* g, gla_dtype in_dtype,
                                       const float* init_state, const int* lens, float* y,
@@ -580,8 +581,9 @@ GLA_API gla_status gla_layer_norm_bwd(const void* dy, gla_dtype dy_dtype, const 
  *   o            [B,T,H,192] out_dtype: in_dtype or GLA_FP32 (written)
  *   lse          [B,H,T] fp32 or NULL (written; the gradient reads it; 4-byte aligned)
  * Scores, softmax statistics and sums are fp32; the softmax weights round once to in_dtype for
- * the product with v, which the tensor cores take in one type.  T <= 2^30.  May be captured into
- * a CUDA graph, as the gradient and the decode step may.
+ * the product with v, which the tensor cores take in one type.  q, k and v of live tokens (and
+ * the gradient's dO) must be finite: a NaN or infinity may reach every row of its sequence, also
+ * rows that do not see it.  T <= 2^30.
  */
 GLA_API gla_status gla_window_attn_fwd(const void* q, const void* k, const void* v,
                                        gla_dtype in_dtype, const int* lens, int window, int sink,

@@ -48,6 +48,13 @@ CASES = [  # B, T, D, type, states, lengths
     (1, 1025, 66, "bf16", False, None),
     (5, 128, 200, "fp16", True, [128, 127, 65, 64, 2]),
     (40, 70, 512, "bf16", True, None),         # one CTA per sequence and slab
+    (1, 700, 33, "bf16", True, [650]),         # odd rows, a cluster of 8
+    (2, 300, 66, "fp32", True, [300, 129]),    # rows of pairs, a cluster of 4
+    (30, 200, 130, "fp16", True, None),
+    (60, 130, 66, "bf16", False, None),        # ... and of 2
+    (60, 130, 64, "bf16", True, [130] * 30 + [64] * 29 + [0]),  # the same from 16-byte rows
+    (30, 129, 65, "fp32", True, None),
+    (1, 1400, 72, "fp16", True, [1399]),       # more rounds than the ring holds
 ]
 
 

@@ -37,6 +37,12 @@ CASES = [  # tokens, channels, type, output type, weights
     (6, 8200, "bf16", "bf16", True), (5, 9001, "fp32", "fp32", True),
     (4, 16384, "fp32", "fp32", True), (3, 16384, "bf16", "fp32", True),
     (3, 16383, "fp16", "fp16", True),
+    # rows enough for a warp each, of each number of accesses
+    (1300, 500, "fp32", "fp32", True), (2500, 512, "bf16", "bf16", True),
+    (1250, 1000, "fp16", "fp32", False), (1250, 1400, "fp32", "fp32", True),
+    (1250, 1528, "bf16", "fp32", True), (5000, 2048, "bf16", "bf16", True),
+    (1218, 2044, "fp32", "fp32", False), (4000, 8, "fp16", "fp16", True),
+    (700, 4096, "bf16", "bf16", True), (700, 4096, "fp32", "fp32", True),
 ]
 
 
