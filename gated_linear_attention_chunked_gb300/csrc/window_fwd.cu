@@ -22,8 +22,17 @@
 //   warps 11..14 the output rows of an item, while the softmax is on the next one
 // The scores run two tiles ahead of the values (and across items), so that the tensor cores go
 // from P V of a tile to the scores of the next but one while the softmax works on the tile
-// between; P has columns of its own, so neither waits for the other's reads.  A tile's scores
-// and sums are each one commit, which also frees the key and value buffers.
+// between.  P takes the place of the scores it came from: products run in the order of their
+// issue, so the next scores there come behind the P V that reads it, and a group writes P without
+// waiting for the P V of the tile before.  A tile's scores and sums are each one commit, which also
+// frees the key and value buffers.
+//
+// Bound by the softmax (its two passes over a tile take the two groups longer than the products
+// do) and, between items, by the wait for the output rows.  Measured, bf16, B=8 T=2048, 16 heads,
+// window 512, 4 sinks: 110.5 us, 2.5 times the copy of its bytes; 126 with P in columns of its own,
+// 117 with masks decided by votes of the warp instead of by the tile's position.  No faster: the
+// next scores ahead of P V (120), output rows held in registers (spills, 127), tiles of a sequence
+// from the last (130: the keys' tiles then leave the L2 between their readers).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -53,40 +62,49 @@ enum Bar : uint32_t {  // +stage (+4 group + quadrant, + quadrant) where there a
   Q_FULL = 0, K_FULL = 2, V_FULL = 4,
   S_FULL = 6,    // a tile's scores are in tensor memory (and its keys have been read)
   O_DONE = 8,    // O += P V has run: P, V and O are free to touch
-  P_READY = 10,  // a group has written P (and read S)
-  O_FREE = 11,   // the output rows have been read
-  DRAIN = 12,
-  REF = 13,      // a group's references of a tile are known
-  SUM = 21,      // both groups' sums of an item are known
-  NBAR = 25
+  P_READY = 10,  // +group: P has been written (over its S)
+  O_FREE = 12,   // the output rows have been read
+  DRAIN = 13,
+  REF = 14,      // a group's references of a tile are known
+  SUM = 22,      // both groups' sums of an item are known
+  NBAR = 26
 };
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
 constexpr uint32_t SMEM_USED = OFF_ABORT + 4, SMEM_BYTES = SMEM_USED + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
-constexpr uint32_t TM_S = 0, TM_O = 256, TM_P = 448;  // columns: S 2 x 128, O 192, P 64
+// Columns: S twice 128, O 192.  A tile's P takes the place of its S, from the front.
+constexpr uint32_t TM_S = 0, TM_O = 256;
 
 constexpr int GROUP = 128, K_WARP = 8, V_WARP = 9, MMA_WARP = 10, OUT_WARP = 11;
 constexpr int THREADS = 15 * 32;
 
-// The items of a CTA, blockIdx.x, + gridDim.x, ...: heads fastest, then tiles of a sequence.
+// The items of a CTA, blockIdx.x, + gridDim.x, ...: heads fastest, then tiles of a sequence.  The
+// step is added digit by digit, so that an item costs no division.
 struct Items {
   const WindowArgs& a;
-  unsigned at, total, tiles;  // the host keeps the count of items below 2^30
-  int b, h, q0, len;
+  int tiles, dh, dj, db;   // tiles of a sequence; the step's heads, tiles and sequences
+  int b, h, j, q0, len;    // (the host keeps the count of items below 2^30)
   __device__ Items(const WindowArgs& a_) : a(a_) {
     tiles = (a.T + BM - 1) / BM;
-    total = (unsigned)a.B * tiles * a.H;
-    at = blockIdx.x - gridDim.x;
+    const int s = gridDim.x / a.H, i = blockIdx.x / a.H;
+    dh = gridDim.x - s * a.H;
+    db = s / tiles;
+    dj = s - db * tiles;
+    // one step ahead of the first
+    h = (int)blockIdx.x - i * a.H - dh;
+    b = i / tiles - db;
+    j = i % tiles - dj;
   }
   __device__ bool next() {
-    at += gridDim.x;
-    if (at >= total) return false;
-    const unsigned r = at / (unsigned)a.H;
-    h = (int)(at - r * a.H);
-    b = (int)(r / tiles);
-    q0 = (int)(r - b * tiles) * BM;
+    h += dh;
+    j += dj;
+    b += db;
+    if (h >= a.H) { h -= a.H; ++j; }
+    if (j >= tiles) { j -= tiles; ++b; }
+    if (b >= a.B) return false;
+    q0 = j * BM;
     len = a.T;
     if (a.lens) len = min(max(__ldg(a.lens + b), 0), a.T);
     return true;
@@ -134,6 +152,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   if (tid == K_WARP * 32) {
     for (uint32_t i = 0; i < P_READY; ++i) mbar_init(cta.bar(i), 1);
     mbar_init(cta.bar(P_READY), GROUP);
+    mbar_init(cta.bar(P_READY + 1), GROUP);
     mbar_init(cta.bar(O_FREE), GROUP);
     mbar_init(cta.bar(DRAIN), 1);
     for (uint32_t q = REF; q < SUM; ++q) mbar_init(cta.bar(q), 32);
@@ -252,14 +271,14 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           if (!(ok = wait(cta, cta.bar(V_FULL + s), (vn >> 1) & 1, ctl))) break;
           if (v_at == 0 && vm > 0 &&
               !(ok = wait(cta, cta.bar(O_FREE), (vm - 1) & 1, ctl))) break;
-          if (!(ok = wait(cta, cta.bar(P_READY), vn & 1, ctl))) break;
+          if (!(ok = wait(cta, cta.bar(P_READY + s), (vn >> 1) & 1, ctl))) break;
           tc_fence_after();
           const uint64_t v = v_desc + (s * V_BYTES >> 4);
           const int steps = tile_cols(vk, v_at, a.sink) >> 4;
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             if (c < steps)
-              mma_f16_ts(tmem + TM_O, tmem + TM_P + 8 * c, v + (c * 2048 >> 4), ID_PV,
+              mma_f16_ts(tmem + TM_O, tmem + TM_S + 128 * s + 8 * c, v + (c * 2048 >> 4), ID_PV,
                          v_at > 0 || c > 0);
           mma_commit(cta.bar(O_DONE + s));
           if (s_live && !(ok = scores())) break;
@@ -287,7 +306,16 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         const int n = n0 + i, s0 = kt.tile(i) * BN;
         const bool whole = s0 + BN - 1 <= it.q0 && s0 + BN <= len &&
                            (it.q0 + BM - 1 - s0 < a.window || s0 + BN <= a.sink);
-        // the columns 32 c .. of the tile that this row sees
+        // The columns of the tile that some row of the warp sees lie in chunks (of 32) ca .. cb - 1;
+        // chunk c is seen by all if full(c).  Chunks from `cols` on are not multiplied.
+        const int t0 = it.q0 + 32 * q4, cols = tile_cols(kt, i, a.sink);
+        const int ca = s0 < a.sink ? 0 : max(0, t0 - a.window + 1 - s0) >> 5;
+        const int cb = (min(min(t0 + 31, len - 1) - s0, cols - 1) >> 5) + 1;
+        auto full = [&](int c) {
+          const int c0 = s0 + 32 * c;
+          return c0 + 31 <= min(t0, len - 1) && (t0 + 31 - c0 < a.window || c0 + 31 < a.sink);
+        };
+        // the columns 32 c .. that this row sees
         auto sees = [&](int c) -> uint32_t {
           const int c0 = s0 + 32 * c;
           return bits_to(min(t, len - 1) - c0) &
@@ -312,16 +340,16 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           }
         } else {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t see = sees(c);
-            if (!__any_sync(0xffffffffu, see != 0u)) continue;
+          for (int c = ca; c < cb; ++c) {
             uint32_t z[32];
             tmem_ld32(ts + 32 * c, z);
             tmem_wait_ld();
-            if (!__all_sync(0xffffffffu, see == ~0u))
+            if (!full(c)) {
+              const uint32_t see = sees(c);
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 if (!((see >> j) & 1)) z[j] = 0xFF800000u;  // -inf
+            }
             maxima(z);
           }
         }
@@ -358,48 +386,40 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
             p[j] = pack2<T>(x.x, x.y);
           }
         };
-        // P's columns and, for the rescaling, O are free once the tile before has been added
-        auto free_p = [&]() -> bool {
-          if (n > 0 &&
-              !(ok = wait_warp(cta, cta.bar(O_DONE + (g ^ 1)), ((n - 1) >> 1) & 1, ctl)))
-            return false;
-          tc_fence_after();
-          return true;
-        };
-        if (whole) {  // all weights first: once P is free they only have to be written
-          uint32_t p[4][16];
+        // P over the columns of S that have been read
+        if (whole) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t z[32];
+            uint32_t z[32], p[16];
             tmem_ld32(ts + 32 * c, z);
             tmem_wait_ld();
-            weights(z, p[c], 0u, false);
+            weights(z, p, 0u, false);
+            tmem_st16(ts + 16 * c, p);
           }
-          if (!free_p()) break;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_st16(trow + TM_P + 16 * c, p[c]);
-        } else if (free_p()) {
+        } else {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t see = sees(c);
+          for (int c = 0; 32 * c < cols; ++c) {
             uint32_t p[16];
-            if (__any_sync(0xffffffffu, see != 0u)) {
+            if (c >= ca && c < cb) {
               uint32_t z[32];
               tmem_ld32(ts + 32 * c, z);
               tmem_wait_ld();
-              if (__all_sync(0xffffffffu, see == ~0u)) weights(z, p, 0u, false);
-              else weights(z, p, see, true);
+              if (full(c)) weights(z, p, 0u, false);
+              else weights(z, p, sees(c), true);
             } else {
 #pragma unroll
               for (int j = 0; j < 16; ++j) p[j] = 0u;
             }
-            tmem_st16(trow + TM_P + 16 * c, p);
+            tmem_st16(ts + 16 * c, p);
           }
         }
-        if (!ok) break;
         acc[0] = add2(acc[0], acc[1]);
         sum += acc[0].x + acc[0].y;
         if (i > 0 && __any_sync(0xffffffffu, scale != 1.f)) {
+          // O once the tile before has been added (and the one before that, whose phase of the
+          // barrier this could be taken for, is: this tile's scores came behind it)
+          if (!(ok = wait_warp(cta, cta.bar(O_DONE + (g ^ 1)), ((n - 1) >> 1) & 1, ctl))) break;
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 6; ++c) {
             uint32_t o[32];
@@ -421,7 +441,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(cta.bar(P_READY));
+        mbar_arrive(cta.bar(P_READY + g));
       }
       if (!ok) break;
       n0 += kt.n;
@@ -453,8 +473,8 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         ref = fmaxf(s0.y, s1.y);
         if (s0.y != -INFINITY) sum = s0.x * ex2(s0.y - ref);
         if (s1.y != -INFINITY) sum = fmaf(s1.x, ex2(s1.y - ref), sum);
-        // the tile before the last has been added (its softmax waited for that): this is the
-        // last one's phase
+        // the last tile's scores came behind the sums of the tile before the one before it, so this
+        // is the last one's phase
         if (!wait_warp(cta, cta.bar(O_DONE + ((n0 - 1) & 1)), ((n0 - 1) >> 1) & 1, ctl)) break;
         tc_fence_after();
         ++m;
