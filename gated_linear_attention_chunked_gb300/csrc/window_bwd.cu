@@ -30,6 +30,12 @@
 // own, at least as long as an ordinary one and at most 16 of a key tile, whose sums go to the
 // workspace as fp32 and are added in order by window_sink_kernel.  Past four tiles of sinks the
 // items of a tile are many enough as they are, and one item takes all queries of its keys.
+//
+// Bound by the hand-over of a tile from its scores to P or Z and on to the sums: the tensor cores
+// are 32 to 40 per cent busy in the three kinds.  Measured, bf16, B=8 T=2048, 16 heads on 4, window
+// 512, 4 sinks, ragged: 208 us (delta 21, the sinks' sums 5), against 277 with the three kinds in
+// one grid and every operand from shared memory.  No faster: masks by the tile's position in place
+// of votes (210).
 #include <cuda_runtime.h>
 
 #include <algorithm>
