@@ -15,27 +15,32 @@
 // with P and Z (dz) written back to tensor memory in 16 bits as the left operand.  All three
 // recompute the scores: eight products where five would do, but no sum crosses a CTA, so there are
 // no atomics on results and they repeat bit for bit; and apart the kinds have the tensor memory
-// for two tiles of scores each, and for the held operand of the longer product (k, or v or dO):
-// an operand of 128 x 16 from shared memory next to one of 64 x 16 takes 1.5 times as long to read
-// as the product takes.  The three grids are programmatic dependents of one another and wait for
-// nothing, so that a CTA of the next kind starts where one of the last has no item left.
+// for two tiles of scores each and for all held operands (Z takes the place of its S, which the
+// next scores there, issued behind the sum that reads Z, may overwrite): an operand of 128 x 16 from
+// shared memory next to one of 64 x 16 takes 1.5 times as long to read as the product takes, and
+// the held tile's shared memory is free for the next item's as soon as it has been copied.  The
+// grids are programmatic dependents of one another: KEYS waits for delta, the others for nothing, so
+// that a CTA of the next kind starts where one of the last has no item left.
 //   warp 8       takes items from a counter and issues the TMA loads: the held tile, and a ring of
 //                four streamed tiles
 //   warp 9       lse and delta of the streamed queries, into shared memory (VALUES, KEYS)
 //   warp 10      tcgen05 issuer and TMEM owner; the scores run two tiles ahead of the sums
-//   warps 0..7   two groups that take an item's tiles in turn (thread = row): mask, P, Z; between
-//                items they bring the held operand into tensor memory
-//   warps 11..14 the output rows of an item, while the others are on the next one
+//   warps 0..7   two groups that take an item's tiles in turn (thread = row): mask, P, Z
+//   warps 11..14 the held operands of the next item into tensor memory, then the output rows of
+//                this one, while the others are on the next
 // Keys that hold sinks are seen by every query behind them.  Those far queries are items of their
 // own, at least as long as an ordinary one and at most 16 of a key tile, whose sums go to the
 // workspace as fp32 and are added in order by window_sink_kernel.  Past four tiles of sinks the
 // items of a tile are many enough as they are, and one item takes all queries of its keys.
 //
-// Bound by the hand-over of a tile from its scores to P or Z and on to the sums: the tensor cores
-// are 32 to 40 per cent busy in the three kinds.  Measured, bf16, B=8 T=2048, 16 heads on 4, window
-// 512, 4 sinks, ragged: 208 us (delta 21, the sinks' sums 5), against 277 with the three kinds in
-// one grid and every operand from shared memory.  No faster: masks by the tile's position in place
-// of votes (210).
+// Bound by the hand-over of a tile from its scores to P or Z and on to the sums, and by the issue of
+// 22 (VALUES: 10) products per 64 streamed rows: ~1,300 cycles a tile where the products take 770.
+// Measured, bf16, B=8 T=2048, 16 heads on 4, window 512, 4 sinks, ragged: 189 us (delta 21, the
+// sinks' sums 4).  Before: 277 with the three kinds in one grid and every operand from shared
+// memory; 207 with half of the held operands in tensor memory, copied by the warps of P and Z; 202
+// with all of them; 196 with delta and the sinks' sums chained to the kinds; 191 with an issuer that
+// keeps its descriptors.  No faster: masks by the tile's position in place of votes (+2 us), an
+// issuer that takes the next item's scores ahead of this item's last sums (+4 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -67,8 +72,8 @@ enum Bar : uint32_t {
   STAT_FULL = 8,   // +stage
   STAT_EMPTY = 12, // +stage
   HELD_FULL = 16,
-  HELD_EMPTY = 17, // the item's scores are complete
-  HELD_READY = 18, // the held operand is in tensor memory
+  HELD_EMPTY = 17, // the item's scores are complete: the held operands may be replaced
+  HELD_READY = 18, // the held operands are in tensor memory (and no more read from shared memory)
   ITEM_FULL = 19,  // +slot
   ITEM_EMPTY = 21, // +slot
   S_FULL = 23,     // +group: its S and D are in tensor memory
@@ -78,22 +83,23 @@ enum Bar : uint32_t {
   DRAIN = 29,
   NBAR = 30
 };
-constexpr uint32_t OFF_ITEM = OFF_BAR + NBAR * 8;  // int item[2]
-constexpr uint32_t OFF_TMEM = OFF_ITEM + 8, OFF_ABORT = OFF_TMEM + 4;
+constexpr uint32_t OFF_ITEM = OFF_BAR + NBAR * 8;  // int4 item[2][2]
+static_assert(OFF_ITEM % 16 == 0, "items are read by 16 bytes");
+constexpr uint32_t OFF_TMEM = OFF_ITEM + 64, OFF_ABORT = OFF_TMEM + 4;
 // The opt-in maximum; the kernel aligns its base to 1024 bytes and does not run (GLA_ERR_LAYOUT)
 // if the padding that takes would not fit.  Dynamic shared memory normally starts aligned.
 constexpr uint32_t SMEM_USED = OFF_ABORT + 4, SMEM_BYTES = 232448;
 static_assert(SMEM_USED <= SMEM_BYTES, "shared memory budget");
 enum Kind : int { VALUES = 0, KEYS = 1, QUERIES = 2 };
-// Tensor memory columns.  VALUES: dv 192, S twice 64, P twice 32, k 48; the others: v or dO 96, dk
-// or dq 96, S and D twice 64, Z twice 32.
+// Tensor memory columns.  VALUES: dv 192, S twice 64, P twice 32, k 48.  The others: S and D twice
+// 64 (Z takes the place of its S, from the front), dk or dq 96, v or dO 96, k or q 48.
 template <int KIND>
 struct Tm {
   static constexpr bool V = KIND == VALUES;
-  static constexpr uint32_t SUM = V ? 0 : 96, HELD = V ? 384 : 0;
-  __device__ static uint32_t s(int g) { return V ? 192 + 64 * g : 192 + 128 * g; }
-  __device__ static uint32_t d(int g) { return 256 + 128 * g; }
-  __device__ static uint32_t p(int g) { return (V ? 320 : 448) + 32 * g; }
+  static constexpr uint32_t SUM = V ? 0 : 256, HX = V ? 384 : 448, HY = 352;
+  __device__ static uint32_t s(int g) { return V ? 192 + 64 * g : 128 * g; }
+  __device__ static uint32_t d(int g) { return 64 + 128 * g; }
+  __device__ static uint32_t p(int g) { return V ? 320 + 32 * g : s(g); }
 };
 
 constexpr int EW = 8, LOAD_WARP = 8, STAT_WARP = 9, MMA_WARP = 10, GROUP = 128;
@@ -140,6 +146,7 @@ __host__ __device__ inline int sink_rows(const BwdPlan& p, int sink) {
 template <class T, class TO>
 __global__ void __launch_bounds__(256)
 window_delta_kernel(WindowArgs a, float* __restrict__ delta, int* __restrict__ counter, DevCtl ctl) {
+  griddep_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x < 3) counter[threadIdx.x] = 0;  // one a kind
   const long long rows = (long long)a.B * a.T * a.H;
   const long long row = (long long)blockIdx.x * 32 + (threadIdx.x >> 3);  // (b T + t) H + h
@@ -188,7 +195,7 @@ struct Item {
   int first, per_head;    // held keys: first streamed tile and tiles per head
   int n;                  // streamed tiles in all
   KeyTiles kt;            // QUERIES: the key tiles
-  __device__ Item() : kt(0, 1, BS, 1, 0) {}
+  __device__ Item() : b(0), head(0), row0(0), len(0), part(-1), first(0), per_head(0), n(0), kt(0, 1, BS, 1, 0) {}
   __device__ void set(int i, const WindowArgs& a, const BwdPlan& p) {
     unsigned r = i;
     auto take = [&](unsigned m) {  // r mod m, then r / m
@@ -221,6 +228,19 @@ struct Item {
       kt = KeyTiles(row0, min(row0 + BH, len), BS, a.window, a.sink);
       n = kt.n;
     }
+  }
+  // Through shared memory, so that only the warp that takes the item divides.
+  __device__ void put(int4* p) const {
+    p[0] = make_int4(b, head, row0, len);
+    p[1] = make_int4(part, HELD_KEYS ? first : kt.lo, HELD_KEYS ? per_head : kt.far, n);
+  }
+  __device__ bool get(const int4* p) {
+    const int4 x = p[0], y = p[1];
+    b = x.x; head = x.y; row0 = x.z; len = x.w;
+    part = y.x; n = y.w;
+    if (HELD_KEYS) { first = y.y; per_head = y.z; }
+    else { kt.lo = y.y; kt.far = y.z; kt.n = y.w; }
+    return b >= 0;
   }
   // columns of streamed tile i that count: fewer in the sinks' tiles in front of the window
   __device__ int cols(int i, int sink) const {
@@ -260,12 +280,13 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
                   float* __restrict__ sink_sums, DevCtl ctl) {
   constexpr bool BF16 = !__is_same(T, __half), STATS = KIND != QUERIES;
   using M = Tm<KIND>;
-  griddep_launch_dependents();  // the next kind needs SMs, and nothing of this one
+  if (KIND != KEYS) griddep_launch_dependents();  // the next kind needs SMs, nothing of this one
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Cta cta;
   cta.base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   if ((uint32_t)(cta.base - smem_raw) + SMEM_USED > SMEM_BYTES) {
     if (threadIdx.x == 0) record_error(ctl, DEV_LAYOUT);
+    griddep_wait();
     return;
   }
   cta.sb = smem_u32(cta.base);
@@ -274,7 +295,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
   uint8_t* const base = cta.base;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t* tmem_slot = (uint32_t*)(base + OFF_TMEM);
-  volatile int* items = (volatile int*)(base + OFF_ITEM);
+  int4* const items = (int4*)(base + OFF_ITEM);
   if (warp == MMA_WARP) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -288,7 +309,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
     }
     mbar_init(cta.bar(HELD_FULL), 1);
     mbar_init(cta.bar(HELD_EMPTY), 1);
-    mbar_init(cta.bar(HELD_READY), EW * 32);
+    mbar_init(cta.bar(HELD_READY), 128);
     for (uint32_t s = 0; s < 2; ++s) {
       mbar_init(cta.bar(ITEM_FULL + s), 1);
       mbar_init(cta.bar(ITEM_EMPTY + s), EW + 4 + (STATS ? 2 : 1));
@@ -300,6 +321,10 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
     mbar_init(cta.bar(DRAIN), 1);
     *cta.abort_flag() = 0;
     fence_barrier_init();
+  }
+  if (KIND == KEYS) {  // the first kind: delta and the counters, for itself and the others
+    griddep_wait();
+    griddep_launch_dependents();
   }
   tc_fence_before();
   __syncthreads();
@@ -314,12 +339,10 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
     if (whole_warp ? !wait_warp(cta, cta.bar(ITEM_FULL + s), (m >> 1) & 1, ctl)
                    : !wait(cta, cta.bar(ITEM_FULL + s), (m >> 1) & 1, ctl))
       return false;
-    const int i = items[s];
+    const bool some = it.get(items + 2 * s);
     if (whole_warp) __syncwarp();
     if (!whole_warp || lane == 0) mbar_arrive(cta.bar(ITEM_EMPTY + s));
-    if (i < 0) return false;
-    it.set(i, a, plan);
-    return true;
+    return some;
   };
 
   if (warp == LOAD_WARP) {
@@ -333,13 +356,14 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
         const uint32_t slot = m & 1;
         if (m >= 2 && !wait(cta, cta.bar(ITEM_EMPTY + slot), ((m >> 1) - 1) & 1, ctl)) break;
         const bool end = ticket >= plan.total(KIND);
-        items[slot] = end ? -1 : ticket;
+        if (end) it.b = -1;
+        else it.set(ticket, a, plan);
+        it.put(items + 2 * slot);
         mbar_arrive(cta.bar(ITEM_FULL + slot));
         if (end) break;
-        it.set(ticket, a, plan);
         ticket = atomicAdd(counter + KIND, 1);
         if (it.n == 0) continue;
-        if (held > 0 && !wait(cta, cta.bar(HELD_EMPTY), (held - 1) & 1, ctl)) break;
+        if (held > 0 && !wait(cta, cta.bar(HELD_READY), (held - 1) & 1, ctl)) break;
         ++held;
         mbar_arrive_expect_tx(cta.bar(HELD_FULL), KIND == VALUES ? 3 * HX_BOX : H_BYTES);
         for (int j = 0; j < 3; ++j) {
@@ -401,29 +425,29 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
       constexpr uint32_t ID_SUM = idesc_f16(128, KIND == VALUES ? kDV : kDK, BF16, BF16, false, true);
       Item<KIND> it;
       int n = 0, held = 0;       // streamed tiles and items with work so far
-      uint32_t ready[2] = {0, 0};  // tiles of each group so far
+      uint32_t phase = 0;        // bit g: parity of the group's tiles so far
       bool ok = true;
-      const uint64_t hx = smem_desc(cta.sb + OFF_HX, 16, 512, SW_64);
+      // stage 0's descriptors (they count in 16 bytes): for the scores, and for the sums
+      const uint64_t sx0 = smem_desc(cta.sb + OFF_S, 16, 512, SW_64);
+      const uint64_t sy0 = smem_desc(cta.sb + OFF_S + 3 * SX_BOX, 16, 1024, SW_128);
+      const uint64_t sum0 = KIND == VALUES
+                                ? smem_desc(cta.sb + OFF_S + 3 * SX_BOX, SY_BOX, 1024, SW_128)
+                                : smem_desc(cta.sb + OFF_S, SX_BOX, 512, SW_64);
       auto scores = [&](int i, int at) -> bool {  // S, D of the item's tile i, tile `at` in all
-        const uint32_t s = at % STAGES, st = cta.sb + OFF_S + s * S_BYTES;
+        const uint32_t s = at % STAGES;
         const int g = i & 1;
         if (!wait(cta, cta.bar(FULL + s), (at / STAGES) & 1, ctl)) return false;
         tc_fence_after();
-        const uint32_t id = ID_S | ((uint32_t)(it.cols(i, a.sink) >> 3) << 17);
-        const uint64_t sx = smem_desc(st, 16, 512, SW_64);
-        const uint64_t sy = smem_desc(st + 3 * SX_BOX, 16, 1024, SW_128);
+        const uint32_t id = ID_S | ((uint32_t)((KIND == QUERIES ? it.cols(i, a.sink) : BS) >> 3) << 17);
+        const uint64_t sx = sx0 + s * (S_BYTES >> 4), sy = sy0 + s * (S_BYTES >> 4);
 #pragma unroll
-        for (int c = 0; c < 6; ++c) {  // (the descriptors count in 16 bytes)
-          const uint64_t b = sx + (((c >> 1) * SX_BOX + (c & 1) * 32) >> 4);
-          if constexpr (KIND == VALUES)
-            mma_f16_ts(tmem + M::s(g), tmem + M::HELD + 8 * c, b, id, c > 0);
-          else
-            mma_f16_ss(tmem + M::s(g), hx + (((c >> 1) * HX_BOX + (c & 1) * 32) >> 4), b, id, c > 0);
-        }
+        for (int c = 0; c < 6; ++c)
+          mma_f16_ts(tmem + M::s(g), tmem + M::HX + 8 * c,
+                     sx + (((c >> 1) * SX_BOX + (c & 1) * 32) >> 4), id, c > 0);
         if constexpr (KIND != VALUES) {
 #pragma unroll
           for (int c = 0; c < 12; ++c)
-            mma_f16_ts(tmem + M::d(g), tmem + M::HELD + 8 * c,
+            mma_f16_ts(tmem + M::d(g), tmem + M::HY + 8 * c,
                        sy + (((c >> 2) * SY_BOX + (c & 3) * 32) >> 4), id, c > 0);
         }
         mma_commit(cta.bar(S_FULL + g));
@@ -433,12 +457,11 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
       for (int m = 0; ok && next_item(it, m, false); ++m) {
         if (it.n == 0) continue;
         ++held;
-        if (!(ok = wait(cta, cta.bar(HELD_FULL), (held - 1) & 1, ctl))) break;
         if (!(ok = wait(cta, cta.bar(HELD_READY), (held - 1) & 1, ctl))) break;
         if (!(ok = scores(0, n))) break;
         if (it.n > 1 && !(ok = scores(1, n + 1))) break;
         for (int i = 0; i < it.n; ++i, ++n) {
-          const uint32_t s = n % STAGES, st = cta.sb + OFF_S + s * S_BYTES;
+          const uint32_t s = n % STAGES;
           const int g = i & 1;
           if (n == ctl.stall_step) {  // the give-up path's diagnostic (see chunk_fwd.cu)
             wait(cta, cta.bar(DRAIN), 0, ctl);
@@ -447,21 +470,21 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
           }
           if (i == 0 && held > 1 && !(ok = wait(cta, cta.bar(SUM_FREE), (held - 2) & 1, ctl)))
             break;
-          if (!(ok = wait(cta, cta.bar(P_READY + g), ready[g]++ & 1, ctl))) break;
+          if (!(ok = wait(cta, cta.bar(P_READY + g), (phase >> g) & 1, ctl))) break;
+          phase ^= 1u << g;
           tc_fence_after();
+          const uint64_t sum = sum0 + s * (S_BYTES >> 4);
           if constexpr (KIND == VALUES) {
-            const uint64_t sy = smem_desc(st + 3 * SX_BOX, SY_BOX, 1024, SW_128);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              mma_f16_ts(tmem + M::SUM, tmem + M::p(g) + 8 * c, sy + (c * 2048 >> 4), ID_SUM,
+              mma_f16_ts(tmem + M::SUM, tmem + M::p(g) + 8 * c, sum + (c * 2048 >> 4), ID_SUM,
                          i > 0 || c > 0);
           } else {
-            const uint64_t sx = smem_desc(st, SX_BOX, 512, SW_64);
-            const int steps = it.cols(i, a.sink) >> 4;
+            const int steps = KIND == QUERIES ? it.cols(i, a.sink) >> 4 : 4;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
               if (c < steps)
-                mma_f16_ts(tmem + M::SUM, tmem + M::p(g) + 8 * c, sx + (c * 1024 >> 4), ID_SUM,
+                mma_f16_ts(tmem + M::SUM, tmem + M::p(g) + 8 * c, sum + (c * 1024 >> 4), ID_SUM,
                            i > 0 || c > 0);
           }
           mma_commit(cta.bar(EMPTY + s));
@@ -479,7 +502,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
     const int q4 = warp & 3, g = warp >> 2, row = 32 * q4 + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
     Item<KIND> it;
-    int n0 = 0, held = 0;  // streamed tiles and items with work before this item
+    int n0 = 0;            // streamed tiles before this item
     uint32_t used = 0;     // tiles of this group so far
     bool ok = true;
     for (int m = 0; ok && next_item(it, m, true); ++m) {
@@ -491,30 +514,6 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
         lse = -__ldg(a.lse + at) * kLog2e;
         del = -__ldg(delta + at);
       }
-      // the held operand into tensor memory, half a row per group, once the item before has no
-      // more scores to take with it
-      if (held > 0 && !(ok = wait_warp(cta, cta.bar(HELD_EMPTY), (held - 1) & 1, ctl))) break;
-      if (!(ok = wait_warp(cta, cta.bar(HELD_FULL), held & 1, ctl))) break;
-      ++held;
-      tc_fence_after();
-      constexpr int CH = KIND == VALUES ? 6 : 12;  // 16-byte chunks of half a row
-#pragma unroll
-      for (int c = 0; c < CH; c += 2) {
-        uint32_t w[8];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int ch = CH * g + c + e;
-          const uint4 u = *(const uint4*)(
-              KIND == VALUES ? base + OFF_HX + (ch >> 2) * HX_BOX + swz_off(row, ch & 3, 64)
-                             : base + OFF_HY + (ch >> 3) * HY_BOX + swz_off(row, ch & 7, 128));
-          w[4 * e] = u.x; w[4 * e + 1] = u.y; w[4 * e + 2] = u.z; w[4 * e + 3] = u.w;
-        }
-        tmem_st8(trow + M::HELD + 4 * (CH * g + c), w);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(cta.bar(HELD_READY));
-
       Walk<KIND> k(it, G);
       if (g && it.n > 1) k.next();
       for (int i = g; i < it.n; i += 2) {
@@ -617,9 +616,39 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
     constexpr int D = KIND == VALUES ? kDV : kDK;
     const int held_sinks = sink_rows(plan, a.sink), heads = STATS ? a.KV : a.H;
     TO* const dst = static_cast<TO*>(KIND == VALUES ? a.dv : KIND == KEYS ? a.dk : a.dq);
-    Item<KIND> it;
+    // The held operands of an item into tensor memory, once the item before has no more scores to
+    // take with them
+    int held = 0;
+    auto hold = [&]() -> bool {
+      if (held > 0 && !wait_warp(cta, cta.bar(HELD_EMPTY), (held - 1) & 1, ctl)) return false;
+      if (!wait_warp(cta, cta.bar(HELD_FULL), held & 1, ctl)) return false;
+      ++held;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < (KIND == VALUES ? 12 : 36); c += 2) {  // 16-byte chunks of a row
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int ch = c < 12 ? c + e : c - 12 + e;
+          const uint4 u = *(const uint4*)(
+              c < 12 ? base + OFF_HX + (ch >> 2) * HX_BOX + swz_off(row, ch & 3, 64)
+                     : base + OFF_HY + (ch >> 3) * HY_BOX + swz_off(row, ch & 7, 128));
+          w[4 * e] = u.x; w[4 * e + 1] = u.y; w[4 * e + 2] = u.z; w[4 * e + 3] = u.w;
+        }
+        tmem_st8(trow + (c < 12 ? M::HX + 4 * c : M::HY + 4 * (c - 12)), w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(cta.bar(HELD_READY));
+      return true;
+    };
+    Item<KIND> it, ahead;
     int done = 0;  // items with work so far
-    for (int m = 0; next_item(it, m, true); ++m) {
+    bool some = next_item(ahead, 0, true), ok = !some || ahead.n == 0 || hold();
+    for (int m = 0; ok && some; ++m) {
+      it = ahead;
+      some = next_item(ahead, m + 1, true);
+      if (some && ahead.n > 0 && !(ok = hold())) break;
       const int r = it.row0 + row;
       const bool live = r < it.len && it.n > 0;
       // rows whose sums are added up later, as fp32 (held keys); the others go out here
@@ -694,6 +723,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
 template <class TO>
 __global__ void __launch_bounds__(kSums / 2)
 window_sink_kernel(WindowArgs a, BwdPlan plan, const float* __restrict__ sums) {
+  griddep_wait();
   const int rows = sink_rows(plan, a.sink);
   const int s = blockIdx.x % rows;
   const long long bk = blockIdx.x / rows;
@@ -746,24 +776,24 @@ cudaError_t run(const WindowArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream) 
       !y(&sv, a.v, a.KV, BS) || !y(&sg, a.dO, a.H, BS))
     return cudaErrorInvalidValue;
   auto kind = [&](auto kern, int k, const CUtensorMap& hx, const CUtensorMap& hy,
-                  const CUtensorMap& sx, const CUtensorMap& sy, bool dependent) -> cudaError_t {
+                  const CUtensorMap& sx, const CUtensorMap& sy) -> cudaError_t {
     const cudaError_t f =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (f != cudaSuccess) return f;
     PdlLaunch l(dim3((unsigned)std::min(plan.total(k), n_sm)), dim3(THREADS), SMEM_BYTES, stream,
-                dependent);
+                true);
     return cudaLaunchKernelEx(&l.cfg, kern, hx, hy, sx, sy, a, plan, (const float*)delta, counter,
                               sums, ctl);
   };
-  // the kind of the longest items first; the first waits for delta as a plain launch does
-  if ((e = kind(window_bwd_kernel<T, TO, KEYS>, KEYS, hk, hv, sq, sg, false)) != cudaSuccess ||
-      (e = kind(window_bwd_kernel<T, TO, VALUES>, VALUES, hk, hv, sq, sg, true)) != cudaSuccess ||
-      (e = kind(window_bwd_kernel<T, TO, QUERIES>, QUERIES, hq, hg, sk, sv, true)) != cudaSuccess)
+  // the kind of the longest items first
+  if ((e = kind(window_bwd_kernel<T, TO, KEYS>, KEYS, hk, hv, sq, sg)) != cudaSuccess ||
+      (e = kind(window_bwd_kernel<T, TO, VALUES>, VALUES, hk, hv, sq, sg)) != cudaSuccess ||
+      (e = kind(window_bwd_kernel<T, TO, QUERIES>, QUERIES, hq, hg, sk, sv)) != cudaSuccess)
     return e;
   if (!plan.sink_tiles) return cudaSuccess;
-  window_sink_kernel<TO><<<(unsigned)((long long)a.B * a.KV * sink_rows(plan, a.sink)), kSums / 2, 0,
-                           stream>>>(a, plan, sums);
-  return cudaGetLastError();
+  PdlLaunch l(dim3((unsigned)((long long)a.B * a.KV * sink_rows(plan, a.sink))), dim3(kSums / 2), 0,
+              stream, true);
+  return cudaLaunchKernelEx(&l.cfg, window_sink_kernel<TO>, a, plan, (const float*)sums);
 }
 
 }  // namespace
