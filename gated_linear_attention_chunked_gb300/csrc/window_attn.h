@@ -46,8 +46,7 @@ struct WindowDecodeArgs {
   int H;
   void* workspace;
 };
-// Parts a sequence's slots are cut into; the parts' results of more than one need the workspace.
-int window_decode_parts(int n, int KV, int H, int slots, int n_sm);
+// For the parts of what is cut (window_decode.cu); 0: nothing is.
 size_t window_decode_workspace_bytes(int n, int KV, int H, int slots, int n_sm);
 cudaError_t launch_window_decode(const WindowDecodeArgs& a, int n_sm, DevCtl ctl,
                                  cudaStream_t stream);

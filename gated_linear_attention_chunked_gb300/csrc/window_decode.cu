@@ -9,10 +9,15 @@
 // which a head count below 16 leaves some idle: the products stay far below the memory time.  A
 // CTA takes one sequence, key head and part of the slots; its warps walk the slots in tiles of 16
 // with rings of their own in shared memory (asynchronous copies, no barrier between warps) and
-// running maxima and sums of their own, which they join at the end.  Where sequences x key heads
-// leave SMs idle the slots are cut into parts, joined by a second kernel in a fixed order.
-// Measured: 256 sequences of 1,028 slots, four key heads, bf16: 101 us (78 % of the copy rate) with
-// rings of three stages, which let two CTAs share an SM; 123 with four.
+// running maxima and sums of their own, which they join at the end.
+//
+// The device holds two CTAs an SM (rings of three stages; with four, one fits, 123 us in place of
+// 101 at 256 sequences of 1,028 slots and four key heads).  As many whole units (sequence, key head,
+// group of query heads) as fill it one or more times run uncut; the slots of the others are cut
+// into the parts that fill the last round, joined by a second kernel in a fixed order.  Measured,
+// bf16, 1,028 slots, 16 heads on four, from a graph: 8 sequences 11.9 us (with parts for two rounds
+// of all units 16.0), 64: 30.0 (42.1), 100: 49.6 (54.3), 128: 56.0 (68.5), 256: 107.9 (111.8; 83 % of
+// the copy rate); 2 sequences of 8,196 slots, 32 heads on four: 20.1 (28.5).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -28,21 +33,29 @@ constexpr int STAGE = SB * (kDK + kDV) * 2;  // 9,216 bytes: a warp's tile of 16
 constexpr int RING = WARPS * STAGES * STAGE;
 constexpr int SMEM = RING + HB * kDK * 2;
 
+// CTAs: a unit each for the first `whole` units, `parts` for each of the `cut` others.
+struct DecodePlan {
+  int whole, cut, parts, part_slots;
+};
+
 __device__ __forceinline__ int slot_of(int t, int window, int sink) {
   return t < sink ? t : sink + (t - sink) % window;
 }
 
 template <class T, class TO>
 __global__ void __launch_bounds__(THREADS)
-window_decode_kernel(WindowDecodeArgs a, int parts, int part_slots, int groups, DevCtl ctl) {
+window_decode_kernel(WindowDecodeArgs a, DecodePlan plan, int groups, DevCtl ctl) {
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sm = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int KV = a.c.KV, G = a.H / KV;
-  const int part = blockIdx.x % parts;
-  const int grp = (blockIdx.x / parts) % groups;
-  const long long nk = blockIdx.x / parts / groups;
-  const int kv = (int)(nk % KV), n = (int)(nk / KV);
+  griddep_launch_dependents();  // the join waits for this whole grid
+  const int cut = (int)blockIdx.x - plan.whole;  // < 0: a whole unit
+  const int parts = cut < 0 ? 1 : plan.parts, part = cut < 0 ? 0 : cut % parts;
+  const int part_slots = cut < 0 ? 1 << 30 : plan.part_slots;
+  const int unit = cut < 0 ? (int)blockIdx.x : plan.whole + cut / parts;
+  const int grp = unit % groups, nk = unit / groups;
+  const int kv = nk % KV, n = nk / KV;
   const int h0 = grp * HB, heads = min(HB, G - h0);  // of this key head's query heads
   const int page = __ldg(a.c.page + n), pos = __ldg(a.pos + n);
   const bool ok = page >= 0 && page < a.c.n_pages && pos >= 0;  // the same for the whole CTA
@@ -212,24 +225,27 @@ window_decode_kernel(WindowDecodeArgs a, int parts, int part_slots, int groups, 
       const float inv = 1.f / sum;  // the new token is always there: sum > 0
       store2(static_cast<TO*>(a.o) + (head + row) * kDV + c, o0 * inv, o1 * inv);
     } else {
-      float* pw = static_cast<float*>(a.workspace) + ((head + row) * parts + part) * (kDV + 2);
+      float* pw = static_cast<float*>(a.workspace) +
+                  ((long long)(unit - plan.whole) * HB + row) * parts * (kDV + 2) + part * (kDV + 2);
       *reinterpret_cast<float2*>(pw + c) = make_float2(o0, o1);
       if (c == 0) *reinterpret_cast<float2*>(pw + kDV) = make_float2(top, sum);
     }
   }
 }
 
-// Joins the parts of one head: o = sum_p exp(m_p - m) o_p / sum_p exp(m_p - m) l_p, in order.
+// Joins the parts of one head of a cut unit: o = sum_p exp(m_p - m) o_p / sum_p exp(m_p - m) l_p, in order.
 template <class TO>
 __global__ void __launch_bounds__(kDV / 2)
-window_join_kernel(const float* __restrict__ part, TO* __restrict__ o, const int* __restrict__ page,
-                   const int* __restrict__ pos, int n_pages, int H, int parts) {
+window_join_kernel(WindowDecodeArgs a, DecodePlan plan, int groups, int rows) {
   griddep_wait();
-  const long long head = blockIdx.x;
-  const int n = (int)(head / H), c = threadIdx.x * 2;
-  const int p = __ldg(page + n);
-  if (p < 0 || p >= n_pages || __ldg(pos + n) < 0) return;  // recorded; o is left as it was
-  const float* pw = part + head * parts * (kDV + 2);
+  const int cut = blockIdx.x / rows, row = blockIdx.x % rows, unit = plan.whole + cut;
+  const int grp = unit % groups, nk = unit / groups, KV = a.c.KV, G = a.H / KV;
+  const int n = nk / KV, c = threadIdx.x * 2, h = grp * HB + row, parts = plan.parts;
+  if (h >= G) return;
+  const int p = __ldg(a.c.page + n);
+  if (p < 0 || p >= a.c.n_pages || __ldg(a.pos + n) < 0) return;  // recorded; o is left as it was
+  const float* pw =
+      static_cast<const float*>(a.workspace) + ((long long)cut * HB + row) * parts * (kDV + 2);
   float top = -INFINITY;
   for (int k = 0; k < parts; ++k) top = fmaxf(top, pw[k * (kDV + 2) + kDV]);
   float sum = 0.f, o0 = 0.f, o1 = 0.f;
@@ -242,7 +258,7 @@ window_join_kernel(const float* __restrict__ part, TO* __restrict__ o, const int
     o1 = fmaf(f, x.y, o1);
   }
   const float inv = 1.f / sum;
-  store2(o + head * kDV + c, o0 * inv, o1 * inv);
+  store2(static_cast<TO*>(a.o) + ((long long)n * a.H + nk % KV * G + h) * kDV + c, o0 * inv, o1 * inv);
 }
 
 // One warp per (sequence, slot): the latest of the prompt's tokens that belongs there.
@@ -278,34 +294,38 @@ window_fill_kernel(WindowCache c, const uint4* __restrict__ k, const uint4* __re
 
 int groups_of(int KV, int H) { return (H / KV + HB - 1) / HB; }
 
+// Parts of at least one round of the warps' tiles (64 slots) each; nothing is cut where two do not
+// fit into the last round.
+DecodePlan make_plan(int n, int KV, int H, int slots, int n_sm) {
+  const long long units = (long long)n * KV * groups_of(KV, H);
+  const int hold = std::max(2 * n_sm, 1), unit = SB * WARPS, rest = (int)(units % hold);
+  const int most = std::min((slots + unit - 1) / unit, 64);
+  const int parts = rest ? std::min(hold / rest, most) : 1;
+  if (parts < 2) return DecodePlan{(int)units, 0, 1, 0};
+  const int part_slots = ((slots + parts - 1) / parts + unit - 1) / unit * unit;
+  return DecodePlan{(int)(units - rest), rest, parts, part_slots};
+}
+
 template <class T, class TO>
 cudaError_t run(const WindowDecodeArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream) {
   const int slots = a.c.window + a.c.sink, KV = a.c.KV;
-  const int parts = window_decode_parts(a.c.n, KV, a.H, slots, n_sm), groups = groups_of(KV, a.H);
-  const int unit = SB * WARPS, part_slots = ((slots + parts - 1) / parts + unit - 1) / unit * unit;
+  const DecodePlan plan = make_plan(a.c.n, KV, a.H, slots, n_sm);
+  const int groups = groups_of(KV, a.H), rows = std::min(HB, a.H / KV);
   auto kern = window_decode_kernel<T, TO>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
-  const long long grid = (long long)a.c.n * KV * groups * parts;
-  kern<<<(unsigned)grid, THREADS, SMEM, stream>>>(a, parts, part_slots, groups, ctl);
-  if ((e = cudaGetLastError()) != cudaSuccess || parts == 1) return e;
-  PdlLaunch l(dim3((unsigned)(a.c.n * a.H)), dim3(kDV / 2), 0, stream, true);
-  return cudaLaunchKernelEx(&l.cfg, window_join_kernel<TO>, (const float*)a.workspace, (TO*)a.o,
-                            a.c.page, a.pos, a.c.n_pages, a.H, parts);
+  kern<<<(unsigned)(plan.whole + plan.cut * plan.parts), THREADS, SMEM, stream>>>(a, plan, groups,
+                                                                                 ctl);
+  if ((e = cudaGetLastError()) != cudaSuccess || !plan.cut) return e;
+  PdlLaunch l(dim3((unsigned)(plan.cut * rows)), dim3(kDV / 2), 0, stream, true);
+  return cudaLaunchKernelEx(&l.cfg, window_join_kernel<TO>, a, plan, groups, rows);
 }
 
 }  // namespace
 
-// Parts: enough CTAs for four per SM, at least one tile round (64 slots) each.
-int window_decode_parts(int n, int KV, int H, int slots, int n_sm) {
-  const long long ctas = (long long)n * KV * groups_of(KV, H);
-  const int most = (slots + SB * WARPS - 1) / (SB * WARPS);
-  const long long want = ctas > 0 ? (4ll * n_sm + ctas - 1) / ctas : 1;
-  return (int)std::max<long long>(1, std::min<long long>({want, (long long)most, 64}));
-}
 size_t window_decode_workspace_bytes(int n, int KV, int H, int slots, int n_sm) {
-  const int parts = window_decode_parts(n, KV, H, slots, n_sm);
-  return parts == 1 ? 0 : (size_t)n * H * parts * (kDV + 2) * sizeof(float);
+  const DecodePlan p = make_plan(n, KV, H, slots, n_sm);
+  return (size_t)p.cut * HB * p.parts * (kDV + 2) * sizeof(float);
 }
 
 cudaError_t launch_window_decode(const WindowDecodeArgs& a, int n_sm, DevCtl ctl,

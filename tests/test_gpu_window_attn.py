@@ -140,7 +140,9 @@ DECODE = [  # active, pages, layers, H, KV, window, sink, type, output type
     (2, 3, 1, 40, 2, 100, 0, "bf16", "bf16"),     # 20 query heads on a key head: two groups
     (5, 5, 1, 16, 1, 200, 64, "bf16", "fp32"),
     (2, 2, 3, 6, 2, 3000, 4, "fp16", "fp16"),     # slots cut into many parts
-    (320, 330, 1, 2, 2, 70, 3, "bf16", "bf16"),   # one part
+    (320, 330, 1, 2, 2, 70, 3, "bf16", "bf16"),   # whole ones, and a last round of parts
+    (100, 101, 1, 40, 2, 190, 10, "bf16", "fp32"),  # the same with two groups
+    (152, 152, 1, 2, 2, 70, 3, "fp16", "fp16"),   # a full round of whole ones
 ]
 
 
@@ -269,3 +271,28 @@ def test_streams_and_graphs_give_the_same_bits(env):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("sink", [0, 5])
+def test_sequences_of_a_ragged_batch_are_independent(env, sink):
+    """Many empty and short sequences between long ones, more items than CTAs: every sequence has
+    the bits of the call on it alone, padding is zero."""
+    gla, torch, _ = env
+    B, T, H, KV = 30, 1500, 4, 2
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    q, k, v, dO = r(B, T, H, 96) * 0.2, r(B, T, KV, 96), r(B, T, KV, 192), r(B, T, H, 192)
+    lens = [1500] + [0] * 9 + [640, 1, 0, 129] + [0] * 7 + [1499] + [64] * 4 + [0, 1000, 0, 0]
+    ld = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = gla.window_attn_fwd(q, k, v, 200, sink, ld)
+    got = gla.window_attn_bwd(q, k, v, o, lse, dO, 200, sink, ld)
+    assert gla.get_device_error() == 0
+    for b, n in enumerate(lens):
+        assert not o[b, n:].any() and all(not g[b, n:].any() for g in got)
+        if n == 0:
+            continue
+        one = [x[b:b + 1] for x in (q, k, v)]
+        ob, lb = gla.window_attn_fwd(*one, 200, sink, ld[b:b + 1])
+        gb = gla.window_attn_bwd(*one, ob, lb, dO[b:b + 1], 200, sink, ld[b:b + 1])
+        assert torch.equal(ob[0], o[b]) and torch.equal(lb[0], lse[b])
+        assert all(torch.equal(x[0], y[b]) for x, y in zip(gb, got))

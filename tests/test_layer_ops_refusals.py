@@ -122,6 +122,7 @@ def test_window_cache(lib):
     assert dec(pos=None) == INVALID and dec(o=None) == INVALID
     assert dec(pos=A + 2) == ALIGN and dec(pk=A + 8) == ALIGN
     assert lib.gla_window_attn_decode_workspace_size(2, 4, 3, 8, 1) == 0
+    assert lib.gla_window_attn_decode_workspace_size(3, 16, 4, 1000, 4) >= 0  # without a device too
 
 
 def test_the_binding_refuses_host_tensors_and_misfits():
