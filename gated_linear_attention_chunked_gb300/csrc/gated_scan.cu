@@ -55,31 +55,75 @@ struct alignas(8 * VEC) Pair {
   float a[VEC], b[VEC];
 };
 
+constexpr uint64_t DRAIN_NS = 4000000000ull;  // limit of the exit-time drain waits
+
+// What a CTA sends to another in a round: a pair of every lane.
+template <int VEC>
+constexpr uint32_t kSent = 32 * sizeof(Pair<VEC>);
+
 template <int VEC, int CL, int WARPS>
 struct Exchange {
   Pair<VEC> warp[2][WARPS][32];
   Pair<VEC> cta[CL > 1 ? 2 : 1][CL > 1 ? CL : 1][32];
   alignas(8) uint64_t bar[2];  // a round's pairs of all CTAs have arrived
+  alignas(8) uint64_t never;   // nothing arrives here (the give-up path's diagnostic)
+  int sent[CL];                // rounds that each CTA of the cluster has sent, once it is done
 
   // Before the first round.  A cluster's CTAs write into each other's memory: every one has to
   // be running, with its barriers set up.
   __device__ __forceinline__ void init() {
-    if constexpr (CL > 1) {
-      if (threadIdx.x == 0) {
+    if (threadIdx.x == 0) {
+      if constexpr (CL > 1) {
         mbar_init(smem_u32(&bar[0]), 1);
         mbar_init(smem_u32(&bar[1]), 1);
-        fence_barrier_init();
       }
-      cg::this_cluster().sync();
+      mbar_init(smem_u32(&never), 1);
+      fence_barrier_init();
     }
+    if constexpr (CL > 1) cg::this_cluster().sync();
   }
-  // After the last round: no CTA leaves while another may still write into it (which only
-  // happens after a wait that gave up).  Orders no memory, so it waits for no store.
-  __device__ __forceinline__ void done() {
+  // At step `stall_step` one CTA of every cluster waits for what never comes, gives up and leaves
+  // without its pair, so that the waits of the others run out as well.
+  __device__ __forceinline__ void stall(int r, const DevCtl& ctl, bool& ok) {
+    if (r == ctl.stall_step && (CL == 1 || cg::this_cluster().block_rank() == CL - 1))
+      ok = ok && mbar_wait(smem_u32(&never), 0, ctl);
+  }
+  // After the last round, or the one before which the CTA gave up; `rounds`: the ones it has sent.
+  // No CTA leaves while a pair may still be on its way into its memory.  One that has gone through
+  // all its waits has everything that was ever sent to it.  One that gave up learns how far the
+  // others got and waits for just that: of its last round the pairs of those that sent it, and of
+  // the next one, which nobody can be past without this CTA's pair, the same.
+  __device__ __forceinline__ void done(int rounds, bool ok, const DevCtl& ctl) {
     if constexpr (CL > 1) {
-      __syncwarp();
-      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      ok = __syncthreads_and(ok);
+      if (threadIdx.x < 32) {  // only these lanes' stores, not the outputs, are waited for
+        if (threadIdx.x < CL)
+          *cg::this_cluster().map_shared_rank(&sent[cg::this_cluster().block_rank()],
+                                              threadIdx.x) = rounds;
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      } else {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      }
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      if (!ok && threadIdx.x == 0) {
+        int behind = 0, ahead = 0;
+        for (int k = 0; k < CL; ++k) {
+          behind += sent[k] < rounds;
+          ahead += sent[k] > rounds;
+        }
+        if (rounds > 0) {  // armed for all CTAs' pairs
+          const uint32_t b = smem_u32(&bar[(rounds - 1) & 1]);
+          if (behind) mbar_complete_tx(b, behind * kSent<VEC>);
+          mbar_wait(b, ((rounds - 1) >> 1) & 1, ctl, DRAIN_NS);
+        }
+        if (ahead) {  // not armed
+          const uint32_t b = smem_u32(&bar[rounds & 1]);
+          mbar_arrive_expect_tx(b, ahead * kSent<VEC>);
+          mbar_wait(b, (rounds >> 1) & 1, ctl, DRAIN_NS);
+        }
+      }
     }
   }
 };
@@ -107,20 +151,21 @@ __device__ __forceinline__ void send(const Pair<VEC>& v, const Pair<VEC>* p, con
 
 // The state entering this warp's tokens, from round r's pair of every warp (and CTA of the
 // cluster) and the state `carry` entering the round, which becomes the one leaving it.  `ok`
-// turns false where a CTA of the cluster did not answer in time.
+// turns false where a CTA of the cluster did not answer in time.  A cluster's CTA in which a
+// thread has given up sends no more: enter() is then false in all its threads, which leave.
 template <int VEC, int CL, int WARPS>
-__device__ __forceinline__ void enter(Exchange<VEC, CL, WARPS>& ex, int r, const Pair<VEC>& own,
+__device__ __forceinline__ bool enter(Exchange<VEC, CL, WARPS>& ex, int r, const Pair<VEC>& own,
                                       float (&carry)[VEC], float (&in)[VEC], const DevCtl& ctl,
                                       bool& ok) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, buf = r & 1;
   ex.warp[buf][w][lane] = own;
   // The buffers alternate: a CTA sends round r + 2 only after it has this one's pairs of round
   // r + 1, which go out behind a barrier that every thread reaches after it has read round r's.
-  __syncthreads();
   if constexpr (CL > 1) {
+    ex.stall(r, ctl, ok);
+    if (!__syncthreads_and(ok)) return ok = false;
     const int rank = (int)cg::this_cluster().block_rank();
-    if (threadIdx.x == 0 && ok)  // (a phase that never completed is not armed again)
-      mbar_arrive_expect_tx(smem_u32(&ex.bar[buf]), CL * 32 * (int)sizeof(Pair<VEC>));
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(smem_u32(&ex.bar[buf]), CL * kSent<VEC>);
     if (w < CL) {
       Pair<VEC> p = ex.warp[buf][0][lane];
 #pragma unroll
@@ -135,7 +180,7 @@ __device__ __forceinline__ void enter(Exchange<VEC, CL, WARPS>& ex, int r, const
       for (int to = w; to < CL; to += WARPS)  // each warp hands the CTA's pair to some of them
         send(p, &ex.cta[buf][rank][lane], &ex.bar[buf], to);
     }
-    ok = ok && mbar_wait(smem_u32(&ex.bar[buf]), (r >> 1) & 1, ctl);
+    ok = mbar_wait(smem_u32(&ex.bar[buf]), (r >> 1) & 1, ctl);
 #pragma unroll
     for (int k = 0; k < CL; ++k) {
       const Pair<VEC> p = ex.cta[buf][k][lane];
@@ -153,6 +198,8 @@ __device__ __forceinline__ void enter(Exchange<VEC, CL, WARPS>& ex, int r, const
         for (int j = 0; j < VEC; ++j) in[j] = fmaf(p.a[j], in[j], p.b[j]);
       }
   } else {
+    __syncthreads();
+    ex.stall(r, ctl, ok);
 #pragma unroll
     for (int k = 0; k < WARPS; ++k) {
       const Pair<VEC> p = ex.warp[buf][k][lane];
@@ -163,6 +210,7 @@ __device__ __forceinline__ void enter(Exchange<VEC, CL, WARPS>& ex, int r, const
       }
     }
   }
+  return true;
 }
 
 // Tokens of sequence b: lens[b], or all T.  A length outside [0, T] is an error; it is recorded
@@ -224,7 +272,8 @@ scan_fwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
   fetch(t0);
   ex.init();
   bool ok = true;
-  for (int at = 0, r = 0; at < T_; at += step, t0 += step, ++r) {
+  int r = 0;
+  for (int at = 0; at < T_; at += step, t0 += step, ++r) {
     float f[S][VEC], a[S][VEC];
     Pair<VEC> own;
 #pragma unroll
@@ -241,7 +290,7 @@ scan_fwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
       }
     if (at + step < T_) fetch(t0 + step);
     float h[VEC];
-    enter(ex, r, own, carry, h, ctl, ok);
+    if (!enter(ex, r, own, carry, h, ctl, ok)) break;
     const bool whole = t0 + S <= len;
     float* yp = y + base + (long long)t0 * D;
 #pragma unroll
@@ -258,7 +307,7 @@ scan_fwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
   if (fin && live && rank == 0 && w == 0)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) fin[(long long)b * D + ch + j] = carry[j];
-  ex.done();
+  ex.done(r, ok, ctl);
 }
 
 template <class T, int VEC, int CL>
@@ -284,7 +333,8 @@ scan_bwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
   const int step = TILE * CL;
   ex.init();
   bool ok = true;
-  for (int at = 0, r = 0; at < T_; at += step, ++r) {
+  int r = 0;
+  for (int at = 0; at < T_; at += step, ++r) {
     const int last = T_ - 1 - (at + rank * TILE + w * S);  // this warp's tokens, from the last
     Pack<T, VEC> xr[S], gr[S];
     Pack<float, VEC> dr[S], hr[S];
@@ -319,7 +369,7 @@ scan_bwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
         own.a[j] *= f[i][j];
       }
     float c[VEC];
-    enter(ex, r, own, carry, c, ctl, ok);
+    if (!enter(ex, r, own, carry, c, ctl, ok)) break;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       const int t = last - i;
@@ -340,7 +390,7 @@ scan_bwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
   if (dinit && live && rank == 0 && w == 0)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dinit[edge + j] = carry[j];
-  ex.done();
+  ex.done(r, ok, ctl);
 }
 
 // ---- the same with tiles brought in by TMA, where rows start on 16 bytes
@@ -411,7 +461,8 @@ scan_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
   float* const yb = y + (long long)b * T_ * D + ch;
 
   bool ok = true;
-  for (int r = 0; r < rounds; ++r) {
+  int r = 0;
+  for (; r < rounds; ++r) {
     const int s = r % STAGES;
     const T* xt = reinterpret_cast<const T*>(smem + s * 2 * BYTES) + w * S * SLAB + 2 * lane;
     const T* gt = xt + TILE * SLAB;
@@ -440,7 +491,7 @@ scan_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
       }
     }
     float h[2];
-    enter(ex, r, own, carry, h, ctl, ok);
+    if (!enter(ex, r, own, carry, h, ctl, ok)) break;
     if (tid == 0 && ok && r + STAGES < rounds) fetch(r + STAGES);
     float* yp = yb + (long long)t0 * D;
 #pragma unroll
@@ -455,14 +506,14 @@ scan_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
   // after a wait that gave up nothing is fetched any more; the copies in flight land before the
   // CTA's memory is given back
   if (!ok && tid == 0)
-    for (int r = max(0, armed - STAGES); r < armed; ++r)
-      mbar_wait(smem_u32(&full[r % STAGES]), (r / STAGES) & 1, ctl, 4000000000ull);
+    for (int k = max(0, armed - STAGES); k < armed; ++k)
+      mbar_wait(smem_u32(&full[k % STAGES]), (k / STAGES) & 1, ctl, DRAIN_NS);
   // the padding that no round has reached
   for (int t = rounds * step + rank * WARPS + w; t < T_; t += WARPS * CL)
     if (live) __stcs(reinterpret_cast<float2*>(yb + (long long)t * D), make_float2(0.f, 0.f));
   if (fin && live && rank == 0 && w == 0)
     *reinterpret_cast<float2*>(fin + (long long)b * D + ch) = make_float2(carry[0], carry[1]);
-  ex.done();
+  ex.done(r, ok, ctl);
 }
 
 template <class T, int CL, int STAGES>
@@ -517,7 +568,8 @@ scan_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
   float* const gb = dg + (long long)b * T_ * D + ch;
 
   bool ok = true;
-  for (int r = 0; r < rounds; ++r) {
+  int r = 0;
+  for (; r < rounds; ++r) {
     const int s = r % STAGES;
     const int row = TILE - 1 - w * S, last = tile_at(r) + row;  // this warp's last token
     const T* xt = reinterpret_cast<const T*>(smem + s * STAGE) + row * SLAB + 2 * lane;
@@ -553,7 +605,7 @@ scan_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
       }
     }
     float c[2];
-    enter(ex, r, own, carry, c, ctl, ok);
+    if (!enter(ex, r, own, carry, c, ctl, ok)) break;
     if (tid == 0 && ok && r + STAGES < rounds) fetch(r + STAGES);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
@@ -573,8 +625,8 @@ scan_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
   // after a wait that gave up nothing is fetched any more; the copies in flight land before the
   // CTA's memory is given back
   if (!ok && tid == 0)
-    for (int r = max(0, armed - STAGES); r < armed; ++r)
-      mbar_wait(smem_u32(&full[r % STAGES]), (r / STAGES) & 1, ctl, 4000000000ull);
+    for (int k = max(0, armed - STAGES); k < armed; ++k)
+      mbar_wait(smem_u32(&full[k % STAGES]), (k / STAGES) & 1, ctl, DRAIN_NS);
   for (int t = len + rank * WARPS + w; t < T_; t += WARPS * CL)  // padding
     if (live) {
       __stcs(reinterpret_cast<float2*>(xb + (long long)t * D), make_float2(0.f, 0.f));
@@ -582,7 +634,7 @@ scan_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
     }
   if (dinit && live && rank == 0 && w == 0)
     *reinterpret_cast<float2*>(dinit + edge) = make_float2(carry[0], carry[1]);
-  ex.done();
+  ex.done(r, ok, ctl);
 }
 
 // One token: state [.., D] in place.  Pure streaming, one thread per VEC channels; with a page

@@ -106,13 +106,16 @@ GLA_API gla_status gla_set_wait_timeout_ns(unsigned long long ns);
  * `stream`. */
 GLA_API gla_status gla_wait_probe(cudaStream_t stream);
 
-/* Diagnostic of the chunk kernels' give-up path (no counterpart in the article).  For calls
- * made after it returns (process-wide), the tensor-core issuer of every CTA of the chunked
- * forward, backward and segment-pass kernels, and of the windowed attention's forward and
- * gradient, on reaching chunk step (streamed tile) `step` of its loop, waits on a barrier whose phase completes only after that loop.  The bounded wait gives up
- * after the limit of gla_set_wait_timeout_ns, records GLA_ERR_TIMEOUT and raises the CTA's
- * abort flag; every role then leaves its loop (one path per warp), drains its copies and
- * tensor-core work, frees its tensor memory and exits.  The call's outputs are then
+/* Diagnostic of the give-up paths (no counterpart in the article).  For calls made after it
+ * returns (process-wide), the tensor-core issuer of every CTA of the chunked forward, backward
+ * and segment-pass kernels, and of the windowed attention's forward and gradient, on reaching
+ * chunk step (streamed tile) `step` of its loop, waits on a barrier whose phase completes only
+ * after that loop.  The bounded wait gives up after the limit of gla_set_wait_timeout_ns, records
+ * GLA_ERR_TIMEOUT and raises the CTA's abort flag; every role then leaves its loop (one path per
+ * warp), drains its copies and tensor-core work, frees its tensor memory and exits.  In the gated
+ * scan one CTA of every cluster (every CTA where there are no clusters) does so at round `step`
+ * of tiles and leaves before it hands on its pair; the others give up waiting for that, and each
+ * leaves only when nothing is on its way into its memory any more.  The call's outputs are then
  * undefined; the context stays usable.  step < 0 (the default) turns it off.  No fault,
  * trap or unbounded wait is involved.  The mbarrier wait instruction suspends the waiting
  * thread until the phase completes (up to a hardware limit), so ordinary waits end before

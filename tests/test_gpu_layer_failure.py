@@ -1,0 +1,72 @@
+"""The bounded waits of the gated scan, without a fault: with gla_set_stall_step one CTA of every
+cluster (every CTA where there are none) waits for what never comes, gives up after the limit (2 ms
+here) and leaves without its pair; the others' waits run out as well.  No CTA leaves while something
+may still be written into its memory.  The host reads GLA_ERR_TIMEOUT and the next calls are right."""
+import time
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+GLA_ERR_TIMEOUT = 5
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    assert torch.cuda.is_available(), "GPU test without a CUDA device"
+    import gated_linear_attention_chunked_gb300 as gla
+    from gated_linear_attention_chunked_gb300 import _build
+    _build.build()
+    gla.load()
+    return gla, torch
+
+
+def _stalled(gla, torch, step, run):
+    """`run` stalls at `step`; before and after it gives the same bits."""
+    want = run()
+    torch.cuda.synchronize()
+    assert gla.get_device_error() == 0
+    for _ in range(2):
+        try:
+            gla.set_wait_timeout_ns(2_000_000)
+            gla.set_stall_step(step)
+            t0 = time.perf_counter()
+            run()
+            torch.cuda.synchronize()
+            dt = time.perf_counter() - t0
+            assert gla.get_device_error() == GLA_ERR_TIMEOUT
+            assert dt < 5.0
+        finally:
+            gla.set_stall_step(-1)
+            gla.set_wait_timeout_ns(0)
+        got = run()
+        torch.cuda.synchronize()
+        assert gla.get_device_error() == 0
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+SCANS = [  # B, T, D, type, steps: with 152 SMs
+    (1, 2000, 64, "bfloat16", (0, 1, 3)),     # a cluster of 8, TMA tiles, four rounds
+    (1, 2000, 68, "float32", (2,)),
+    (3, 700, 66, "float32", (0, 1)),          # 8, rows of pairs
+    (3, 700, 65, "float16", (0, 1)),          # 8, odd rows
+    (60, 130, 64, "float16", (0, 1)),         # a cluster of 2
+    (60, 300, 256, "bfloat16", (0, 2, 4)),    # none, TMA
+    (120, 130, 65, "float32", (1,)),          # none, odd rows
+]
+
+
+@pytest.mark.parametrize("call", ["fwd", "bwd"])
+@pytest.mark.parametrize("B,T,D,dt,step", [(*s[:4], k) for s in SCANS for k in s[4]])
+def test_scan_gives_up_and_the_next_call_is_the_same(env, call, B, T, D, dt, step):
+    gla, torch = env
+    gen = torch.Generator(device="cuda").manual_seed(T + D)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    x, g = (r(B, T, D).to(getattr(torch, dt)) for _ in range(2))
+    dy, init = r(B, T, D), r(B, D)
+    y, _ = gla.gated_scan_fwd(x, g, init)
+    if call == "fwd":
+        _stalled(gla, torch, step, lambda: gla.gated_scan_fwd(x, g, init))
+    else:
+        _stalled(gla, torch, step, lambda: gla.gated_scan_bwd(x, g, y, dy, init, init))
