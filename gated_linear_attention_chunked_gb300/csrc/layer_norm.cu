@@ -31,6 +31,7 @@ namespace {
 constexpr int MAX_WARPS = 32;
 constexpr int RING_MOST = 6;  // rows of a warp's ring in the forward
 constexpr int RING_SPACE = 192 * 1024;
+constexpr uint64_t DRAIN_NS = 4000000000ull;  // limit of the exit-time drain waits
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -252,7 +253,7 @@ layer_norm_fwd_ring_kernel(const TX* __restrict__ x, const float* __restrict__ w
                            float* __restrict__ mean, float* __restrict__ rstd, long long n, int D,
                            float eps, int stages, DevCtl ctl) {
   extern __shared__ __align__(128) uint8_t smem[];  // the rings, then the weights
-  __shared__ alignas(8) uint64_t full[12][RING_MOST];
+  __shared__ alignas(8) uint64_t full[12][RING_MOST], never;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int row_bytes = D * (int)sizeof(TX);
   float* const sw = reinterpret_cast<float*>(smem + warps * stages * row_bytes);
@@ -269,6 +270,7 @@ layer_norm_fwd_ring_kernel(const TX* __restrict__ x, const float* __restrict__ w
   };
   if (lane == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&full[w][s]), 1);
+    if (w == 0) mbar_init(smem_u32(&never), 1);
     fence_barrier_init();
     fence_proxy_async();
     for (int k = 0; k < stages && k < mine; ++k) fetch(k);
@@ -285,6 +287,7 @@ layer_norm_fwd_ring_kernel(const TX* __restrict__ x, const float* __restrict__ w
   bool ok = true;
   for (int k = 0; k < mine; ++k) {
     const long long row = first + k * step;
+    if (k == ctl.stall_step) ok = ok && mbar_wait(smem_u32(&never), 0, ctl);  // the diagnostic
     ok = ok && mbar_wait(smem_u32(&full[w][k % stages]), (k / stages) & 1, ctl);
     const TX* xt = reinterpret_cast<const TX*>(ring + (k % stages) * row_bytes);
     Pack<TX, V> in[NV];
@@ -348,7 +351,7 @@ layer_norm_fwd_ring_kernel(const TX* __restrict__ x, const float* __restrict__ w
   // CTA's memory is given back
   if (!ok && lane == 0)
     for (int k = max(0, armed - stages); k < armed; ++k)
-      mbar_wait(smem_u32(&full[w][k % stages]), (k / stages) & 1, ctl, 4000000000ull);
+      mbar_wait(smem_u32(&full[w][k % stages]), (k / stages) & 1, ctl, DRAIN_NS);
 }
 
 // ---- gradient, rows that 16-byte accesses divide and of which the ring holds eight: a CTA takes R
@@ -366,7 +369,7 @@ layer_norm_bwd_ring_kernel(const TY* __restrict__ dy, const TX* __restrict__ x,
   constexpr int R = RING_R, P = NV * V / 2;
   griddep_launch_dependents();  // the reduction launched next waits for this whole grid
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ alignas(8) uint64_t full[RING_STAGES];
+  __shared__ alignas(8) uint64_t full[RING_STAGES], never;
   __shared__ float4 stat[2][16];
   const int t = threadIdx.x, lane = t & 31, w = t >> 5, warps = blockDim.x >> 5;
   const int x_bytes = R * D * (int)sizeof(TX), stage = x_bytes + R * D * (int)sizeof(TY);
@@ -385,6 +388,7 @@ layer_norm_bwd_ring_kernel(const TY* __restrict__ dy, const TX* __restrict__ x,
   };
   if (t == 0) {
     for (int s = 0; s < RING_STAGES; ++s) mbar_init(smem_u32(&full[s]), 1);
+    mbar_init(smem_u32(&never), 1);
     fence_barrier_init();
     fence_proxy_async();
     for (int k = 0; k < RING_STAGES && k < mine; ++k) fetch(k);
@@ -421,6 +425,7 @@ layer_norm_bwd_ring_kernel(const TY* __restrict__ dy, const TX* __restrict__ x,
     const int s = k % RING_STAGES;
     const long long row0 = (blockIdx.x + (long long)k * gridDim.x) * R;
     stats_of(k + 1, m_next, rs_next);
+    if (k == ctl.stall_step) ok = ok && mbar_wait(smem_u32(&never), 0, ctl);  // the diagnostic
     ok = ok && mbar_wait(smem_u32(&full[s]), (k / RING_STAGES) & 1, ctl);
     const TX* xt = reinterpret_cast<const TX*>(smem + s * stage);
     const TY* gt = reinterpret_cast<const TY*>(smem + s * stage + x_bytes);
@@ -505,7 +510,7 @@ layer_norm_bwd_ring_kernel(const TY* __restrict__ dy, const TX* __restrict__ x,
   // CTA's memory is given back
   if (!ok && t == 0)
     for (int k = max(0, armed - RING_STAGES); k < armed; ++k)
-      mbar_wait(smem_u32(&full[k % RING_STAGES]), (k / RING_STAGES) & 1, ctl, 4000000000ull);
+      mbar_wait(smem_u32(&full[k % RING_STAGES]), (k / RING_STAGES) & 1, ctl, DRAIN_NS);
   float* p = part + (long long)blockIdx.x * 2 * D;
 #pragma unroll
   for (int i = 0; i < NV; ++i)

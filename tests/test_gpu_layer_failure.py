@@ -1,7 +1,7 @@
-"""The bounded waits of the gated scan, without a fault: with gla_set_stall_step one CTA of every
-cluster (every CTA where there are none) waits for what never comes, gives up after the limit (2 ms
-here) and leaves without its pair; the others' waits run out as well.  No CTA leaves while something
-may still be written into its memory.  The host reads GLA_ERR_TIMEOUT and the next calls are right."""
+"""The bounded waits of the gated scan and the layer norm, without a fault: with gla_set_stall_step
+one CTA of every cluster (every CTA where there are none) waits for what never comes, gives up after
+the limit (2 ms here) and leaves without its pair; the others' waits run out as well.  The norm's
+rings stop fetching.  No CTA leaves while something may still be written into its memory.  The host reads GLA_ERR_TIMEOUT and the next calls are right."""
 import time
 
 import pytest
@@ -70,3 +70,19 @@ def test_scan_gives_up_and_the_next_call_is_the_same(env, call, B, T, D, dt, ste
         _stalled(gla, torch, step, lambda: gla.gated_scan_fwd(x, g, init))
     else:
         _stalled(gla, torch, step, lambda: gla.gated_scan_bwd(x, g, y, dy, init, init))
+
+
+@pytest.mark.parametrize("call", ["fwd", "bwd"])
+@pytest.mark.parametrize("n,D,dt,step", [(5000, 2048, "bfloat16", 0), (5000, 2048, "bfloat16", 1),
+                                         (20000, 512, "float16", 3), (9000, 1020, "float32", 4)])
+def test_norm_rings_give_up_and_the_next_call_is_the_same(env, call, n, D, dt, step):
+    gla, torch = env
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    x, dy = (torch.randn(n, D, generator=gen, device="cuda").to(getattr(torch, dt))
+             for _ in range(2))
+    w = torch.randn(D, generator=gen, device="cuda")
+    _, m, r = gla.layer_norm_fwd(x, w)
+    if call == "fwd":
+        _stalled(gla, torch, step, lambda: gla.layer_norm_fwd(x, w))
+    else:
+        _stalled(gla, torch, step, lambda: gla.layer_norm_bwd(dy, x, w, m, r))
