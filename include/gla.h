@@ -113,11 +113,12 @@ GLA_API gla_status gla_wait_probe(cudaStream_t stream);
  * after that loop.  The bounded wait gives up after the limit of gla_set_wait_timeout_ns, records
  * GLA_ERR_TIMEOUT and raises the CTA's abort flag; every role then leaves its loop (one path per
  * warp), drains its copies and tensor-core work, frees its tensor memory and exits.  In the gated
- * scan one CTA of every cluster (every CTA where there are no clusters) does so at round `step`
- * of tiles and leaves before it hands on its pair; the others give up waiting for that, and each
- * leaves only when nothing is on its way into its memory any more.  The layer norm's rings (rows
- * that they take) give up at their row, or pair of rows, `step`, and drain.  The call's outputs
- * are then undefined; the context stays usable.  step < 0 (the default) turns it off.  No fault,
+ * scan one CTA of every cluster (without clusters every CTA, of those whose tiles come by TMA)
+ * does so at round `step` of tiles and leaves before it hands on its pair; the others give up
+ * waiting for that, and each leaves only when nothing is on its way into its memory any more.
+ * The layer norm's rings (rows that they take) give up at their row, or pair of rows, `step`, and
+ * drain.  The call's outputs are then undefined; the context stays usable.  step < 0 (the
+ * default) turns it off.  No fault,
  * trap or unbounded wait is involved.  The mbarrier wait instruction suspends the waiting
  * thread until the phase completes (up to a hardware limit), so ordinary waits end before
  * any limit of the timer can be checked: a stall like this is what makes a wait run out. */
