@@ -24,7 +24,8 @@ SOURCES = ["api.cu", "decode.cu", "convert.cu", "chunk_fwd.cu", "chunk_bwd.cu", 
            "api_layer.cu", "gated_scan.cu", "layer_norm.cu",
            "window_fwd.cu", "window_bwd.cu", "window_decode.cu"]
 HEADERS = ["ptx.cuh", "tmap.h", "kernels.h", "scan_common.cuh", "elem.cuh",
-           "gated_scan.h", "layer_norm.h", "window_attn.h", "mma.cuh", "window_common.cuh"]
+           "gated_scan.h", "layer_norm.h", "window_attn.h", "mma.cuh", "window_common.cuh",
+           "window_wait.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",

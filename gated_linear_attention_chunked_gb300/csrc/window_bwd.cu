@@ -46,17 +46,15 @@
 #include <algorithm>
 #include <cmath>
 
-#include "scan_common.cuh"
 #include "tmap.h"
 #include "window_common.cuh"
+#include "window_wait.cuh"
 
 namespace gla {
 namespace {
 
 using scan::Cta;
 using scan::DRAIN_NS;
-using scan::wait;
-using scan::wait_warp;
 
 constexpr int BH = 128, BS = 64, STAGES = 4;  // rows held, rows streamed
 constexpr int kSums = kDK + kDV;              // dk and dv of a key
@@ -88,7 +86,7 @@ static_assert(OFF_ITEM % 16 == 0, "items are read by 16 bytes");
 constexpr uint32_t OFF_TMEM = OFF_ITEM + 64, OFF_ABORT = OFF_TMEM + 4;
 // The opt-in maximum; the kernel aligns its base to 1024 bytes and does not run (GLA_ERR_LAYOUT)
 // if the padding that takes would not fit.  Dynamic shared memory normally starts aligned.
-constexpr uint32_t SMEM_USED = OFF_ABORT + 4, SMEM_BYTES = 232448;
+constexpr uint32_t SMEM_USED = OFF_ABORT + 4 * kWaitWords, SMEM_BYTES = 232448;
 static_assert(SMEM_USED <= SMEM_BYTES, "shared memory budget");
 enum Kind : int { VALUES = 0, KEYS = 1, QUERIES = 2 };
 // Tensor memory columns.  VALUES: dv 192, S twice 64, P twice 32, k 48.  The others: S and D twice
@@ -102,7 +100,7 @@ struct Tm {
   __device__ static uint32_t p(int g) { return V ? 320 + 32 * g : s(g); }
 };
 
-constexpr int EW = 8, LOAD_WARP = 8, STAT_WARP = 9, MMA_WARP = 10, GROUP = 128;
+constexpr int EW = 8, LOAD_WARP = 8, STAT_WARP = 9, MMA_WARP = 10, OUT_WARP = 11, GROUP = 128;
 constexpr int THREADS = 15 * 32;
 
 // How the work is cut into items, the same for every part of the call.
@@ -319,7 +317,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
     mbar_init(cta.bar(SUM_DONE), 1);
     mbar_init(cta.bar(SUM_FREE), 128);
     mbar_init(cta.bar(DRAIN), 1);
-    *cta.abort_flag() = 0;
+    for (uint32_t i = 0; i < kWaitWords; ++i) cta.abort_flag()[i] = 0;
     fence_barrier_init();
   }
   if (KIND == KEYS) {  // the first kind: delta and the counters, for itself and the others
@@ -336,8 +334,8 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
   // by whole warps, or by the single MMA thread.
   auto next_item = [&](Item<KIND>& it, int m, bool whole_warp) -> bool {
     const uint32_t s = m & 1;
-    if (whole_warp ? !wait_warp(cta, cta.bar(ITEM_FULL + s), (m >> 1) & 1, ctl)
-                   : !wait(cta, cta.bar(ITEM_FULL + s), (m >> 1) & 1, ctl))
+    if (whole_warp ? !await_warp(cta, cta.bar(ITEM_FULL + s), (m >> 1) & 1, ctl)
+                   : !await(cta, cta.bar(ITEM_FULL + s), (m >> 1) & 1, ctl))
       return false;
     const bool some = it.get(items + 2 * s);
     if (whole_warp) __syncwarp();
@@ -354,7 +352,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
       int ticket = atomicAdd(counter + KIND, 1);
       for (int m = 0; ok; ++m) {
         const uint32_t slot = m & 1;
-        if (m >= 2 && !wait(cta, cta.bar(ITEM_EMPTY + slot), ((m >> 1) - 1) & 1, ctl)) break;
+        if (m >= 2 && !await(cta, cta.bar(ITEM_EMPTY + slot), ((m >> 1) - 1) & 1, ctl)) break;
         const bool end = ticket >= plan.total(KIND);
         if (end) it.b = -1;
         else it.set(ticket, a, plan);
@@ -363,7 +361,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
         if (end) break;
         ticket = atomicAdd(counter + KIND, 1);
         if (it.n == 0) continue;
-        if (held > 0 && !wait(cta, cta.bar(HELD_READY), (held - 1) & 1, ctl)) break;
+        if (held > 0 && !await(cta, cta.bar(HELD_READY), (held - 1) & 1, ctl)) break;
         ++held;
         mbar_arrive_expect_tx(cta.bar(HELD_FULL), KIND == VALUES ? 3 * HX_BOX : H_BYTES);
         for (int j = 0; j < 3; ++j) {
@@ -375,7 +373,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
         }
         for (Walk<KIND> k(it, G); k.i < it.n; k.next(), ++n) {
           const uint32_t s = n % STAGES, st = cta.sb + OFF_S + s * S_BYTES;
-          if (n >= STAGES && !(ok = wait(cta, cta.bar(EMPTY + s), (n / STAGES - 1) & 1, ctl)))
+          if (n >= STAGES && !(ok = await(cta, cta.bar(EMPTY + s), (n / STAGES - 1) & 1, ctl)))
             break;
           const int r = k.row();
           mbar_arrive_expect_tx(cta.bar(FULL + s), S_BYTES);
@@ -408,7 +406,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
             x[j] = t0 + c < it.len ? -__ldg(a.lse + at + c) * kLog2e : 0.f;
             x[2 + j] = t0 + c < it.len ? -__ldg(delta + at + c) : 0.f;
           }
-          if (n >= STAGES && !(ok = wait_warp(cta, cta.bar(STAT_EMPTY + s), (n / STAGES - 1) & 1,
+          if (n >= STAGES && !(ok = await_warp(cta, cta.bar(STAT_EMPTY + s), (n / STAGES - 1) & 1,
                                               ctl)))
             break;
           float* st = (float*)(base + OFF_STAT + s * 512);
@@ -436,7 +434,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
       auto scores = [&](int i, int at) -> bool {  // S, D of the item's tile i, tile `at` in all
         const uint32_t s = at % STAGES;
         const int g = i & 1;
-        if (!wait(cta, cta.bar(FULL + s), (at / STAGES) & 1, ctl)) return false;
+        if (!await(cta, cta.bar(FULL + s), (at / STAGES) & 1, ctl)) return false;
         tc_fence_after();
         const uint32_t id = ID_S | ((uint32_t)((KIND == QUERIES ? it.cols(i, a.sink) : BS) >> 3) << 17);
         const uint64_t sx = sx0 + s * (S_BYTES >> 4), sy = sy0 + s * (S_BYTES >> 4);
@@ -457,20 +455,20 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
       for (int m = 0; ok && next_item(it, m, false); ++m) {
         if (it.n == 0) continue;
         ++held;
-        if (!(ok = wait(cta, cta.bar(HELD_READY), (held - 1) & 1, ctl))) break;
+        if (!(ok = await(cta, cta.bar(HELD_READY), (held - 1) & 1, ctl))) break;
         if (!(ok = scores(0, n))) break;
         if (it.n > 1 && !(ok = scores(1, n + 1))) break;
         for (int i = 0; i < it.n; ++i, ++n) {
           const uint32_t s = n % STAGES;
           const int g = i & 1;
           if (n == ctl.stall_step) {  // the give-up path's diagnostic (see chunk_fwd.cu)
-            wait(cta, cta.bar(DRAIN), 0, ctl);
+            await(cta, cta.bar(DRAIN), 0, ctl);
             ok = false;
             break;
           }
-          if (i == 0 && held > 1 && !(ok = wait(cta, cta.bar(SUM_FREE), (held - 2) & 1, ctl)))
+          if (i == 0 && held > 1 && !(ok = await(cta, cta.bar(SUM_FREE), (held - 2) & 1, ctl)))
             break;
-          if (!(ok = wait(cta, cta.bar(P_READY + g), (phase >> g) & 1, ctl))) break;
+          if (!(ok = await(cta, cta.bar(P_READY + g), (phase >> g) & 1, ctl))) break;
           phase ^= 1u << g;
           tc_fence_after();
           const uint64_t sum = sum0 + s * (S_BYTES >> 4);
@@ -488,6 +486,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
                            i > 0 || c > 0);
           }
           mma_commit(cta.bar(EMPTY + s));
+          made_step(cta, STEP_TILE, n + 1);
           if (i == it.n - 1) mma_commit(cta.bar(SUM_DONE));
           // the group has read its scores, and the commit behind the new ones also says that the
           // sum above is done: P or Z may be written again
@@ -532,10 +531,10 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
                                        (x0 + BS - 1 - it.row0 < a.window || it.row0 + BH <= a.sink)
                                  : x0 + BS - 1 <= it.row0 && x0 + BS <= len &&
                                        (it.row0 + BH - 1 - x0 < a.window || x0 + BS <= a.sink);
-        if (!(ok = wait_warp(cta, cta.bar(S_FULL + g), used++ & 1, ctl))) break;
+        if (!(ok = await_warp(cta, cta.bar(S_FULL + g), used++ & 1, ctl))) break;
         // (behind the scores' wait: every earlier tile of the stage has been through here)
         if (STATS &&
-            !(ok = wait_warp(cta, cta.bar(STAT_FULL + n % STAGES), (n / STAGES) & 1, ctl)))
+            !(ok = await_warp(cta, cta.bar(STAT_FULL + n % STAGES), (n / STAGES) & 1, ctl)))
           break;
         tc_fence_after();
         const float* stat = (const float*)(base + OFF_STAT + (n % STAGES) * 512);
@@ -620,8 +619,8 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
     // take with them
     int held = 0;
     auto hold = [&]() -> bool {
-      if (held > 0 && !wait_warp(cta, cta.bar(HELD_EMPTY), (held - 1) & 1, ctl)) return false;
-      if (!wait_warp(cta, cta.bar(HELD_FULL), held & 1, ctl)) return false;
+      if (held > 0 && !await_warp(cta, cta.bar(HELD_EMPTY), (held - 1) & 1, ctl)) return false;
+      if (!await_warp(cta, cta.bar(HELD_FULL), held & 1, ctl)) return false;
       ++held;
       tc_fence_after();
 #pragma unroll
@@ -658,7 +657,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
                         (KIND == VALUES ? 0 : kDV);
       const int from = STATS ? held_sinks : 0, to = it.part < 0 ? a.T : 0;
       if (it.n > 0) {
-        if (!wait_warp(cta, cta.bar(SUM_DONE), done & 1, ctl)) break;
+        if (!await_warp(cta, cta.bar(SUM_DONE), done & 1, ctl)) break;
         ++done;
         tc_fence_after();
       }
@@ -705,6 +704,7 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
             reinterpret_cast<uint4*>(p + (long long)o * heads * D + k)[lane & 3] = u;
         }
       }
+      if (tid == OUT_WARP * 32) made_step(cta, STEP_ITEM, m + 1);
     }
   }
 

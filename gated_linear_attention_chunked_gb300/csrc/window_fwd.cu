@@ -39,17 +39,15 @@
 #include <algorithm>
 #include <cmath>
 
-#include "scan_common.cuh"
 #include "tmap.h"
 #include "window_common.cuh"
+#include "window_wait.cuh"
 
 namespace gla {
 namespace {
 
 using scan::Cta;
 using scan::DRAIN_NS;
-using scan::wait;
-using scan::wait_warp;
 
 constexpr int BM = 128, BN = 128;
 constexpr uint32_t K_BOX = 8192, V_BOX = 16384;  // 128 rows x 64 B, x 128 B
@@ -72,7 +70,7 @@ enum Bar : uint32_t {  // +stage (+4 group + quadrant, + quadrant) where there a
 };
 constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr uint32_t OFF_ABORT = OFF_TMEM + 4;
-constexpr uint32_t SMEM_USED = OFF_ABORT + 4, SMEM_BYTES = SMEM_USED + 1024;
+constexpr uint32_t SMEM_USED = OFF_ABORT + 4 * kWaitWords, SMEM_BYTES = SMEM_USED + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
 // Columns: S twice 128, O 192.  A tile's P takes the place of its S, from the front.
@@ -158,7 +156,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     mbar_init(cta.bar(DRAIN), 1);
     for (uint32_t q = REF; q < SUM; ++q) mbar_init(cta.bar(q), 32);
     for (uint32_t q = SUM; q < NBAR; ++q) mbar_init(cta.bar(q), 64);
-    *cta.abort_flag() = 0;
+    for (uint32_t i = 0; i < kWaitWords; ++i) cta.abort_flag()[i] = 0;
     fence_barrier_init();
     prefetch_tensormap(&map_q);
     prefetch_tensormap(&map_k);
@@ -181,7 +179,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         const KeyTiles kt = it.keys();
         for (int i = 0; i < kt.n; ++i, ++n) {
           const uint32_t s = n & 1;
-          if (n >= 2 && !(ok = wait(cta, cta.bar(S_FULL + s), ((n >> 1) - 1) & 1, ctl))) break;
+          if (n >= 2 && !(ok = await(cta, cta.bar(S_FULL + s), ((n >> 1) - 1) & 1, ctl))) break;
           // with an item between, the scores of two tiles ago are past the item before it: its
           // queries' buffer is free
           if (i == 0) {
@@ -213,7 +211,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         const KeyTiles kt = it.keys();
         for (int i = 0; i < kt.n; ++i, ++n) {
           const uint32_t s = n & 1;
-          if (n >= 2 && !(ok = wait(cta, cta.bar(O_DONE + s), ((n >> 1) - 1) & 1, ctl))) break;
+          if (n >= 2 && !(ok = await(cta, cta.bar(O_DONE + s), ((n >> 1) - 1) & 1, ctl))) break;
           mbar_arrive_expect_tx(cta.bar(V_FULL + s), V_BYTES);
           for (int j = 0; j < 3; ++j)
             tma_load_4d(cta.sb + OFF_V + s * V_BYTES + j * V_BOX, &map_v, cta.bar(V_FULL + s),
@@ -239,8 +237,8 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       if (s_live) { sk = si.keys(); ++sm; }
       auto scores = [&]() -> bool {  // S[sn & 1] = Q K^T
         const uint32_t s = sn & 1, qs = sm & 1;
-        if (s_at == 0 && !wait(cta, cta.bar(Q_FULL + qs), (sm >> 1) & 1, ctl)) return false;
-        if (!wait(cta, cta.bar(K_FULL + s), (sn >> 1) & 1, ctl)) return false;
+        if (s_at == 0 && !await(cta, cta.bar(Q_FULL + qs), (sm >> 1) & 1, ctl)) return false;
+        if (!await(cta, cta.bar(K_FULL + s), (sn >> 1) & 1, ctl)) return false;
         tc_fence_after();
         const uint32_t id = ID_S | ((uint32_t)(tile_cols(sk, s_at, a.sink) >> 3) << 17);
         const uint64_t q = q_desc + (qs * K_BYTES >> 4), k = k_desc + (s * K_BYTES >> 4);
@@ -265,14 +263,14 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         for (v_at = 0; v_at < vk.n; ++v_at, ++vn) {
           const uint32_t s = vn & 1;
           if (vn == ctl.stall_step) {  // the give-up path's diagnostic (see chunk_fwd.cu)
-            wait(cta, cta.bar(DRAIN), 0, ctl);
+            await(cta, cta.bar(DRAIN), 0, ctl);
             ok = false;
             break;
           }
-          if (!(ok = wait(cta, cta.bar(V_FULL + s), (vn >> 1) & 1, ctl))) break;
+          if (!(ok = await(cta, cta.bar(V_FULL + s), (vn >> 1) & 1, ctl))) break;
           if (v_at == 0 && vm > 0 &&
-              !(ok = wait(cta, cta.bar(O_FREE), (vm - 1) & 1, ctl))) break;
-          if (!(ok = wait(cta, cta.bar(P_READY + s), (vn >> 1) & 1, ctl))) break;
+              !(ok = await(cta, cta.bar(O_FREE), (vm - 1) & 1, ctl))) break;
+          if (!(ok = await(cta, cta.bar(P_READY + s), (vn >> 1) & 1, ctl))) break;
           tc_fence_after();
           const uint64_t v = v_desc + (s * V_BYTES >> 4);
           const int steps = tile_cols(vk, v_at, a.sink) >> 4;
@@ -282,6 +280,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
               mma_f16_ts(tmem + TM_O, tmem + TM_S + 128 * s + 8 * c, v + (c * 2048 >> 4), ID_PV,
                          v_at > 0 || c > 0);
           mma_commit(cta.bar(O_DONE + s));
+          made_step(cta, STEP_TILE, vn + 1);
           if (s_live && !(ok = scores())) break;
         }
       }
@@ -322,7 +321,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           return bits_to(min(t, len - 1) - c0) &
                  (~bits_to(t - a.window - c0) | bits_to(a.sink - 1 - c0));
         };
-        if (!(ok = wait_warp(cta, cta.bar(S_FULL + g), (n >> 1) & 1, ctl))) break;
+        if (!(ok = await_warp(cta, cta.bar(S_FULL + g), (n >> 1) & 1, ctl))) break;
         tc_fence_after();
         const uint32_t ts = trow + TM_S + 128 * g;
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -358,7 +357,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         // the other group's reference of the tile before (and, as the item begins, no more
         // than its word that it is past that tile)
         if (n > 0 &&
-            !(ok = wait_warp(cta, cta.bar(REF + 4 * (g ^ 1) + q4), ((n - 1) >> 1) & 1, ctl)))
+            !(ok = await_warp(cta, cta.bar(REF + 4 * (g ^ 1) + q4), ((n - 1) >> 1) & 1, ctl)))
           break;
         const float before = i > 0 ? refs[(g ^ 1) * 128 + row] : -INFINITY;
         // a row that has seen nothing yet has o = 0 and takes any scale
@@ -419,7 +418,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         if (i > 0 && __any_sync(0xffffffffu, scale != 1.f)) {
           // O once the tile before has been added (and the one before that, whose phase of the
           // barrier this could be taken for, is: this tile's scores came behind it)
-          if (!(ok = wait_warp(cta, cta.bar(O_DONE + (g ^ 1)), ((n - 1) >> 1) & 1, ctl))) break;
+          if (!(ok = await_warp(cta, cta.bar(O_DONE + (g ^ 1)), ((n - 1) >> 1) & 1, ctl))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 6; ++c) {
@@ -433,7 +432,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         }
         if (s0 + BN > len && len < a.T) {
           // values of padding may be anything, and 0 x NaN is NaN: zero their rows
-          if (!(ok = wait_warp(cta, cta.bar(V_FULL + g), (n >> 1) & 1, ctl))) break;
+          if (!(ok = await_warp(cta, cta.bar(V_FULL + g), (n >> 1) & 1, ctl))) break;
           const int r0 = len - s0, cnt = (BN - r0) * 24;
           for (int x = row; x < cnt; x += GROUP)
             *(uint4*)(base + OFF_V + g * V_BYTES + (x % 24 / 8) * V_BOX + (r0 + x / 24) * 128 +
@@ -447,7 +446,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       if (!ok) break;
       n0 += kt.n;
       // one item at a time: the output warps have taken the sums of the item before
-      if (m > 0 && !(ok = wait_warp(cta, cta.bar(O_FREE), (m - 1) & 1, ctl))) break;
+      if (m > 0 && !(ok = await_warp(cta, cta.bar(O_FREE), (m - 1) & 1, ctl))) break;
       sums[(m & 1) * 256 + g * 128 + row] = make_float2(sum, ref);
       mbar_arrive(cta.bar(SUM + q4));
     }
@@ -459,7 +458,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     uint8_t* const stg = base + OFF_STG + q4 * 4096;
     constexpr int CB = WIDE ? 16 : 32;  // channels of 64 bytes
     Items it(a);
-    int n0 = 0, m = 0;
+    int n0 = 0, m = 0, seen = 0;
     while (it.next()) {
       const int t = it.q0 + row;
       const bool live_item = it.q0 < it.len, live = t < it.len;
@@ -469,14 +468,14 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       float ref = -INFINITY, sum = 0.f;
       if (live_item) {
         n0 += it.keys().n;
-        if (!wait_warp(cta, cta.bar(SUM + q4), m & 1, ctl)) break;
+        if (!await_warp(cta, cta.bar(SUM + q4), m & 1, ctl)) break;
         const float2 s0 = sums[(m & 1) * 256 + row], s1 = sums[(m & 1) * 256 + 128 + row];
         ref = fmaxf(s0.y, s1.y);
         if (s0.y != -INFINITY) sum = s0.x * ex2(s0.y - ref);
         if (s1.y != -INFINITY) sum = fmaf(s1.x, ex2(s1.y - ref), sum);
         // the last tile's scores came behind the sums of the tile before the one before it, so this
         // is the last one's phase
-        if (!wait_warp(cta, cta.bar(O_DONE + ((n0 - 1) & 1)), ((n0 - 1) >> 1) & 1, ctl)) break;
+        if (!await_warp(cta, cta.bar(O_DONE + ((n0 - 1) & 1)), ((n0 - 1) >> 1) & 1, ctl)) break;
         tc_fence_after();
         ++m;
       }
@@ -527,6 +526,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       if (a.lse && t < a.T)
         a.lse[((long long)it.b * a.H + it.h) * a.T + t] =
             live ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+      if (tid == OUT_WARP * 32) made_step(cta, STEP_ITEM, ++seen);
     }
   }
 

@@ -93,8 +93,11 @@ GLA_API const char* gla_status_string(gla_status s);
 GLA_API gla_status gla_get_device_error(void);
 
 /* Wall-clock limit, in nanoseconds, of every bounded wait inside the chunk
- * kernels (default 2e9).  A wait that runs out records GLA_ERR_TIMEOUT and
- * the kernel finishes early without touching memory outside its tensors.
+ * kernels and the operators around the mixer (default 2e9).  A wait that runs
+ * out records GLA_ERR_TIMEOUT and the kernel finishes early without touching
+ * memory outside its tensors.
+ * In the windowed attention's forward and gradient, some of whose waits last as long as a tile of
+ * queries takes to see all its keys, the limit counts from the last step that the CTA made.
  * Applies to calls made after it returns.  ns == 0 restores the default. */
 GLA_API gla_status gla_set_wait_timeout_ns(unsigned long long ns);
 

@@ -85,3 +85,50 @@ def test_norm_rings_give_up_and_the_next_call_is_the_same(env, call, n, D, dt, s
         _stalled(gla, torch, step, lambda: gla.layer_norm_fwd(x, w))
     else:
         _stalled(gla, torch, step, lambda: gla.layer_norm_bwd(dy, x, w, m, r))
+
+
+def test_window_waits_last_as_long_as_an_item(env):
+    """With a window of all of T an item streams 1,024 tiles forward and 4,096 in the gradient (0.9 and
+    2.7 ms); a limit of 0.2 ms, two hundred tiles, does not end it."""
+    gla, torch = env
+    T = 131072
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    q, k, v, dO = r(1, T, 2, 96) * 0.1, r(1, T, 1, 96), r(1, T, 1, 192), r(1, T, 2, 192)
+    o, lse = gla.window_attn_fwd(q, k, v, T)
+    want = gla.window_attn_bwd(q, k, v, o, lse, dO, T)
+    assert gla.get_device_error() == 0
+    try:
+        gla.set_wait_timeout_ns(200_000)
+        o2, lse2 = gla.window_attn_fwd(q, k, v, T)
+        assert gla.get_device_error() == 0
+        got = gla.window_attn_bwd(q, k, v, o, lse, dO, T)
+        assert gla.get_device_error() == 0
+    finally:
+        gla.set_wait_timeout_ns(0)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_window_waits_last_through_sequences_without_tokens(env):
+    """Between the batch's first and last sequences the output rows of some 400 items a CTA are zeros
+    (0.4 ms of stores), while the next item's sums wait for them; a limit of 0.2 ms does not end it."""
+    gla, torch = env
+    B, T = 2000, 2048
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    lens[:20] = lens[-20:] = T
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    q, k, v, dO = r(B, T, 2, 96) * 0.1, r(B, T, 1, 96), r(B, T, 1, 192), r(B, T, 2, 192)
+    o, lse = gla.window_attn_fwd(q, k, v, 256, 3, lens)
+    want = gla.window_attn_bwd(q, k, v, o, lse, dO, 256, 3, lens)
+    assert gla.get_device_error() == 0
+    try:
+        gla.set_wait_timeout_ns(200_000)
+        o2, lse2 = gla.window_attn_fwd(q, k, v, 256, 3, lens)
+        got = gla.window_attn_bwd(q, k, v, o, lse, dO, 256, 3, lens)
+        assert gla.get_device_error() == 0
+    finally:
+        gla.set_wait_timeout_ns(0)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
