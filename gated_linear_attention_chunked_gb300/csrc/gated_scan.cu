@@ -8,8 +8,12 @@
 // Both directions are a scan of pairs (a, b): the map c -> a c + b of a token, composed as
 // (a2, b2) o (a1, b1) = (a2 a1, a2 b1 + b2).  The forward's pair is (f, (1 - f) x); the
 // gradient runs from the last token with c_t = f_t G_t, i.e. the pair (f, f dy).  1 - f is
-// sigmoid(-g), taken from the same exponential, so neither loses digits where it is small; all
-// arithmetic and the carried state are fp32.
+// sigmoid(-g), taken from the same exponential, so neither loses digits where it is small.  All
+// arithmetic and the carried state are fp32, in which f near 1 (long memory) keeps 1 - f only to 2^-25,
+// an error of the same sign at every token.  So a thread sums 1 - a beside a over its 16 (gradient: 8)
+// tokens, 1 - f a = (1 - a) + a (1 - f), and a near 1 is rounded once, not token by token: at a constant
+// g = 10, x ~ 1 + N(0,1) and 50,021 tokens the state is off by 2.6e-5 where a alone gave 4.7e-4.  (Pairs
+// that carry 1 - a itself from thread to thread: 2e-6, but 238 us in place of 222 at B=2 T=50021 D=1536.)
 //
 // Bound by HBM: a token and channel cost 8 bytes forward (bf16 x, g in, fp32 y out) and 20
 // backward (x, g, y, dy in, dx, dg out), against ~20 and ~30 instructions.  One pass over memory:
@@ -20,10 +24,10 @@
 // runs its tokens from the state entering them.  Where sequences x slabs leave SMs idle, a
 // cluster of up to 8 CTAs takes consecutive tiles of the same slab and sends its CTAs' pairs
 // around through distributed shared memory, counted on barriers there (a cluster barrier in
-// their place also waited for the output stores: 272 us against 216 at B=2 T=50021 D=1536); no
+// their place also waited for the output stores: 272 us against 216 then at B=2 T=50021 D=1536); no
 // flag in global memory, no workspace, and the order of composition is fixed by the sizes, so
 // results repeat bit for bit.  Measured (bf16, against the copy rate): forward B=8 T=2048 D=2048
-// 47.3 us (84 %), gradient B=8 T=2047 105.6 us (94 %).
+// 47.3 us (84 %), gradient B=8 T=2047 104.6 us (94 %), forward B=2 T=50021 D=1536 222 us (82 %).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -53,6 +57,32 @@ __device__ __forceinline__ void gates(float g, float& f, float& u) {
 template <int VEC>
 struct alignas(8 * VEC) Pair {
   float a[VEC], b[VEC];
+};
+__device__ __forceinline__ float2 vec(const float (&x)[2]) { return make_float2(x[0], x[1]); }
+__device__ __forceinline__ void put(float (&x)[2], float2 y) { x[0] = y.x; x[1] = y.y; }
+// A thread's pair as it goes through its tokens: a, and 1 - a beside it (u).  token2: both channels in
+// one instruction, with which the forward's sum costs nothing (47.3 us at B=8 T=2048 D=2048 either way,
+// one by one 49.3).
+template <int VEC>
+struct Compose : Pair<VEC> {
+  float u[VEC];
+  __device__ __forceinline__ Compose() {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) { this->a[j] = 1.f; this->b[j] = u[j] = 0.f; }
+  }
+  __device__ __forceinline__ void token(int j, float f, float g) {  // f and 1 - f
+    u[j] = fmaf(this->a[j], g, u[j]);
+    this->a[j] *= f;
+  }
+  __device__ __forceinline__ void token2(const float (&f)[VEC], const float (&g)[VEC]) {
+    put(u, fma2(vec(this->a), vec(g), vec(u)));
+    put(this->a, mul2(vec(this->a), vec(f)));
+  }
+  __device__ __forceinline__ const Pair<VEC>& pair() {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) this->a[j] = u[j] < 0.5f ? 1.f - u[j] : this->a[j];
+    return *this;
+  }
 };
 
 constexpr uint64_t DRAIN_NS = 4000000000ull;  // limit of the exit-time drain waits
@@ -274,9 +304,7 @@ scan_fwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
   int r = 0;
   for (int at = 0; at < T_; at += step, t0 += step, ++r) {
     float f[S][VEC], a[S][VEC];
-    Pair<VEC> own;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) { own.a[j] = 1.f; own.b[j] = 0.f; }
+    Compose<VEC> own;
 #pragma unroll
     for (int i = 0; i < S; ++i)
 #pragma unroll
@@ -285,11 +313,11 @@ scan_fwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
         gates(gr[i].get(j), f[i][j], u);
         a[i][j] = u * xr[i].get(j);
         own.b[j] = fmaf(f[i][j], own.b[j], a[i][j]);
-        own.a[j] *= f[i][j];
+        own.token(j, f[i][j], u);
       }
     if (at + step < T_) fetch(t0 + step);
     float h[VEC];
-    if (!enter(ex, r, own, carry, h, ctl, ok)) break;
+    if (!enter(ex, r, own.pair(), carry, h, ctl, ok)) break;
     const bool whole = t0 + S <= len;
     float* yp = y + base + (long long)t0 * D;
 #pragma unroll
@@ -355,9 +383,7 @@ scan_bwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
         hr[i].fill(0.f);
       }
     }
-    Pair<VEC> own;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) { own.a[j] = 1.f; own.b[j] = 0.f; }
+    Compose<VEC> own;
     float f[S][VEC], u[S][VEC];
 #pragma unroll
     for (int i = 0; i < S; ++i)
@@ -365,10 +391,10 @@ scan_bwd_kernel(const T* __restrict__ x, const T* __restrict__ g, const float* _
       for (int j = 0; j < VEC; ++j) {
         gates(gr[i].get(j), f[i][j], u[i][j]);
         own.b[j] = f[i][j] * (own.b[j] + dr[i].get(j));
-        own.a[j] *= f[i][j];
+        own.token(j, f[i][j], u[i][j]);
       }
     float c[VEC];
-    if (!enter(ex, r, own, carry, c, ctl, ok)) break;
+    if (!enter(ex, r, own.pair(), carry, c, ctl, ok)) break;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       const int t = last - i;
@@ -472,34 +498,28 @@ scan_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
     const bool stall = CL == 1 && r == ctl.stall_step;
     ok = ok && mbar_wait(smem_u32(stall ? &ex.never : &full[s]), stall ? 0 : (r / STAGES) & 1, ctl);
     float f[S][2], a[S][2];
-    Pair<2> own;
-    own.a[0] = own.a[1] = 1.f;
-    own.b[0] = own.b[1] = 0.f;
+    Compose<2> own;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       const float2 xv = tile_pair(xt + i * SLAB), gv = tile_pair(gt + i * SLAB);
-      const float xs[2] = {xv.x, xv.y}, gs[2] = {gv.x, gv.y};
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float u;
-        gates(gs[j], f[i][j], u);
-        a[i][j] = u * xs[j];
-        if (!whole && t0 + i >= len) {  // past the sequence: the identity
-          f[i][j] = 1.f;
-          a[i][j] = 0.f;
-        }
-        own.b[j] = fmaf(f[i][j], own.b[j], a[i][j]);
-        own.a[j] *= f[i][j];
+      float u[2];
+      gates(gv.x, f[i][0], u[0]);
+      gates(gv.y, f[i][1], u[1]);
+      put(a[i], mul2(vec(u), xv));
+      if (!whole && t0 + i >= len) {  // past the sequence: the identity
+        f[i][0] = f[i][1] = 1.f;
+        a[i][0] = a[i][1] = u[0] = u[1] = 0.f;
       }
+      put(own.b, fma2(vec(f[i]), vec(own.b), vec(a[i])));
+      own.token2(f[i], u);
     }
     float h[2];
-    if (!enter(ex, r, own, carry, h, ctl, ok)) break;
+    if (!enter(ex, r, own.pair(), carry, h, ctl, ok)) break;
     if (tid == 0 && ok && r + STAGES < rounds) fetch(r + STAGES);
     float* yp = yb + (long long)t0 * D;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) h[j] = fmaf(f[i][j], h[j], a[i][j]);
+      put(h, fma2(vec(f[i]), vec(h), vec(a[i])));
       if (live && (whole || t0 + i < T_))
         __stcs(reinterpret_cast<float2*>(yp + (long long)i * D),
                whole || t0 + i < len ? make_float2(h[0], h[1]) : make_float2(0.f, 0.f));
@@ -583,9 +603,7 @@ scan_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
     const bool stall = CL == 1 && r == ctl.stall_step;
     ok = ok && mbar_wait(smem_u32(stall ? &ex.never : &full[s]), stall ? 0 : (r / STAGES) & 1, ctl);
     float f[S][2], v[S][2], d[S][2], k[S][2];  // f, 1 - f, dy, f (1 - f) (h_{t-1} - x)
-    Pair<2> own;
-    own.a[0] = own.a[1] = 1.f;
-    own.b[0] = own.b[1] = 0.f;
+    Compose<2> own;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       const float2 x2 = tile_pair(xt - i * SLAB), g2 = tile_pair(gt - i * SLAB);
@@ -603,12 +621,22 @@ scan_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_x,
           f[i][j] = 1.f;
           v[i][j] = d[i][j] = k[i][j] = 0.f;
         }
-        own.b[j] = f[i][j] * (own.b[j] + d[i][j]);
-        own.a[j] *= f[i][j];
+      }
+      // (in one instruction for both channels; in a cluster that was slower, 304 us against 297 at B=2
+      // T=20021 D=1536)
+      if constexpr (CL == 1) {
+        put(own.b, mul2(vec(f[i]), add2(vec(own.b), vec(d[i]))));
+        own.token2(f[i], v[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          own.b[j] = f[i][j] * (own.b[j] + d[i][j]);
+          own.token(j, f[i][j], v[i][j]);
+        }
       }
     }
     float c[2];
-    if (!enter(ex, r, own, carry, c, ctl, ok)) break;
+    if (!enter(ex, r, own.pair(), carry, c, ctl, ok)) break;
     if (tid == 0 && ok && r + STAGES < rounds) fetch(r + STAGES);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
@@ -672,7 +700,9 @@ scan_decode_kernel(float* __restrict__ state, const int* __restrict__ page, int 
   for (int j = 0; j < VEC; ++j) {
     float f, u;
     gates(gr.get(j), f, u);
-    h.set(j, fmaf(f, h.get(j), u * xr.get(j)));
+    // h + u (x - h) where f is near 1 (of an infinite h that would be none)
+    const float xj = xr.get(j), hj = h.get(j), r = fmaf(u, xj - hj, hj);
+    h.set(j, u < 0.5f && fabsf(r) < INFINITY ? r : fmaf(f, hj, u * xj));
   }
   h.store(sp);
   h.store(y + at);

@@ -500,7 +500,8 @@ GLA_API gla_status gla_conv_decode_step(float* state, const float* x, const floa
  *                the state after lens[b] tokens (0: init_state).  A length outside [0, T] is
  *                read as the nearer end and sets the device error word to GLA_ERR_RANGE
  *   y            [B,T,D] fp32 (written)      final_state [B,D] fp32 or NULL (written)
- * All arithmetic is fp32; nothing is allocated; results repeat bit for bit.
+ * All arithmetic is fp32, and 1 - f keeps its digits where it is small (gates far above 0, memory of
+ * thousands of tokens); nothing is allocated; results repeat bit for bit.
  */
 GLA_API gla_status gla_gated_scan_fwd(const void* x, const void* g, gla_dtype in_dtype,
                                       const float* init_state, const int* lens, float* y,
