@@ -9,19 +9,6 @@
 
 namespace gla {
 
-template <class T>
-__device__ __forceinline__ float to_f32(T x) {
-  if constexpr (sizeof(T) == 4) return x;
-  else if constexpr (sizeof(T) == 2 && __is_same(T, __half)) return __half2float(x);
-  else return __bfloat162float(x);
-}
-template <class T>
-__device__ __forceinline__ T from_f32(float x) {
-  if constexpr (sizeof(T) == 4) return x;
-  else if constexpr (__is_same(T, __half)) return __float2half_rn(x);
-  else return __float2bfloat16_rn(x);
-}
-
 // V consecutive elements of type T as one access of V * sizeof(T) bytes (2, 4, 8, 16; 32 bytes
 // as two of 16), which the address must be a multiple of.
 template <class T, int V>

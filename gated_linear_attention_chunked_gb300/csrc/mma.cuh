@@ -100,18 +100,6 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// `rows` rows of a [T, heads, 8 CHUNKS] tensor of one sequence and head into a tile, by
-// `threads` threads; rows from `end` on are zeros and not read.
-template <int CHUNKS, class T>
-__device__ __forceinline__ void copy_rows(uint32_t tile, const T* base, long long stride, int row0,
-                                          int rows, int end, int tid, int threads) {
-  for (int i = tid; i < rows * CHUNKS; i += threads) {
-    const int r = i / CHUNKS, c = i % CHUNKS;
-    const bool ok = row0 + r < end;
-    copy16(tile + tile_off<CHUNKS>(r, c), base + (ok ? (row0 + r) * stride : 0) + c * 8, ok);
-  }
-}
-
 // True in one lane of a converged warp.  Inside the branch on it the compiler knows that one lane
 // runs and keeps tensor-core descriptors in uniform registers: a 128 x 64 x 16 product from tensor
 // memory issues in 29 cycles, in 45 inside a branch on the lane's number.

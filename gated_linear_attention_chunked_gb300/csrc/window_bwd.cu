@@ -263,11 +263,6 @@ struct Walk {
   }
 };
 
-// Bits 0 .. n of a 32-bit word (none for n < 0).
-__device__ __forceinline__ uint32_t bits_to(int n) {
-  return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1;
-}
-
 template <class T, class TO, int KIND>
 __global__ void __launch_bounds__(THREADS, 1)
 window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
@@ -519,13 +514,8 @@ window_bwd_kernel(const __grid_constant__ CUtensorMap held_x,
         const int n = n0 + i, x0 = k.row();
         // the 32 columns from c that the row sees, or is seen by
         auto sees = [&](int c) -> uint32_t {
-          const int c0 = x0 + c;
-          if (STATS) {
-            const int end = r < a.sink ? len - 1 : (int)min((long long)len, (long long)r + a.window) - 1;
-            return bits_to(end - c0) & ~bits_to(r - 1 - c0);
-          }
-          return bits_to(min(r, len - 1) - c0) &
-                 (~bits_to(r - a.window - c0) | bits_to(a.sink - 1 - c0));
+          return STATS ? queries_seeing(r, x0 + c, len, a.window, a.sink)
+                       : keys_seen(r, x0 + c, len, a.window, a.sink);
         };
         const bool whole = STATS ? it.row0 + BH - 1 <= x0 && x0 + BS <= len &&
                                        (x0 + BS - 1 - it.row0 < a.window || it.row0 + BH <= a.sink)

@@ -8,9 +8,19 @@ namespace gla {
 
 constexpr int kCK = kDK / 8, kCV = kDV / 8;  // 16-byte chunks of a key and a value row
 
-// Query t sees key s: itself, the window - 1 tokens before it, and the first `sink` tokens.
-__device__ __forceinline__ bool window_sees(int t, int s, int window, int sink) {
-  return s <= t && (t - s < window || s < sink);
+// Query t sees key s if s <= t and (t - s < window or s < sink), within the sequence's len tokens.  As
+// bits of a 32-bit word, 0 .. n (none for n < 0):
+__device__ __forceinline__ uint32_t bits_to(int n) {
+  return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1;
+}
+// the keys c0 .. c0 + 31 that query t sees,
+__device__ __forceinline__ uint32_t keys_seen(int t, int c0, int len, int window, int sink) {
+  return bits_to(min(t, len - 1) - c0) & (~bits_to(t - window - c0) | bits_to(sink - 1 - c0));
+}
+// and the queries c0 .. c0 + 31 that see key s.
+__device__ __forceinline__ uint32_t queries_seeing(int s, int c0, int len, int window, int sink) {
+  const int end = s < sink ? len - 1 : (int)min((long long)len, (long long)s + window) - 1;
+  return bits_to(end - c0) & ~bits_to(s - 1 - c0);
 }
 
 // The key tiles (of BN keys) that the queries [q0, q1) see: those of the window, lo .. hi, and

@@ -120,10 +120,6 @@ struct Items {
 __device__ __forceinline__ int tile_cols(const KeyTiles& kt, int i, int sink) {
   return i < kt.far ? min(BN, (sink - kt.tile(i) * BN + 15) & ~15) : BN;
 }
-// Bits 0 .. n of a 32-bit word (none for n < 0).
-__device__ __forceinline__ uint32_t bits_to(int n) {
-  return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -317,9 +313,7 @@ window_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         };
         // the columns 32 c .. that this row sees
         auto sees = [&](int c) -> uint32_t {
-          const int c0 = s0 + 32 * c;
-          return bits_to(min(t, len - 1) - c0) &
-                 (~bits_to(t - a.window - c0) | bits_to(a.sink - 1 - c0));
+          return keys_seen(t, s0 + 32 * c, len, a.window, a.sink);
         };
         if (!(ok = await_warp(cta, cta.bar(S_FULL + g), (n >> 1) & 1, ctl))) break;
         tc_fence_after();
