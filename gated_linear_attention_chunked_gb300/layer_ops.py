@@ -88,6 +88,21 @@ def _end(ctx):
         ctx.__exit__(None, None, None)
 
 
+# The C ABI's sizes and indexes are 32-bit, and ctypes cuts off what is above without a word.
+_MOST = 2 ** 31 - 1
+
+
+def _fit(*values):
+    """Refuses sizes and indexes that the C ABI's int does not hold."""
+    if max(values) > _MOST or min(values) < -_MOST:
+        raise ValueError(f"sizes and indexes must fit 32 bits, got {values}")
+
+
+def _reach(window, sink):
+    """Window and sinks of a call on whole sequences, where any value past T means all of T."""
+    return max(min(window, _MOST), -1), max(min(sink, _MOST), -1)
+
+
 def _scratch(nbytes, dev, workspace):
     """(pointer, bytes, tensor) of the caller's workspace or a new one."""
     if workspace is None:
@@ -108,6 +123,7 @@ def gated_scan_fwd(x, g, init_state=None, lens=None, *, want_final_state=True, o
     x, g [B,T,D] (bf16/fp16/fp32), init_state [B,D] fp32, lens [B] int32: tokens of each sequence,
     the rest is padding.  Returns (y fp32 [B,T,D], final_state fp32 [B,D] or None)."""
     B, T, D = x.shape
+    _fit(B, T, D)
     t = x.dtype
     dev, ctx = _begin(x, "x", stream)
     try:
@@ -130,6 +146,7 @@ def gated_scan_bwd(x, g, y, dy, init_state=None, d_final_state=None, lens=None, 
     """Gradient of gated_scan_fwd (gla_gated_scan_bwd); y: the forward's output, dy [B,T,D] fp32.
     Returns (dx, dg, d_init_state or None), fp32."""
     B, T, D = x.shape
+    _fit(B, T, D)
     t = x.dtype
     dev, ctx = _begin(x, "x", stream)
     try:
@@ -154,6 +171,7 @@ def gated_scan_decode_step(state, x, g, *, out=None, stream=None):
     """One token of the gated scan (gla_gated_scan_decode_step): state [..., D] fp32 is updated in
     place, x, g the same shape (bf16/fp16/fp32).  Returns y fp32 (the new state)."""
     D = x.shape[-1]
+    _fit(D, 0)
     t = x.dtype
     dev, ctx = _begin(x, "x", stream)
     try:
@@ -175,6 +193,7 @@ def gated_scan_decode_step_paged(pool, page, x, g, *, layer0=0, out=None, stream
     x, g [n_active,L,D].  Returns y fp32 [n_active,L,D]."""
     n, L, D = x.shape
     P, PL, _ = pool.shape
+    _fit(n, P, PL, layer0, L, D)
     t = x.dtype
     dev, ctx = _begin(x, "x", stream)
     try:
@@ -197,6 +216,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, out_dtype=None, want_
     bias [D] fp32.  out_dtype: x's type (default) or fp32.  Returns (y, mean, rstd), the last two
     fp32 [...] or None."""
     D = x.shape[-1]
+    _fit(D, 0)
     t = x.dtype
     dev, ctx = _begin(x, "x", stream)
     try:
@@ -220,6 +240,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, out_dtype=None, want_
 
 
 def layer_norm_bwd_workspace_size(n_tokens, D) -> int:
+    _fit(D, 0)
     return _library().gla_layer_norm_bwd_workspace_size(n_tokens, D)
 
 
@@ -228,6 +249,7 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, *, workspace=None, stream=None):
     also dx's type; mean, rstd as the forward returned them.  Returns (dx, d_weight, d_bias), the
     last two fp32 [D]."""
     D = x.shape[-1]
+    _fit(D, 0)
     t = x.dtype
     n = x.numel() // max(D, 1)
     dev, ctx = _begin(x, "x", stream)
@@ -259,6 +281,8 @@ def window_attn_fwd(q, k, v, window, sink=0, lens=None, *, out_dtype=None, want_
     Returns (o [B,T,H,192], lse fp32 [B,H,T] or None)."""
     B, T, H, dk = q.shape
     KV, dv = v.shape[2], v.shape[3]
+    _fit(B, T, H, KV, dk, dv)
+    window, sink = _reach(window, sink)
     t = q.dtype
     dev, ctx = _begin(q, "q", stream)
     try:
@@ -281,6 +305,8 @@ def window_attn_fwd(q, k, v, window, sink=0, lens=None, *, out_dtype=None, want_
 
 
 def window_attn_bwd_workspace_size(B, T, H, KV, window, sink=0) -> int:
+    _fit(B, T, H, KV)
+    window, sink = _reach(window, sink)
     return _library().gla_window_attn_bwd_workspace_size(B, T, H, KV, window, sink)
 
 
@@ -291,6 +317,8 @@ def window_attn_bwd(q, k, v, o, lse, dO, window, sink=0, lens=None, *, workspace
     dv), of o's type."""
     B, T, H, dk_ = q.shape
     KV, dv_ = v.shape[2], v.shape[3]
+    _fit(B, T, H, KV, dk_, dv_)
+    window, sink = _reach(window, sink)
     t = q.dtype
     dev, ctx = _begin(q, "q", stream)
     try:
@@ -323,6 +351,7 @@ def window_cache_fill(pool_k, pool_v, page, k, v, window, sink=0, lens=None, *, 
     B, T, KV, dk = k.shape
     dv = v.shape[-1]
     P, PL = pool_k.shape[:2]
+    _fit(B, T, KV, dk, dv, P, PL, layer, window, sink)
     t = k.dtype
     slots = window + sink
     dev, ctx = _begin(k, "k", stream)
@@ -341,6 +370,7 @@ def window_cache_fill(pool_k, pool_v, page, k, v, window, sink=0, lens=None, *, 
 
 
 def window_attn_decode_workspace_size(n_active, H, KV, window, sink=0) -> int:
+    _fit(n_active, H, KV, window, sink)
     return _library().gla_window_attn_decode_workspace_size(n_active, H, KV, window, sink)
 
 
@@ -353,6 +383,7 @@ def window_attn_decode_step(pool_k, pool_v, page, pos, q, k, v, window, sink=0, 
     n, H, dk = q.shape
     KV, dv = v.shape[1], v.shape[2]
     P, PL = pool_k.shape[:2]
+    _fit(n, H, KV, dk, dv, P, PL, layer, window, sink)
     t = q.dtype
     slots = window + sink
     dev, ctx = _begin(q, "q", stream)
