@@ -27,7 +27,11 @@
 // their place also waited for the output stores: 272 us against 216 then at B=2 T=50021 D=1536); no
 // flag in global memory, no workspace, and the order of composition is fixed by the sizes, so
 // results repeat bit for bit.  Measured (bf16, against the copy rate): forward B=8 T=2048 D=2048
-// 47.3 us (84 %), gradient B=8 T=2047 104.6 us (94 %), forward B=2 T=50021 D=1536 222 us (82 %).
+// 47.3 us (84 %), gradient B=8 T=2047 105 us (94 %), forward B=2 T=50021 D=1536 222 us (82 %), gradient
+// B=2 T=20021 294 us (62 %: a tile of 147 KB leaves one CTA an SM, so that 384 of them take three rounds).
+// Rows that 16 bytes do not divide go through registers, by pairs or singly: B=8 T=2048, forward D=1022
+// fp32 36 us (floor 29.6) and D=1023 bf16 41 (19.8), gradient 82 (59.3) and 92 (49.4).  Decode step, 1,280
+// rows of 2048 bf16: 6.0 us from a graph with the pool in L2, 9.2 from twelve pools in turn (6.2).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

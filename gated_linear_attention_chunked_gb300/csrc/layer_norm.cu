@@ -14,10 +14,15 @@
 // or a batch's decode step) are loaded to registers instead, a CTA per row or R rows; there the
 // squares are taken per warp about the warp's own mean, and the warps' are joined by
 //   m = sum(k_i m_i) / D,   q = sum(q_i + k_i (m_i - m)^2).
-// dw and db: every CTA leaves its sums in the workspace, and a second kernel adds them up in the
-// order of the CTAs, so results repeat bit for bit.  All arithmetic is fp32, with one rounding
-// to the output's type.  Measured: forward 65536 x 2048 bf16 94 us (a plain copy of as many bytes
-// 82), 136 before the rings; gradient 65536 x 1536, bf16 x, fp32 dy 155 us (a copy 149), before 258.
+// dw and db: every thread adds the rows of its CTA one after the other, every CTA leaves its sums in
+// the workspace, and a second kernel adds them up in the order of the CTAs, so results repeat bit for
+// bit.  All arithmetic is fp32, with one rounding to the output's type; the chain of a thread is n over
+// the CTAs rows long, and 65,536 rows leave dw off by 3e-7 of its size.  Measured: forward 65536 x 2048
+// bf16 94 us (a plain copy of as many bytes 82), 136 before the rings; gradient 65536 x 1536, bf16 x,
+// fp32 dy 155 us (a copy 149), before 258.  Rows that the rings do not take, of as many bytes as those:
+// forward 32768 x 4096 bf16 142 us and 16384 x 8192 128 (floor 79), 65536 x 1001 bf16 160 (39) and fp32
+// 161 (77); gradient 32768 x 4096 and 16384 x 8192, bf16 x, fp32 dy 339 us (198), 65536 x 1001 bf16 151
+// (58).  Above 8,192 channels the gradient's 1,024 threads spill 160 to 240 bytes each.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -354,7 +359,7 @@ layer_norm_fwd_ring_kernel(const TX* __restrict__ x, const float* __restrict__ w
       mbar_wait(smem_u32(&full[w][k % stages]), (k / stages) & 1, ctl, DRAIN_NS);
 }
 
-// ---- gradient, rows that 16-byte accesses divide and of which the ring holds eight: a CTA takes R
+// ---- gradient, rows that 16-byte accesses divide and of which the ring holds twelve: a CTA takes R
 // rows at a time from a ring of bulk copies in shared memory, thread t the channels (t + threads i) V ..
 // The 2 R sums of a warp are taken by halving the values with the lanes (6 shuffles for 4 sums
 // in place of 20), and joined over the warps behind the one barrier the same way.
@@ -597,8 +602,9 @@ struct Fwd {
     if constexpr (V > 1 && V * sizeof(TX) != 16) {
       return cudaErrorInvalidValue;
     } else {
-      // A warp per row where there are rows enough for every SM to have 16 of them; a CTA per
-      // row where there are not (16 rows of 2048: 22 us a call either way, the launch's).
+      // A warp per row where there are more than 8 rows for every SM; a CTA per row where there are
+      // not (16 rows of 2048: 22 us a call either way, the launch's), and above 2,048 channels, for
+      // which the ring is not built (4096 channels: 142 us for the bytes that take 94 at 2048).
       if constexpr (V > 1) {
         if (a.D <= 2048 && a.n > 8ll * n_sm) {
           constexpr int U = 2048 / (32 * V);  // accesses of a lane for 2048 channels

@@ -20,7 +20,11 @@
 // shared memory next to one of 64 x 16 takes 1.5 times as long to read as the product takes, and
 // the held tile's shared memory is free for the next item's as soon as it has been copied.  The
 // grids are programmatic dependents of one another: KEYS waits for delta, the others for nothing, so
-// that a CTA of the next kind starts where one of the last has no item left.
+// that a CTA of the next kind starts where one of the last has no item left.  They may read delta and
+// the counters all the same: a CTA of KEYS lets its dependent start only behind its own wait, that is
+// when delta's grid is complete and its writes are in memory, VALUES starts when all of them have, and
+// QUERIES when all of VALUES has started; and no cache holds older values, as nothing reads either
+// between the start of delta's grid and its end.  That rests on KEYS being launched first.
 //   warp 8       takes items from a counter and issues the TMA loads: the held tile, and a ring of
 //                four streamed tiles
 //   warp 9       lse and delta of the streamed queries, into shared memory (VALUES, KEYS)
@@ -35,12 +39,14 @@
 //
 // Bound by the hand-over of a tile from its scores to P or Z and on to the sums, and by the issue of
 // 22 (VALUES: 10) products per 64 streamed rows: ~1,300 cycles a tile where the products take 770.
-// Measured, bf16, B=8 T=2048, 16 heads on 4, window 512, 4 sinks, ragged: 189 us (delta 21, the
-// sinks' sums 4).  Before: 277 with the three kinds in one grid and every operand from shared
-// memory; 207 with half of the held operands in tensor memory, copied by the warps of P and Z; 202
-// with all of them; 196 with delta and the sinks' sums chained to the kinds; 191 with an issuer that
-// keeps its descriptors.  No faster: masks by the tile's position in place of votes (+2 us), an
-// issuer that takes the next item's scores ahead of this item's last sums (+4 us).
+// Measured, bf16, B=8 T=2048, 16 heads on 4, window 512, 4 sinks: 340 us, with 10,600 of the 16,384
+// tokens live 237, 9,097 208, 6,609 169 (delta 21, the sinks' sums 4).  As the mean of the last two,
+// 192 now (waits whose limit follows the CTA's steps cost 2 of them), before: 277 with the three kinds
+// in one grid and every operand from shared memory; 207 with half of the held operands in tensor
+// memory, copied by the warps of P and Z; 202 with all of them; 196 with delta and the sinks' sums
+// chained to the kinds; 191 with an issuer that keeps its descriptors.  No faster: masks by the tile's
+// position in place of votes (+2 us), an issuer that takes the next item's scores ahead of this item's
+// last sums (+4 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -11,13 +11,16 @@
 // with rings of their own in shared memory (asynchronous copies, no barrier between warps) and
 // running maxima and sums of their own, which they join at the end.
 //
-// The device holds two CTAs an SM (rings of three stages; with four, one fits, 123 us in place of
-// 101 at 256 sequences of 1,028 slots and four key heads).  As many whole units (sequence, key head,
+// The device holds two CTAs an SM (rings of three stages; with four, one fits, 123 us in place of the
+// 101 then at 256 sequences of mixed ages, 1,028 slots, four key heads).  As many whole units (sequence, key head,
 // group of query heads) as fill it one or more times run uncut; the slots of the others are cut
 // into the parts that fill the last round, joined by a second kernel in a fixed order.  Measured,
-// bf16, 1,028 slots, 16 heads on four, from a graph: 8 sequences 11.9 us (with parts for two rounds
-// of all units 16.0), 64: 30.0 (42.1), 100: 49.6 (54.3), 128: 56.0 (68.5), 256: 107.9 (111.8; 83 % of
-// the copy rate); 2 sequences of 8,196 slots, 32 heads on four: 20.1 (28.5).
+// bf16, 1,028 slots, all filled, 16 heads on four, from a graph: 8 sequences 11.9 us (with parts for
+// two rounds of all units 16.0), 64: 29.5 (42.1), 100: 49.0 (54.3), 128: 55.8 (68.5), 256: 106.1
+// (111.8; 84 % of the copy rate); 2 sequences of 8,196 slots, 32 heads on four: 19.9 (28.5).  256
+// sequences of mixed ages, a quarter of them still filling their page (79 us at the copy rate): 95.2,
+// 97 a call.  The cache fill, one warp a slot, copies 64 prompts of 2,048 tokens into such pages in 56 us
+// (45 at the copy rate), 256 in 211 (179), one of 8,192 in 2.9.
 #include <cuda_runtime.h>
 
 #include <algorithm>

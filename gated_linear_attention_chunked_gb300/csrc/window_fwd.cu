@@ -30,8 +30,9 @@
 // Bound by a tile's chain: its P V (770 cycles), the scores two tiles on behind it (380), their
 // softmax (1,800) and the hand-overs take 3,550 cycles for two tiles, 1,775 a tile where the products
 // take 1,150; between items, by the wait for the output rows.  Measured, bf16, B=8 T=2048, 16 heads,
-// window 512, 4 sinks: 110.5 us, 2.5 times the copy of its bytes; 126 with P in columns of its own,
-// 117 with masks decided by votes of the warp instead of by the tile's position.  No faster: the
+// window 512, 4 sinks: 107.5 us, 2.4 times the copy of its bytes (110.4 before the waits of
+// window_wait.cuh, with which fewer registers spill); then 126 with P in columns of its own, 117 with
+// masks decided by votes of the warp instead of by the tile's position.  No faster: the
 // next scores ahead of P V (120), output rows held in registers (spills, 127), tiles of a sequence
 // from the last (130: the keys' tiles then leave the L2 between their readers).
 #include <cuda_runtime.h>

@@ -496,9 +496,9 @@ GLA_API gla_status gla_conv_decode_step(float* state, const float* x, const floa
  *                x must be finite where g = +inf
  *   init_state   [B,D] fp32 or NULL (= zeros)
  *   lens         [B] int32 (device) or NULL (= all T): tokens lens[b].. of sequence b are
- *                padding: neither x nor g is read there, y is written as 0 and final_state is
- *                the state after lens[b] tokens (0: init_state).  A length outside [0, T] is
- *                read as the nearer end and sets the device error word to GLA_ERR_RANGE
+ *                padding: x and g may hold anything there, NaN included, y is written as 0 and
+ *                final_state is the state after lens[b] tokens (0: init_state).  A length outside
+ *                [0, T] is read as the nearer end and sets the device error word to GLA_ERR_RANGE
  *   y            [B,T,D] fp32 (written)      final_state [B,D] fp32 or NULL (written)
  * All arithmetic is fp32, and 1 - f keeps its digits where it is small (gates far above 0, memory of
  * thousands of tokens); nothing is allocated; results repeat bit for bit.
@@ -511,8 +511,9 @@ GLA_API gla_status gla_gated_scan_fwd(const void* x, const void* g, gla_dtype in
 /* Its gradient for the scalar loss sum(y . dy) + <d_final_state, final_state>, with
  * G_t = dy_t + f_{t+1} G_{t+1} (G_T = dy_T + d_final_state):
  *   dx_t = (1 - f_t) G_t,  dg_t = f_t (1 - f_t) (h_{t-1} - x_t) G_t,  d_init_state = f_1 G_1
- *   y            [B,T,D] fp32: the forward's output for the same inputs (read)
- *   dy           [B,T,D] fp32; not read on padding
+ *   y            [B,T,D] fp32: the forward's output for the same inputs (read; y and dy may hold
+ *                anything on padding)
+ *   dy           [B,T,D] fp32
  *   d_final_state [B,D] fp32 or NULL (= zeros)
  *   dx, dg       [B,T,D] fp32 (written; 0 on padding)
  *   d_init_state [B,D] fp32 or NULL (written)
@@ -561,7 +562,7 @@ GLA_API gla_status gla_layer_norm_fwd(const void* x, gla_dtype x_dtype, const fl
  *   dy, dx       [n_tokens,D] dy_dtype: x_dtype or GLA_FP32 (dx written)
  *   mean, rstd   [n_tokens] fp32, as the forward wrote them
  *   d_weight, d_bias [D] fp32 or NULL (written; summed in a fixed order: deterministic; zeros
- *                if n_tokens == 0)
+ *                if n_tokens == 0).  At most n_tokens / 152 + 400 fp32 additions one after the other
  *   workspace    gla_layer_norm_bwd_workspace_size() bytes, 256-byte aligned (partial sums).
  *                The size depends on the device current at the call.
  */
@@ -583,9 +584,10 @@ GLA_API gla_status gla_layer_norm_bwd(const void* dy, gla_dtype dy_dtype, const 
  *   q            [B,T,H,96] in_dtype (GLA_BF16 or GLA_FP16; GLA_FP32 -> GLA_ERR_UNSUPPORTED)
  *   k            [B,T,KV,96], v [B,T,KV,192] in_dtype; KV divides H: query head h reads key head
  *                h / (H / KV).  No internal scaling: callers pre-scale q
- *   lens         [B] int32 (device) or NULL (= all T): tokens lens[b].. of sequence b are padding,
- *                neither read nor seen; there o is written as 0 and lse as -inf.  A length outside
- *                [0, T] is read as the nearer end and sets the device error word to GLA_ERR_RANGE
+ *   lens         [B] int32 (device) or NULL (= all T): tokens lens[b].. of sequence b are padding:
+ *                q, k and v may hold anything there, NaN included, and no token sees them; o is
+ *                written as 0 and lse as -inf.  A length outside [0, T] is read as the nearer end
+ *                and sets the device error word to GLA_ERR_RANGE
  *   window >= 1, sink >= 0 (values past T mean all of T)
  *   o            [B,T,H,192] out_dtype: in_dtype or GLA_FP32 (written)
  *   lse          [B,H,T] fp32 or NULL (written; the gradient reads it; 4-byte aligned)
@@ -607,10 +609,9 @@ GLA_API gla_status gla_window_attn_fwd(const void* q, const void* k, const void*
  *                by row only, so it may be a view: o_strides, a HOST array of three element
  *                strides (sequence, token, head; non-negative, the channels adjacent, every row
  *                16-byte aligned), or NULL for the layout of the forward
- *   dO           [B,T,H,192] in_dtype; not read on padding
+ *   dO           [B,T,H,192] in_dtype; on padding it, o and lse may hold anything
  *   dq, dk, dv   the shapes of q, k, v, of out_dtype (written; 0 on padding)
- *   workspace    gla_window_attn_bwd_workspace_size() bytes, 256-byte aligned.  The size depends
- *                on the device current at the call.
+ *   workspace    gla_window_attn_bwd_workspace_size() bytes, 256-byte aligned
  * p and dz round once to in_dtype for their products; fp16 callers scale their loss so that dz
  * stays in that type's range.  All sums run in a fixed order: results repeat bit for bit.
  */
