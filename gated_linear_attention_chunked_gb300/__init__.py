@@ -15,6 +15,9 @@ Functions (same names as the C ABI, without the ``gla_`` prefix):
   gated_scan_fwd, _bwd, _decode_step, _decode_step_paged   (the operators around the mixer, bound
   layer_norm_fwd, layer_norm_bwd                            in layer_ops.py)
   window_attn_fwd, _bwd, _decode_step, window_cache_fill
+  rotary, rotary_turns                                     (serving with the windowed attention, bound
+  window_attn_chunk, window_cache_append                    in serving_ops.py)
+  window_attn8_decode_step, window_cache8_read
   get_device_error(), set_wait_timeout_ns(ns), status_string(code)
 """
 from __future__ import annotations
@@ -132,8 +135,8 @@ def load(path: str | None = None):
 
 
 def _layer_calls():
-    """Argument and result types of the operators that layer_ops.py binds."""
-    _L, _F = ctypes.c_longlong, ctypes.c_float
+    """Argument and result types of the operators that layer_ops.py and serving_ops.py bind."""
+    _L, _F, _D = ctypes.c_longlong, ctypes.c_float, ctypes.c_double
     return {
         "gated_scan_fwd": ([_P, _P, _I] + [_P] * 4 + [_I] * 3 + [_P], _I),
         "gated_scan_bwd": ([_P, _P, _I] + [_P] * 8 + [_I] * 3 + [_P], _I),
@@ -151,17 +154,29 @@ def _layer_calls():
         "window_attn_decode_workspace_size": ([_I] * 5, _S),
         "window_attn_decode_step": ([_P, _P, _I, _P, _P] + [_I] * 6 + [_P] * 4 + [_I, _P, _S] +
                                     [_I] * 4 + [_P], _I),
+        # serving_ops.py
+        "rotary_turns": ([_I, _D, _I] + [_D] * 4 + [_P], _I),
+        "rotary": ([_P, _P, _P, _I] * 2 + [_I, _I, _P, _P, _F] + [_I] * 6 + [_P], _I),
+        "window_cache_append": ([_P, _P, _I] + [_P] * 7 + [_I] * 10 + [_P], _I),
+        "window_cache8_read": ([_P] * 4 + [_I] * 6 + [_P, _P] + [_I] * 4 + [_P], _I),
+        "window_attn_chunk_workspace_size": ([_I] * 6, _S),
+        "window_attn_chunk": ([_P] * 6 + [_I] * 7 + [_P] * 3 + [_I, _P, _I, _P, _S] + [_I] * 4 + [_P],
+                              _I),
+        "window_attn8_decode_workspace_size": ([_I] * 5, _S),
+        "window_attn8_decode_step": ([_P] * 5 + [_I] * 6 + [_P] * 3 + [_I, _P, _I, _P, _S] + [_I] * 4 +
+                                     [_P], _I),
     }
 
 
 def __getattr__(name: str):
-    """The operators of layer_ops.py, on first use (that module needs torch, this one's import
-    does not)."""
-    if name.startswith(("gated_scan_", "layer_norm_", "window_")):
-        from . import layer_ops
-        if hasattr(layer_ops, name):
-            globals()[name] = f = getattr(layer_ops, name)
-            return f
+    """The operators of layer_ops.py and serving_ops.py, on first use (those modules need torch, this
+    one's import does not)."""
+    if name.startswith(("gated_scan_", "layer_norm_", "window_", "rotary")):
+        from . import layer_ops, serving_ops
+        for module in (layer_ops, serving_ops):
+            if hasattr(module, name):
+                globals()[name] = f = getattr(module, name)
+                return f
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

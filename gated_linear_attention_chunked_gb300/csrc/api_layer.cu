@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "api_checks.h"
 #include "gated_scan.h"
 #include "gla.h"
 #include "kernels.h"
@@ -13,27 +14,7 @@
 
 namespace {
 
-constexpr long long kMaxInt = (1ll << 31) - 1;
-
-template <class... P>
-bool aligned16(P... p) {
-  return ((reinterpret_cast<uintptr_t>(p) | ...) & 15u) == 0;
-}
-template <class... P>
-bool aligned4(P... p) {
-  return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) == 0;
-}
-bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
-bool valid_dtype(gla_dtype t) { return t == GLA_BF16 || t == GLA_FP16 || t == GLA_FP32; }
-
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return n;
-}
-
-gla_status done(cudaError_t e) { return e == cudaSuccess ? GLA_OK : GLA_ERR_CUDA; }
+using namespace gla::api;
 
 gla_status check_scan_sizes(int B, int T, int D, gla_dtype t) {
   if (B <= 0 || T <= 0 || D <= 0) return GLA_ERR_INVALID_ARG;
@@ -45,15 +26,6 @@ gla_status check_scan_sizes(int B, int T, int D, gla_dtype t) {
   return GLA_OK;
 }
 
-// Sizes and types of the windowed attention; the tensors' element counts stay below 2^40.
-gla_status check_window(gla_dtype in, gla_dtype out, int window, int sink, int H, int KV, int dk,
-                        int dv) {
-  if (H <= 0 || KV <= 0 || H % KV != 0 || window <= 0 || sink < 0) return GLA_ERR_INVALID_ARG;
-  if (dk != gla::kDK || dv != gla::kDV || (in != GLA_BF16 && in != GLA_FP16) ||
-      (out != in && out != GLA_FP32))
-    return GLA_ERR_UNSUPPORTED;
-  return GLA_OK;
-}
 gla_status check_window_batch(int B, int T, int H) {
   if (B <= 0 || T <= 0) return GLA_ERR_INVALID_ARG;
   if (T > (1 << 30) || (long long)B * T > (1ll << 32) / H ||
@@ -61,17 +33,6 @@ gla_status check_window_batch(int B, int T, int H) {
     return GLA_ERR_UNSUPPORTED;
   return GLA_OK;
 }
-// Slots of a page and of the whole pool.
-gla_status check_window_pool(int n_pages, int pool_layers, int layer, int window, int sink,
-                             int KV) {
-  if (n_pages <= 0 || pool_layers <= 0 || layer < 0 || layer >= pool_layers)
-    return GLA_ERR_INVALID_ARG;
-  if (window > (1 << 30) - sink || KV > (1 << 16) ||
-      (long long)n_pages * pool_layers > (1ll << 40) / ((long long)(window + sink) * KV))
-    return GLA_ERR_UNSUPPORTED;
-  return GLA_OK;
-}
-
 }  // namespace
 
 extern "C" {
@@ -273,14 +234,6 @@ gla_status gla_window_cache_fill(const void* k, const void* v, gla_dtype cache_d
   gla::WindowCache c{pool_k, pool_v, page, B, n_pages, pool_layers, layer, KV, window, sink,
                      cache_dtype};
   return done(gla::launch_window_fill(c, k, v, lens, T, ctl, stream));
-}
-
-static gla_status check_window_active(int n_active, int H, int window, int sink) {
-  if (n_active < 0) return GLA_ERR_INVALID_ARG;
-  // CTAs: at most 64 parts of each (sequence, head)
-  if (window > (1 << 30) - sink || (long long)n_active * H > kMaxInt / 64)
-    return GLA_ERR_UNSUPPORTED;
-  return GLA_OK;
 }
 
 size_t gla_window_attn_decode_workspace_size(int n_active, int H, int KV, int window, int sink) {

@@ -23,8 +23,8 @@
  *    memory; scratch comes from the caller's `workspace`.
  *  - Streams: calls enqueue work on `stream` (NULL = legacy default stream)
  *    and return without synchronising.  gla_chunk_fwd, gla_chunk_bwd,
- *    gla_decode_step and the gated scan, layer norm and windowed attention
- *    calls can be captured into a CUDA graph (stream capture) once the device
+ *    gla_decode_step and the gated scan, layer norm, windowed attention and
+ *    rotary calls can be captured into a CUDA graph (stream capture) once the device
  *    has run them eagerly: a replay gives exactly the results of the same
  *    calls made then on the captured buffers' contents.  A workspace serves
  *    one call at a time: graphs or streams that share one must not overlap.
@@ -664,6 +664,136 @@ GLA_API gla_status gla_window_attn_decode_step(void* pool_k, void* pool_v, gla_d
                                                const void* v, void* o, gla_dtype out_dtype,
                                                void* workspace, size_t workspace_bytes, int H,
                                                int KV, int dk, int dv, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions for the windowed attention's queries and keys (or any heads): of each head's
+ * first R channels the R / 2 pairs (a, b) are turned by an angle that grows with the token's position,
+ *
+ *   a' = scale (a cos w - b sin w),  b' = scale (a sin w + b cos w),  w = 2 pi turns_i pos
+ *
+ * and channels R .. D-1 pass.  Pair i is channels (i, i + R / 2), or (2 i, 2 i + 1) if interleaved.
+ * inverse != 0 negates the angles: with the same scale that is the gradient, d_x from d_y.
+ *
+ *   q, k         [B,T,H,D] and [B,T,KV,D] in_dtype; KV == 0: no keys (k, k_out NULL).  Each may be a
+ *                view: *_strides, a HOST array of three element strides (sequence, token, head;
+ *                non-negative, the channels adjacent), or NULL for a contiguous one; here only the
+ *                element's own alignment is asked for
+ *   q_out, k_out [B,T,H|KV,D] out_dtype: in_dtype or GLA_FP32 (written, contiguous).  May be q and k
+ *                themselves, where those have no strides and the types are the same
+ *   turns        [R / 2] (device): turns per position in units of 2^-64 (gla_rotary_turns)
+ *   pos          [B,T] int32 (device) or NULL: token t of each sequence is at position t
+ *   scale        finite; 1, or what a scaled table asks for
+ * Angles are exact to pos 2^-65 turns, their sines and cosines and the sums fp32, one rounding to
+ * out_dtype.  D <= 4096.  B == 0 or T == 0 returns GLA_OK.
+ */
+GLA_API gla_status gla_rotary(const void* q, const long long* q_strides, void* q_out, int H,
+                              const void* k, const long long* k_strides, void* k_out, int KV,
+                              gla_dtype in_dtype, gla_dtype out_dtype,
+                              const unsigned long long* turns, const int* pos, float scale,
+                              int interleaved, int inverse, int B, int T, int D, int R,
+                              cudaStream_t stream);
+
+/* The table of gla_rotary on the HOST: pair i turns by base^(-2 i / R) radians per position (base > 1),
+ * and for contexts `factor` (>= 1) times as long as those trained on
+ *   GLA_ROTARY_LINEAR  by that / factor
+ *   GLA_ROTARY_BASE    with base factor^(R / (R - 2)), which slows the last pair by factor, the first not
+ *   GLA_ROTARY_PARTS   pairs that turn at least `high` times within the trained `context` tokens as they
+ *                      are, those that turn at most `low` times (0 <= low < high) divided by factor,
+ *                      between them mixed in proportion
+ * (context, low and high are read by the last one only, factor by all but GLA_ROTARY_PLAIN).
+ */
+typedef enum {
+  GLA_ROTARY_PLAIN = 0,
+  GLA_ROTARY_LINEAR = 1,
+  GLA_ROTARY_BASE = 2,
+  GLA_ROTARY_PARTS = 3
+} gla_rotary_scaling;
+GLA_API gla_status gla_rotary_turns(int R, double base, gla_rotary_scaling scaling, double factor,
+                                    double context, double low, double high,
+                                    unsigned long long* turns);
+
+/* ---------------------------------------------------------------------------
+ * Serving with the windowed attention in chunks, and with pages of 8 bits.
+ *
+ * Packed tokens: a call's n sequences lie one behind the other in n_tokens rows,
+ *   start        [n + 1] int32 (device), not decreasing, within [0, n_tokens]: sequence b has rows
+ *                start[b] .. start[b+1] - 1 (none is allowed); rows outside all of them are neither
+ *                read nor written
+ *   pos          [n] int32 (device): the position of its first row = the tokens its page holds
+ *   page         [n] int32 (device), as in gla_window_cache_fill: distinct
+ * A sequence whose page, position (negative, or its last past 2^31 - 2) or rows are out of range is left
+ * untouched and sets the device error word to GLA_ERR_RANGE.
+ *
+ * Pages (pool_k, pool_v as in gla_window_cache_fill, slots = sink + window) of 16 bits have in_dtype, and
+ * pool_e is NULL.  Of 8 bits, pool_k [n_pages,pool_layers,slots,KV,96] and pool_v [..,192] are signed
+ * whole numbers c and
+ *   pool_e       [n_pages,pool_layers,KV,slots,2] signed 8-bit exponents, of a slot's key and value:
+ * a row x is held as c 2^e with e = floor(log2(max |x|)) - 6, at least -24 (fp16) or -126 (bf16), and c =
+ * x 2^-e rounded to even, within +-127: off by at most 2^(e-1), or less than 2^e for fp16 values above
+ * 127.5 2^e.  c 2^e is a value of in_dtype.  An infinity is held as 127 times 2^9 (fp16) or 2^121, NaN as 0.
+ *
+ * gla_window_cache_append: keys and values k [n_tokens,KV,96], v [n_tokens,KV,192] go into their
+ * sequences' pages behind the tokens that are there: each slot gets the last token that belongs there,
+ * the others stay as they are.
+ *   count        [n] int32 (device) or NULL: only the first count[b] tokens of a sequence go in (drafts
+ *                that were turned down stay out; prompts padded to one length).  Outside [0, its rows]
+ *                it is read as the nearer end and sets the device error word to GLA_ERR_RANGE
+ * n == 0 or n_tokens == 0 returns GLA_OK without launching.
+ */
+GLA_API gla_status gla_window_cache_append(const void* k, const void* v, gla_dtype in_dtype,
+                                           const int* pos, const int* start, const int* count,
+                                           void* pool_k, void* pool_v, signed char* pool_e,
+                                           const int* page, int n, int n_tokens, int n_pages,
+                                           int pool_layers, int layer, int window, int sink,
+                                           int KV, int dk, int dv, cudaStream_t stream);
+
+/* gla_window_attn_chunk: the attention of a call's packed tokens over their sequences' pages and each
+ * other: row i of a sequence, at position t = pos[b] + i, sees of the tokens 0 .. t the last `window`
+ * and the first `sink`, those below pos[b] as the page holds them, the others as given.  The pages are
+ * only read: gla_window_cache_append puts the tokens in afterwards, all or those that are kept.
+ *   q            [n_tokens,H,96], k [n_tokens,KV,96], v [n_tokens,KV,192] in_dtype (GLA_BF16 or
+ *                GLA_FP16), H / KV <= 64
+ *   o            [n_tokens,H,192] out_dtype: in_dtype or GLA_FP32 (written)
+ *   workspace    gla_window_attn_chunk_workspace_size() bytes, 256-byte aligned (0: not needed).  The
+ *                size depends on the device current at the call
+ * Softmax, sums and roundings as in gla_window_attn_fwd; slots that no token has reached and rows of
+ * other sequences may hold anything, NaN included.  Results repeat bit for bit.  n == 0 or n_tokens == 0
+ * returns GLA_OK without launching.
+ */
+GLA_API size_t gla_window_attn_chunk_workspace_size(int n, int n_tokens, int H, int KV, int window,
+                                                    int sink);
+GLA_API gla_status gla_window_attn_chunk(const void* pool_k, const void* pool_v,
+                                         const signed char* pool_e, const int* page,
+                                         const int* pos, const int* start, int n, int n_tokens,
+                                         int n_pages, int pool_layers, int layer, int window,
+                                         int sink, const void* q, const void* k, const void* v,
+                                         gla_dtype in_dtype, void* o, gla_dtype out_dtype,
+                                         void* workspace, size_t workspace_bytes, int H, int KV,
+                                         int dk, int dv, cudaStream_t stream);
+
+/* gla_window_attn8_decode_step: gla_window_attn_decode_step (whose rules for page, pos, o and the
+ * workspace hold) over pages of 8 bits: q, k, v of in_dtype; the token's key and value go into the page
+ * as codes, and o[n] takes them as given. */
+GLA_API size_t gla_window_attn8_decode_workspace_size(int n_active, int H, int KV, int window,
+                                                      int sink);
+GLA_API gla_status gla_window_attn8_decode_step(void* pool_k, void* pool_v, signed char* pool_e,
+                                                const int* page, const int* pos, int n_active,
+                                                int n_pages, int pool_layers, int layer,
+                                                int window, int sink, const void* q,
+                                                const void* k, const void* v, gla_dtype in_dtype,
+                                                void* o, gla_dtype out_dtype, void* workspace,
+                                                size_t workspace_bytes, int H, int KV, int dk,
+                                                int dv, cudaStream_t stream);
+
+/* gla_window_cache8_read: layer `layer` of pages page[0 .. n-1] as rows of 16 bits, by slot: k
+ * [n,slots,KV,96], v [n,slots,KV,192] out_dtype (written), the layout of a 16-bit pool's layer.  Slots that
+ * no token has reached give what their bytes say.  A page out of range leaves its rows of k and v
+ * untouched and sets the device error word to GLA_ERR_RANGE; pages may repeat. */
+GLA_API gla_status gla_window_cache8_read(const void* pool_k, const void* pool_v,
+                                          const signed char* pool_e, const int* page, int n,
+                                          int n_pages, int pool_layers, int layer, int window,
+                                          int sink, void* k, void* v, gla_dtype out_dtype, int KV,
+                                          int dk, int dv, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
