@@ -182,7 +182,10 @@ gla_status gla_window_attn8_decode_step(void* pool_k, void* pool_v, signed char*
 static gla_status check_chunk(int n, int n_tokens, int H, int KV, int window, int sink) {
   gla_status st = check_packed(n, n_tokens, H);
   if (st != GLA_OK) return st;
-  if (window > (1 << 30) - sink || H / KV > gla::kChunkMostHeads) return GLA_ERR_UNSUPPORTED;
+  // (a page's bytes of a layer stay below 2^40, the largest step of a tensor map)
+  if (window > (1 << 30) - sink || H / KV > gla::kChunkMostHeads ||
+      (window + (long long)sink) * KV > kMaxInt)
+    return GLA_ERR_UNSUPPORTED;
   return GLA_OK;
 }
 

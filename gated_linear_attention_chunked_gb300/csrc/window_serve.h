@@ -55,7 +55,7 @@ struct ChunkArgs {
   int H;
   void* workspace;
 };
-constexpr int kChunkMostHeads = 64;  // query heads on a key head
+constexpr int kChunkMostHeads = 128;  // query heads on a key head
 size_t window_chunk_workspace_bytes(int n, int n_tokens, int KV, int H, int window, int sink,
                                     int n_sm);
 cudaError_t launch_window_chunk(const ChunkArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream);

@@ -752,7 +752,7 @@ GLA_API gla_status gla_window_cache_append(const void* k, const void* v, gla_dty
  * and the first `sink`, those below pos[b] as the page holds them, the others as given.  The pages are
  * only read: gla_window_cache_append puts the tokens in afterwards, all or those that are kept.
  *   q            [n_tokens,H,96], k [n_tokens,KV,96], v [n_tokens,KV,192] in_dtype (GLA_BF16 or
- *                GLA_FP16), H / KV <= 64
+ *                GLA_FP16), H / KV <= 128
  *   o            [n_tokens,H,192] out_dtype: in_dtype or GLA_FP32 (written)
  *   workspace    gla_window_attn_chunk_workspace_size() bytes, 256-byte aligned (0: not needed).  The
  *                size depends on the device current at the call
