@@ -18,9 +18,8 @@
 //            shared memory before the roles start.
 //   parts    where the items do not fill the device, each one's tiles are cut into parts that leave
 //            (o, reference, sum) in fp32 in the workspace, joined in order by a second kernel.
-//   codes    the output warps, idle while an item is walked, turn the 8-bit rows of a page's tile into
-//            the swizzled 16-bit operands, c 2^e exactly; rows come from L2, where TMA prefetches have
-//            put them four tiles ahead.  They do so for the next item's first two tiles before they take the
+//   codes    come by TMA as they are, and the output warps, idle while an item is walked, turn them into
+//            the swizzled 16-bit operands, c 2^e exactly.  They do so for the next item's first two tiles before they take the
 //            output rows, so that the scores stay two tiles ahead across items.
 #pragma once
 #include <cuda_runtime.h>
@@ -42,41 +41,57 @@ using scan::DRAIN_NS;
 constexpr int BM = 128, BN = 128;
 constexpr uint32_t K_BOX = 8192, V_BOX = 16384;  // 128 rows x 64 B, x 128 B
 constexpr uint32_t K_BYTES = 3 * K_BOX, V_BYTES = 3 * V_BOX;
-constexpr int LIST = 64;                         // items of a CTA
+constexpr int LIST = 48;                         // items of a CTA
 constexpr int AHEAD = 4;                         // tiles that codes are prefetched ahead
 
-// The sequence's keys that an item walks, and which of them are its part's.
-struct Item {
-  int row0, i0, n_tok;            // first packed row; first token of the sequence's new ones; tokens
-  int tokens, pos, page, kv;      // of the sequence
-  int unit;                       // (tile, key head), part: where its partial results go
-  int n0, l1, h1, l2, h2;         // tiles of the page: 0 .. n0-1, l1 .. h1-1, l2 .. h2-1
-  int far, lo;                    // of the new tokens: 0 .. far-1, lo ..
-  int tb, te;                     // tiles tb .. te-1 of all these are this part's
+// Tokens of one sequence with the query heads of a key head, and the key tiles of one part of them: tile
+// i of an item is tile i + d of the page (128 slots each) or of the sequence's new tokens, d by where i
+// lies: page tiles below n0, n1 and n2 in the three runs of slots that are seen, then new tokens below nf
+// that hold sinks, then the window's.
+struct alignas(16) Item {
+  int n0, n1, n2, nf;
+  int d1, d2, d3, d4;
+  int w[8];                       // whole tiles, which every row sees: w[0] .. w[1]-1, w[2] .., w[4] .., w[6] ..
+  int row0, i0, n_tok, tokens;    // first packed row; its index and count in the sequence's new tokens
+  int pos, page, kv, unit;        // page and layer; (tile, key head): where its partial results go
+  int tb, te;                     // tiles tb .. te-1 are this part's
   int ns, a_lo, a_hi, b_lo, base; // slots seen: 0 .. ns-1, a_lo .. a_hi-1, b_lo .. (all for the first row);
                                   // slot sink + r of the first ring run holds token base + r
+  int pad;
 };
-static_assert(sizeof(Item) == 22 * 4, "words");
+static_assert(sizeof(Item) == 128, "whole 16-byte accesses");
 
-constexpr uint32_t OFF_Q = 0, OFF_K = 2 * K_BYTES, OFF_V = 4 * K_BYTES;
-constexpr uint32_t OFF_STG = OFF_V + 2 * V_BYTES;  // output staging, 4 KB per output warp
-constexpr uint32_t OFF_REF = OFF_STG + 4 * 4096;   // float ref[2][128]: each group's reference
-constexpr uint32_t OFF_SUM = OFF_REF + 1024;       // float2 sum[2][2][128]: (sum, ref), by item
-constexpr uint32_t OFF_ITEM = OFF_SUM + 4096;
-constexpr uint32_t OFF_BAR = OFF_ITEM + LIST * sizeof(Item);
-static_assert(OFF_BAR % 8 == 0, "barriers");
-// As in window_fwd.cu.  K_CODES, V_CODES: a tile's codes have been turned into operands; the loaders and
-// the output warps arrive there for every tile, also for one that asks nothing of them, so that none falls
-// two phases behind a barrier that it waits for, which its parity would not show.
+// As in window_fwd.cu.  RAW, RAW + 1: a tile's codes of keys, of values have come; RAW_FREE: they have been
+// read.  K_CODES, V_CODES: they have been turned into operands; the loaders and the output warps arrive
+// there for every tile, also for one that asks nothing of them, so that none falls two phases behind a
+// barrier that it waits for, which its parity would not show.
 enum Bar : uint32_t {
   Q_FULL = 0, K_FULL = 2, V_FULL = 4, S_FULL = 6, O_DONE = 8, P_READY = 10, O_FREE = 12, DRAIN = 13,
-  REF = 14, SUM = 22, K_CODES = 26, V_CODES = 28, NBAR = 30
+  REF = 14, SUM = 22, RAW = 26, RAW_FREE = 28, K_CODES = 30, V_CODES = 32, NBAR = 34
 };
-constexpr uint32_t OFF_TMEM = OFF_BAR + NBAR * 8;
-constexpr uint32_t OFF_COUNT = OFF_TMEM + 4;
-constexpr uint32_t OFF_ABORT = OFF_COUNT + 4;
-constexpr uint32_t SMEM_USED = OFF_ABORT + 4 * kWaitWords, SMEM_BYTES = SMEM_USED + 1024;
-static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+constexpr uint32_t RAW_K = BN * kDK, RAW_V = BN * kDV;
+// Shared memory.  With codes, whose raw tiles take room, there is one buffer of queries (the next item's come
+// when the scores of the one before are done, ahead of its last products), and output rows are staged in
+// half the width.
+template <bool CODES>
+struct Layout {
+  static constexpr uint32_t QS = CODES ? 1 : 2;            // buffers of queries
+  static constexpr uint32_t STG_ROW = CODES ? 64 : 128;    // bytes of a staged row
+  static constexpr uint32_t Q = 0, K = QS * K_BYTES, V = K + 2 * K_BYTES;
+  static constexpr uint32_t RAWS = V + 2 * V_BYTES;        // codes of keys, of values
+  static constexpr uint32_t STG = RAWS + (CODES ? RAW_K + RAW_V : 0);  // 32 rows per output warp
+  static constexpr uint32_t REFS = STG + 4 * 32 * STG_ROW; // float ref[2][128]: each group's reference
+  static constexpr uint32_t SUMS = REFS + 1024;            // float2 sum[2][2][128]: (sum, ref), by item
+  static constexpr uint32_t ITEM = SUMS + 4096;
+  static constexpr uint32_t BAR = ITEM + LIST * sizeof(Item);
+  static constexpr uint32_t TMEM = BAR + NBAR * 8;
+  static constexpr uint32_t COUNT = TMEM + 4;              // items, their tiles
+  static constexpr uint32_t INFO = COUNT + 8;              // uint32 [4]: tiles for the issuer (TileInfo)
+  static constexpr uint32_t ABORT = INFO + 16;
+  static constexpr uint32_t USED = ABORT + 4 * kWaitWords, BYTES = USED + 1024;
+  static_assert(BYTES <= 232448, "shared memory budget");
+  static_assert(BAR % 8 == 0 && STG % 512 == 0 && RAWS % 128 == 0, "alignment");
+};
 
 // Columns: S twice 128, O 192.  A tile's P takes the place of its S, from the front.
 constexpr uint32_t TM_S = 0, TM_O = 256;
@@ -109,9 +124,8 @@ struct Partials {
 __device__ __forceinline__ int ceil_tiles(int n) { return n <= 0 ? 0 : (n - 1) / BN + 1; }
 
 // Item of tokens i0 .. of a sequence, part `part` of `parts`.
-__device__ __forceinline__ Item make_item(const WindowCache& c, const Sequence& s, int per, int i0, int kv,
-                                          int unit, int part, int parts) {
-  Item it;
+static __device__ __noinline__ void make_item(Item& it, const WindowCache& c, const Sequence& s, int per, int i0,
+                                       int kv, int unit, int part, int parts) {
   it.i0 = i0;
   it.n_tok = min(per, s.tokens - i0);
   it.row0 = s.first + i0;
@@ -121,57 +135,86 @@ __device__ __forceinline__ Item make_item(const WindowCache& c, const Sequence& 
   it.kv = kv;
   it.unit = unit;
   const int slots = c.window + c.sink, p0 = s.pos + i0, i1 = i0 + it.n_tok;
-  it.ns = min(c.sink, s.pos);
-  it.a_lo = it.a_hi = 0;
-  it.b_lo = slots;
-  it.base = 0;
+  const int ns = min(c.sink, s.pos);
+  int a_lo = 0, a_hi = 0, b_lo = slots, base = 0;
+  int a_all = 0, b_all = slots;   // from where the last row sees
   if (s.pos > c.sink) {
     const int last = s.pos - 1 - c.sink, lr = last % c.window;
-    it.base = s.pos - 1 - lr;
-    const int x = p0 - it.base - c.window + 1;  // ring place of the oldest token seen
-    it.a_lo = c.sink + max(0, x);
-    it.a_hi = c.sink + lr + 1;
-    if (it.a_lo >= it.a_hi) it.a_lo = it.a_hi;
+    base = s.pos - 1 - lr;
+    const int x = p0 - base - c.window + 1, y = x + it.n_tok - 1;  // ring place of the oldest token seen
+    a_hi = c.sink + lr + 1;
+    a_lo = min(c.sink + max(0, x), a_hi);
+    a_all = min(c.sink + max(0, y), a_hi);
     // behind the newest token are those of the round before, if there was one
-    if (it.base > c.sink) it.b_lo = min(max(it.a_hi, c.sink + x + c.window), slots);
+    if (base > c.sink) {
+      b_lo = min(max(a_hi, c.sink + x + c.window), slots);
+      b_all = min(max(a_hi, c.sink + y + c.window), slots);
+    }
   }
-  it.n0 = ceil_tiles(it.ns);
-  it.l1 = max(it.a_lo / BN, it.n0);
-  it.h1 = it.a_lo < it.a_hi ? max(ceil_tiles(it.a_hi), it.l1) : it.l1;
-  it.l2 = max(it.b_lo / BN, it.h1);
-  it.h2 = it.b_lo < slots ? max(ceil_tiles(slots), it.l2) : it.l2;
-  const KeyTiles kt(i0, i1, BN, c.window, max(c.sink - s.pos, 0));
-  it.far = kt.far;
-  it.lo = kt.lo;
-  const long long n = it.n0 + it.h1 - it.l1 + it.h2 - it.l2 + kt.n;
+  const int n0 = ceil_tiles(ns);
+  const int l1 = max(a_lo / BN, n0), h1 = a_lo < a_hi ? max(ceil_tiles(a_hi), l1) : l1;
+  const int l2 = max(b_lo / BN, h1), h2 = b_lo < slots ? max(ceil_tiles(slots), l2) : l2;
+  const int sinks = max(c.sink - s.pos, 0);  // of the new tokens
+  const KeyTiles kt(i0, i1, BN, c.window, sinks);
+  it.n0 = n0;
+  it.n1 = n0 + h1 - l1;
+  it.n2 = it.n1 + h2 - l2;
+  it.nf = it.n2 + kt.far;
+  it.d1 = l1 - n0;
+  it.d2 = l2 - it.n1;
+  it.d3 = -it.n2;
+  it.d4 = kt.lo - it.nf;
+  it.ns = ns;
+  it.a_lo = a_lo;
+  it.a_hi = a_hi;
+  it.b_lo = b_lo;
+  it.base = base;
+  // slots that all rows see: 0 .. ns-1, a_all .. a_hi-1, b_all .., joined where they meet
+  const int s_end = a_all > ns ? ns : b_all > a_hi ? max(a_hi, ns) : slots;
+  const int a_end = b_all > a_hi ? a_hi : slots, a_from = a_all > ns ? a_all : 0;
+  it.w[0] = 0;
+  it.w[1] = min(s_end / BN, n0);
+  it.w[2] = n0 + max((a_from + BN - 1) / BN, l1) - l1;
+  it.w[3] = n0 + min(a_end / BN, h1) - l1;
+  it.w[4] = it.n1 + max(((b_all > a_hi ? b_all : a_from) + BN - 1) / BN, l2) - l2;
+  it.w[5] = it.n1 + min(slots / BN, h2) - l2;
+  // new tokens: of tiles before the first row, those inside the last row's window
+  const int in = max(i1 - c.window, 0), w_lo = max((in + BN - 1) / BN, kt.lo);
+  it.w[6] = it.nf + w_lo - kt.lo;
+  it.w[7] = it.nf + (i0 + 1) / BN - kt.lo;
+  const long long n = it.n2 + kt.n;
   it.tb = (int)(n * part / parts);
   it.te = (int)(n * (part + 1) / parts);
-  return it;
 }
 
 struct Tile {
   bool fresh;   // of the new tokens
+  bool whole;   // all rows see all its columns
   int s0;       // first slot, or first of the sequence's new tokens
-  int cols;     // columns that some row may see, rounded to 16
 };
-__device__ __forceinline__ Tile tile_of(const Item& it, const WindowCache& c, int i) {
+__device__ __forceinline__ Tile tile_of(const Item& it, int i) {
+  const int4 n = *reinterpret_cast<const int4*>(&it.n0), d = *reinterpret_cast<const int4*>(&it.d1);
+  const int4 u = *reinterpret_cast<const int4*>(it.w), v = *reinterpret_cast<const int4*>(it.w + 4);
   Tile t;
-  const int n1 = it.n0 + it.h1 - it.l1, n2 = n1 + it.h2 - it.l2;
-  t.fresh = i >= n2;
+  t.fresh = i >= n.z;
+  t.s0 = BN * (i + (i < n.x ? 0 : i < n.y ? d.x : i < n.z ? d.y : i < n.w ? d.z : d.w));
+  t.whole = (i >= u.x && i < u.y) || (i >= u.z && i < u.w) || (i >= v.x && i < v.y) || (i >= v.z && i < v.w);
+  return t;
+}
+// Columns of tile i that some row may see, rounded to 16.
+__device__ __forceinline__ int cols_of(const Item& it, const WindowCache& c, const Tile& t, int i) {
+  if (t.whole) return BN;
   int end;
   if (t.fresh) {
-    const int j = i - n2;
-    t.s0 = BN * (j < it.far ? j : it.lo + j - it.far);
-    end = j < it.far && t.s0 / BN < it.lo ? min(c.sink - it.pos, it.i0 + it.n_tok) : it.i0 + it.n_tok;
+    end = it.i0 + it.n_tok;
+    if (i < it.nf) end = min(c.sink - it.pos, end);
   } else {
-    t.s0 = BN * (i < it.n0 ? i : i < n1 ? it.l1 + i - it.n0 : it.l2 + i - n1);
     const int slots = c.window + c.sink;
     end = it.ns;
     if (it.a_lo < min(it.a_hi, t.s0 + BN)) end = max(end, it.a_hi);
     if (it.b_lo < min(slots, t.s0 + BN)) end = slots;
   }
-  t.cols = min(BN, (end - t.s0 + 15) & ~15);
-  return t;
+  return min(BN, (end - t.s0 + 15) & ~15);
 }
 // The columns c0 .. c0 + 31 of a tile that token i of the sequence's new ones sees.
 __device__ __forceinline__ uint32_t columns_seen(const Item& it, const WindowCache& c, bool fresh, int i,
@@ -209,7 +252,8 @@ __device__ __forceinline__ uint4 values_of(uint32_t lo, uint32_t hi, float s) {
     whole_of<T, false>(hi, o.z, o.w);
     o = make_uint4(scaled<T>(o.x, s), scaled<T>(o.y, s), scaled<T>(o.z, s), scaled<T>(o.w, s));
   } else {
-    // (2^23 + u) s - (2^23 + 128) s, exact in one fp32 operation
+    // 0x4B000000 | u is 2^23 + u: (2^23 + u) s - (2^23 + 128) s, exact in one fp32 operation, and its upper
+    // half the bf16 value.  (Four steps in bf16 arithmetic take a third longer.)
     const float2 s2 = make_float2(s, s), off = make_float2(-8388736.f * s, -8388736.f * s);
     const uint32_t m = 0x4B000000u;
     uint32_t* w = &o.x;
@@ -227,9 +271,73 @@ __device__ __forceinline__ uint4 values_of(uint32_t lo, uint32_t hi, float s) {
   return o;
 }
 
+// The tiles of a CTA's items, one after the other.
+struct Walk {
+  int x, i;
+  __device__ __forceinline__ void settle(const Item* items, int n) {
+    while (x < n && i >= items[x].te)
+      if (++x < n) i = items[x].tb;
+  }
+  __device__ __forceinline__ void begin(const Item* items, int n) {
+    x = 0;
+    i = n ? items[0].tb : 0;
+    settle(items, n);
+  }
+  __device__ __forceinline__ void step(const Item* items, int n) {
+    ++i;
+    settle(items, n);
+  }
+};
+
+// Rows 32 q4 .. + 31 of a raw tile of codes as operands, in pieces of 16 codes (two 16-byte chunks).  Two
+// lanes take a key row's piece pairs, one of each 32-channel box, in 2 steps of 16 rows; four lanes a value
+// row's, one of each 64-channel box, in 4 steps of 8 rows: so the eight lanes that a load or a store serves
+// at once fall into different banks.  sc: 2^e of row `lane` (0 where there is none).
+// (Rolled, and out of line: its code has to stay in the instruction cache beside the other roles'.)
+template <class T, int LANES, uint32_t BOX>
+static __device__ __noinline__ void put_rows(const uint8_t* raw, uint8_t* dst, float sc, int row0) {
+  const int lane = threadIdx.x & 31, l = lane / LANES, ch = 2 * (lane % LANES);
+  const uint8_t* from = raw + (row0 + l) * (LANES * 48) + lane % LANES * 16;
+#pragma unroll 1
+  for (int h = 0; h < LANES; h += 2) {
+    uint4 x[6];  // all loads ahead of the stores, which the compiler takes for writing over them
+#pragma unroll
+    for (int j = 0; j < 6; ++j)
+      x[j] = *(const uint4*)(from + j / 3 * (32 / LANES) * (LANES * 48) + j % 3 * LANES * 16);
+    from += 2 * (32 / LANES) * (LANES * 48);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = 32 / LANES * (h + j) + l, row = row0 + r;
+      const float f = __shfl_sync(0xffffffffu, sc, r);
+      uint8_t* const to = dst + swz_off(row, ch, LANES * 32);
+      uint8_t* const to1 = dst + swz_off(row, ch + 1, LANES * 32);
+#pragma unroll
+      for (int b = 0; b < 3; ++b) {
+        *(uint4*)(to + b * BOX) = values_of<T>(x[3 * j + b].x, x[3 * j + b].y, f);
+        *(uint4*)(to1 + b * BOX) = values_of<T>(x[3 * j + b].z, x[3 * j + b].w, f);
+      }
+    }
+  }
+  fence_proxy_async();
+}
+// The exponents of row `lane` of a tile's rows 32 q4 .. as two bytes; -128 where no token is.
+__device__ __forceinline__ int exponents(const Item& it, const Tile& t, const ServeCache& cache, int q4,
+                                         int lane) {
+  const WindowCache& c = cache.c;
+  const int slots = c.window + c.sink, slot = t.s0 + 32 * q4 + lane;
+  if (t.fresh || slot >= min(it.pos, slots)) return 0x8080;
+  return __ldg(reinterpret_cast<const unsigned short*>(cache.exps) +
+               ((long long)it.page * c.KV + it.kv) * slots + slot);
+}
+
+// What the issuer has to know of a tile, from the loader of keys: looked up by the issuer itself it costs a
+// tile of 2,100 cycles a thousand.
+enum TileInfo : uint32_t { INFO_FRESH = 1, INFO_FIRST = 2, INFO_COLS = ~15u };  // and the columns
+
 struct Maps {
   CUtensorMap q, k, v;    // the call's rows
-  CUtensorMap pk, pv;     // the pages: 16-bit rows, or codes (for prefetches)
+  CUtensorMap pk, pv;     // the pages: 16-bit rows, or codes
+  CUtensorMap fk, fv;     // the pages in whole rows, for prefetches
 };
 
 // Loads of a tile's keys or values: from the page or the call's rows.
@@ -251,14 +359,15 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
   Cta cta;
   cta.base = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   cta.sb = smem_u32(cta.base);
-  cta.bar_off = OFF_BAR;
-  cta.abort_off = OFF_ABORT;
+  using L = Layout<CODES>;
+  cta.bar_off = L::BAR;
+  cta.abort_off = L::ABORT;
   uint8_t* const base = cta.base;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const WindowCache& c = a.cache.c;
   const int KV = c.KV, G = a.H / KV;
-  uint32_t* tmem_slot = (uint32_t*)(base + OFF_TMEM);
-  Item* const items = (Item*)(base + OFF_ITEM);
+  uint32_t* tmem_slot = (uint32_t*)(base + L::TMEM);
+  Item* const items = (Item*)(base + L::ITEM);
   if (SPLIT) griddep_launch_dependents();  // the join waits for this whole grid
   if (warp == MMA_WARP) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -271,9 +380,12 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
     mbar_init(cta.bar(O_FREE), GROUP);
     mbar_init(cta.bar(DRAIN), 1);
     for (uint32_t q = REF; q < SUM; ++q) mbar_init(cta.bar(q), 32);
-    for (uint32_t q = SUM; q < K_CODES; ++q) mbar_init(cta.bar(q), 64);
+    for (uint32_t q = SUM; q < RAW; ++q) mbar_init(cta.bar(q), 64);
+    for (uint32_t q = RAW; q < RAW_FREE; ++q) mbar_init(cta.bar(q), 1);
+    for (uint32_t q = RAW_FREE; q < K_CODES; ++q) mbar_init(cta.bar(q), 128);
     for (uint32_t q = K_CODES; q < NBAR; ++q) mbar_init(cta.bar(q), 128 + 1);
     for (uint32_t i = 0; i < kWaitWords; ++i) cta.abort_flag()[i] = 0;
+    ((int*)(base + L::COUNT))[1] = 0;
     fence_barrier_init();
     prefetch_tensormap(&maps.q);
     prefetch_tensormap(&maps.k);
@@ -284,7 +396,7 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
   {
     // ------------------------------------------------------------ the CTA's items
     // Tiles of a thread's slice of the sequences, their sums up to each slice, and a search.
-    int* const upto = (int*)(base + OFF_STG);
+    int* const upto = (int*)(base + L::STG);
     int* const warps = upto + THREADS + 1;
     const int slice = (c.n + THREADS - 1) / THREADS;
     const int b0 = min(tid * slice, c.n), b1 = min(b0 + slice, c.n);
@@ -324,7 +436,8 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
           left -= n;
           s = sequence(c, a.tok, ++b, ctl);
         }
-        items[tid] = make_item(c, s, plan.per, left * plan.per, unit % KV, unit, part, plan.parts);
+        make_item(items[tid], c, s, plan.per, left * plan.per, unit % KV, unit, part, plan.parts);
+        atomicAdd((int*)(base + L::COUNT) + 1, items[tid].te - items[tid].tb);
         if (SPLIT && part == 0 && unit % KV == 0) {
           const Partials ps(a.workspace, plan.units, plan.parts);
           ps.tiles[2 + 2 * t] = items[tid].row0;
@@ -334,40 +447,51 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
     }
     if (SPLIT && blockIdx.x == 0 && tid == 0) *(int*)a.workspace = tiles;
     if (tid == 0)
-      *(int*)(base + OFF_COUNT) =
+      *(int*)(base + L::COUNT) =
           (int)min((long long)LIST, max(0ll, (all - blockIdx.x + gridDim.x - 1) / gridDim.x));
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int n_items = *(const int*)(base + OFF_COUNT);
+  const int n_items = *(const int*)(base + L::COUNT);
+  volatile uint32_t* const info = (volatile uint32_t*)(base + L::INFO);
 
   if (warp == K_WARP) {
     // ------------------------------------------------------------ TMA: queries and keys
     if (lane == 0) {
       const uint32_t q_bytes = 3u * 64u * plan.per * G;
-      int n = 0, m = 0, q_armed = 0;  // key tiles and items so far
-      uint32_t armed = 0;             // stages that a load was sent to
+      int n = 0, m = 0, q_armed = 0, raw = 0;  // key tiles and items so far; tiles of codes
+      uint32_t armed = 0;                      // stages that a load was sent to
       Parities turn;
       bool ok = true;
       for (int x = 0; ok && x < n_items; ++x) {
         const Item& it = items[x];
         if (it.tb == it.te) continue;
-        const uint32_t qs = m++ & 1;
+        const uint32_t qs = m++ % L::QS;
         for (int i = it.tb; i < it.te; ++i, ++n) {
           const uint32_t s = n & 1;
+          const Tile t = tile_of(it, i);
+          if (CODES && !t.fresh) {
+            // ahead of the stage, into the raw tile's place
+            if (raw > 0 && !(ok = await(cta, cta.bar(RAW_FREE), (raw - 1) & 1, ctl))) break;
+            ++raw;
+            mbar_arrive_expect_tx(cta.bar(RAW), RAW_K);
+            tma_load_4d(cta.sb + L::RAWS, &maps.pk, cta.bar(RAW), 0, it.kv, t.s0, it.page);
+          }
           if (n >= 2 && !(ok = await(cta, cta.bar(S_FULL + s), ((n >> 1) - 1) & 1, ctl))) break;
-          // with an item between, the scores of two tiles ago are past the item before it: its
-          // queries' buffer is free
           if (i == it.tb) {
+            // of two buffers the one is free: with an item between, the scores of two tiles ago are past
+            // the item before it; a single one is when the last tile's scores are done
+            if (L::QS == 1 && n > 0 && !(ok = await(cta, cta.bar(S_FULL + (s ^ 1)), ((n - 1) >> 1) & 1, ctl)))
+              break;
             ++q_armed;
             mbar_arrive_expect_tx(cta.bar(Q_FULL + qs), q_bytes);
             for (int j = 0; j < 3; ++j)
-              tma_load_4d(cta.sb + OFF_Q + qs * K_BYTES + j * K_BOX, &maps.q, cta.bar(Q_FULL + qs),
+              tma_load_4d(cta.sb + L::Q + qs * K_BYTES + j * K_BOX, &maps.q, cta.bar(Q_FULL + qs),
                           32 * j, it.kv * G, it.row0, 0);
           }
-          const Tile t = tile_of(it, c, i);
+          info[n & 3] = cols_of(it, c, t, i) | (t.fresh ? INFO_FRESH : 0) | (i == it.tb ? INFO_FIRST : 0);
           if (CODES) mbar_arrive(cta.bar(K_CODES + s));
           if (CODES && !t.fresh) continue;
           const Source src(it, t, &maps.k, &maps.pk);
@@ -375,15 +499,16 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
           turn.take(s);
           mbar_arrive_expect_tx(cta.bar(K_FULL + s), K_BYTES);
           for (int j = 0; j < 3; ++j)
-            tma_load_4d(cta.sb + OFF_K + s * K_BYTES + j * K_BOX, src.map, cta.bar(K_FULL + s), 32 * j,
+            tma_load_4d(cta.sb + L::K + s * K_BYTES + j * K_BOX, src.map, cta.bar(K_FULL + s), 32 * j,
                         it.kv, src.row, src.outer);
         }
       }
       // every armed load has landed before the CTA may exit
-      for (int s = 0; s < 2; ++s) {
+      if (raw > 0) mbar_wait(cta.bar(RAW), (raw - 1) & 1, ctl, DRAIN_NS);
+      for (int s = 0; s < 2; ++s)
         if ((armed >> s) & 1) mbar_wait(cta.bar(K_FULL + s), turn.take(s) ^ 1, ctl, DRAIN_NS);
-        if (q_armed > s) mbar_wait(cta.bar(Q_FULL + s), ((q_armed - 1 - s) >> 1) & 1, ctl, DRAIN_NS);
-      }
+      for (int s = 0; s < (int)L::QS; ++s)
+        if (q_armed > s) mbar_wait(cta.bar(Q_FULL + s), ((q_armed - 1 - s) / L::QS) & 1, ctl, DRAIN_NS);
     }
   } else if (warp == V_WARP) {
     // ------------------------------------------------------------ TMA: values
@@ -391,29 +516,30 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
       int n = 0;
       uint32_t armed = 0;
       Parities turn;
-      [[maybe_unused]] int px = 0, pi = n_items ? items[0].tb : 0, pn = 0;  // the prefetches' walk
+      int raw = 0;
+      Walk ahead;  // the prefetches'
+      ahead.begin(items, n_items);
+      int an = 0;
       bool ok = true;
       for (int x = 0; ok && x < n_items; ++x) {
         const Item& it = items[x];
         for (int i = it.tb; i < it.te; ++i, ++n) {
           const uint32_t s = n & 1;
-          if constexpr (CODES) {
-            while (px < n_items && pn <= n + AHEAD) {
-              if (pi >= items[px].te) {
-                if (++px < n_items) pi = items[px].tb;
-                continue;
-              }
-              const Tile t = tile_of(items[px], c, pi);
-              if (!t.fresh) {
-                tma_prefetch_4d(&maps.pk, 0, items[px].kv, t.s0, items[px].page);
-                tma_prefetch_4d(&maps.pv, 0, items[px].kv, t.s0, items[px].page);
-              }
-              ++pi;
-              ++pn;
-            }
+          for (; ahead.x < n_items && an <= n + AHEAD; ++an, ahead.step(items, n_items)) {
+            const Item& to = items[ahead.x];
+            const Tile t = tile_of(to, ahead.i);
+            if (t.fresh) continue;
+            tma_prefetch_4d(&maps.fk, 0, to.kv, t.s0, to.page);
+            tma_prefetch_4d(&maps.fv, 0, to.kv, t.s0, to.page);
+          }
+          const Tile t = tile_of(it, i);
+          if (CODES && !t.fresh) {
+            if (raw > 0 && !(ok = await(cta, cta.bar(RAW_FREE + 1), (raw - 1) & 1, ctl))) break;
+            ++raw;
+            mbar_arrive_expect_tx(cta.bar(RAW + 1), RAW_V);
+            tma_load_4d(cta.sb + L::RAWS + RAW_K, &maps.pv, cta.bar(RAW + 1), 0, it.kv, t.s0, it.page);
           }
           if (n >= 2 && !(ok = await(cta, cta.bar(O_DONE + s), ((n >> 1) - 1) & 1, ctl))) break;
-          const Tile t = tile_of(it, c, i);
           if (CODES) mbar_arrive(cta.bar(V_CODES + s));
           if (CODES && !t.fresh) continue;
           const Source src(it, t, &maps.v, &maps.pv);
@@ -421,10 +547,11 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
           turn.take(s);
           mbar_arrive_expect_tx(cta.bar(V_FULL + s), V_BYTES);
           for (int j = 0; j < 3; ++j)
-            tma_load_4d(cta.sb + OFF_V + s * V_BYTES + j * V_BOX, src.map, cta.bar(V_FULL + s), 64 * j,
+            tma_load_4d(cta.sb + L::V + s * V_BYTES + j * V_BOX, src.map, cta.bar(V_FULL + s), 64 * j,
                         it.kv, src.row, src.outer);
         }
       }
+      if (raw > 0) mbar_wait(cta.bar(RAW + 1), (raw - 1) & 1, ctl, DRAIN_NS);
       for (int s = 0; s < 2; ++s)
         if ((armed >> s) & 1) mbar_wait(cta.bar(V_FULL + s), turn.take(s) ^ 1, ctl, DRAIN_NS);
     }
@@ -433,34 +560,31 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
     if (elect_one()) {
       constexpr uint32_t ID_S = idesc_f16(128, 0, BF16, BF16, false, false);
       constexpr uint32_t ID_PV = idesc_f16(128, 192, BF16, BF16, false, true);
-      const uint64_t q_desc = smem_desc(cta.sb + OFF_Q, 16, 512, SW_64);
-      const uint64_t k_desc = smem_desc(cta.sb + OFF_K, 16, 512, SW_64);
-      const uint64_t v_desc = smem_desc(cta.sb + OFF_V, V_BOX, 1024, SW_128);
-      // the scores' walk (two tiles ahead) and the values'
-      int sx = -1, sn = 0, sm = -1, s_at = 0, vn = 0, vm = -1;
-      auto next_item = [&]() -> bool {
-        while (++sx < n_items)
-          if (items[sx].tb < items[sx].te) {
-            ++sm;
-            s_at = items[sx].tb;
-            return true;
-          }
-        return false;
-      };
-      bool s_live = next_item();
+      const uint64_t q_desc = smem_desc(cta.sb + L::Q, 16, 512, SW_64);
+      const uint64_t k_desc = smem_desc(cta.sb + L::K, 16, 512, SW_64);
+      const uint64_t v_desc = smem_desc(cta.sb + L::V, V_BOX, 1024, SW_128);
+      // the scores run two tiles ahead of the values
+      const int total = ((const int*)(base + L::COUNT))[1];
+      int sn = 0, sm = -1, vm = -1;
+      uint32_t kept = 0;  // the infos of the tiles whose scores have been asked for, a half word each
       Parities turn;
-      // stage s has tile t, the CTA's n-th: keys (what 0) or values (2)
-      auto filled = [&](const Tile& t, uint32_t what, uint32_t s, int n) -> bool {
+      // stage s has the CTA's n-th tile: keys (what 0) or values (2)
+      auto filled = [&](bool fresh, uint32_t what, uint32_t s, int n) -> bool {
         if (CODES && !await(cta, cta.bar(K_CODES + what + s), (n >> 1) & 1, ctl)) return false;
-        return (CODES && !t.fresh) || await(cta, cta.bar(K_FULL + what + s), turn.take(what + s), ctl);
+        return (CODES && !fresh) || await(cta, cta.bar(K_FULL + what + s), turn.take(what + s), ctl);
       };
       auto scores = [&]() -> bool {  // S[sn & 1] = Q K^T
-        const uint32_t s = sn & 1, qs = sm & 1;
-        const Item& it = items[sx];
-        if (s_at == it.tb && !await(cta, cta.bar(Q_FULL + qs), (sm >> 1) & 1, ctl)) return false;
-        const Tile t = tile_of(it, c, s_at);
-        const uint32_t id = ID_S | ((uint32_t)(t.cols >> 3) << 17);
-        if (!filled(t, 0, s, sn)) return false;
+        const uint32_t s = sn & 1;
+        // the info comes with the loader's arrival, codes: at the operands' barrier
+        if (!CODES && !await(cta, cta.bar(K_FULL + s), turn.take(s), ctl)) return false;
+        if (CODES && !await(cta, cta.bar(K_CODES + s), (sn >> 1) & 1, ctl)) return false;
+        const uint32_t k1 = info[sn & 3];
+        if (CODES && (k1 & INFO_FRESH) && !await(cta, cta.bar(K_FULL + s), turn.take(s), ctl)) return false;
+        if (k1 & INFO_FIRST) ++sm;
+        const uint32_t qs = sm % L::QS;
+        if ((k1 & INFO_FIRST) && !await(cta, cta.bar(Q_FULL + qs), (sm / L::QS) & 1, ctl)) return false;
+        const uint32_t id = ID_S | ((k1 & INFO_COLS) << 14);
+        kept = s ? (kept & 0xFFFFu) | k1 << 16 : (kept & 0xFFFF0000u) | k1;
         tc_fence_after();
         const uint64_t q = q_desc + (qs * K_BYTES >> 4), k = k_desc + (s * K_BYTES >> 4);
 #pragma unroll
@@ -470,38 +594,32 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
         }
         mma_commit(cta.bar(S_FULL + s));
         ++sn;
-        if (++s_at == it.te) s_live = next_item();
         return true;
       };
       bool ok = true;
-      for (int i = 0; i < 2 && ok && s_live; ++i) ok = scores();
-      for (int x = 0; ok && x < n_items; ++x) {
-        const Item& it = items[x];
-        if (it.tb == it.te) continue;
-        ++vm;
-        for (int i = it.tb; i < it.te; ++i, ++vn) {
-          const uint32_t s = vn & 1;
-          if (vn == ctl.stall_step) {  // the give-up path's diagnostic (see chunk_fwd.cu)
-            await(cta, cta.bar(DRAIN), 0, ctl);
-            ok = false;
-            break;
-          }
-          const Tile t = tile_of(it, c, i);
-          const int steps = t.cols >> 4;
-          if (!(ok = filled(t, 2, s, vn))) break;
-          if (i == it.tb && vm > 0 && !(ok = await(cta, cta.bar(O_FREE), (vm - 1) & 1, ctl))) break;
-          if (!(ok = await(cta, cta.bar(P_READY + s), (vn >> 1) & 1, ctl))) break;
-          tc_fence_after();
-          const uint64_t v = v_desc + (s * V_BYTES >> 4);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < steps)
-              mma_f16_ts(tmem + TM_O, tmem + TM_S + 128 * s + 8 * j, v + (j * 2048 >> 4), ID_PV,
-                         i > it.tb || j > 0);
-          mma_commit(cta.bar(O_DONE + s));
-          made_step(cta, STEP_TILE, vn + 1);
-          if (s_live && !(ok = scores())) break;
+      for (int i = 0; i < 2 && ok && sn < total; ++i) ok = scores();
+      for (int vn = 0; ok && vn < total; ++vn) {
+        const uint32_t s = vn & 1;
+        if (vn == ctl.stall_step) {  // the give-up path's diagnostic (see chunk_fwd.cu)
+          await(cta, cta.bar(DRAIN), 0, ctl);
+          break;
         }
+        const uint32_t k1 = s ? kept >> 16 : kept & 0xFFFFu;
+        const int steps = (int)k1 >> 4;
+        const bool first = k1 & INFO_FIRST;
+        if (!filled(k1 & INFO_FRESH, 2, s, vn)) break;
+        if (first && ++vm > 0 && !await(cta, cta.bar(O_FREE), (vm - 1) & 1, ctl)) break;
+        if (!await(cta, cta.bar(P_READY + s), (vn >> 1) & 1, ctl)) break;
+        tc_fence_after();
+        const uint64_t v = v_desc + (s * V_BYTES >> 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < steps)
+            mma_f16_ts(tmem + TM_O, tmem + TM_S + 128 * s + 8 * j, v + (j * 2048 >> 4), ID_PV,
+                       !first || j > 0);
+        mma_commit(cta.bar(O_DONE + s));
+        made_step(cta, STEP_TILE, vn + 1);
+        if (sn < total) ok = scores();
       }
       mma_commit(cta.bar(DRAIN));
       mbar_wait(cta.bar(DRAIN), 0, ctl, DRAIN_NS);
@@ -513,8 +631,8 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
     const int q4 = warp & 3, g = warp >> 2, row = 32 * q4 + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
     const int tok = row / G, tok_a = 32 * q4 / G, tok_b = (32 * q4 + 31) / G;  // of a tile's tokens
-    float* refs = (float*)(base + OFF_REF);
-    float2* sums = (float2*)(base + OFF_SUM);
+    float* refs = (float*)(base + L::REFS);
+    float2* sums = (float2*)(base + L::SUMS);
     int n0 = 0, m = 0;      // tiles and items before this one
     uint32_t v_turn = 0;    // parity of the group's next tile of values that comes by TMA
     bool ok = true;
@@ -523,27 +641,33 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
       if (it.tb == it.te) continue;
       // rows past the item's tokens see nothing; a warp of such rows only keeps step
       const bool live = tok < it.n_tok && row < plan.per * G, awake = tok_a < it.n_tok;
-      const bool all_live = tok_b < it.n_tok && 32 * q4 + 31 < plan.per * G;
       const int at = it.i0 + tok, ends = it.i0 + (lane & 4 ? min(tok_b, it.n_tok - 1) : tok_a);
       float ref = -INFINITY, sum = 0.f;  // this row's, as of the group's last tile
       for (int i = it.tb + ((n0 ^ g) & 1); i < it.te; i += 2) {
         const int n = n0 + i - it.tb;
-        const Tile t = tile_of(it, c, i);
+        const Tile t = tile_of(it, i);
         // chunks of 32 columns that all rows of the warp see, and that some do: what its first and its
         // last row both see, those between do too; a chunk that neither sees, none does
-        uint32_t full = 0, some = 0;
-        if (awake) {
+        uint32_t full = awake ? 15u : 0u, some = full;
+        if (!t.whole && awake) {
           const uint32_t see = columns_seen(it, c, t.fresh, ends, t.s0 + 32 * (lane & 3));
           full = __ballot_sync(0xffffffffu, see == ~0u);
           some = __ballot_sync(0xffffffffu, see != 0u);
-          full = all_live ? full & (full >> 4) & 15u : 0u;
+          full = full & (full >> 4) & 15u;
           some = (some | (some >> 4)) & 15u;
         }
+        const int cols = cols_of(it, c, t, i);
         if (!(ok = await_warp(cta, cta.bar(S_FULL + g), (n >> 1) & 1, ctl))) break;
         tc_fence_after();
         const uint32_t ts = trow + TM_S + 128 * g;
         auto sees = [&](int j) -> uint32_t {
           return live ? columns_seen(it, c, t.fresh, at, t.s0 + 32 * j) : 0u;
+        };
+        auto hide = [&](uint32_t (&z)[32], int j) {  // the columns that this row does not see
+          const uint32_t see = sees(j);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((see >> e) & 1)) z[e] = 0xFF800000u;  // -inf
         };
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         auto maxima = [&](const uint32_t (&z)[32]) {
@@ -551,31 +675,17 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
           for (int j = 0; j < 16; ++j)
             m4[j & 3] = max3(m4[j & 3], __uint_as_float(z[2 * j]), __uint_as_float(z[2 * j + 1]));
         };
-        if (full == 15u) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t z[32];
-            tmem_ld32(ts + 32 * j, z);
-            tmem_wait_ld();
-            maxima(z);
-          }
-        } else {
 #pragma unroll 1
-          for (int j = 0; j < 4; ++j) {
-            if (!((some >> j) & 1)) continue;
-            uint32_t z[32];
-            tmem_ld32(ts + 32 * j, z);
-            tmem_wait_ld();
-            if (!((full >> j) & 1)) {
-              const uint32_t see = sees(j);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((see >> e) & 1)) z[e] = 0xFF800000u;  // -inf
-            }
-            maxima(z);
-          }
+        for (int j = 0; j < 4; ++j) {
+          if (!((some >> j) & 1)) continue;
+          uint32_t z[32];
+          tmem_ld32(ts + 32 * j, z);
+          tmem_wait_ld();
+          if (!((full >> j) & 1)) hide(z, j);
+          maxima(z);
         }
-        const float top = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * kLog2e;
+        // (a row of no token may hold anything, and reaches none but itself)
+        const float top = live ? max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * kLog2e : -INFINITY;
         // the other group's reference of the tile before (and, as the item begins, no more
         // than its word that it is past that tile)
         if (n > 0 &&
@@ -593,48 +703,31 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
           const float sub = ref == -INFINITY ? 0.f : -ref;
           const float2 sub2 = make_float2(sub, sub), l2e = make_float2(kLog2e, kLog2e);
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          // weights of 32 columns from their scores, as pairs, and their sum
-          auto weights = [&](const uint32_t (&z)[32], uint32_t (&p)[16], uint32_t see, bool masked) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float2 y = fma2(make_float2(__uint_as_float(z[2 * j]), __uint_as_float(z[2 * j + 1])),
-                              l2e, sub2);
-              y.x = ex2(y.x);
-              y.y = ex2(y.y);
-              if (masked) {
-                y.x = (see >> (2 * j)) & 1 ? y.x : 0.f;
-                y.y = (see >> (2 * j + 1)) & 1 ? y.y : 0.f;
-              }
-              acc[j & 1] = add2(acc[j & 1], y);
-              p[j] = pack2<T>(y.x, y.y);
-            }
-          };
-          // P over the columns of S that have been read
-          if (full == 15u) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t z[32], p[16];
+          // P over the columns of S that have been read: weights of 32 columns from their scores, as pairs.
+          // (One rolled loop for all tiles: a copy of it for whole ones, unrolled, pushes other roles' code
+          // out of the instruction cache.)
+#pragma unroll 1
+          for (int j = 0; 32 * j < cols; ++j) {
+            uint32_t p[16];
+            if ((some >> j) & 1) {
+              uint32_t z[32];
               tmem_ld32(ts + 32 * j, z);
               tmem_wait_ld();
-              weights(z, p, 0u, false);
-              tmem_st16(ts + 16 * j, p);
-            }
-          } else {
-#pragma unroll 1
-            for (int j = 0; 32 * j < t.cols; ++j) {
-              uint32_t p[16];
-              if ((some >> j) & 1) {
-                uint32_t z[32];
-                tmem_ld32(ts + 32 * j, z);
-                tmem_wait_ld();
-                if ((full >> j) & 1) weights(z, p, 0u, false);
-                else weights(z, p, sees(j), true);
-              } else {
+              if (!((full >> j) & 1)) hide(z, j);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) p[e] = 0u;
+              for (int e = 0; e < 16; ++e) {
+                float2 y = fma2(make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])),
+                                l2e, sub2);
+                y.x = ex2(y.x);
+                y.y = ex2(y.y);
+                acc[e & 1] = add2(acc[e & 1], y);
+                p[e] = pack2<T>(y.x, y.y);
               }
-              tmem_st16(ts + 16 * j, p);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) p[e] = 0u;
             }
+            tmem_st16(ts + 16 * j, p);
           }
           acc[0] = add2(acc[0], acc[1]);
           sum += acc[0].x + acc[0].y;
@@ -659,11 +752,11 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
         const int kept = t.fresh ? it.tokens - t.s0 : CODES ? BN : it.pos - t.s0;
         const uint32_t v_now = v_turn;
         if (!CODES || t.fresh) v_turn ^= 1;
-        if (awake && kept < t.cols) {
+        if (awake && kept < cols) {
           if (!(ok = await_warp(cta, cta.bar(V_FULL + g), v_now, ctl))) break;
-          const int step = 32 * min((min(it.n_tok, plan.per) * G + 31) / 32, 4), cnt = (t.cols - kept) * 24;
+          const int step = 32 * min((min(it.n_tok, plan.per) * G + 31) / 32, 4), cnt = (cols - kept) * 24;
           for (int y = row; y < cnt; y += step)
-            *(uint4*)(base + OFF_V + g * V_BYTES + (y % 24 / 8) * V_BOX + (kept + y / 24) * 128 +
+            *(uint4*)(base + L::V + g * V_BYTES + (y % 24 / 8) * V_BOX + (kept + y / 24) * 128 +
                       (y & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async();
         }
@@ -683,74 +776,54 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
     // ------------------------------------------------------------ output rows (and codes)
     const int q4 = warp & 3, row = 32 * q4 + lane;  // the quadrant that the warp may read
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
-    const float2* sums = (const float2*)(base + OFF_SUM);
-    uint8_t* const stg = base + OFF_STG + q4 * 4096;
+    const float2* sums = (const float2*)(base + L::SUMS);
+    constexpr int SR = L::STG_ROW, SUBS = SR / 64, LPR = SR / 16;  // staged rows: 64-byte parts, lanes of a row
+    uint8_t* const stg = base + L::STG + q4 * 32 * SR;
     constexpr int CB = WIDE ? 16 : 32;  // channels of 64 bytes
+    const uint32_t by_G = (65536 + G - 1) / G;
     int n0 = 0, m = 0, seen = 0, n = 0;  // tiles and items before this one; tiles filled
     bool ok = true;
 
-    // Tile n of the CTA, i of item `it`, if it is one of codes: rows 32 q4 .. + 31 by this warp, a row's
-    // 16-byte pieces by adjacent lanes.
-    [[maybe_unused]] auto fill = [&](const Item& it, int i) -> bool {
-      const uint32_t s = n & 1;
-      const Tile t = tile_of(it, c, i);
-      const int slots = c.window + c.sink, r0 = t.s0 + 32 * q4, kept = min(it.pos, slots) - r0;
-      const long long first = ((long long)it.page * slots + r0) * KV + it.kv;
-      uint4 w[6], w2[6];
-      float2 sc = make_float2(1.f, 1.f);  // row `lane`: 2^e of its key and value
-      auto load = [&](uint4 (&d)[6], const void* p, int pieces, int from) {
-#pragma unroll
-        for (int j = 0; j < 6; ++j) {
-          const int z = (from + j) * 32 + lane, r = z / pieces;
-          d[j] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < kept)
-            d[j] = __ldg(static_cast<const uint4*>(p) + (first + (long long)r * KV) * pieces + z % pieces);
-        }
-      };
-      auto put = [&](const uint4 (&x)[6], uint8_t* dst, int pieces, int from, uint32_t box, int per_box,
-                     float scale) {
-#pragma unroll
-        for (int j = 0; j < 6; ++j) {
-          const int z = (from + j) * 32 + lane, r = z / pieces, ch = 2 * (z % pieces);
-          const float f = __shfl_sync(0xffffffffu, scale, r);
-          uint8_t* const to = dst + ch / per_box * box;
-          const int e = ch % per_box, bytes = per_box * 16;
-          *(uint4*)(to + swz_off(32 * q4 + r, e, bytes)) = values_of<T>(x[j].x, x[j].y, f);
-          *(uint4*)(to + swz_off(32 * q4 + r, e + 1, bytes)) = values_of<T>(x[j].z, x[j].w, f);
-        }
-        fence_proxy_async();
-      };
-      if (!t.fresh) {
-        load(w, c.k, 6, 0);
-        load(w2, c.v, 12, 0);
-        if (lane < kept) {
-          const unsigned short e = __ldg(reinterpret_cast<const unsigned short*>(a.cache.exps) +
-                                         ((long long)it.page * KV + it.kv) * slots + r0 + lane);
-          sc = make_float2(scale_of((signed char)(e & 255)), scale_of((signed char)(e >> 8)));
-        }
-      }
-      if (n >= 2 && !await_warp(cta, cta.bar(S_FULL + s), ((n >> 1) - 1) & 1, ctl)) return false;
-      if (!t.fresh) put(w, base + OFF_K + s * K_BYTES, 6, 0, K_BOX, 4, sc.x);
-      mbar_arrive(cta.bar(K_CODES + s));
-      if (!t.fresh) load(w, c.v, 12, 6);
-      if (n >= 2 && !await_warp(cta, cta.bar(O_DONE + s), ((n >> 1) - 1) & 1, ctl)) return false;
-      if (!t.fresh) {
-        put(w2, base + OFF_V + s * V_BYTES, 12, 0, V_BOX, 8, sc.y);
-        put(w, base + OFF_V + s * V_BYTES, 12, 6, V_BOX, 8, sc.y);
-      }
-      mbar_arrive(cta.bar(V_CODES + s));
-      ++n;
-      return true;
+    // Codes: rows 32 q4 .. + 31 of each tile by this warp.
+    [[maybe_unused]] int raw = 0, exps = 0;  // tiles of codes so far; the next tile's exponents
+    [[maybe_unused]] bool codes_next = false;
+    [[maybe_unused]] Walk at{0, 0};
+    [[maybe_unused]] auto look = [&]() {
+      if (at.x >= n_items) return;
+      const Tile t = tile_of(items[at.x], at.i);
+      codes_next = !t.fresh;
+      exps = exponents(items[at.x], t, a.cache, q4, lane);
     };
-    [[maybe_unused]] int fx = 0, fi = n_items ? items[0].tb : 0;  // the next tile to fill
+    if constexpr (CODES) {
+      at.begin(items, n_items);
+      look();
+    }
     // Fills up to tile `stop` of item `upto`.
     [[maybe_unused]] auto fill_to = [&](int upto, int stop) -> bool {
-      while (fx < n_items && fx <= upto) {
-        const int end = fx < upto ? items[fx].te : min(stop, items[fx].te);
-        for (; fi < end; ++fi)
-          if (!fill(items[fx], fi)) return false;
-        if (fx == upto) break;
-        if (++fx < n_items) fi = items[fx].tb;
+      while (at.x < n_items && (at.x < upto || (at.x == upto && at.i < stop))) {
+        const uint32_t s = n & 1;
+        const bool codes = codes_next;
+        asm volatile("" : "+r"(exps));  // (not taken apart where it is loaded, a tile ahead)
+        const int ek = (signed char)(exps & 255), ev = (signed char)(exps >> 8);
+        const float sk = ek < -126 ? 0.f : pow2(ek), sv = ev < -126 ? 0.f : pow2(ev);
+        at.step(items, n_items);
+        look();
+        if (n >= 2 && !await_warp(cta, cta.bar(S_FULL + s), ((n >> 1) - 1) & 1, ctl)) return false;
+        if (codes) {
+          if (!await_warp(cta, cta.bar(RAW), raw & 1, ctl)) return false;
+          put_rows<T, 2, K_BOX>(base + L::RAWS, base + L::K + s * K_BYTES, sk, 32 * q4);
+          mbar_arrive(cta.bar(RAW_FREE));
+        }
+        mbar_arrive(cta.bar(K_CODES + s));
+        if (n >= 2 && !await_warp(cta, cta.bar(O_DONE + s), ((n >> 1) - 1) & 1, ctl)) return false;
+        if (codes) {
+          if (!await_warp(cta, cta.bar(RAW + 1), raw & 1, ctl)) return false;
+          put_rows<T, 4, V_BOX>(base + L::RAWS + RAW_K, base + L::V + s * V_BYTES, sv, 32 * q4);
+          mbar_arrive(cta.bar(RAW_FREE + 1));
+          ++raw;
+        }
+        mbar_arrive(cta.bar(V_CODES + s));
+        ++n;
       }
       return true;
     };
@@ -760,10 +833,8 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
       const bool live_item = it.tb < it.te;
       if constexpr (CODES) {
         // all of this item's tiles, and the first two of the next one that has any
-        int next = x + 1;
-        while (next < n_items && items[next].tb == items[next].te) ++next;
         if (!(ok = fill_to(x, it.te))) break;
-        if (next < n_items && !(ok = fill_to(next, items[next].tb + 2))) break;
+        if (at.x < n_items && !(ok = fill_to(at.x, items[at.x].tb + 2))) break;
       }
       float ref = -INFINITY, sum = 0.f;
       if (live_item) {
@@ -793,48 +864,77 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
       }
       if (live_item) {
         const bool awake = 32 * q4 < rows;
-        // 32 rows of 128 bytes at a time go through shared memory, so that eight lanes write a row
-#pragma unroll 1
-        for (int k = 0; k < kDV / (2 * CB); ++k) {
-          if (awake) {
-            __syncwarp();
+        // 32 rows of SR bytes at a time go through shared memory, so that LPR lanes write a row
+        auto stage = [&](int e, const uint32_t (&w)[16]) {  // 64 bytes of this lane's row
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t o[CB];
-              if constexpr (WIDE) tmem_ld16(trow + TM_O + CB * (2 * k + e), o);
-              else tmem_ld32(trow + TM_O + CB * (2 * k + e), o);
-              tmem_wait_ld();
+          for (int ch = 0; ch < 4; ++ch)
+            *(uint4*)(stg + swz_off(lane, 4 * e + ch, SR)) =
+                make_uint4(w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+        };
+        auto emit = [&](int k) {  // channels SUBS CB k ..
+          __syncwarp();
 #pragma unroll
-              for (int ch = 0; ch < 4; ++ch) {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  if constexpr (WIDE) {
-                    w[j] = __float_as_uint(__uint_as_float(o[4 * ch + j]) * inv);
-                  } else {
-                    const float lo = __uint_as_float(o[8 * ch + 2 * j]) * inv;
-                    const float hi = __uint_as_float(o[8 * ch + 2 * j + 1]) * inv;
-                    w[j] = pack2<TO>(lo, hi);
-                  }
-                }
-                *(uint4*)(stg + swz_off(lane, 4 * e + ch, 128)) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
+          for (int ch = 0; ch < LPR; ++ch) {
+            const int r = 32 / LPR * ch + lane / LPR, rr = 32 * q4 + r;
+            const uint4 y = *(const uint4*)(stg + swz_off(r, lane % LPR, SR));
+            if (rr < rows) {
+              // row rr's token and head: rr / G by a product, exact for rr, G <= 128
+              const int to = SPLIT ? rr : rr + (int)((uint32_t)rr * by_G >> 16) * (a.H - G);
+              reinterpret_cast<uint4*>(out + (long long)to * kDV + SUBS * CB * k)[lane % LPR] = y;
             }
           }
-          if (k == kDV / (2 * CB) - 1) {
-            tc_fence_before();
-            mbar_arrive(cta.bar(O_FREE));
-          }
-          if (awake) {
-            __syncwarp();
+          __syncwarp();
+        };
+        if constexpr (WIDE) {
+#pragma unroll 1
+          for (int k = 0; k < kDV / (SUBS * CB); ++k) {
+            if (awake)
 #pragma unroll
-            for (int ch = 0; ch < 8; ++ch) {
-              const int r = 4 * ch + (lane >> 3), rr = 32 * q4 + r;
-              const uint4 y = *(const uint4*)(stg + swz_off(r, lane & 7, 128));
-              if (rr < rows) {
-                const long long to = SPLIT ? rr : (long long)(rr / G) * a.H + rr % G;
-                reinterpret_cast<uint4*>(out + to * kDV + 2 * CB * k)[lane & 7] = y;
+              for (int e = 0; e < SUBS; ++e) {
+                uint32_t o[16];
+                tmem_ld16(trow + TM_O + CB * (SUBS * k + e), o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
+                stage(e, o);
               }
+            if (k == kDV / (SUBS * CB) - 1) {
+              tc_fence_before();
+              mbar_arrive(cta.bar(O_FREE));
+            }
+            if (awake) emit(k);
+          }
+        } else {
+          // all of the row is read and rounded before any of it is written, so that the next item's products
+          // wait less: blocks of 32 channels, the last ones to the staging, the others in registers
+          constexpr int HOLD = kDV / CB - SUBS;
+          uint32_t w[HOLD][16], last[16];
+          auto rounded = [&](int blk, uint32_t (&y)[16]) {
+            uint32_t o[32];
+            tmem_ld32(trow + TM_O + CB * blk, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              y[j] = pack2<TO>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+          };
+          if (awake) {
+#pragma unroll
+            for (int e = 0; e < SUBS; ++e) {
+              rounded(HOLD + e, last);
+              stage(e, last);
+            }
+#pragma unroll
+            for (int k = 0; k < HOLD; ++k) rounded(k, w[k]);
+          }
+          tc_fence_before();
+          mbar_arrive(cta.bar(O_FREE));
+          if (awake) {
+            emit(HOLD / SUBS);
+#pragma unroll
+            for (int k = 0; k < HOLD / SUBS; ++k) {
+#pragma unroll
+              for (int e = 0; e < SUBS; ++e) stage(e, w[SUBS * k + e]);
+              emit(k);
             }
           }
         }
@@ -905,9 +1005,9 @@ template <class T, class TO, bool CODES, bool SPLIT>
 cudaError_t launch(const Maps& maps, const ChunkArgs& a, const Plan& plan, DevCtl ctl,
                    cudaStream_t stream) {
   auto kern = window_chunk_kernel<T, TO, CODES, SPLIT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<CODES>::BYTES);
   if (e != cudaSuccess) return e;
-  kern<<<plan.grid, THREADS, SMEM_BYTES, stream>>>(maps, a, plan, ctl);
+  kern<<<plan.grid, THREADS, Layout<CODES>::BYTES, stream>>>(maps, a, plan, ctl);
   return cudaGetLastError();
 }
 
@@ -922,16 +1022,18 @@ cudaError_t run(const ChunkArgs& a, const Plan& plan, DevCtl ctl, cudaStream_t s
   bool ok = make_map(&m.q, a.q, type, 2, kDK, a.H, N, 1, 32, G, plan.per, CU_TENSOR_MAP_SWIZZLE_64B) &&
             make_map(&m.k, a.k, type, 2, kDK, c.KV, N, 1, 32, 1, BN, CU_TENSOR_MAP_SWIZZLE_64B) &&
             make_map(&m.v, a.v, type, 2, kDV, c.KV, N, 1, 64, 1, BN, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (CODES)
-    ok = ok &&
-         make_map(&m.pk, c.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kDK, c.KV, slots, pages, kDK, 1, BN,
-                  CU_TENSOR_MAP_SWIZZLE_NONE) &&
-         make_map(&m.pv, c.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kDV, c.KV, slots, pages, kDV, 1, BN,
-                  CU_TENSOR_MAP_SWIZZLE_NONE);
-  else
+  const auto row = CODES ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type;
+  const int size = CODES ? 1 : 2;
+  ok = ok && make_map(&m.fk, c.k, row, size, kDK, c.KV, slots, pages, kDK, 1, BN, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+       make_map(&m.fv, c.v, row, size, kDV, c.KV, slots, pages, kDV, 1, BN, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (CODES) {
+    m.pk = m.fk;
+    m.pv = m.fv;
+  } else {
     ok = ok &&
          make_map(&m.pk, c.k, type, 2, kDK, c.KV, slots, pages, 32, 1, BN, CU_TENSOR_MAP_SWIZZLE_64B) &&
          make_map(&m.pv, c.v, type, 2, kDV, c.KV, slots, pages, 64, 1, BN, CU_TENSOR_MAP_SWIZZLE_128B);
+  }
   if (!ok) return cudaErrorInvalidValue;
   if (plan.parts > 1) return launch<T, float, CODES, true>(m, a, plan, ctl, stream);
   if (a.out_type == GLA_FP32) return launch<T, float, CODES, false>(m, a, plan, ctl, stream);
