@@ -53,11 +53,11 @@ struct alignas(16) Item {
   int d1, d2, d3, d4;
   int w[8];                       // whole tiles, which every row sees: w[0] .. w[1]-1, w[2] .., w[4] .., w[6] ..
   int row0, i0, n_tok, tokens;    // first packed row; its index and count in the sequence's new tokens
-  int pos, page, kv, unit;        // page and layer; (tile, key head): where its partial results go
+  int pos, page, kv, sink;        // page and layer
   int tb, te;                     // tiles tb .. te-1 are this part's
   int ns, a_lo, a_hi, b_lo, base; // slots seen: 0 .. ns-1, a_lo .. a_hi-1, b_lo .. (all for the first row);
                                   // slot sink + r of the first ring run holds token base + r
-  int pad;
+  int slots;
 };
 static_assert(sizeof(Item) == 128, "whole 16-byte accesses");
 
@@ -125,7 +125,7 @@ __device__ __forceinline__ int ceil_tiles(int n) { return n <= 0 ? 0 : (n - 1) /
 
 // Item of tokens i0 .. of a sequence, part `part` of `parts`.
 static __device__ __noinline__ void make_item(Item& it, const WindowCache& c, const Sequence& s, int per, int i0,
-                                       int kv, int unit, int part, int parts) {
+                                       int kv, int part, int parts) {
   it.i0 = i0;
   it.n_tok = min(per, s.tokens - i0);
   it.row0 = s.first + i0;
@@ -133,8 +133,9 @@ static __device__ __noinline__ void make_item(Item& it, const WindowCache& c, co
   it.pos = s.pos;
   it.page = s.page * c.pool_layers + c.layer;
   it.kv = kv;
-  it.unit = unit;
-  const int slots = c.window + c.sink, p0 = s.pos + i0, i1 = i0 + it.n_tok;
+  it.sink = c.sink;
+  it.slots = c.window + c.sink;
+  const int slots = it.slots, p0 = s.pos + i0, i1 = i0 + it.n_tok;
   const int ns = min(c.sink, s.pos);
   int a_lo = 0, a_hi = 0, b_lo = slots, base = 0;
   int a_all = 0, b_all = slots;   // from where the last row sees
@@ -187,45 +188,67 @@ static __device__ __noinline__ void make_item(Item& it, const WindowCache& c, co
   it.te = (int)(n * (part + 1) / parts);
 }
 
+// What the roles ask of an item's tiles.  With codes, out of line (Ask<true>): every role asks, and with the
+// conversion of codes their code no longer shares the instruction cache (192 us inlined, 159 not); without,
+// inlined (Ask<false>: 103 us, 110 not).
 struct Tile {
-  bool fresh;   // of the new tokens
-  bool whole;   // all rows see all its columns
-  int s0;       // first slot, or first of the sequence's new tokens
+  int s0;         // first slot, or first of the sequence's new tokens
+  unsigned bits;
+  __device__ __forceinline__ bool fresh() const { return bits & 1; }  // of the new tokens
+  __device__ __forceinline__ bool whole() const { return bits & 2; }  // all rows see all its columns
 };
-__device__ __forceinline__ Tile tile_of(const Item& it, int i) {
+__device__ __forceinline__ Tile tile_inline(const Item& it, int i) {
   const int4 n = *reinterpret_cast<const int4*>(&it.n0), d = *reinterpret_cast<const int4*>(&it.d1);
   const int4 u = *reinterpret_cast<const int4*>(it.w), v = *reinterpret_cast<const int4*>(it.w + 4);
   Tile t;
-  t.fresh = i >= n.z;
   t.s0 = BN * (i + (i < n.x ? 0 : i < n.y ? d.x : i < n.z ? d.y : i < n.w ? d.z : d.w));
-  t.whole = (i >= u.x && i < u.y) || (i >= u.z && i < u.w) || (i >= v.x && i < v.y) || (i >= v.z && i < v.w);
+  const bool whole = (i >= u.x && i < u.y) || (i >= u.z && i < u.w) || (i >= v.x && i < v.y) ||
+                     (i >= v.z && i < v.w);
+  t.bits = (i >= n.z ? 1 : 0) | (whole ? 2 : 0);
   return t;
 }
 // Columns of tile i that some row may see, rounded to 16.
-__device__ __forceinline__ int cols_of(const Item& it, const WindowCache& c, const Tile& t, int i) {
-  if (t.whole) return BN;
+__device__ __forceinline__ int cols_inline(const Item& it, Tile t, int i) {
+  if (t.whole()) return BN;
   int end;
-  if (t.fresh) {
+  if (t.fresh()) {
     end = it.i0 + it.n_tok;
-    if (i < it.nf) end = min(c.sink - it.pos, end);
+    if (i < it.nf) end = min(it.sink - it.pos, end);
   } else {
-    const int slots = c.window + c.sink;
     end = it.ns;
     if (it.a_lo < min(it.a_hi, t.s0 + BN)) end = max(end, it.a_hi);
-    if (it.b_lo < min(slots, t.s0 + BN)) end = slots;
+    if (it.b_lo < min(it.slots, t.s0 + BN)) end = it.slots;
   }
   return min(BN, (end - t.s0 + 15) & ~15);
 }
 // The columns c0 .. c0 + 31 of a tile that token i of the sequence's new ones sees.
-__device__ __forceinline__ uint32_t columns_seen(const Item& it, const WindowCache& c, bool fresh, int i,
-                                                 int c0) {
-  if (fresh) return keys_seen(i, c0, it.tokens, c.window, max(c.sink - it.pos, 0));
-  const int x = it.pos - it.base + i - c.window + 1, slots = c.window + c.sink;
-  return bits_to(it.ns - 1 - c0) | (bits_to(it.a_hi - 1 - c0) & ~bits_to(c.sink + max(0, x) - 1 - c0)) |
-         (it.base > c.sink && it.a_hi > 0
-              ? bits_to(slots - 1 - c0) & ~bits_to(max(it.a_hi, c.sink + x + c.window) - 1 - c0)
+__device__ __forceinline__ uint32_t seen_inline(const Item& it, bool fresh, int i, int c0) {
+  const int window = it.slots - it.sink;
+  if (fresh) return keys_seen(i, c0, it.tokens, window, max(it.sink - it.pos, 0));
+  const int x = it.pos - it.base + i - window + 1;
+  return bits_to(it.ns - 1 - c0) | (bits_to(it.a_hi - 1 - c0) & ~bits_to(it.sink + max(0, x) - 1 - c0)) |
+         (it.base > it.sink && it.a_hi > 0
+              ? bits_to(it.slots - 1 - c0) & ~bits_to(max(it.a_hi, it.sink + x + window) - 1 - c0)
               : 0u);
 }
+
+static __device__ __noinline__ Tile tile_call(const Item& it, int i) { return tile_inline(it, i); }
+static __device__ __noinline__ int cols_call(const Item& it, Tile t, int i) { return cols_inline(it, t, i); }
+static __device__ __noinline__ uint32_t seen_call(const Item& it, bool fresh, int i, int c0) {
+  return seen_inline(it, fresh, i, c0);
+}
+template <bool CALL>
+struct Ask {
+  static __device__ __forceinline__ Tile tile(const Item& it, int i) {
+    return CALL ? tile_call(it, i) : tile_inline(it, i);
+  }
+  static __device__ __forceinline__ int cols(const Item& it, Tile t, int i) {
+    return CALL ? cols_call(it, t, i) : cols_inline(it, t, i);
+  }
+  static __device__ __forceinline__ uint32_t seen(const Item& it, bool fresh, int i, int c0) {
+    return CALL ? seen_call(it, fresh, i, c0) : seen_inline(it, fresh, i, c0);
+  }
+};
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -325,7 +348,7 @@ __device__ __forceinline__ int exponents(const Item& it, const Tile& t, const Se
                                          int lane) {
   const WindowCache& c = cache.c;
   const int slots = c.window + c.sink, slot = t.s0 + 32 * q4 + lane;
-  if (t.fresh || slot >= min(it.pos, slots)) return 0x8080;
+  if (t.fresh() || slot >= min(it.pos, slots)) return 0x8080;
   return __ldg(reinterpret_cast<const unsigned short*>(cache.exps) +
                ((long long)it.page * c.KV + it.kv) * slots + slot);
 }
@@ -346,8 +369,8 @@ struct Source {
   int row, outer;
   __device__ __forceinline__ Source(const Item& it, const Tile& t, const CUtensorMap* fresh,
                                     const CUtensorMap* page)
-      : map(t.fresh ? fresh : page),
-        row(t.fresh ? it.row0 - it.i0 + t.s0 : t.s0), outer(t.fresh ? 0 : it.page) {}
+      : map(t.fresh() ? fresh : page),
+        row(t.fresh() ? it.row0 - it.i0 + t.s0 : t.s0), outer(t.fresh() ? 0 : it.page) {}
 };
 
 template <class T, class TO, bool CODES, bool SPLIT>
@@ -436,7 +459,7 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
           left -= n;
           s = sequence(c, a.tok, ++b, ctl);
         }
-        make_item(items[tid], c, s, plan.per, left * plan.per, unit % KV, unit, part, plan.parts);
+        make_item(items[tid], c, s, plan.per, left * plan.per, unit % KV, part, plan.parts);
         atomicAdd((int*)(base + L::COUNT) + 1, items[tid].te - items[tid].tb);
         if (SPLIT && part == 0 && unit % KV == 0) {
           const Partials ps(a.workspace, plan.units, plan.parts);
@@ -471,8 +494,8 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
         const uint32_t qs = m++ % L::QS;
         for (int i = it.tb; i < it.te; ++i, ++n) {
           const uint32_t s = n & 1;
-          const Tile t = tile_of(it, i);
-          if (CODES && !t.fresh) {
+          const Tile t = Ask<CODES>::tile(it, i);
+          if (CODES && !t.fresh()) {
             // ahead of the stage, into the raw tile's place
             if (raw > 0 && !(ok = await(cta, cta.bar(RAW_FREE), (raw - 1) & 1, ctl))) break;
             ++raw;
@@ -491,9 +514,9 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
               tma_load_4d(cta.sb + L::Q + qs * K_BYTES + j * K_BOX, &maps.q, cta.bar(Q_FULL + qs),
                           32 * j, it.kv * G, it.row0, 0);
           }
-          info[n & 3] = cols_of(it, c, t, i) | (t.fresh ? INFO_FRESH : 0) | (i == it.tb ? INFO_FIRST : 0);
+          info[n & 3] = Ask<CODES>::cols(it, t, i) | (t.fresh() ? INFO_FRESH : 0) | (i == it.tb ? INFO_FIRST : 0);
           if (CODES) mbar_arrive(cta.bar(K_CODES + s));
-          if (CODES && !t.fresh) continue;
+          if (CODES && !t.fresh()) continue;
           const Source src(it, t, &maps.k, &maps.pk);
           armed |= 1u << s;
           turn.take(s);
@@ -527,13 +550,13 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
           const uint32_t s = n & 1;
           for (; ahead.x < n_items && an <= n + AHEAD; ++an, ahead.step(items, n_items)) {
             const Item& to = items[ahead.x];
-            const Tile t = tile_of(to, ahead.i);
-            if (t.fresh) continue;
+            const Tile t = Ask<CODES>::tile(to, ahead.i);
+            if (t.fresh()) continue;
             tma_prefetch_4d(&maps.fk, 0, to.kv, t.s0, to.page);
             tma_prefetch_4d(&maps.fv, 0, to.kv, t.s0, to.page);
           }
-          const Tile t = tile_of(it, i);
-          if (CODES && !t.fresh) {
+          const Tile t = Ask<CODES>::tile(it, i);
+          if (CODES && !t.fresh()) {
             if (raw > 0 && !(ok = await(cta, cta.bar(RAW_FREE + 1), (raw - 1) & 1, ctl))) break;
             ++raw;
             mbar_arrive_expect_tx(cta.bar(RAW + 1), RAW_V);
@@ -541,7 +564,7 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
           }
           if (n >= 2 && !(ok = await(cta, cta.bar(O_DONE + s), ((n >> 1) - 1) & 1, ctl))) break;
           if (CODES) mbar_arrive(cta.bar(V_CODES + s));
-          if (CODES && !t.fresh) continue;
+          if (CODES && !t.fresh()) continue;
           const Source src(it, t, &maps.v, &maps.pv);
           armed |= 1u << s;
           turn.take(s);
@@ -645,23 +668,23 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
       float ref = -INFINITY, sum = 0.f;  // this row's, as of the group's last tile
       for (int i = it.tb + ((n0 ^ g) & 1); i < it.te; i += 2) {
         const int n = n0 + i - it.tb;
-        const Tile t = tile_of(it, i);
+        const Tile t = Ask<CODES>::tile(it, i);
         // chunks of 32 columns that all rows of the warp see, and that some do: what its first and its
         // last row both see, those between do too; a chunk that neither sees, none does
         uint32_t full = awake ? 15u : 0u, some = full;
-        if (!t.whole && awake) {
-          const uint32_t see = columns_seen(it, c, t.fresh, ends, t.s0 + 32 * (lane & 3));
+        if (!t.whole() && awake) {
+          const uint32_t see = Ask<CODES>::seen(it, t.fresh(), ends, t.s0 + 32 * (lane & 3));
           full = __ballot_sync(0xffffffffu, see == ~0u);
           some = __ballot_sync(0xffffffffu, see != 0u);
           full = full & (full >> 4) & 15u;
           some = (some | (some >> 4)) & 15u;
         }
-        const int cols = cols_of(it, c, t, i);
+        const int cols = Ask<CODES>::cols(it, t, i);
         if (!(ok = await_warp(cta, cta.bar(S_FULL + g), (n >> 1) & 1, ctl))) break;
         tc_fence_after();
         const uint32_t ts = trow + TM_S + 128 * g;
         auto sees = [&](int j) -> uint32_t {
-          return live ? columns_seen(it, c, t.fresh, at, t.s0 + 32 * j) : 0u;
+          return live ? Ask<CODES>::seen(it, t.fresh(), at, t.s0 + 32 * j) : 0u;
         };
         auto hide = [&](uint32_t (&z)[32], int j) {  // the columns that this row does not see
           const uint32_t see = sees(j);
@@ -749,9 +772,9 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
         }
         // values behind the tokens of a page or a sequence may be anything, and 0 x NaN is NaN: zero
         // their rows (codes: the output warps did)
-        const int kept = t.fresh ? it.tokens - t.s0 : CODES ? BN : it.pos - t.s0;
+        const int kept = t.fresh() ? it.tokens - t.s0 : CODES ? BN : it.pos - t.s0;
         const uint32_t v_now = v_turn;
-        if (!CODES || t.fresh) v_turn ^= 1;
+        if (!CODES || t.fresh()) v_turn ^= 1;
         if (awake && kept < cols) {
           if (!(ok = await_warp(cta, cta.bar(V_FULL + g), v_now, ctl))) break;
           const int step = 32 * min((min(it.n_tok, plan.per) * G + 31) / 32, 4), cnt = (cols - kept) * 24;
@@ -790,8 +813,8 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
     [[maybe_unused]] Walk at{0, 0};
     [[maybe_unused]] auto look = [&]() {
       if (at.x >= n_items) return;
-      const Tile t = tile_of(items[at.x], at.i);
-      codes_next = !t.fresh;
+      const Tile t = Ask<CODES>::tile(items[at.x], at.i);
+      codes_next = !t.fresh();
       exps = exponents(items[at.x], t, a.cache, q4, lane);
     };
     if constexpr (CODES) {
@@ -885,17 +908,29 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
           }
           __syncwarp();
         };
-        if constexpr (WIDE) {
+        auto rounded = [&](int blk, uint32_t (&y)[16]) {  // 64 bytes of this lane's row
+          if constexpr (WIDE) {
+            tmem_ld16(trow + TM_O + CB * blk, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * inv);
+          } else {
+            uint32_t o[32];
+            tmem_ld32(trow + TM_O + CB * blk, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              y[j] = pack2<TO>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+          }
+        };
+        if constexpr (WIDE || CODES) {
 #pragma unroll 1
           for (int k = 0; k < kDV / (SUBS * CB); ++k) {
             if (awake)
 #pragma unroll
               for (int e = 0; e < SUBS; ++e) {
                 uint32_t o[16];
-                tmem_ld16(trow + TM_O + CB * (SUBS * k + e), o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
+                rounded(SUBS * k + e, o);
                 stage(e, o);
               }
             if (k == kDV / (SUBS * CB) - 1) {
@@ -909,14 +944,6 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
           // wait less: blocks of 32 channels, the last ones to the staging, the others in registers
           constexpr int HOLD = kDV / CB - SUBS;
           uint32_t w[HOLD][16], last[16];
-          auto rounded = [&](int blk, uint32_t (&y)[16]) {
-            uint32_t o[32];
-            tmem_ld32(trow + TM_O + CB * blk, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              y[j] = pack2<TO>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-          };
           if (awake) {
 #pragma unroll
             for (int e = 0; e < SUBS; ++e) {
