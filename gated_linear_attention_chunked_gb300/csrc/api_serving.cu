@@ -161,6 +161,8 @@ gla_status gla_window_attn8_decode_step(void* pool_k, void* pool_v, signed char*
   if (st != GLA_OK || (st = check_window_active(n_active, H, window, sink)) != GLA_OK ||
       (st = check_window_pool(n_pages, pool_layers, layer, window, sink, KV)) != GLA_OK)
     return st;
+  // (a page's bytes of a layer stay below 2^40, the largest step of a tensor map)
+  if ((window + (long long)sink) * KV > kMaxInt) return GLA_ERR_UNSUPPORTED;
   if (n_active == 0) return GLA_OK;
   if (!pool_k || !pool_v || !pool_e || !page || !pos || !q || !k || !v || !o)
     return GLA_ERR_INVALID_ARG;
@@ -189,12 +191,20 @@ static gla_status check_chunk(int n, int n_tokens, int H, int KV, int window, in
   return GLA_OK;
 }
 
+static size_t chunk_bytes(int n, int n_tokens, int H, int KV, int window, int sink, bool codes) {
+  return n == 0 || n_tokens == 0
+             ? 0
+             : gla::window_chunk_workspace_bytes(n, n_tokens, KV, H, window, sink, codes, sm_count());
+}
+
 size_t gla_window_attn_chunk_workspace_size(int n, int n_tokens, int H, int KV, int window,
                                             int sink) {
   if (check_window(GLA_BF16, GLA_BF16, window, sink, H, KV, gla::kDK, gla::kDV) != GLA_OK ||
-      check_chunk(n, n_tokens, H, KV, window, sink) != GLA_OK || n == 0 || n_tokens == 0)
+      check_chunk(n, n_tokens, H, KV, window, sink) != GLA_OK)
     return 0;
-  return gla::window_chunk_workspace_bytes(n, n_tokens, KV, H, window, sink, sm_count());
+  // enough for pages of either kind
+  return std::max(chunk_bytes(n, n_tokens, H, KV, window, sink, false),
+                  chunk_bytes(n, n_tokens, H, KV, window, sink, true));
 }
 
 gla_status gla_window_attn_chunk(const void* pool_k, const void* pool_v,
@@ -213,7 +223,7 @@ gla_status gla_window_attn_chunk(const void* pool_k, const void* pool_v,
     return GLA_ERR_INVALID_ARG;
   if (!aligned16(pool_k, pool_v, pool_e, q, k, v, o) || !aligned4(page, pos, start))
     return GLA_ERR_ALIGNMENT;
-  const size_t need = gla_window_attn_chunk_workspace_size(n, n_tokens, H, KV, window, sink);
+  const size_t need = chunk_bytes(n, n_tokens, H, KV, window, sink, pool_e != nullptr);
   if (need && (!workspace || workspace_bytes < need)) return GLA_ERR_WORKSPACE;
   if (need && !aligned256(workspace)) return GLA_ERR_ALIGNMENT;
   gla::DevCtl ctl;

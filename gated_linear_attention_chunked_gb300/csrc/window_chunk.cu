@@ -35,6 +35,13 @@ Plan make_plan(int n, int n_tokens, int KV, int H, int window, int sink, int n_s
   return p;
 }
 
+// Over pages of 8 bits, sequences of a few rows each go to warp-level products (window_rows8.cuh), which
+// turn a code into an operand in registers; here it goes through shared memory, and a tile of 128 rows is
+// mostly empty.
+bool is_short(int n, int n_tokens, int KV, int H) {
+  return (long long)n_tokens * (H / KV) <= 32ll * std::min(n, n_tokens);
+}
+
 template <class TO>
 cudaError_t join(const ChunkArgs& a, const Plan& plan, cudaStream_t stream) {
   const int rows = plan.per * (a.H / a.cache.c.KV);
@@ -45,13 +52,17 @@ cudaError_t join(const ChunkArgs& a, const Plan& plan, cudaStream_t stream) {
 }  // namespace
 
 size_t window_chunk_workspace_bytes(int n, int n_tokens, int KV, int H, int window, int sink,
-                                    int n_sm) {
+                                    bool codes, int n_sm) {
+  if (codes && is_short(n, n_tokens, KV, H))
+    return window_short8_workspace_bytes(n, n_tokens, KV, H, window + sink, n_sm);
   const Plan p = make_plan(n, n_tokens, KV, H, window, sink, n_sm);
   return p.parts > 1 ? Partials::bytes(p.units, p.parts) : 0;
 }
 
 cudaError_t launch_window_chunk(const ChunkArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream) {
   const WindowCache& c = a.cache.c;
+  if (a.cache.exps && is_short(c.n, a.tok.n_tokens, c.KV, a.H))
+    return launch_window_short8(a, n_sm, ctl, stream);
   const Plan plan = make_plan(c.n, a.tok.n_tokens, c.KV, a.H, c.window, c.sink, n_sm);
   cudaError_t e;
   if (a.cache.exps) e = launch8(a, plan, ctl, stream);

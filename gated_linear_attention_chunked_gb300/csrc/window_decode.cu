@@ -26,15 +26,20 @@
 #include <algorithm>
 #include <cmath>
 
-#include "window_parts.cuh"
+#include "window_common.cuh"
 
 namespace gla {
 namespace {
 
-constexpr int WARPS = 4, THREADS = 32 * WARPS, SB = 16, STAGES = 3, HB = kPartRows;
+constexpr int WARPS = 4, THREADS = 32 * WARPS, SB = 16, STAGES = 3, HB = 16;
 constexpr int STAGE = SB * (kDK + kDV) * 2;  // 9,216 bytes: a warp's tile of 16 slots
 constexpr int RING = WARPS * STAGES * STAGE;
 constexpr int SMEM = RING + HB * kDK * 2;
+
+// CTAs: a unit each for the first `whole` units, `parts` for each of the `cut` others.
+struct DecodePlan {
+  int whole, cut, parts, part_slots;
+};
 
 __device__ __forceinline__ int slot_of(int t, int window, int sink) {
   return t < sink ? t : sink + (t - sink) % window;
@@ -290,41 +295,40 @@ window_fill_kernel(WindowCache c, const uint4* __restrict__ k, const uint4* __re
   for (int x = lane; x < c.KV * kCV; x += 32) pv[x] = __ldg(v + src * kCV + x);
 }
 
-DecodePlan make_plan(int n, int KV, int H, int slots, int n_sm) {
-  return make_decode_plan((long long)n * KV * decode_groups(KV, H), slots, SB * WARPS, n_sm);
-}
+int groups_of(int KV, int H) { return (H / KV + HB - 1) / HB; }
 
-template <class TO>
-cudaError_t join(const WindowDecodeArgs& a, const DecodePlan& plan, cudaStream_t stream) {
-  const int groups = decode_groups(a.c.KV, a.H), rows = std::min(HB, a.H / a.c.KV);
-  PdlLaunch l(dim3((unsigned)(plan.cut * rows)), dim3(kDV / 2), 0, stream, true);
-  return cudaLaunchKernelEx(&l.cfg, window_join_kernel<TO>, a, plan, groups, rows);
+// Parts of at least one round of the warps' tiles (64 slots) each; nothing is cut where two do not
+// fit into the last round.
+DecodePlan make_plan(int n, int KV, int H, int slots, int n_sm) {
+  const long long units = (long long)n * KV * groups_of(KV, H);
+  const int hold = std::max(2 * n_sm, 1), unit = SB * WARPS, rest = (int)(units % hold);
+  const int most = std::min((slots + unit - 1) / unit, 64);
+  const int parts = rest ? std::min(hold / rest, most) : 1;
+  if (parts < 2) return DecodePlan{(int)units, 0, 1, 0};
+  const int part_slots = ((slots + parts - 1) / parts + unit - 1) / unit * unit;
+  return DecodePlan{(int)(units - rest), rest, parts, part_slots};
 }
 
 template <class T, class TO>
 cudaError_t run(const WindowDecodeArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream) {
   const int slots = a.c.window + a.c.sink, KV = a.c.KV;
   const DecodePlan plan = make_plan(a.c.n, KV, a.H, slots, n_sm);
-  const int groups = decode_groups(KV, a.H);
+  const int groups = groups_of(KV, a.H), rows = std::min(HB, a.H / KV);
   auto kern = window_decode_kernel<T, TO>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)(plan.whole + plan.cut * plan.parts), THREADS, SMEM, stream>>>(a, plan, groups,
                                                                                  ctl);
   if ((e = cudaGetLastError()) != cudaSuccess || !plan.cut) return e;
-  return join<TO>(a, plan, stream);
+  PdlLaunch l(dim3((unsigned)(plan.cut * rows)), dim3(kDV / 2), 0, stream, true);
+  return cudaLaunchKernelEx(&l.cfg, window_join_kernel<TO>, a, plan, groups, rows);
 }
 
 }  // namespace
 
 size_t window_decode_workspace_bytes(int n, int KV, int H, int slots, int n_sm) {
-  return decode_plan_bytes(make_plan(n, KV, H, slots, n_sm));
-}
-
-cudaError_t launch_window_join(const WindowDecodeArgs& a, const DecodePlan& plan,
-                               cudaStream_t stream) {
-  if (a.out_type == GLA_FP32) return join<float>(a, plan, stream);
-  return a.out_type == GLA_BF16 ? join<__nv_bfloat16>(a, plan, stream) : join<__half>(a, plan, stream);
+  const DecodePlan p = make_plan(n, KV, H, slots, n_sm);
+  return (size_t)p.cut * HB * p.parts * (kDV + 2) * sizeof(float);
 }
 
 cudaError_t launch_window_decode(const WindowDecodeArgs& a, int n_sm, DevCtl ctl,

@@ -55,9 +55,12 @@ struct ChunkArgs {
   int H;
   void* workspace;
 };
+// The same over 8-bit pages where sequences have a few rows (token, query head) each (window_decode8.cu).
+size_t window_short8_workspace_bytes(int n, int n_tokens, int KV, int H, int slots, int n_sm);
+cudaError_t launch_window_short8(const ChunkArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream);
 constexpr int kChunkMostHeads = 128;  // query heads on a key head
 size_t window_chunk_workspace_bytes(int n, int n_tokens, int KV, int H, int window, int sink,
-                                    int n_sm);
+                                    bool codes, int n_sm);
 cudaError_t launch_window_chunk(const ChunkArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream);
 
 }  // namespace gla
