@@ -4,16 +4,22 @@
 namespace gla {
 namespace {
 
+// Units have 8 rows where a sequence has no more (a second group of 8 would turn the page's codes into
+// operands again), else 16.
+int unit_rows(long long rows) { return rows <= 8 ? 8 : 16; }
+
 rows8::Plan decode_plan(int n, int KV, int H, int slots, int n_sm) {
-  const long long units = (long long)n * KV * ((H / KV + rows8::HB - 1) / rows8::HB);
-  return rows8::make_plan(units, units, slots, n_sm);
+  const int G = H / KV, rows = unit_rows(G);
+  const long long units = (long long)n * KV * ((G + rows - 1) / rows);
+  return rows8::make_plan(units, units, rows, slots, n_sm);
 }
 // Units of packed tokens: how the rows fall into sequences only the device knows.
 rows8::Plan short_plan(int n, int n_tokens, int KV, int H, int slots, int n_sm) {
-  const int G = H / KV, some = std::min(n, n_tokens), each = (n_tokens + some - 1) / some;
-  const long long most = ((long long)n_tokens * G / rows8::HB + some) * KV;
-  const long long likely = (long long)some * ((each * (long long)G + rows8::HB - 1) / rows8::HB) * KV;
-  return rows8::make_plan(most, std::min(likely, most), slots, n_sm);
+  const int some = std::min(n, n_tokens);
+  const long long each = (long long)((n_tokens + some - 1) / some) * (H / KV);  // rows
+  const int rows = unit_rows(each);
+  const long long most = ((long long)n_tokens * (H / KV) / rows + some) * KV;
+  return rows8::make_plan(most, std::min(some * ((each + rows - 1) / rows) * KV, most), rows, slots, n_sm);
 }
 
 }  // namespace

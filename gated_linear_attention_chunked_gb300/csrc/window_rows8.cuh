@@ -1,10 +1,9 @@
 // window_rows8.cuh -- the windowed attention of few new tokens per sequence over pages of 8 bits: one each
-// (the decode step) or a handful (drafts).  16 rows, (token, query head) of one key head, are a unit and the
-// rows of a warp-level tensor-core product; a CTA takes a unit, or a part of its page's slots, its four
-// warps walk the slots in tiles of 32 with rings of their own (TMA), running maxima and sums of their own,
-// and join them at the end.
+// (the decode step) or a handful (drafts).  8 NT rows, (token, query head) of one key head, are a unit; a
+// CTA takes a unit, or a part of its page's slots, in rounds of 128: its four warps take 32 slots each from a
+// ring that one thread's TMA fills, with running maxima and sums of their own, and join them at the end.
 //
-//   z = 2^e (q . c),  o = sum p 2^e c / sum p   with the rows' codes c as fp16 operands, exactly
+//   z = 2^e (c . q),  o = sum p 2^e c / sum p   with the rows' codes c as fp16 operands, exactly
 //
 // whatever the call's type: fp16 is a byte permute and a subtraction away from a code (0x6400 | u is 1024 +
 // u), bf16 twice as much.  Queries of bf16 are scaled by a power of two per row into fp16's range; the
@@ -12,10 +11,14 @@
 // by 2^-11 of itself or by 2^-25 of the weight of the page's largest row.  The new tokens' own keys and values are
 // taken as given, in the call's type, a tile of 16 at a time straight from global memory.
 //
-// Bound by HBM: 290 bytes a slot and key head, with 600 instructions a warp and tile; three CTAs an SM
-// hide the latencies of each other's begin and end.  Keys are read eight channels at a time, in an order of
-// the channels that the query's registers share; values by transposed loads of pairs of channels, which come
-// apart in the same permutes.
+// The codes are the products' first operand (16 slots by channels; 16 channels by slots), the rows their
+// columns, eight at a time: most calls have four or eight rows, and a row takes 24 registers of sums a
+// thread where as the first operand's it would take 48.  Keys are read eight channels at a time, in
+// an order of the channels that the query's registers share; values by transposed loads of pairs of
+// channels, which come apart in the permutes that make operands of them.  Weights go from the scores' layout
+// to an operand's by matrix transposes between the lanes.
+//
+// Bound by the instructions: a code costs 1.25 of them, and the floor is HBM's 290 bytes a slot and key head.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -29,12 +32,17 @@
 namespace gla {
 namespace rows8 {
 
-constexpr int WARPS = 4, THREADS = 32 * WARPS, SB = 32, STAGES = 2, HB = 16;
-constexpr int V_BOX = SB * 64, OFF_KEYS = 3 * V_BOX;  // a stage: values in 3 boxes of 64 channels, keys
-constexpr int STAGE = OFF_KEYS + SB * kDK;             // 9,216 bytes
-constexpr int RING = WARPS * STAGES * STAGE;
-constexpr int OFF_BAR = RING;                          // mbarrier [warp][stage]
-constexpr int SMEM = RING + WARPS * STAGES * 8 + 1024;
+constexpr int WARPS = 4, THREADS = 32 * WARPS, SB = 32, STAGES = 2;
+constexpr int ROUND = WARPS * SB;                        // slots of a stage, a tile of 32 for each warp
+constexpr int V_BOX = ROUND * 64, OFF_KEYS = 3 * V_BOX;  // values in 3 boxes of 64 channels, keys
+constexpr int STAGE = OFF_KEYS + ROUND * kDK;            // 36,864 bytes
+constexpr int RING = STAGES * STAGE;
+constexpr int JOIN_ROW = kDV + 4;                        // floats; the rows of a store in different banks
+constexpr int OFF_BAR = RING;                            // mbarrier [stage], int [stage]: warps done with it
+constexpr int OFF_FACTORS = OFF_BAR + STAGES * 16;       // float2 [warp][32]: a tile's 2^e
+constexpr int EXPS = 2 * SB + 16;                          // a tile's exponents, from a word's start
+constexpr int OFF_EXPS = OFF_FACTORS + WARPS * 32 * 8;     // [warp][stage]
+constexpr int SMEM = OFF_EXPS + WARPS * STAGES * EXPS + 1024;
 constexpr uint64_t DRAIN_NS = 4000000000ull;
 
 struct Args {
@@ -50,7 +58,7 @@ struct Args {
 // CTAs: a unit each for the first `whole` units, `parts` for each of the others.
 struct Plan {
   long long units;   // at most
-  int whole, parts, part_slots;
+  int whole, parts, part_slots, rows;  // rows of a unit: 8 or 16
 };
 struct Maps {
   CUtensorMap k, v;
@@ -66,7 +74,7 @@ __host__ __device__ inline size_t table_bytes(long long cut) {
 __host__ __device__ inline size_t workspace_bytes(const Plan& p) {
   const long long cut = p.units - p.whole;
   return p.parts > 1 && cut > 0
-             ? table_bytes(cut) + (size_t)cut * HB * p.parts * (kDV + 2) * sizeof(float)
+             ? table_bytes(cut) + (size_t)cut * p.rows * p.parts * (kDV + 2) * sizeof(float)
              : 0;
 }
 
@@ -92,15 +100,32 @@ struct Seen {
   }
 };
 
+// Four bytes global -> shared, of which `bytes` are read and the others zeros.
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // Codes as fp16 values of whole numbers: bytes 0, 1 and 2, 3, or (EVEN) 0, 2 and 1, 3.
 template <bool EVEN>
 __device__ __forceinline__ void whole16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   whole_of<__half, EVEN>(w, lo, hi);
 }
 
-template <class T, class TO>
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {  // 8 x 8 of 16 bits between the lanes
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <class T, class TO, int NT>
 __global__ void __launch_bounds__(THREADS, 3)
 rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
+  constexpr int HB = 8 * NT, NR = 2 * NT;  // rows of a unit, and those of a thread's scores
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ int found[4];
@@ -113,9 +138,11 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
   const int parts = cut < 0 ? 1 : plan.parts, part = cut < 0 ? 0 : cut % parts;
   const int part_slots = cut < 0 ? 1 << 30 : plan.part_slots;
   const int unit = cut < 0 ? (int)blockIdx.x : plan.whole + cut / parts;
-  const uint32_t bar = sm + OFF_BAR + w * STAGES * 8;
-  if (tid < WARPS * STAGES) {
-    mbar_init(sm + OFF_BAR + 8 * tid, 1);
+  const uint32_t bar = sm + OFF_BAR;
+  int* const passed = reinterpret_cast<int*>(smem + OFF_BAR + STAGES * 8);
+  if (tid < STAGES) {
+    mbar_init(bar + 8 * tid, 1);
+    passed[tid] = 0;
     fence_barrier_init();
   }
   if (tid == 0) {
@@ -133,6 +160,16 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     b = unit / groups / KV;
     s.first = b;
     s.tokens = 1;
+    {
+      // the token's rows, which are asked for one behind the other below: 128 bytes a thread
+      const T* q = static_cast<const T*>(a.q) + ((long long)b * a.H + kv * G + grp * HB) * kDK;
+      const int n = (min(HB, G - grp * HB) * kDK + 63) / 64;
+      if (tid < n) prefetch_l2(q + 64 * tid);
+      else if (tid >= 32 && tid < 35)
+        prefetch_l2(static_cast<const T*>(a.v) + ((long long)b * KV + kv) * kDV + 64 * (tid - 32));
+      else if (tid >= 64 && tid < 66)
+        prefetch_l2(static_cast<const T*>(a.k) + ((long long)b * KV + kv) * kDK + 64 * (tid - 64));
+    }
     s.pos = __ldg(a.tok.pos + b);
     s.page = __ldg(c.page + b);
     if (s.page < 0 || s.page >= c.n_pages || s.pos < 0) {
@@ -212,71 +249,90 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
   };
 
   const int tiles = hi > lo ? (hi - lo + SB * WARPS - 1) / (SB * WARPS) : 0;
-  auto first_slot = [&](int i) { return lo + (i * WARPS + w) * SB; };
+  auto first_slot = [&](int i) { return lo + i * ROUND + w * SB; };
   const signed char* pe = a.cache.exps + ((long long)page * KV + kv) * seen.slots * 2;
-  auto fetch = [&](int i) {  // warp w's tile i: slots lo + (i WARPS + w) SB ..
+  const int skew = (int)(reinterpret_cast<uintptr_t>(pe) & 2);
+  auto fetch = [&](int i) {  // round i, by one thread: slots lo + i ROUND ..
+    if (i >= tiles) return;
+    const uint32_t st = sm + i % STAGES * STAGE, full = bar + 8 * (i % STAGES);
+    mbar_arrive_expect_tx(full, STAGE);
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      tma_load_4d(st + j * V_BOX, &maps.v, full, 64 * j, kv, lo + i * ROUND, page);
+    tma_load_4d(st + OFF_KEYS, &maps.k, full, 0, kv, lo + i * ROUND, page);
+  };
+  auto fetch_exps = [&](int i) {  // of the warp's tile of round i
+    // exponents, two bytes a slot, in words: where the row starts in the middle of one, from there
     const int s0 = first_slot(i);
-    if (i < tiles && s0 < hi && lane == 0) {
-      const uint32_t st = sm + (w * STAGES + i % STAGES) * STAGE, full = bar + 8 * (i % STAGES);
-      mbar_arrive_expect_tx(full, STAGE);
-#pragma unroll
-      for (int j = 0; j < 3; ++j) tma_load_4d(st + j * V_BOX, &maps.v, full, 64 * j, kv, s0, page);
-      tma_load_4d(st + OFF_KEYS, &maps.k, full, 0, kv, s0, page);
+    if (i < tiles && s0 < hi && lane <= SB / 2) {
+      const long long from = 2ll * s0 - skew + 4 * lane;  // byte of the row
+      copy4(sm + OFF_EXPS + (w * STAGES + i % STAGES) * EXPS + 4 * lane,
+            pe + (from < 2ll * hi ? from : 2ll * s0 - skew), (int)min(max(2ll * hi - from, 0ll), 4ll));
     }
+    copy_commit();
   };
-  auto exponents = [&](int i) -> uint32_t {  // of slot `lane` of the tile, two bytes; 0x8080: none
-    const int slot = first_slot(i) + lane;
-    return i < tiles && slot < hi ? __ldg(reinterpret_cast<const unsigned short*>(pe) + slot) : 0x8080u;
-  };
+  if (tid == 0)
+    for (int i = 0; i < STAGES; ++i) fetch(i);
 #pragma unroll
-  for (int i = 0; i < STAGES; ++i) fetch(i);
-  uint32_t ex_next = exponents(0);
+  for (int i = 0; i < STAGES; ++i) fetch_exps(i);
 
-  // ---- queries: rows g and g + 8 (zeros behind the unit's); step 2 j + h of the product has channels
-  // 32 j + 8 t + 4 h .. + 3 of thread t of a row's four
+  // ---- queries: row 8 n + g of the unit's (the last one again behind them); step 2 j + h of the product
+  // has channels 32 j + 8 t + 4 h .. + 3 of thread t of a row's four
   const int g = lane >> 2, t = lane & 3, t2 = t * 2;
-  int at[2];  // the rows' positions
-  uint32_t qf[kDK / 16][4];
+  auto token = [&](int r) { return (grp * HB + min(r, rows - 1)) / G; };  // of row r
+  uint32_t qf[NT][kDK / 16][2];
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int R = grp * HB + min(g + 8 * r, rows - 1), i = R / G;
-    at[r] = s.pos + i;
+  for (int n = 0; n < NT; ++n) {
+    const int R = grp * HB + min(8 * n + g, rows - 1), i = R / G;
     const T* q = static_cast<const T*>(a.q) + ((long long)(s.first + i) * a.H + kv * G + R - i * G) * kDK;
 #pragma unroll
     for (int j = 0; j < kDK / 16; ++j) {
       const uint2 x = __ldg(reinterpret_cast<const uint2*>(q + 32 * (j >> 1) + 8 * t + 4 * (j & 1)));
-      qf[j][r] = x.x;
-      qf[j][2 + r] = x.y;
+      qf[n][j][0] = x.x;
+      qf[n][j][1] = x.y;
     }
   }
-  float acc[kDV / 8][4];
+  // A thread's scores are of slots g, g + 8 and rows 8 n + t2, + 1 (NR of them); its sums of channels
+  // 16 c + 2 g (0, 1) and + 1 (2, 3) and the same rows.
+  int at[NR];  // the rows' positions
 #pragma unroll
-  for (int j = 0; j < kDV / 8; ++j)
+  for (int r = 0; r < NR; ++r) at[r] = s.pos + token(8 * (r >> 1) + t2 + (r & 1));
+  float acc[kDV / 16][NT][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // base 2; l of this thread's columns
+  for (int j = 0; j < kDV / 16; ++j)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[j][n][k] = 0.f;
+  float m[NR], l[NR];  // base 2; l of this thread's slots
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+  }
   int e_ref = 0;  // acc is in units of 2^e_ref (-60 at least: what is below 2^-78 in a page is lost)
 
-  // The maxima of a tile's scores (base 2) over the quad; o and the sums go to a new reference only
-  // when one passes the old by more than 8 (weights of up to 2^8 lose nothing in fp16).
-  auto refer = [&](float (&top)[2]) {
+  // The maxima of a tile's scores (base 2) over its slots; o and the sums go to a new reference only when
+  // one passes the old by more than 8 (weights of up to 2^8 lose nothing in fp16).
+  auto refer = [&](float (&top)[NR]) {
     bool up = false;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      top[r] = quad_max(top[r]);
+    for (int r = 0; r < NR; ++r) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], d));
       up |= top[r] > m[r] + 8.f;
     }
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < NR; ++r) {
         const float now = top[r] > m[r] + 8.f ? top[r] : m[r];
         const float keep = now == m[r] || m[r] == -INFINITY ? 1.f : ex2(m[r] - now);
         m[r] = now;
         l[r] *= keep;
 #pragma unroll
-        for (int j = 0; j < kDV / 8; ++j) {
-          acc[j][2 * r] *= keep;
-          acc[j][2 * r + 1] *= keep;
+        for (int j = 0; j < kDV / 16; ++j) {
+          acc[j][r >> 1][r & 1] *= keep;
+          acc[j][r >> 1][2 + (r & 1)] *= keep;
         }
       }
     }
@@ -288,65 +344,69 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     const T* nk = static_cast<const T*>(a.k) + ((long long)s.first * KV + kv) * kDK;
     const T* nv = static_cast<const T*>(a.v) + ((long long)s.first * KV + kv) * kDV;
 #pragma unroll 1
-    for (int j0 = 16 * w; j0 <= i1; j0 += 16 * WARPS) {
+    for (int j0 = 16 * (WARPS - 1 - w); j0 <= i1; j0 += 16 * WARPS) {  // (the last warp has a tile less)
       if (j0 + 15 <= i0 - c.window && j0 >= sinks) continue;
-      float z[2][4];
+      float z[NT][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int tok = j0 + 8 * n + g;
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) z[n][j] = 0.f;
+        for (int k = 0; k < 4; ++k) z[n][k] = 0.f;
+      const bool in0 = j0 + g <= i1, in1 = j0 + g + 8 <= i1;
+      const T* key = nk + (long long)(j0 + g) * KV * kDK + 8 * t;
 #pragma unroll
-        for (int j = 0; j < kDK / 16; ++j) {
-          uint2 x = make_uint2(0u, 0u);
-          if (tok <= i1)
-            x = __ldg(reinterpret_cast<const uint2*>(nk + (long long)tok * KV * kDK + 32 * (j >> 1) +
-                                                     8 * t + 4 * (j & 1)));
-          mma16816<T>(z[n], qf[j], x.x, x.y);
-        }
+      for (int j = 0; j < kDK / 16; ++j) {
+        uint2 x = make_uint2(0u, 0u), y = x;
+        if (in0) x = __ldg(reinterpret_cast<const uint2*>(key + 32 * (j >> 1) + 4 * (j & 1)));
+        if (in1)
+          y = __ldg(reinterpret_cast<const uint2*>(key + 8ll * KV * kDK + 32 * (j >> 1) + 4 * (j & 1)));
+        const uint32_t x4[4] = {x.x, y.x, x.y, y.y};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816<T>(z[n], x4, qf[n][j][0], qf[n][j][1]);
       }
-      float top[2] = {-INFINITY, -INFINITY};
+      float top[NR];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t see = keys_seen(at[r] - s.pos, j0, i1 + 1, c.window, sinks);
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float& x = z[n][2 * r + j];
-            x = (see >> (8 * n + t2 + j)) & 1 ? x * kLog2e : -INFINITY;
-            top[r] = fmaxf(top[r], x);
-          }
+      for (int r = 0; r < NR; ++r) {
+        const uint32_t see = keys_seen(at[r] - s.pos, j0, i1 + 1, c.window, sinks) >> g;
+        float &z0 = z[r >> 1][r & 1], &z1 = z[r >> 1][2 + (r & 1)];
+        z0 = see & 1 ? z0 * kLog2e : -INFINITY;
+        z1 = (see >> 8) & 1 ? z1 * kLog2e : -INFINITY;
+        top[r] = fmaxf(z0, z1);
       }
       refer(top);
-      uint32_t pf[4];
+      uint32_t pf[NT][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float base = m[r] == -INFINITY ? 0.f : m[r];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float p0 = ex2(z[n][2 * r] - base), p1 = ex2(z[n][2 * r + 1] - base);
-          l[r] += p0 + p1;
-          pf[2 * n + r] = pack2<T>(p0, p1);
+        for (int k = 0; k < 2; ++k) {
+          float p[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = 2 * n + j;
+            p[j] = ex2(z[n][2 * k + j] - (m[r] == -INFINITY ? 0.f : m[r]));
+            l[r] += p[j];
+          }
+          pf[n][k] = transposed(pack2<T>(p[0], p[1]));
         }
-      }
       // channels 16 j + 2 g, + 1 of tokens t2, + 1 and + 8, + 9
+      const T* val = nv + (long long)(j0 + t2) * KV * kDV + 2 * g;
 #pragma unroll
       for (int j = 0; j < kDV / 16; ++j) {
         uint32_t x[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int tok = j0 + t2 + (n & 1) + 8 * (n >> 1);
-          x[n] = 0u;
-          if (tok <= i1)
-            x[n] = __ldg(reinterpret_cast<const uint32_t*>(nv + (long long)tok * KV * kDV + 16 * j + 2 * g));
+        for (int k = 0; k < 4; ++k) {
+          const int d = (k & 1) + 8 * (k >> 1);
+          x[k] = 0u;
+          if (j0 + t2 + d <= i1)
+            x[k] = __ldg(reinterpret_cast<const uint32_t*>(val + (long long)d * KV * kDV + 16 * j));
         }
-        mma16816<T>(acc[2 * j], pf, __byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
-        mma16816<T>(acc[2 * j + 1], pf, __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+        const uint32_t x4[4] = {__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                                __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[2], x[3], 0x7632)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816<T>(acc[j][n], x4, pf[n][0], pf[n][1]);
       }
     }
     // a single token's codes go into its slot, which it does not see
-    if (!a.tok.start && grp == 0 && w == WARPS - 1) {
+    if (!a.tok.start && grp == 0 && w == WARPS - 2) {
       uint4 x[3];
       uint2 o[3];
       const bool key = lane < 4, value = lane >= 8 && lane < 16;
@@ -370,149 +430,194 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
   }
 
   // ---- queries as fp16, scaled into its range by a power of two per row
-  float zs[2] = {kLog2e, kLog2e};
+  float zs[NR];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) zs[r] = 1.f;
   if constexpr (!__is_same(T, __half)) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int n = 0; n < NT; ++n) {
       uint32_t top = 0;
 #pragma unroll
-      for (int j = 0; j < kDK / 16; ++j) top = top2<T>(top, top2<T>(qf[j][r], qf[j][2 + r]));
+      for (int j = 0; j < kDK / 16; ++j) top = top2<T>(top, top2<T>(qf[n][j][0], qf[n][j][1]));
       top = top2<T>(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = top2<T>(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const float2 f = halves<T>(top);
       const int e = min(max((int)(__float_as_uint(fmaxf(f.x, f.y)) >> 23) - 127, -100), 100);
       const float down = pow2(-e);
-      zs[r] = pow2(e) * kLog2e;
 #pragma unroll
       for (int j = 0; j < kDK / 16; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float2 x = halves<T>(qf[j][2 * h + r]);
-          qf[j][2 * h + r] = pack2<__half>(x.x * down, x.y * down);
+          const float2 x = halves<T>(qf[n][j][h]);
+          qf[n][j][h] = pack2<__half>(x.x * down, x.y * down);
         }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) zs[2 * n + j] = pow2(__shfl_sync(0xffffffffu, e, 4 * (t2 + j)));
     }
   }
 
   // ---- the page
+  float2* const factors = reinterpret_cast<float2*>(smem + OFF_FACTORS) + 32 * w;
+  // where the lane's 16 bytes of a transposed load lie: chunks lane / 16, and + 2
+  const int row = lane & 15, swz = (row >> 1) & 3;
+  const uint32_t v_at[2] = {(uint32_t)(row * 64 + (((lane >> 4) ^ swz) << 4)),
+                            (uint32_t)(row * 64 + (((2 + (lane >> 4)) ^ swz) << 4))};
 #pragma unroll 1
   for (int i = 0; i < tiles; ++i) {
     const int s0 = first_slot(i);
-    if (s0 >= hi) break;  // (and so are the warp's later tiles)
-    const uint32_t ex = ex_next;
-    ex_next = exponents(i + 1);
+    if (s0 >= hi) break;  // (in the last round)
+    copy_wait<STAGES - 1>();
+    __syncwarp();
     if (!__all_sync(0xffffffffu, mbar_wait(bar + 8 * (i % STAGES), (i / STAGES) & 1, ctl))) {
       // the loads on their way land before the ring is used again and before the CTA may exit
-      for (int j = i; j < min(i + STAGES, tiles) && first_slot(j) < hi; ++j)
+      for (int j = i; j < min(i + STAGES, tiles); ++j)
         mbar_wait(bar + 8 * (j % STAGES), (j / STAGES) & 1, ctl, DRAIN_NS);
       break;
     }
-    const uint32_t so = (w * STAGES + i % STAGES) * STAGE;
-    const uint8_t* keys = smem + so + OFF_KEYS;
-    float z[4][4];
+    const uint32_t so = i % STAGES * STAGE + w * SB * 64;  // the warp's values, in the first box
+    const uint8_t* keys = smem + i % STAGES * STAGE + OFF_KEYS + w * SB * kDK;
+    float z[2][NT][4];  // slots 16 h + g, + 8
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {  // slots 8 n ..
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) z[n][j] = 0.f;
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < kDK / 32; ++j) {
-        const uint2 x = *reinterpret_cast<const uint2*>(keys + (8 * n + g) * kDK + 32 * j + 8 * t);
-        uint32_t b0, b1;
-        whole16<false>(x.x, b0, b1);
-        mma16816<__half>(z[n], qf[2 * j], b0, b1);
-        whole16<false>(x.y, b0, b1);
-        mma16816<__half>(z[n], qf[2 * j + 1], b0, b1);
+        for (int k = 0; k < 4; ++k) z[h][n][k] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kDK / 32; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint2 x = *reinterpret_cast<const uint2*>(keys + (16 * h + g) * kDK + 32 * j + 8 * t);
+        const uint2 y = *reinterpret_cast<const uint2*>(keys + (16 * h + 8 + g) * kDK + 32 * j + 8 * t);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t x4[4];
+          whole16<false>(k ? x.y : x.x, x4[0], x4[2]);
+          whole16<false>(k ? y.y : y.x, x4[1], x4[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma16816<__half>(z[h][n], x4, qf[n][2 * j + k][0], qf[n][2 * j + k][1]);
+        }
       }
-    }
     // the largest exponent of the values that are seen so far: o in its units.  (The first row sees what any
     // does.  A slot that none sees may be written meanwhile.)
-    uint32_t see[2] = {~0u, ~0u};
-    int e_top = (int)(signed char)(ex >> 8);
-    if (!whole(s0)) {
-      const uint32_t there = bits_to(hi - 1 - s0);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) see[r] = seen.bits(at[r], s0) & there;
-      if (!((seen.bits(s.pos + i0, s0) >> lane) & 1)) e_top = -128;
-    }
-    e_top = max(__reduce_max_sync(0xffffffffu, e_top), -60);
+    const bool all = whole(s0);
+    const char2 ex = reinterpret_cast<const char2*>(smem + OFF_EXPS + (w * STAGES + i % STAGES) * EXPS +
+                                                    skew)[lane];
+    int ev = (signed char)ex.y;
+    if (!all && !((seen.bits(s.pos + i0, s0) >> lane) & 1)) ev = -128;
+    const int e_top = max(__reduce_max_sync(0xffffffffu, ev), -60);
     if (e_top > e_ref || i == 0) {
       const float f = pow2(max(e_ref - e_top, -126));
       e_ref = e_top;
       if (i > 0 || part == 0)
 #pragma unroll
-        for (int j = 0; j < kDV / 8; ++j)
+        for (int j = 0; j < kDV / 16; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[j][k] *= f;
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[j][n][k] *= f;
     }
-    // this thread's columns: slots 8 n + t2, + 1
-    float sv[4][2], top[2] = {-INFINITY, -INFINITY};
+    // factors of slot `lane`, and then of this thread's, 8 k + g
+    factors[lane] = make_float2(scale_of((signed char)ex.x) * kLog2e, pow2(max(ev - e_ref, -126)));
+    __syncwarp();
+    float2 f[4];
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+    for (int k = 0; k < 4; ++k) f[k] = factors[8 * k + g];
+    float top[NR];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t e = __shfl_sync(0xffffffffu, ex, 8 * n + t2 + j);
-        const float sk = scale_of((signed char)(e & 255));
-        sv[n][j] = pow2(max((int)(signed char)(e >> 8) - e_ref, -126));
+    for (int r = 0; r < NR; ++r) top[r] = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float& x = z[n][2 * r + j];
-          x = (see[r] >> (8 * n + t2 + j)) & 1 ? x * (sk * zs[r]) : -INFINITY;
-          top[r] = fmaxf(top[r], x);
-        }
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) z[k >> 1][r >> 1][2 * (k & 1) + (r & 1)] *= f[k].x;
+    if (!all) {
+      const uint32_t there = bits_to(hi - 1 - s0);
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const uint32_t see = (seen.bits(at[r], s0) & there) >> g;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (!((see >> (8 * k)) & 1)) z[k >> 1][r >> 1][2 * (k & 1) + (r & 1)] = -INFINITY;
       }
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top[r] = fmaxf(top[r], z[k >> 1][r >> 1][2 * (k & 1) + (r & 1)]);
+      top[r] *= zs[r];
+    }
     refer(top);
-    uint32_t pf[2][4];
+    uint32_t pf[2][NT][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float base = m[r] == -INFINITY ? 0.f : m[r];
+    for (int n = 0; n < NT; ++n) {
+      float base[2];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float p0 = ex2(z[n][2 * r] - base), p1 = ex2(z[n][2 * r + 1] - base);
-        l[r] += p0 + p1;
-        pf[n >> 1][2 * (n & 1) + r] = pack2<__half>(p0 * sv[n][0], p1 * sv[n][1]);
+      for (int j = 0; j < 2; ++j) base[j] = m[2 * n + j] == -INFINITY ? 0.f : m[2 * n + j];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float p[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          p[j] = ex2(fmaf(z[k >> 1][n][2 * (k & 1) + j], zs[2 * n + j], -base[j]));
+          l[2 * n + j] += p[j];
+        }
+        pf[k >> 1][n][k & 1] = transposed(pack2<__half>(p[0] * f[k].y, p[1] * f[k].y));
       }
     }
+    // codes of slots 16 h + t2, + 1 (x[0]) and + 8, + 9 (x[1]), channels 16 ch + 2 g, + 1; x[2], x[3]:
+    // channels 16 ch + 16 + ..; a row's chunks are swizzled by row / 2 & 3, the same for both h
 #pragma unroll
     for (int h = 0; h < 2; ++h)  // slots 16 h ..
 #pragma unroll
       for (int ch = 0; ch < kDV / 16; ch += 2) {
-        // codes of slots 16 h + t2, + 1 (x[0]) and + 8, + 9 (x[1]), channels 16 ch + 2 g, + 1; x[2],
-        // x[3]: channels 16 ch + 16 + ..
-        const int row = 16 * h + (lane & 15), cc = ch + (lane >> 4);
         uint32_t x[4];
-        ldsm4t(x, sm + so + (cc >> 2) * V_BOX + row * 64 + (((cc & 3) ^ ((row >> 1) & 3)) << 4));
+        ldsm4t(x, sm + so + (ch & 2 ? v_at[1] : v_at[0]) + (ch >> 2) * V_BOX + h * 1024);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          uint32_t e0, o0, e1, o1;
-          whole16<true>(x[2 * y], e0, o0);
-          whole16<true>(x[2 * y + 1], e1, o1);
-          mma16816<__half>(acc[2 * (ch + y)], pf[h], e0, e1);
-          mma16816<__half>(acc[2 * (ch + y) + 1], pf[h], o0, o1);
+          uint32_t x4[4];
+          whole16<true>(x[2 * y], x4[0], x4[1]);
+          whole16<true>(x[2 * y + 1], x4[2], x4[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816<__half>(acc[ch + y][n], x4, pf[h][n][0], pf[h][n][1]);
         }
       }
-    __syncwarp();  // the stage is free for the copy of the next round
-    fetch(i + STAGES);
+    // the warp that is the last to leave the stage has it filled again: one thread's loads for all four (by
+    // each warp for itself they take 1,000 of a tile's 4,000 cycles)
+    __syncwarp();
+    fetch_exps(i + STAGES);
+    if (lane == 0) {
+      __threadfence_block();
+      if (atomicAdd(passed + i % STAGES, 1) == WARPS - 1) {
+        passed[i % STAGES] = 0;
+        fence_proxy_async();
+        fetch(i + STAGES);
+      }
+    }
+    __syncwarp();
   }
+  copy_wait<0>();
   __syncthreads();
 
   // ---- join the warps: o, m and l of each row through shared memory
-  float* so = reinterpret_cast<float*>(smem);              // [WARPS][HB][kDV]
-  float* sml = so + WARPS * HB * kDV;                      // [WARPS][HB][2]
-  static_assert(WARPS * HB * (kDV + 2) * 4 <= RING, "the join fits the ring");
+  float* so = reinterpret_cast<float*>(smem);              // [WARPS][HB][JOIN_ROW]
+  float* sml = so + WARPS * HB * JOIN_ROW;                 // [WARPS][HB][2]
+  static_assert(WARPS * HB * (JOIN_ROW + 2) * 4 <= RING, "the join fits the ring");
   const float unit_of = pow2(min(max(e_ref, -126), 127));
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int row = g + 8 * r;
-    const float sum = quad_sum(l[r]);
-    if (t == 0) {
+  for (int r = 0; r < NR; ++r) {
+    const int row = 8 * (r >> 1) + t2 + (r & 1);
+    float sum = l[r];
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (g == 0) {
       sml[(w * HB + row) * 2] = m[r];
       sml[(w * HB + row) * 2 + 1] = sum;
     }
-    // columns t2, t2 + 1 of the even block are channels 16 j + 4 t, + 2, of the odd one + 1, + 3
 #pragma unroll
     for (int j = 0; j < kDV / 16; ++j)
-      *reinterpret_cast<float4*>(so + (w * HB + row) * kDV + 16 * j + 4 * t) =
-          make_float4(acc[2 * j][2 * r] * unit_of, acc[2 * j + 1][2 * r] * unit_of,
-                      acc[2 * j][2 * r + 1] * unit_of, acc[2 * j + 1][2 * r + 1] * unit_of);
+      *reinterpret_cast<float2*>(so + (w * HB + row) * JOIN_ROW + 16 * j + 2 * g) =
+          make_float2(acc[j][r >> 1][r & 1] * unit_of, acc[j][r >> 1][2 + (r & 1)] * unit_of);
   }
   __syncthreads();
   for (int x = tid; x < rows * (kDV / 2); x += THREADS) {
@@ -525,7 +630,7 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
 #pragma unroll
     for (int k = 0; k < WARPS; ++k) {
       const float f = ex2(sml[(k * HB + row) * 2] - base);
-      const float2 o = *reinterpret_cast<const float2*>(so + (k * HB + row) * kDV + ch);
+      const float2 o = *reinterpret_cast<const float2*>(so + (k * HB + row) * JOIN_ROW + ch);
       sum = fmaf(f, sml[(k * HB + row) * 2 + 1], sum);
       o0 = fmaf(f, o.x, o0);
       o1 = fmaf(f, o.y, o1);
@@ -550,7 +655,7 @@ template <class TO>
 __global__ void __launch_bounds__(kDV / 2)
 rows8_join_kernel(Args a, Plan plan) {
   griddep_wait();
-  const int cut = blockIdx.x / HB, row = blockIdx.x % HB, parts = plan.parts;
+  const int HB = plan.rows, cut = blockIdx.x / HB, row = blockIdx.x % HB, parts = plan.parts;
   const CutUnit* table = static_cast<const CutUnit*>(a.workspace);
   if (plan.whole + cut >= table->first) return;  // (the first word: units)
   const CutUnit u = table[1 + cut];
@@ -579,13 +684,13 @@ rows8_join_kernel(Args a, Plan plan) {
 // `units` at most, `likely` so many: as many whole ones as fill the device one or more times, and parts of
 // the others that fill it once more, of at least one round of the warps' tiles (128 slots); nothing is
 // cut where two do not fit.
-inline Plan make_plan(long long units, long long likely, int slots, int n_sm) {
+inline Plan make_plan(long long units, long long likely, int rows, int slots, int n_sm) {
   const int hold = std::max(3 * n_sm, 1), unit = SB * WARPS, rest = (int)(likely % hold);
   const int most = std::min((slots + unit - 1) / unit, 64);
   const int parts = rest ? std::min(hold / rest, most) : 1;
-  if (parts < 2) return Plan{units, (int)units, 1, 0};
+  if (parts < 2) return Plan{units, (int)units, 1, 0, rows};
   const int part_slots = ((slots + parts - 1) / parts + unit - 1) / unit * unit;
-  return Plan{units, (int)(likely - rest), parts, part_slots};
+  return Plan{units, (int)(likely - rest), parts, part_slots, rows};
 }
 
 inline bool make_maps(Maps* m, const ServeCache& cache) {
@@ -597,7 +702,7 @@ inline bool make_maps(Maps* m, const ServeCache& cache) {
     const int d = i ? kDV : kDK;
     cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)c.KV, (cuuint64_t)slots, (cuuint64_t)pages};
     cuuint64_t strides[3] = {(cuuint64_t)d, (cuuint64_t)d * c.KV, (cuuint64_t)d * c.KV * slots};
-    cuuint32_t box[4] = {i ? 64u : (cuuint32_t)kDK, 1u, (cuuint32_t)SB, 1u};
+    cuuint32_t box[4] = {i ? 64u : (cuuint32_t)kDK, 1u, (cuuint32_t)ROUND, 1u};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     if (fn(i ? &m->v : &m->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i ? c.v : c.k, dims, strides, box, estr,
            CU_TENSOR_MAP_INTERLEAVE_NONE, i ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -607,20 +712,24 @@ inline bool make_maps(Maps* m, const ServeCache& cache) {
   return true;
 }
 
-template <class T, class TO>
+template <class T, class TO, int NT>
 cudaError_t run(const Args& a, const Plan& plan, DevCtl ctl, cudaStream_t stream) {
   Maps m;
   if (!make_maps(&m, a.cache)) return cudaErrorInvalidValue;
-  auto kern = rows8_kernel<T, TO>;
+  auto kern = rows8_kernel<T, TO, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   const long long cut = plan.units - plan.whole;
   kern<<<(unsigned)(plan.whole + cut * plan.parts), THREADS, SMEM, stream>>>(m, a, plan, ctl);
   if ((e = cudaGetLastError()) != cudaSuccess || plan.parts == 1) return e;
-  PdlLaunch l(dim3((unsigned)(cut * HB)), dim3(kDV / 2), 0, stream, true);
+  PdlLaunch l(dim3((unsigned)(cut * plan.rows)), dim3(kDV / 2), 0, stream, true);
   return cudaLaunchKernelEx(&l.cfg, rows8_join_kernel<TO>, a, plan);
 }
 
+template <class T, class TO>
+cudaError_t run(const Args& a, const Plan& plan, DevCtl ctl, cudaStream_t stream) {
+  return plan.rows == 8 ? run<T, TO, 1>(a, plan, ctl, stream) : run<T, TO, 2>(a, plan, ctl, stream);
+}
 inline cudaError_t launch(const Args& a, gla_dtype out, const Plan& plan, DevCtl ctl, cudaStream_t stream) {
   const bool wide = out == GLA_FP32;
   if (a.cache.c.type == GLA_BF16)
