@@ -39,10 +39,13 @@ constexpr int STAGE = OFF_KEYS + ROUND * kDK;            // 36,864 bytes
 constexpr int RING = STAGES * STAGE;
 constexpr int JOIN_ROW = kDV + 4;                        // floats; the rows of a store in different banks
 constexpr int OFF_BAR = RING;                            // mbarrier [stage], int [stage]: warps done with it
-constexpr int OFF_FACTORS = OFF_BAR + STAGES * 16;       // float2 [warp][32]: a tile's 2^e
-constexpr int EXPS = 2 * SB + 16;                          // a tile's exponents, from a word's start
-constexpr int OFF_EXPS = OFF_FACTORS + WARPS * 32 * 8;     // [warp][stage]
+constexpr int OFF_FOUND = OFF_BAR + STAGES * 16;         // int [4]: the unit
+constexpr int OFF_FACTORS = OFF_FOUND + 16;              // float2 [warp][32]: a tile's 2^e; before, sums
+constexpr int EXPS = 2 * SB + 16;                        // a tile's exponents, from a word's start
+constexpr int OFF_EXPS = OFF_FACTORS + WARPS * 32 * 8;   // [warp][stage]
 constexpr int SMEM = OFF_EXPS + WARPS * STAGES * EXPS + 1024;
+static_assert(3 * (SMEM + 1024) <= 228 * 1024, "three CTAs on an SM");
+static_assert((THREADS + 1 + WARPS) * 4 <= WARPS * 32 * 8, "the sums fit where the factors go");
 constexpr uint64_t DRAIN_NS = 4000000000ull;
 
 struct Args {
@@ -128,7 +131,6 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
   constexpr int HB = 8 * NT, NR = 2 * NT;  // rows of a unit, and those of a thread's scores
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ int found[4];
   const uint32_t sm = smem_u32(smem);
   const WindowCache& c = a.cache.c;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -139,6 +141,7 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
   const int part_slots = cut < 0 ? 1 << 30 : plan.part_slots;
   const int unit = cut < 0 ? (int)blockIdx.x : plan.whole + cut / parts;
   const uint32_t bar = sm + OFF_BAR;
+  int* const found = reinterpret_cast<int*>(smem + OFF_FOUND);
   int* const passed = reinterpret_cast<int*>(smem + OFF_BAR + STAGES * 8);
   if (tid < STAGES) {
     mbar_init(bar + 8 * tid, 1);
@@ -179,7 +182,8 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     __syncthreads();
   } else {
     // sums of groups over a slice of the sequences a thread, and a search
-    __shared__ int upto[THREADS + 1], sums[WARPS];
+    int* const upto = reinterpret_cast<int*>(smem + OFF_FACTORS);
+    int* const sums = upto + THREADS + 1;
     const int slice = (c.n + THREADS - 1) / THREADS;
     const int lo = min(tid * slice, c.n), hi = min(lo + slice, c.n);
     int mine = 0;
