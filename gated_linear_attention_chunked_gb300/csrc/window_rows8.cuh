@@ -1,24 +1,26 @@
 // window_rows8.cuh -- the windowed attention of few new tokens per sequence over pages of 8 bits: one each
 // (the decode step) or a handful (drafts).  8 NT rows, (token, query head) of one key head, are a unit; a
-// CTA takes a unit, or a part of its page's slots, in rounds of 128: its four warps take 32 slots each from a
-// ring that one thread's TMA fills, with running maxima and sums of their own, and join them at the end.
+// CTA takes a unit, or a part of its page's slots, in rounds that one thread's TMA brings: each of its four
+// warps multiplies a quarter of a round's keys, and then a quarter of the channels of all its values.
 //
 //   z = 2^e (c . q),  o = sum p 2^e c / sum p   with the rows' codes c as fp16 operands, exactly
 //
-// whatever the call's type: fp16 is a byte permute and a subtraction away from a code (0x6400 | u is 1024 +
-// u), bf16 twice as much.  Queries of bf16 are scaled by a power of two per row into fp16's range; the
-// values' 2^e goes into the weight, relative to the largest e of the tiles so far, so that a weight rounds
-// by 2^-11 of itself or by 2^-25 of the weight of the page's largest row.  The new tokens' own keys and values are
-// taken as given, in the call's type, a tile of 16 at a time straight from global memory.
+// whatever the call's type.  An operand is (c + 128) 2^-24, a value without an exponent: an exclusive or and
+// a byte permute; the 128 comes off by a product with the queries' sum before and the weights' sum after.
+// Queries of bf16 are scaled by a power of two per row into fp16's range; the values' 2^e goes into the
+// weight, relative to a common e_ref within 4 of the largest so far, so that a weight rounds by 2^-11 of
+// itself or by 2^-25 of the weight of the page's largest row.  The new tokens' own keys and values are taken as
+// given, in the call's type, straight from global memory, behind the page.
 //
 // The codes are the products' first operand (16 slots by channels; 16 channels by slots), the rows their
-// columns, eight at a time: most calls have four or eight rows, and a row takes 24 registers of sums a
-// thread where as the first operand's it would take 48.  Keys are read eight channels at a time, in
-// an order of the channels that the query's registers share; values by transposed loads of pairs of
-// channels, which come apart in the permutes that make operands of them.  Weights go from the scores' layout
-// to an operand's by matrix transposes between the lanes.
+// columns, eight at a time: most calls have four or eight rows.  Keys are read eight channels at a time, in an
+// order of the channels that the queries share; values by transposed loads of pairs of channels, which come
+// apart in the permutes.  Weights go to all four warps through shared memory, in units of a maximum that all
+// share: they are worked out before it is known whether a score passes it by more than 8, and again in the
+// rare round where one does, so that a round has one barrier.
 //
-// Bound by the instructions: a code costs 1.25 of them, and the floor is HBM's 290 bytes a slot and key head.
+// Bound by latency and by the instructions: a code costs 0.75 of them; the floor is HBM's 290 bytes a slot and
+// key head.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -32,21 +34,44 @@
 namespace gla {
 namespace rows8 {
 
-constexpr int WARPS = 4, THREADS = 32 * WARPS, SB = 32, STAGES = 2;
-constexpr int ROUND = WARPS * SB;                        // slots of a stage, a tile of 32 for each warp
-constexpr int V_BOX = ROUND * 64, OFF_KEYS = 3 * V_BOX;  // values in 3 boxes of 64 channels, keys
-constexpr int STAGE = OFF_KEYS + ROUND * kDK;            // 36,864 bytes
-constexpr int RING = STAGES * STAGE;
-constexpr int JOIN_ROW = kDV + 4;                        // floats; the rows of a store in different banks
-constexpr int OFF_BAR = RING;                            // mbarrier [stage], int [stage]: warps done with it
-constexpr int OFF_FOUND = OFF_BAR + STAGES * 16;         // int [4]: the unit
-constexpr int OFF_FACTORS = OFF_FOUND + 16;              // float2 [warp][32]: a tile's 2^e; before, sums
-constexpr int EXPS = 2 * SB + 16;                        // a tile's exponents, from a word's start
-constexpr int OFF_EXPS = OFF_FACTORS + WARPS * 32 * 8;   // [warp][stage]
-constexpr int SMEM = OFF_EXPS + WARPS * STAGES * EXPS + 1024;
-static_assert(3 * (SMEM + 1024) <= 228 * 1024, "three CTAs on an SM");
-static_assert((THREADS + 1 + WARPS) * 4 <= WARPS * 32 * 8, "the sums fit where the factors go");
+constexpr int WARPS = 4, THREADS = 32 * WARPS, SB = 16;
+constexpr int ROUND = WARPS * SB;                  // slots
+constexpr int OFF_KEYS = ROUND * kDV;              // a stage: values, keys
+constexpr int STAGE = OFF_KEYS + ROUND * kDK;      // 18,432 bytes
+constexpr int EXPS = 2 * SB + 16;                  // the exponents of a warp's slots, from a word's start
+constexpr int P_ROW = 2 * ROUND + 16;              // bytes of a row's weights
+constexpr int TILES = kDV / 16 / WARPS;            // a warp's channels, 16 each
 constexpr uint64_t DRAIN_NS = 4000000000ull;
+static_assert(kDV % (16 * WARPS) == 0, "the warps' channels");
+
+// Stages of the ring and CTAs that an SM holds, by the groups of 8 rows: with 5, 4 and 3 CTAs of two stages the
+// decode step of 256 tokens on 1,028 slots of 4 key heads took as long (69 us), but 96 chunks of two and four
+// tokens on 2,052 slots 65 and 74 us in place of 48 and 57; four groups with three stages leave room for two
+// CTAs only (96 chunks of eight tokens: 101 us in place of 94).
+template <int NT>
+constexpr int kStages = NT == 4 ? 2 : 3;
+constexpr int kHold = 3;
+
+// What the warps of a unit of NT groups of 8 rows share.
+template <int NT>
+struct Shared {
+  uint64_t full[kStages<NT>];          // mbarriers
+  uint8_t exps[WARPS][kStages<NT>][EXPS];
+  alignas(16) uint8_t weights[2][8 * NT * P_ROW];  // of two rounds, [row][slot]
+  uint2 q[NT][kDK / 16][32];           // the second operand of the scores' products
+  float z0[8 * NT], zs[8 * NT];        // of a row: - q . (code 0), a score's factor
+  float top[WARPS][8 * NT], sum[WARPS][8 * NT], zero[WARPS][8 * NT];
+  int e_top[WARPS];
+  int found[4];
+  int upto[THREADS + 1], sums[WARPS];  // units before a slice of the sequences
+};
+template <int NT>
+constexpr int smem_bytes() {
+  return kStages<NT> * STAGE + (int)sizeof(Shared<NT>) + 1024;
+}
+static_assert(kHold * (smem_bytes<1>() + 1024) <= 228 * 1024 && kHold * (smem_bytes<2>() + 1024) <= 228 * 1024 &&
+                  kHold * (smem_bytes<4>() + 1024) <= 228 * 1024,
+              "shared memory");
 
 struct Args {
   ServeCache cache;
@@ -113,25 +138,28 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-// Codes as fp16 values of whole numbers: bytes 0, 1 and 2, 3, or (EVEN) 0, 2 and 1, 3.
-template <bool EVEN>
-__device__ __forceinline__ void whole16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  whole_of<__half, EVEN>(w, lo, hi);
+// Codes c as fp16 values (c + 128) 2^-24, which have no exponent to be put in: codes 0, 2 and 1, 3 of a word.
+__device__ __forceinline__ void whole16(uint32_t w, uint32_t& even, uint32_t& odd) {
+  const uint32_t u = w ^ 0x80808080u;
+  even = __byte_perm(u, 0u, 0x4240);
+  odd = __byte_perm(u, 0u, 0x4341);
 }
+constexpr uint32_t kZero16 = 0x00800080u;  // of code 0
 
-__device__ __forceinline__ uint32_t transposed(uint32_t x) {  // 8 x 8 of 16 bits between the lanes
-  uint32_t y;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
+// Two 8 x 8 matrices of 16 bits to shared memory, transposed; lanes 0 .. 15 have their rows' addresses.
+__device__ __forceinline__ void stsm2t(uint32_t at, uint32_t x, uint32_t y) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
 }
 
 template <class T, class TO, int NT>
-__global__ void __launch_bounds__(THREADS, 3)
+__global__ void __launch_bounds__(THREADS, kHold)
 rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
-  constexpr int HB = 8 * NT, NR = 2 * NT;  // rows of a unit, and those of a thread's scores
+  constexpr int HB = 8 * NT, NR = 2 * NT;  // rows of a unit, and those of a thread
+  constexpr int STAGES = kStages<NT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  const uint32_t sm = smem_u32(smem);
+  Shared<NT>& sh = *reinterpret_cast<Shared<NT>*>(smem + STAGES * STAGE);
+  const uint32_t sm = smem_u32(smem), bar = smem_u32(sh.full);
   const WindowCache& c = a.cache.c;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int KV = c.KV, G = a.H / KV;
@@ -140,12 +168,8 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
   const int parts = cut < 0 ? 1 : plan.parts, part = cut < 0 ? 0 : cut % parts;
   const int part_slots = cut < 0 ? 1 << 30 : plan.part_slots;
   const int unit = cut < 0 ? (int)blockIdx.x : plan.whole + cut / parts;
-  const uint32_t bar = sm + OFF_BAR;
-  int* const found = reinterpret_cast<int*>(smem + OFF_FOUND);
-  int* const passed = reinterpret_cast<int*>(smem + OFF_BAR + STAGES * 8);
   if (tid < STAGES) {
     mbar_init(bar + 8 * tid, 1);
-    passed[tid] = 0;
     fence_barrier_init();
   }
   if (tid == 0) {
@@ -182,8 +206,7 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     __syncthreads();
   } else {
     // sums of groups over a slice of the sequences a thread, and a search
-    int* const upto = reinterpret_cast<int*>(smem + OFF_FACTORS);
-    int* const sums = upto + THREADS + 1;
+    int *const upto = sh.upto, *const sums = sh.sums;
     const int slice = (c.n + THREADS - 1) / THREADS;
     const int lo = min(tid * slice, c.n), hi = min(lo + slice, c.n);
     int mine = 0;
@@ -209,18 +232,18 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
       for (;; ++i) {
         const int n = (sequence(c, a.tok, i, ctl).tokens * G + HB - 1) / HB * KV;
         if (left < n) {
-          found[0] = i;
-          found[1] = left / (n / KV);
-          found[2] = left % (n / KV);
+          sh.found[0] = i;
+          sh.found[1] = left / (n / KV);
+          sh.found[2] = left % (n / KV);
           break;
         }
         left -= n;
       }
     }
     __syncthreads();
-    b = found[0];
-    kv = found[1];
-    grp = found[2];
+    b = sh.found[0];
+    kv = sh.found[1];
+    grp = sh.found[2];
     s = sequence(c, a.tok, b, ctl);
   }
   const int rows = min(HB, s.tokens * G - grp * HB);  // <= 0: a sequence that is left as it is
@@ -252,163 +275,473 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     return s0 + SB <= hi && (s0 + SB <= s_end || (s0 >= a_from && s0 + SB <= a_end) || s0 >= b_from);
   };
 
-  const int tiles = hi > lo ? (hi - lo + SB * WARPS - 1) / (SB * WARPS) : 0;
-  auto first_slot = [&](int i) { return lo + i * ROUND + w * SB; };
-  const signed char* pe = a.cache.exps + ((long long)page * KV + kv) * seen.slots * 2;
-  const int skew = (int)(reinterpret_cast<uintptr_t>(pe) & 2);
-  auto fetch = [&](int i) {  // round i, by one thread: slots lo + i ROUND ..
-    if (i >= tiles) return;
+  // ---- rounds of 64 slots
+  const int rounds = hi > lo ? (hi - lo + ROUND - 1) / ROUND : 0;
+  int sent = 0;             // (thread 0)
+  auto fetch = [&](int i) {  // by one thread: slots lo + i ROUND ..
+    if (i >= rounds) return;
     const uint32_t st = sm + i % STAGES * STAGE, full = bar + 8 * (i % STAGES);
     mbar_arrive_expect_tx(full, STAGE);
-#pragma unroll
-    for (int j = 0; j < 3; ++j)
-      tma_load_4d(st + j * V_BOX, &maps.v, full, 64 * j, kv, lo + i * ROUND, page);
+    tma_load_5d(st, &maps.v, full, 0, 0, kv, lo + i * ROUND, page);
     tma_load_4d(st + OFF_KEYS, &maps.k, full, 0, kv, lo + i * ROUND, page);
-  };
-  auto fetch_exps = [&](int i) {  // of the warp's tile of round i
-    // exponents, two bytes a slot, in words: where the row starts in the middle of one, from there
-    const int s0 = first_slot(i);
-    if (i < tiles && s0 < hi && lane <= SB / 2) {
-      const long long from = 2ll * s0 - skew + 4 * lane;  // byte of the row
-      copy4(sm + OFF_EXPS + (w * STAGES + i % STAGES) * EXPS + 4 * lane,
-            pe + (from < 2ll * hi ? from : 2ll * s0 - skew), (int)min(max(2ll * hi - from, 0ll), 4ll));
-    }
-    copy_commit();
+    sent = i + 1;
   };
   if (tid == 0)
     for (int i = 0; i < STAGES; ++i) fetch(i);
+  auto first_slot = [&](int i) { return lo + i * ROUND + w * SB; };
+  const signed char* pe = a.cache.exps + ((long long)page * KV + kv) * seen.slots * 2;
+  const int skew = (int)(reinterpret_cast<uintptr_t>(pe) & 2);
+  auto fetch_exps = [&](int i) {  // of the warp's slots of round i
+    // exponents, two bytes a slot, in words: where the row starts in the middle of one, from there
+    const int s0 = first_slot(i);
+    if (i < rounds && s0 < hi && lane <= SB / 2) {
+      const long long from = 2ll * s0 - skew + 4 * lane;  // byte of the row
+      if (from < 2ll * hi)
+        copy4(smem_u32(sh.exps[w][i % STAGES]) + 4 * lane, pe + from,
+              (int)min(2ll * hi - from, 4ll));
+    }
+    copy_commit();
+  };
 #pragma unroll
   for (int i = 0; i < STAGES; ++i) fetch_exps(i);
 
-  // ---- queries: row 8 n + g of the unit's (the last one again behind them); step 2 j + h of the product
-  // has channels 32 j + 8 t + 4 h .. + 3 of thread t of a row's four
+  // ---- queries: step 2 j + h of the product has channels 32 j + 8 t + 4 h .. + 3 of thread t of a row's
+  // four.  Each group of eight rows by a warp: scaled into fp16's range by a power of two per row, in the order
+  // of the codes' operands (channels 0, 2 and 1, 3 of four).
   const int g = lane >> 2, t = lane & 3, t2 = t * 2;
-  auto token = [&](int r) { return (grp * HB + min(r, rows - 1)) / G; };  // of row r
-  uint32_t qf[NT][kDK / 16][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int R = grp * HB + min(8 * n + g, rows - 1), i = R / G;
+  auto row_of = [&](int r) { return grp * HB + min(r, rows - 1); };  // (the last one again behind them)
+  auto load_q = [&](int n, uint32_t (&qf)[kDK / 16][2]) {
+    const int R = row_of(8 * n + g), i = R / G;
     const T* q = static_cast<const T*>(a.q) + ((long long)(s.first + i) * a.H + kv * G + R - i * G) * kDK;
 #pragma unroll
     for (int j = 0; j < kDK / 16; ++j) {
       const uint2 x = __ldg(reinterpret_cast<const uint2*>(q + 32 * (j >> 1) + 8 * t + 4 * (j & 1)));
-      qf[n][j][0] = x.x;
-      qf[n][j][1] = x.y;
+      qf[j][0] = x.x;
+      qf[j][1] = x.y;
     }
+  };
+  static_assert(NT <= WARPS, "a warp for each group of rows");
+  if (w < NT) {
+    uint32_t qf[kDK / 16][2];
+    load_q(w, qf);
+    float up = 16777216.f * kLog2e;
+    if constexpr (!__is_same(T, __half)) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < kDK / 16; ++j) top = top2<T>(top, top2<T>(qf[j][0], qf[j][1]));
+      top = top2<T>(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = top2<T>(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float2 f = halves<T>(top);
+      const int e = min(max((int)(__float_as_uint(fmaxf(f.x, f.y)) >> 23) - 127, -100), 100);
+      const float down = pow2(-e);
+      up *= pow2(e);
+#pragma unroll
+      for (int j = 0; j < kDK / 16; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 x = halves<T>(qf[j][h]);
+          qf[j][h] = pack2<__half>(x.x * down, x.y * down);
+        }
+    }
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint32_t zero[4] = {kZero16, kZero16, kZero16, kZero16};
+#pragma unroll
+    for (int j = 0; j < kDK / 16; ++j) {
+      const uint2 y = make_uint2(__byte_perm(qf[j][0], qf[j][1], 0x5410), __byte_perm(qf[j][0], qf[j][1], 0x7632));
+      sh.q[w][j][lane] = y;
+      mma16816<__half>(x, zero, y.x, y.y);
+    }
+    if (g == 0) *reinterpret_cast<float2*>(sh.z0 + 8 * w + t2) = make_float2(-x[0], -x[1]);
+    if (t == 0) sh.zs[8 * w + g] = up;
   }
-  // A thread's scores are of slots g, g + 8 and rows 8 n + t2, + 1 (NR of them); its sums of channels
-  // 16 c + 2 g (0, 1) and + 1 (2, 3) and the same rows.
-  int at[NR];  // the rows' positions
+  __syncthreads();
+
+  // A thread's scores are of slots g, g + 8, .. of the warp's and rows 8 n + t2, + 1 (NR of them); its sums of
+  // channels 16 (TILES w + c) + 2 g (0, 1) and + 1 (2, 3) and the same rows.
+  float z0[NR], zs[NR];
 #pragma unroll
-  for (int r = 0; r < NR; ++r) at[r] = s.pos + token(8 * (r >> 1) + t2 + (r & 1));
-  float acc[kDV / 16][NT][4];
+  for (int r = 0; r < NR; ++r) {
+    z0[r] = sh.z0[8 * (r >> 1) + t2 + (r & 1)];
+    zs[r] = sh.zs[8 * (r >> 1) + t2 + (r & 1)];
+  }
+  auto at = [&](int r) { return s.pos + row_of(8 * (r >> 1) + t2 + (r & 1)) / G; };  // a row's position
+  float acc[TILES][NT][4], wsum[NT][4];  // wsum: of the warp's own slots, of code 0
 #pragma unroll
-  for (int j = 0; j < kDV / 16; ++j)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int k = 0; k < 4; ++k) {
+      wsum[n][k] = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[j][n][k] = 0.f;
-  float m[NR], l[NR];  // base 2; l of this thread's slots
+      for (int j = 0; j < TILES; ++j) acc[j][n][k] = 0.f;
+    }
+  float m[NR], l[NR];  // base 2, the same in all warps; l of this thread's slots
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
   }
-  int e_ref = 0;  // acc is in units of 2^e_ref (-60 at least: what is below 2^-78 in a page is lost)
+  int e_ref = -1000;  // acc is in units of 2^(e_ref - 24); -60 at least: what is below 2^-78 in a page is lost
 
-  // The maxima of a tile's scores (base 2) over its slots; o and the sums go to a new reference only when
-  // one passes the old by more than 8 (weights of up to 2^8 lose nothing in fp16).
-  auto refer = [&](float (&top)[NR]) {
-    bool up = false;
+  // The rare round in which a score passes a row's maximum by more than 8, or an exponent e_ref by more than 4
+  // (weights of up to 2^12 lose nothing in fp16): new ones for all, and the sums in their units.
+  auto refer = [&](float (&top)[NR], int e_top) {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], d));
-      up |= top[r] > m[r] + 8.f;
+      if (g == 0) sh.top[w][8 * (r >> 1) + t2 + (r & 1)] = top[r];
     }
-    if (__any_sync(0xffffffffu, up)) {
+    if (lane == 0) sh.e_top[w] = e_top;
+    __syncthreads();
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const float now = top[r] > m[r] + 8.f ? top[r] : m[r];
-        const float keep = now == m[r] || m[r] == -INFINITY ? 1.f : ex2(m[r] - now);
-        m[r] = now;
-        l[r] *= keep;
+    for (int k = 0; k < WARPS; ++k) e_top = max(e_top, sh.e_top[k]);
+    const float f = e_top > e_ref + 4 ? pow2(max(e_ref - e_top, -126)) : 1.f;
+    if (e_top > e_ref + 4) e_ref = e_top;
 #pragma unroll
-        for (int j = 0; j < kDV / 16; ++j) {
-          acc[j][r >> 1][r & 1] *= keep;
-          acc[j][r >> 1][2 + (r & 1)] *= keep;
-        }
+    for (int r = 0; r < NR; ++r) {
+      float all = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) all = fmaxf(all, sh.top[k][8 * (r >> 1) + t2 + (r & 1)]);
+      const float now = all > m[r] + 8.f ? all : m[r];
+      const float keep = now == m[r] || m[r] == -INFINITY ? 1.f : ex2(m[r] - now);
+      m[r] = now;
+      l[r] *= keep;
+      wsum[r >> 1][r & 1] *= keep * f;
+#pragma unroll
+      for (int j = 0; j < TILES; ++j) {
+        acc[j][r >> 1][r & 1] *= keep * f;
+        acc[j][r >> 1][2 + (r & 1)] *= keep * f;
       }
     }
   };
 
-  // ---- the new tokens, by tiles of 16 in turn
-  if (part == 0) {
-    const int sinks = max(c.sink - s.pos, 0);
-    const T* nk = static_cast<const T*>(a.k) + ((long long)s.first * KV + kv) * kDK;
-    const T* nv = static_cast<const T*>(a.v) + ((long long)s.first * KV + kv) * kDV;
+  // ---- the page
+  // where the lane's 16 bytes of a transposed load lie: slot `lane` of 32, the warp's channels, swizzled by the
+  // address
+  uint32_t v_at[TILES];
+#pragma unroll
+  for (int j = 0; j < TILES; ++j) {
+    const int x = lane * kDV + 16 * (TILES * w + j);
+    v_at[j] = sm + (x ^ ((x >> 3) & 48));
+  }
+  const uint32_t p_sm = smem_u32(sh.weights[0]);
+  const uint32_t p_to = p_sm + (lane & 7) * P_ROW + (w * SB + ((lane >> 3) & 1) * 8) * 2;  // its row of the stores
+  const uint32_t p_from = p_sm + (lane & 7) * P_ROW + (lane >> 3) * 16;               // and of the loads
+  bool dead = false;  // a wait ran out: no more loads, and nothing of use comes out
 #pragma unroll 1
-    for (int j0 = 16 * (WARPS - 1 - w); j0 <= i1; j0 += 16 * WARPS) {  // (the last warp has a tile less)
-      if (j0 + 15 <= i0 - c.window && j0 >= sinks) continue;
-      float z[NT][4];
+  for (int i = 0; i < rounds; ++i) {
+    const int s0 = first_slot(i);
+    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(bar + 8 * (i % STAGES), (i / STAGES) & 1, ctl));
+    copy_wait<STAGES - 1>();
+    __syncwarp();
+    float z[SB / 16][NT][4];  // slots 16 h + g, + 8
+    float2 f[SB / 8];         // the factors of the thread's slots, 8 k + g
+    int ev = -128;
+    float ks = 0.f;
+    bool up = false;
+    if (s0 < hi) {
+      const uint8_t* keys = smem + i % STAGES * STAGE + OFF_KEYS + w * SB * kDK;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int h = 0; h < SB / 16; ++h)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) z[n][k] = 0.f;
-      const bool in0 = j0 + g <= i1, in1 = j0 + g + 8 <= i1;
-      const T* key = nk + (long long)(j0 + g) * KV * kDK + 8 * t;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < kDK / 16; ++j) {
-        uint2 x = make_uint2(0u, 0u), y = x;
-        if (in0) x = __ldg(reinterpret_cast<const uint2*>(key + 32 * (j >> 1) + 4 * (j & 1)));
-        if (in1)
-          y = __ldg(reinterpret_cast<const uint2*>(key + 8ll * KV * kDK + 32 * (j >> 1) + 4 * (j & 1)));
-        const uint32_t x4[4] = {x.x, y.x, x.y, y.y};
+          for (int k = 0; k < 4; ++k) z[h][n][k] = z0[2 * n + (k & 1)];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816<T>(z[n], x4, qf[n][j][0], qf[n][j][1]);
+      for (int j = 0; j < kDK / 32; ++j) {
+        uint2 q[2][NT];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) q[k][n] = sh.q[n][2 * j + k][lane];
+#pragma unroll
+        for (int h = 0; h < SB / 16; ++h) {
+          const uint2 x = *reinterpret_cast<const uint2*>(keys + (16 * h + g) * kDK + 32 * j + 8 * t);
+          const uint2 y = *reinterpret_cast<const uint2*>(keys + (16 * h + 8 + g) * kDK + 32 * j + 8 * t);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t x4[4];
+            whole16(k ? x.y : x.x, x4[0], x4[2]);
+            whole16(k ? y.y : y.x, x4[1], x4[3]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<__half>(z[h][n], x4, q[k][n].x, q[k][n].y);
+          }
+        }
       }
-      float top[NR];
+      // factors of slot `lane`, and from there of this thread's.  (The first row sees what any does.  A slot
+      // that none sees may be written meanwhile.)
+      const bool all = whole(s0);
+      const char2 ex = reinterpret_cast<const char2*>(sh.exps[w][i % STAGES] + skew)[lane & (SB - 1)];
+      ev = (signed char)ex.y;
+      const uint32_t there = bits_to(min(hi - s0, SB) - 1);
+      if (!all && !(((seen.bits(s.pos + i0, s0) & there) >> (lane & (SB - 1))) & 1)) ev = -128;
+      ks = scale_of((signed char)ex.x);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const uint32_t see = keys_seen(at[r] - s.pos, j0, i1 + 1, c.window, sinks) >> g;
-        float &z0 = z[r >> 1][r & 1], &z1 = z[r >> 1][2 + (r & 1)];
-        z0 = see & 1 ? z0 * kLog2e : -INFINITY;
-        z1 = (see >> 8) & 1 ? z1 * kLog2e : -INFINITY;
-        top[r] = fmaxf(z0, z1);
+      for (int k = 0; k < SB / 8; ++k) f[k].x = __shfl_sync(0xffffffffu, ks, 8 * k + g);
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int k = 0; k < SB / 8; ++k) {
+          float& x = z[k >> 1][r >> 1][2 * (k & 1) + (r & 1)];
+          x = x * zs[r] * f[k].x;
+        }
+      if (!all) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const uint32_t see = (seen.bits(at(r), s0) & there) >> g;
+#pragma unroll
+          for (int k = 0; k < SB / 8; ++k)
+            if (!((see >> (8 * k)) & 1)) z[k >> 1][r >> 1][2 * (k & 1) + (r & 1)] = -INFINITY;
+        }
       }
-      refer(top);
-      uint32_t pf[NT][2];
+    } else {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int h = 0; h < SB / 16; ++h)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) z[h][n][k] = -INFINITY;
+    }
+    __syncwarp();
+    fetch_exps(i + STAGES);
+    const int e_top = max(__reduce_max_sync(0xffffffffu, ev), -60);
+    float top[NR], part_sum[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      top[r] = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < SB / 8; ++k) top[r] = fmaxf(top[r], z[k >> 1][r >> 1][2 * (k & 1) + (r & 1)]);
+      up |= top[r] > m[r] + 8.f;
+    }
+    up |= e_top > e_ref + 4;
+    auto weigh = [&] {
+      const float vs = pow2(min(max(ev - e_ref, -126), 8));
+#pragma unroll
+      for (int k = 0; k < SB / 8; ++k) f[k].y = __shfl_sync(0xffffffffu, vs, 8 * k + g);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float base[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          base[j] = m[2 * n + j] == -INFINITY ? 0.f : m[2 * n + j];
+          part_sum[2 * n + j] = 0.f;
+        }
+        uint32_t pf[SB / 8];
+#pragma unroll
+        for (int k = 0; k < SB / 8; ++k) {
           float p[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int r = 2 * n + j;
-            p[j] = ex2(z[n][2 * k + j] - (m[r] == -INFINITY ? 0.f : m[r]));
-            l[r] += p[j];
+            p[j] = ex2(z[k >> 1][n][2 * (k & 1) + j] - base[j]);
+            part_sum[2 * n + j] += p[j];
           }
-          pf[n][k] = transposed(pack2<T>(p[0], p[1]));
+          pf[k] = pack2<__half>(p[0] * f[k].y, p[1] * f[k].y);
         }
-      // channels 16 j + 2 g, + 1 of tokens t2, + 1 and + 8, + 9
-      const T* val = nv + (long long)(j0 + t2) * KV * kDV + 2 * g;
+        static_assert(SB == 16, "a store of two matrices");
+        stsm2t(p_to + (i & 1) * (HB * P_ROW) + n * (8 * P_ROW), pf[0], pf[1]);
+      }
+    };
+    weigh();
+    const bool again = __syncthreads_or(up);
+    // all warps are done with the round before
+    if (tid == 0 && i > 0 && !dead) {
+      fence_proxy_async();
+      fetch(i - 1 + STAGES);
+    }
+    if (again) {
+      refer(top, e_top);
+      weigh();
+      __syncthreads();
+    }
 #pragma unroll
-      for (int j = 0; j < kDV / 16; ++j) {
+    for (int r = 0; r < NR; ++r) l[r] += part_sum[r];
+    // codes of slots 2 t, + 1 (x[0]) and + 8, + 9 (x[1]) of the first 16 of 32, x[2], x[3]: of the others
+    const uint32_t st = i % STAGES * STAGE, p_at = p_from + (i & 1) * (HB * P_ROW);
+    const int left = hi - (lo + i * ROUND);
+#pragma unroll
+    for (int y = 0; y < ROUND / 32; ++y) {
+      if (32 * y >= left) break;
+      uint32_t pf[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) ldsm4(pf[n], p_at + n * (8 * P_ROW) + 64 * y);
+#pragma unroll
+      for (int j = 0; j < TILES; ++j) {
         uint32_t x[4];
+        ldsm4t(x, v_at[j] + st + y * (32 * kDV));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x4[4];
+          whole16(x[2 * h], x4[0], x4[1]);
+          whole16(x[2 * h + 1], x4[2], x4[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816<__half>(acc[j][n], x4, pf[n][2 * h], pf[n][2 * h + 1]);
+        }
+      }
+      if (y == w >> 1) {
+        const uint32_t zero[4] = {kZero16, kZero16, kZero16, kZero16};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma16816<__half>(wsum[n], zero, w & 1 ? pf[n][2] : pf[n][0], w & 1 ? pf[n][3] : pf[n][1]);
+        }
+      }
+    }
+  }
+  copy_wait<0>();
+  // 128 off the codes, and the sums' own units
+  if (g == 0) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      *reinterpret_cast<float2*>(sh.zero[w] + 8 * n + t2) = make_float2(wsum[n][0], wsum[n][1]);
+  }
+  __syncthreads();
+  {
+    const float unit_of = pow2(min(max(e_ref, -126), 127));
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      float zero = 0.f;
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) zero += sh.zero[k][8 * (r >> 1) + t2 + (r & 1)];
+#pragma unroll
+      for (int j = 0; j < TILES; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float& x = acc[j][r >> 1][2 * h + (r & 1)];
+          x = (x - zero) * 16777216.f * unit_of;
+        }
+    }
+  }
+
+  // ---- the new tokens, 16 a warp
+  const T* nk = static_cast<const T*>(a.k) + ((long long)s.first * KV + kv) * kDK;
+  const T* nv = static_cast<const T*>(a.v) + ((long long)s.first * KV + kv) * kDV;
+  if (part == 0) {
+    const int sinks = max(c.sink - s.pos, 0);
+#pragma unroll 1
+    for (int j0 = 0, odd = rounds & 1; j0 <= i1; j0 += 16 * WARPS) {
+      if (j0 + 16 * WARPS - 1 <= i0 - c.window && j0 >= sinks) continue;
+      const int mine = j0 + 16 * w;
+      float z[NT][4], top[NR], part_sum[NR];
+      bool up = false;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) top[r] = -INFINITY;
+      if (mine <= i1) {
+        uint32_t key[kDK / 16][4];
+        const bool in0 = mine + g <= i1, in1 = mine + g + 8 <= i1;
+        const T* from = nk + (long long)(mine + g) * KV * kDK + 8 * t;
+#pragma unroll
+        for (int j = 0; j < kDK / 16; ++j) {
+          uint2 x = make_uint2(0u, 0u), y = x;
+          if (in0) x = __ldg(reinterpret_cast<const uint2*>(from + 32 * (j >> 1) + 4 * (j & 1)));
+          if (in1)
+            y = __ldg(reinterpret_cast<const uint2*>(from + 8ll * KV * kDK + 32 * (j >> 1) + 4 * (j & 1)));
+          key[j][0] = x.x, key[j][1] = y.x, key[j][2] = x.y, key[j][3] = y.y;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint32_t qf[kDK / 16][2];
+          load_q(n, qf);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) z[n][k] = 0.f;
+#pragma unroll
+          for (int j = 0; j < kDK / 16; ++j) mma16816<T>(z[n], key[j], qf[j][0], qf[j][1]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const uint32_t see = mine <= i1 ? keys_seen(at(r) - s.pos, mine, i1 + 1, c.window, sinks) >> g : 0u;
+        float &x = z[r >> 1][r & 1], &y = z[r >> 1][2 + (r & 1)];
+        x = see & 1 ? x * kLog2e : -INFINITY;
+        y = (see >> 8) & 1 ? y * kLog2e : -INFINITY;
+        top[r] = fmaxf(x, y);
+        up |= top[r] > m[r] + 8.f;
+      }
+      const uint32_t buf = p_sm + odd * (HB * P_ROW);
+      auto weigh = [&] {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float base = m[2 * n + j] == -INFINITY ? 0.f : m[2 * n + j];
+            z[n][j] = ex2(z[n][j] - base);
+            z[n][2 + j] = ex2(z[n][2 + j] - base);
+            part_sum[2 * n + j] = z[n][j] + z[n][2 + j];
+          }
+          stsm2t(buf + (8 * n + (lane & 7)) * P_ROW + (16 * w + ((lane >> 3) & 1) * 8) * 2,
+                 pack2<T>(z[n][0], z[n][1]), pack2<T>(z[n][2], z[n][3]));
+        }
+      };
+      if (__syncthreads_or(up)) refer(top, -1000);
+      weigh();
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < NR; ++r) l[r] += part_sum[r];
+#pragma unroll 1
+      for (int y = 0; y < WARPS && j0 + 16 * y <= i1; ++y) {
+        // channels 2 g, + 1 of 16 and tokens t2, + 1 and + 8, + 9
+        const int tok = j0 + 16 * y + t2;
+        const T* val = nv + (long long)tok * KV * kDV + 16 * TILES * w + 2 * g;
+        uint32_t x[TILES][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int d = (k & 1) + 8 * (k >> 1);
-          x[k] = 0u;
-          if (j0 + t2 + d <= i1)
-            x[k] = __ldg(reinterpret_cast<const uint32_t*>(val + (long long)d * KV * kDV + 16 * j));
-        }
-        const uint32_t x4[4] = {__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632),
-                                __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[2], x[3], 0x7632)};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816<T>(acc[j][n], x4, pf[n][0], pf[n][1]);
+          for (int j = 0; j < TILES; ++j) {
+            x[j][k] = 0u;
+            if (tok + d <= i1)
+              x[j][k] = __ldg(reinterpret_cast<const uint32_t*>(val + (long long)d * KV * kDV + 16 * j));
+          }
+        }
+        const uint8_t* weights = sh.weights[odd] + g * P_ROW + (16 * y + t2) * 2;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint32_t p0 = *reinterpret_cast<const uint32_t*>(weights + n * (8 * P_ROW));
+          const uint32_t p1 = *reinterpret_cast<const uint32_t*>(weights + n * (8 * P_ROW) + 16);
+#pragma unroll
+          for (int j = 0; j < TILES; ++j) {
+            const uint32_t x4[4] = {__byte_perm(x[j][0], x[j][1], 0x5410), __byte_perm(x[j][0], x[j][1], 0x7632),
+                                    __byte_perm(x[j][2], x[j][3], 0x5410), __byte_perm(x[j][2], x[j][3], 0x7632)};
+            mma16816<T>(acc[j][n], x4, p0, p1);
+          }
+        }
       }
+      odd ^= 1;
     }
+  }
+
+  // ---- the rows' sums of all warps, and the outputs
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
+    if (g == 0) sh.sum[w][8 * (r >> 1) + t2 + (r & 1)] = l[r];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const int row = 8 * (r >> 1) + t2 + (r & 1), ch = 16 * TILES * w + 2 * g;
+    if (row >= rows) continue;
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) sum += sh.sum[k][row];
+    if (parts == 1) {
+      const int R = grp * HB + row, i = R / G;
+      const float inv = 1.f / sum;  // the token itself is there: sum > 0
+      TO* o = static_cast<TO*>(a.o) + ((long long)(s.first + i) * a.H + kv * G + R - i * G) * kDV + ch;
+#pragma unroll
+      for (int j = 0; j < TILES; ++j)
+        store2(o + 16 * j, acc[j][r >> 1][r & 1] * inv, acc[j][r >> 1][2 + (r & 1)] * inv);
+    } else {
+      const long long cuts = plan.units - plan.whole;
+      float* pw = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + table_bytes(cuts)) +
+                  (((long long)(unit - plan.whole) * HB + row) * parts + part) * (kDV + 2);
+#pragma unroll
+      for (int j = 0; j < TILES; ++j)
+        *reinterpret_cast<float2*>(pw + ch + 16 * j) =
+            make_float2(acc[j][r >> 1][r & 1], acc[j][r >> 1][2 + (r & 1)]);
+      if (w == 0 && g == 0) *reinterpret_cast<float2*>(pw + kDV) = make_float2(m[r], sum);
+    }
+  }
+  if (part == 0) {
     // a single token's codes go into its slot, which it does not see
     if (!a.tok.start && grp == 0 && w == WARPS - 2) {
       uint4 x[3];
@@ -432,226 +765,8 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
       if (lane == 8) to[1] = (signed char)e;
     }
   }
-
-  // ---- queries as fp16, scaled into its range by a power of two per row
-  float zs[NR];
-#pragma unroll
-  for (int r = 0; r < NR; ++r) zs[r] = 1.f;
-  if constexpr (!__is_same(T, __half)) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < kDK / 16; ++j) top = top2<T>(top, top2<T>(qf[n][j][0], qf[n][j][1]));
-      top = top2<T>(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = top2<T>(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float2 f = halves<T>(top);
-      const int e = min(max((int)(__float_as_uint(fmaxf(f.x, f.y)) >> 23) - 127, -100), 100);
-      const float down = pow2(-e);
-#pragma unroll
-      for (int j = 0; j < kDK / 16; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float2 x = halves<T>(qf[n][j][h]);
-          qf[n][j][h] = pack2<__half>(x.x * down, x.y * down);
-        }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) zs[2 * n + j] = pow2(__shfl_sync(0xffffffffu, e, 4 * (t2 + j)));
-    }
-  }
-
-  // ---- the page
-  float2* const factors = reinterpret_cast<float2*>(smem + OFF_FACTORS) + 32 * w;
-  // where the lane's 16 bytes of a transposed load lie: chunks lane / 16, and + 2
-  const int row = lane & 15, swz = (row >> 1) & 3;
-  const uint32_t v_at[2] = {(uint32_t)(row * 64 + (((lane >> 4) ^ swz) << 4)),
-                            (uint32_t)(row * 64 + (((2 + (lane >> 4)) ^ swz) << 4))};
-#pragma unroll 1
-  for (int i = 0; i < tiles; ++i) {
-    const int s0 = first_slot(i);
-    if (s0 >= hi) break;  // (in the last round)
-    copy_wait<STAGES - 1>();
-    __syncwarp();
-    if (!__all_sync(0xffffffffu, mbar_wait(bar + 8 * (i % STAGES), (i / STAGES) & 1, ctl))) {
-      // the loads on their way land before the ring is used again and before the CTA may exit
-      for (int j = i; j < min(i + STAGES, tiles); ++j)
-        mbar_wait(bar + 8 * (j % STAGES), (j / STAGES) & 1, ctl, DRAIN_NS);
-      break;
-    }
-    const uint32_t so = i % STAGES * STAGE + w * SB * 64;  // the warp's values, in the first box
-    const uint8_t* keys = smem + i % STAGES * STAGE + OFF_KEYS + w * SB * kDK;
-    float z[2][NT][4];  // slots 16 h + g, + 8
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) z[h][n][k] = 0.f;
-#pragma unroll
-    for (int j = 0; j < kDK / 32; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint2 x = *reinterpret_cast<const uint2*>(keys + (16 * h + g) * kDK + 32 * j + 8 * t);
-        const uint2 y = *reinterpret_cast<const uint2*>(keys + (16 * h + 8 + g) * kDK + 32 * j + 8 * t);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t x4[4];
-          whole16<false>(k ? x.y : x.x, x4[0], x4[2]);
-          whole16<false>(k ? y.y : y.x, x4[1], x4[3]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma16816<__half>(z[h][n], x4, qf[n][2 * j + k][0], qf[n][2 * j + k][1]);
-        }
-      }
-    // the largest exponent of the values that are seen so far: o in its units.  (The first row sees what any
-    // does.  A slot that none sees may be written meanwhile.)
-    const bool all = whole(s0);
-    const char2 ex = reinterpret_cast<const char2*>(smem + OFF_EXPS + (w * STAGES + i % STAGES) * EXPS +
-                                                    skew)[lane];
-    int ev = (signed char)ex.y;
-    if (!all && !((seen.bits(s.pos + i0, s0) >> lane) & 1)) ev = -128;
-    const int e_top = max(__reduce_max_sync(0xffffffffu, ev), -60);
-    if (e_top > e_ref || i == 0) {
-      const float f = pow2(max(e_ref - e_top, -126));
-      e_ref = e_top;
-      if (i > 0 || part == 0)
-#pragma unroll
-        for (int j = 0; j < kDV / 16; ++j)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) acc[j][n][k] *= f;
-    }
-    // factors of slot `lane`, and then of this thread's, 8 k + g
-    factors[lane] = make_float2(scale_of((signed char)ex.x) * kLog2e, pow2(max(ev - e_ref, -126)));
-    __syncwarp();
-    float2 f[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = factors[8 * k + g];
-    float top[NR];
-#pragma unroll
-    for (int r = 0; r < NR; ++r) top[r] = -INFINITY;
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) z[k >> 1][r >> 1][2 * (k & 1) + (r & 1)] *= f[k].x;
-    if (!all) {
-      const uint32_t there = bits_to(hi - 1 - s0);
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const uint32_t see = (seen.bits(at[r], s0) & there) >> g;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (!((see >> (8 * k)) & 1)) z[k >> 1][r >> 1][2 * (k & 1) + (r & 1)] = -INFINITY;
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) top[r] = fmaxf(top[r], z[k >> 1][r >> 1][2 * (k & 1) + (r & 1)]);
-      top[r] *= zs[r];
-    }
-    refer(top);
-    uint32_t pf[2][NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float base[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) base[j] = m[2 * n + j] == -INFINITY ? 0.f : m[2 * n + j];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float p[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          p[j] = ex2(fmaf(z[k >> 1][n][2 * (k & 1) + j], zs[2 * n + j], -base[j]));
-          l[2 * n + j] += p[j];
-        }
-        pf[k >> 1][n][k & 1] = transposed(pack2<__half>(p[0] * f[k].y, p[1] * f[k].y));
-      }
-    }
-    // codes of slots 16 h + t2, + 1 (x[0]) and + 8, + 9 (x[1]), channels 16 ch + 2 g, + 1; x[2], x[3]:
-    // channels 16 ch + 16 + ..; a row's chunks are swizzled by row / 2 & 3, the same for both h
-#pragma unroll
-    for (int h = 0; h < 2; ++h)  // slots 16 h ..
-#pragma unroll
-      for (int ch = 0; ch < kDV / 16; ch += 2) {
-        uint32_t x[4];
-        ldsm4t(x, sm + so + (ch & 2 ? v_at[1] : v_at[0]) + (ch >> 2) * V_BOX + h * 1024);
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          uint32_t x4[4];
-          whole16<true>(x[2 * y], x4[0], x4[1]);
-          whole16<true>(x[2 * y + 1], x4[2], x4[3]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816<__half>(acc[ch + y][n], x4, pf[h][n][0], pf[h][n][1]);
-        }
-      }
-    // the warp that is the last to leave the stage has it filled again: one thread's loads for all four (by
-    // each warp for itself they take 1,000 of a tile's 4,000 cycles)
-    __syncwarp();
-    fetch_exps(i + STAGES);
-    if (lane == 0) {
-      __threadfence_block();
-      if (atomicAdd(passed + i % STAGES, 1) == WARPS - 1) {
-        passed[i % STAGES] = 0;
-        fence_proxy_async();
-        fetch(i + STAGES);
-      }
-    }
-    __syncwarp();
-  }
-  copy_wait<0>();
-  __syncthreads();
-
-  // ---- join the warps: o, m and l of each row through shared memory
-  float* so = reinterpret_cast<float*>(smem);              // [WARPS][HB][JOIN_ROW]
-  float* sml = so + WARPS * HB * JOIN_ROW;                 // [WARPS][HB][2]
-  static_assert(WARPS * HB * (JOIN_ROW + 2) * 4 <= RING, "the join fits the ring");
-  const float unit_of = pow2(min(max(e_ref, -126), 127));
-#pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const int row = 8 * (r >> 1) + t2 + (r & 1);
-    float sum = l[r];
-#pragma unroll
-    for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (g == 0) {
-      sml[(w * HB + row) * 2] = m[r];
-      sml[(w * HB + row) * 2 + 1] = sum;
-    }
-#pragma unroll
-    for (int j = 0; j < kDV / 16; ++j)
-      *reinterpret_cast<float2*>(so + (w * HB + row) * JOIN_ROW + 16 * j + 2 * g) =
-          make_float2(acc[j][r >> 1][r & 1] * unit_of, acc[j][r >> 1][2 + (r & 1)] * unit_of);
-  }
-  __syncthreads();
-  for (int x = tid; x < rows * (kDV / 2); x += THREADS) {
-    const int row = x / (kDV / 2), ch = x % (kDV / 2) * 2;
-    float top = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < WARPS; ++k) top = fmaxf(top, sml[(k * HB + row) * 2]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll
-    for (int k = 0; k < WARPS; ++k) {
-      const float f = ex2(sml[(k * HB + row) * 2] - base);
-      const float2 o = *reinterpret_cast<const float2*>(so + (k * HB + row) * JOIN_ROW + ch);
-      sum = fmaf(f, sml[(k * HB + row) * 2 + 1], sum);
-      o0 = fmaf(f, o.x, o0);
-      o1 = fmaf(f, o.y, o1);
-    }
-    if (parts == 1) {
-      const int R = grp * HB + row, i = R / G;
-      const float inv = 1.f / sum;  // the token itself is there: sum > 0
-      store2(static_cast<TO*>(a.o) + ((long long)(s.first + i) * a.H + kv * G + R - i * G) * kDV + ch,
-             o0 * inv, o1 * inv);
-    } else {
-      const long long cuts = plan.units - plan.whole;
-      float* pw = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + table_bytes(cuts)) +
-                  (((long long)(unit - plan.whole) * HB + row) * parts + part) * (kDV + 2);
-      *reinterpret_cast<float2*>(pw + ch) = make_float2(o0, o1);
-      if (ch == 0) *reinterpret_cast<float2*>(pw + kDV) = make_float2(top, sum);
-    }
-  }
+  if (dead && tid == 0)  // the loads on their way land before the CTA may exit
+    for (int i = max(sent - STAGES, 0); i < sent; ++i) mbar_wait(bar + 8 * (i % STAGES), (i / STAGES) & 1, ctl, DRAIN_NS);
 }
 
 // Joins the parts of a row of a cut unit, in order: o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.
@@ -686,10 +801,9 @@ rows8_join_kernel(Args a, Plan plan) {
 }
 
 // `units` at most, `likely` so many: as many whole ones as fill the device one or more times, and parts of
-// the others that fill it once more, of at least one round of the warps' tiles (128 slots); nothing is
-// cut where two do not fit.
+// the others that fill it once more, of at least two rounds; nothing is cut where two do not fit.
 inline Plan make_plan(long long units, long long likely, int rows, int slots, int n_sm) {
-  const int hold = std::max(3 * n_sm, 1), unit = SB * WARPS, rest = (int)(likely % hold);
+  const int hold = std::max(kHold * n_sm, 1), unit = 2 * ROUND, rest = (int)(likely % hold);
   const int most = std::min((slots + unit - 1) / unit, 64);
   const int parts = rest ? std::min(hold / rest, most) : 1;
   if (parts < 2) return Plan{units, (int)units, 1, 0, rows};
@@ -701,19 +815,19 @@ inline bool make_maps(Maps* m, const ServeCache& cache) {
   auto fn = encode_tiled_fn();
   if (!fn) return false;
   const WindowCache& c = cache.c;
-  const long long slots = c.window + c.sink, pages = (long long)c.n_pages * c.pool_layers;
-  for (int i = 0; i < 2; ++i) {
-    const int d = i ? kDV : kDK;
-    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)c.KV, (cuuint64_t)slots, (cuuint64_t)pages};
-    cuuint64_t strides[3] = {(cuuint64_t)d, (cuuint64_t)d * c.KV, (cuuint64_t)d * c.KV * slots};
-    cuuint32_t box[4] = {i ? 64u : (cuuint32_t)kDK, 1u, (cuuint32_t)ROUND, 1u};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    if (fn(i ? &m->v : &m->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i ? c.v : c.k, dims, strides, box, estr,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, i ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return false;
-  }
-  return true;
+  const cuuint64_t slots = c.window + c.sink, pages = (cuuint64_t)((long long)c.n_pages * c.pool_layers);
+  const cuuint64_t KV = c.KV, k_dims[4] = {kDK, KV, slots, pages};
+  const cuuint64_t k_strides[3] = {kDK, kDK * KV, kDK * KV * slots};
+  const cuuint64_t v_dims[5] = {64, kDV / 64, KV, slots, pages};
+  const cuuint64_t v_strides[4] = {64, kDV, kDV * KV, kDV * KV * slots};
+  const cuuint32_t k_box[4] = {kDK, 1, ROUND, 1}, v_box[5] = {64, kDV / 64, 1, ROUND, 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return fn(&m->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.k, k_dims, k_strides, k_box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+         fn(&m->v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, c.v, v_dims, v_strides, v_box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <class T, class TO, int NT>
@@ -721,10 +835,10 @@ cudaError_t run(const Args& a, const Plan& plan, DevCtl ctl, cudaStream_t stream
   Maps m;
   if (!make_maps(&m, a.cache)) return cudaErrorInvalidValue;
   auto kern = rows8_kernel<T, TO, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NT>());
   if (e != cudaSuccess) return e;
   const long long cut = plan.units - plan.whole;
-  kern<<<(unsigned)(plan.whole + cut * plan.parts), THREADS, SMEM, stream>>>(m, a, plan, ctl);
+  kern<<<(unsigned)(plan.whole + cut * plan.parts), THREADS, smem_bytes<NT>(), stream>>>(m, a, plan, ctl);
   if ((e = cudaGetLastError()) != cudaSuccess || plan.parts == 1) return e;
   PdlLaunch l(dim3((unsigned)(cut * plan.rows)), dim3(kDV / 2), 0, stream, true);
   return cudaLaunchKernelEx(&l.cfg, rows8_join_kernel<TO>, a, plan);
@@ -732,7 +846,9 @@ cudaError_t run(const Args& a, const Plan& plan, DevCtl ctl, cudaStream_t stream
 
 template <class T, class TO>
 cudaError_t run(const Args& a, const Plan& plan, DevCtl ctl, cudaStream_t stream) {
-  return plan.rows == 8 ? run<T, TO, 1>(a, plan, ctl, stream) : run<T, TO, 2>(a, plan, ctl, stream);
+  return plan.rows == 8    ? run<T, TO, 1>(a, plan, ctl, stream)
+         : plan.rows == 16 ? run<T, TO, 2>(a, plan, ctl, stream)
+                           : run<T, TO, 4>(a, plan, ctl, stream);
 }
 inline cudaError_t launch(const Args& a, gla_dtype out, const Plan& plan, DevCtl ctl, cudaStream_t stream) {
   const bool wide = out == GLA_FP32;
