@@ -28,7 +28,7 @@ SOURCES = ["api.cu", "decode.cu", "convert.cu", "chunk_fwd.cu", "chunk_bwd.cu", 
 HEADERS = ["ptx.cuh", "tmap.h", "kernels.h", "scan_common.cuh", "elem.cuh",
            "gated_scan.h", "layer_norm.h", "window_attn.h", "mma.cuh", "window_common.cuh",
            "window_wait.cuh", "api_checks.h", "rotary.h", "window_serve.h", "code8.cuh",
-           "window_packed.cuh", "window_chunk.cuh", "window_rows8.cuh"]
+           "window_packed.cuh", "window_chunk.cuh", "window_rows8.cuh", "window_join.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",

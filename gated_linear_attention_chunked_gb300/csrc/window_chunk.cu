@@ -21,7 +21,7 @@ Plan make_plan(int n, int n_tokens, int KV, int H, int window, int sink, int n_s
   const long long items = std::max(1ll, n_tokens / tokens) * ((tokens + p.per - 1) / p.per) * KV;
   const double tiles = (window + (double)sink + p.per) / BN + 1.5;
   double best = 1e30;
-  for (int parts = 1; parts <= 64 && parts * 2 <= tiles + 1; ++parts) {
+  for (int parts = 1; parts <= kMostParts && parts * 2 <= tiles + 1; ++parts) {
     const double rounds = (double)((items * parts + n_sm - 1) / n_sm);
     const double cost = rounds * (tiles / parts + 2 + (parts > 1 ? 2 : 0)) + (parts > 1 ? 2 : 0);
     if (cost < best) {
@@ -45,7 +45,7 @@ bool is_short(int n, int n_tokens, int KV, int H) {
 template <class TO>
 cudaError_t join(const ChunkArgs& a, const Plan& plan, cudaStream_t stream) {
   const int rows = plan.per * (a.H / a.cache.c.KV);
-  PdlLaunch l(dim3((unsigned)plan.units, (unsigned)((rows + 7) / 8)), dim3(256), 0, stream, true);
+  PdlLaunch l(dim3((unsigned)plan.units, (unsigned)rows), dim3(JOIN_THREADS), 0, stream, true);
   return cudaLaunchKernelEx(&l.cfg, window_chunk_join_kernel<TO>, a, plan);
 }
 

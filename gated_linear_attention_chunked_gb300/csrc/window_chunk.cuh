@@ -29,6 +29,7 @@
 
 #include "code8.cuh"
 #include "tmap.h"
+#include "window_join.cuh"
 #include "window_packed.cuh"
 #include "window_wait.cuh"
 
@@ -978,38 +979,22 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
   }
 }
 
-// One warp per row of a cut unit: o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p, in order.
+// One block per row of a cut unit.
 template <class TO>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(JOIN_THREADS)
 window_chunk_join_kernel(ChunkArgs a, Plan plan) {
   griddep_wait();
   const Partials ps(a.workspace, plan.units, plan.parts);
-  const int KV = a.cache.c.KV, G = a.H / KV, lane = threadIdx.x & 31;
-  const int unit = blockIdx.x, t = unit / KV, kv = unit % KV, row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int KV = a.cache.c.KV, G = a.H / KV;
+  const int unit = blockIdx.x, t = unit / KV, kv = unit % KV, row = blockIdx.y;
   if (t >= ps.tiles[0]) return;
   const int row0 = ps.tiles[2 + 2 * t];
   if (row >= ps.tiles[3 + 2 * t] * G) return;
   const long long at = (long long)unit * plan.parts * BM + row;
-  float top = -INFINITY;
-  for (int p = 0; p < plan.parts; ++p) top = fmaxf(top, ps.ml[at + (long long)p * BM].x);
-  float sum = 0.f, o[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int p = 0; p < plan.parts; ++p) {
-    const float2 ml = ps.ml[at + (long long)p * BM];
-    if (ml.x == -INFINITY) continue;  // a part that this row sees nothing of
-    const float f = ex2(ml.x - top);
-    sum = fmaf(f, ml.y, sum);
-    const float2* src = reinterpret_cast<const float2*>(ps.o + (at + (long long)p * BM) * kDV);
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      const float2 y = src[32 * j + lane];
-      o[2 * j] = fmaf(f, y.x, o[2 * j]);
-      o[2 * j + 1] = fmaf(f, y.y, o[2 * j + 1]);
-    }
-  }
-  const float inv = 1.f / sum;  // the token itself is in one of the parts: sum > 0
-  TO* out = static_cast<TO*>(a.o) + (((long long)row0 + row / G) * a.H + kv * G + row % G) * kDV;
-#pragma unroll
-  for (int j = 0; j < 3; ++j) store2(out + 64 * j + 2 * lane, o[2 * j] * inv, o[2 * j + 1] * inv);
+  join_row(
+      plan.parts, [&](int p) { return ps.ml[at + (long long)p * BM]; },
+      [&](int p) { return ps.o + (at + (long long)p * BM) * kDV; },
+      static_cast<TO*>(a.o) + (((long long)row0 + row / G) * a.H + kv * G + row % G) * kDV);
 }
 
 // Rows [outer, rows, heads, d] of 16 bits as boxes of `box_d` channels, `box_h` heads, `box_r` rows.

@@ -29,6 +29,7 @@
 
 #include "code8.cuh"
 #include "tmap.h"
+#include "window_join.cuh"
 #include "window_packed.cuh"
 
 namespace gla {
@@ -769,9 +770,9 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     for (int i = max(sent - STAGES, 0); i < sent; ++i) mbar_wait(bar + 8 * (i % STAGES), (i / STAGES) & 1, ctl, DRAIN_NS);
 }
 
-// Joins the parts of a row of a cut unit, in order: o = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p.
+// One block per row of a cut unit.
 template <class TO>
-__global__ void __launch_bounds__(kDV / 2)
+__global__ void __launch_bounds__(JOIN_THREADS)
 rows8_join_kernel(Args a, Plan plan) {
   griddep_wait();
   const int HB = plan.rows, cut = blockIdx.x / HB, row = blockIdx.x % HB, parts = plan.parts;
@@ -782,32 +783,22 @@ rows8_join_kernel(Args a, Plan plan) {
   const float* pw = reinterpret_cast<const float*>(static_cast<const char*>(a.workspace) +
                                                    table_bytes(plan.units - plan.whole)) +
                     ((long long)cut * HB + row) * parts * (kDV + 2);
-  const int c = threadIdx.x * 2;
-  float top = -INFINITY;
-  for (int k = 0; k < parts; ++k) top = fmaxf(top, pw[k * (kDV + 2) + kDV]);
-  float sum = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int k = 0; k < parts; ++k) {
-    const float2 ml = *reinterpret_cast<const float2*>(pw + k * (kDV + 2) + kDV);
-    const float2 x = *reinterpret_cast<const float2*>(pw + k * (kDV + 2) + c);
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-    sum = fmaf(f, ml.y, sum);
-    o0 = fmaf(f, x.x, o0);
-    o1 = fmaf(f, x.y, o1);
-  }
-  const float inv = 1.f / sum;
   const int KV = a.cache.c.KV, G = a.H / KV, R = u.row0 + row, i = R / G;
-  store2(static_cast<TO*>(a.o) + ((long long)(u.first + i) * a.H + u.kv * G + R - i * G) * kDV + c, o0 * inv,
-         o1 * inv);
+  join_row(
+      parts, [&](int p) { return *reinterpret_cast<const float2*>(pw + p * (kDV + 2) + kDV); },
+      [&](int p) { return pw + p * (kDV + 2); },
+      static_cast<TO*>(a.o) + ((long long)(u.first + i) * a.H + u.kv * G + R - i * G) * kDV);
 }
 
 // `units` at most, `likely` so many: as many whole ones as fill the device one or more times, and parts of
 // the others that fill it once more, of at least two rounds; nothing is cut where two do not fit.
 inline Plan make_plan(long long units, long long likely, int rows, int slots, int n_sm) {
-  const int hold = std::max(kHold * n_sm, 1), unit = 2 * ROUND, rest = (int)(likely % hold);
-  const int most = std::min((slots + unit - 1) / unit, 64);
-  const int parts = rest ? std::min(hold / rest, most) : 1;
-  if (parts < 2) return Plan{units, (int)units, 1, 0, rows};
-  const int part_slots = ((slots + parts - 1) / parts + unit - 1) / unit * unit;
+  const int hold = std::max(kHold * n_sm, 1), rest = (int)(likely % hold);
+  const int most = std::min((slots + 2 * ROUND - 1) / (2 * ROUND), kMostParts);
+  const int cut = rest ? std::min(hold / rest, most) : 1;
+  if (cut < 2) return Plan{units, (int)units, 1, 0, rows};
+  const int part_slots = ((slots + cut - 1) / cut + ROUND - 1) / ROUND * ROUND;
+  const int parts = (slots + part_slots - 1) / part_slots;
   return Plan{units, (int)(likely - rest), parts, part_slots, rows};
 }
 
@@ -840,7 +831,7 @@ cudaError_t run(const Args& a, const Plan& plan, DevCtl ctl, cudaStream_t stream
   const long long cut = plan.units - plan.whole;
   kern<<<(unsigned)(plan.whole + cut * plan.parts), THREADS, smem_bytes<NT>(), stream>>>(m, a, plan, ctl);
   if ((e = cudaGetLastError()) != cudaSuccess || plan.parts == 1) return e;
-  PdlLaunch l(dim3((unsigned)(cut * plan.rows)), dim3(kDV / 2), 0, stream, true);
+  PdlLaunch l(dim3((unsigned)(cut * plan.rows)), dim3(JOIN_THREADS), 0, stream, true);
   return cudaLaunchKernelEx(&l.cfg, rows8_join_kernel<TO>, a, plan);
 }
 
