@@ -43,7 +43,6 @@ constexpr int BM = 128, BN = 128;
 constexpr uint32_t K_BOX = 8192, V_BOX = 16384;  // 128 rows x 64 B, x 128 B
 constexpr uint32_t K_BYTES = 3 * K_BOX, V_BYTES = 3 * V_BOX;
 constexpr int LIST = 48;                         // items of a CTA
-constexpr int AHEAD = 4;                         // tiles that codes are prefetched ahead
 
 // Tokens of one sequence with the query heads of a key head, and the key tiles of one part of them: tile
 // i of an item is tile i + d of the page (128 slots each) or of the sequence's new tokens, d by where i
@@ -361,7 +360,6 @@ enum TileInfo : uint32_t { INFO_FRESH = 1, INFO_FIRST = 2, INFO_COLS = ~15u };  
 struct Maps {
   CUtensorMap q, k, v;    // the call's rows
   CUtensorMap pk, pv;     // the pages: 16-bit rows, or codes
-  CUtensorMap fk, fv;     // the pages in whole rows, for prefetches
 };
 
 // Loads of a tile's keys or values: from the page or the call's rows.
@@ -541,21 +539,11 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
       uint32_t armed = 0;
       Parities turn;
       int raw = 0;
-      Walk ahead;  // the prefetches'
-      ahead.begin(items, n_items);
-      int an = 0;
       bool ok = true;
       for (int x = 0; ok && x < n_items; ++x) {
         const Item& it = items[x];
         for (int i = it.tb; i < it.te; ++i, ++n) {
           const uint32_t s = n & 1;
-          for (; ahead.x < n_items && an <= n + AHEAD; ++an, ahead.step(items, n_items)) {
-            const Item& to = items[ahead.x];
-            const Tile t = Ask<CODES>::tile(to, ahead.i);
-            if (t.fresh()) continue;
-            tma_prefetch_4d(&maps.fk, 0, to.kv, t.s0, to.page);
-            tma_prefetch_4d(&maps.fv, 0, to.kv, t.s0, to.page);
-          }
           const Tile t = Ask<CODES>::tile(it, i);
           if (CODES && !t.fresh()) {
             if (raw > 0 && !(ok = await(cta, cta.bar(RAW_FREE + 1), (raw - 1) & 1, ctl))) break;
@@ -1034,13 +1022,10 @@ cudaError_t run(const ChunkArgs& a, const Plan& plan, DevCtl ctl, cudaStream_t s
   bool ok = make_map(&m.q, a.q, type, 2, kDK, a.H, N, 1, 32, G, plan.per, CU_TENSOR_MAP_SWIZZLE_64B) &&
             make_map(&m.k, a.k, type, 2, kDK, c.KV, N, 1, 32, 1, BN, CU_TENSOR_MAP_SWIZZLE_64B) &&
             make_map(&m.v, a.v, type, 2, kDV, c.KV, N, 1, 64, 1, BN, CU_TENSOR_MAP_SWIZZLE_128B);
-  const auto row = CODES ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type;
-  const int size = CODES ? 1 : 2;
-  ok = ok && make_map(&m.fk, c.k, row, size, kDK, c.KV, slots, pages, kDK, 1, BN, CU_TENSOR_MAP_SWIZZLE_NONE) &&
-       make_map(&m.fv, c.v, row, size, kDV, c.KV, slots, pages, kDV, 1, BN, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (CODES) {
-    m.pk = m.fk;
-    m.pv = m.fv;
+    const auto code = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    ok = ok && make_map(&m.pk, c.k, code, 1, kDK, c.KV, slots, pages, kDK, 1, BN, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+         make_map(&m.pv, c.v, code, 1, kDV, c.KV, slots, pages, kDV, 1, BN, CU_TENSOR_MAP_SWIZZLE_NONE);
   } else {
     ok = ok &&
          make_map(&m.pk, c.k, type, 2, kDK, c.KV, slots, pages, 32, 1, BN, CU_TENSOR_MAP_SWIZZLE_64B) &&
