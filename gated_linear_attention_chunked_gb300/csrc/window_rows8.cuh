@@ -56,7 +56,7 @@ constexpr int kHold = 3;
 // What the warps of a unit of NT groups of 8 rows share.
 template <int NT>
 struct Shared {
-  uint64_t full[kStages<NT>];          // mbarriers
+  uint64_t full[kStages<NT>], behind;  // mbarriers: a stage is there; the rounds are over
   uint8_t exps[WARPS][kStages<NT>][EXPS];
   alignas(16) uint8_t weights[2][8 * NT * P_ROW];  // of two rounds, [row][slot]
   uint2 q[NT][kDK / 16][32];           // the second operand of the scores' products
@@ -169,8 +169,8 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
   const int parts = cut < 0 ? 1 : plan.parts, part = cut < 0 ? 0 : cut % parts;
   const int part_slots = cut < 0 ? 1 << 30 : plan.part_slots;
   const int unit = cut < 0 ? (int)blockIdx.x : plan.whole + cut / parts;
-  if (tid < STAGES) {
-    mbar_init(bar + 8 * tid, 1);
+  if (tid <= STAGES) {
+    mbar_init(tid < STAGES ? bar + 8 * tid : smem_u32(&sh.behind), 1);
     fence_barrier_init();
   }
   if (tid == 0) {
@@ -433,6 +433,8 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
   for (int i = 0; i < rounds; ++i) {
     const int s0 = first_slot(i);
     if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(bar + 8 * (i % STAGES), (i / STAGES) & 1, ctl));
+    if (i == ctl.stall_step && w == 0)  // the give-up path's diagnostic (see chunk_fwd.cu)
+      dead = !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.behind), 0, ctl));
     copy_wait<STAGES - 1>();
     __syncwarp();
     float z[SB / 16][NT][4];  // slots 16 h + g, + 8
@@ -588,6 +590,7 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     }
   }
   copy_wait<0>();
+  if (tid == 0) mbar_arrive(smem_u32(&sh.behind));
   // 128 off the codes, and the sums' own units
   if (g == 0) {
 #pragma unroll
