@@ -140,7 +140,7 @@ gla_status gla_window_cache8_read(const void* pool_k, const void* pool_v,
   const gla::ServeCache c{{const_cast<void*>(pool_k), const_cast<void*>(pool_v), page, n, n_pages,
                            pool_layers, layer, KV, window, sink, out_dtype},
                           const_cast<signed char*>(pool_e)};
-  return done(gla::launch_window_read8(c, k, v, ctl, stream));
+  return done(gla::launch_window_read8(c, k, v, nullptr, nullptr, ctl, stream));
 }
 
 size_t gla_window_attn8_decode_workspace_size(int n_active, int H, int KV, int window, int sink) {

@@ -112,11 +112,12 @@ append_kernel(AppendArgs a, long long rows, DevCtl ctl) {
   }
 }
 
-// One thread per 16 codes.  Rows: [n, slots, KV], of 6 (keys) and 12 (values) such pieces.
+// One thread per 16 codes.  Rows: [n, slots, KV], of 6 (keys) and 12 (values) such pieces.  pos: only slots
+// that hold a token; copies: where page n went, n or (its own out of range) -1.
 template <class T>
 __global__ void __launch_bounds__(THREADS)
 read8_kernel(ServeCache cache, uint4* __restrict__ k, uint4* __restrict__ v, long long rows,
-             DevCtl ctl) {
+             const int* __restrict__ pos, int* __restrict__ copies, DevCtl ctl) {
   const WindowCache& c = cache.c;
   const int slots = c.window + c.sink;
   const long long x = (long long)blockIdx.x * THREADS + threadIdx.x, row = x / 18;
@@ -125,10 +126,13 @@ read8_kernel(ServeCache cache, uint4* __restrict__ k, uint4* __restrict__ v, lon
   const long long ns = row / c.KV;
   const int kv = (int)(row - ns * c.KV), n = (int)(ns / slots), s = (int)(ns - (long long)n * slots);
   const int page = __ldg(c.page + n);
-  if (page < 0 || page >= c.n_pages) {
+  const bool there = page >= 0 && page < c.n_pages;
+  if (copies && s == 0 && kv == 0 && piece == 0) copies[n] = there ? n : -1;
+  if (!there) {
     if (s == 0 && piece == 0) record_error(ctl, DEV_RANGE);
     return;
   }
+  if (pos && s >= __ldg(pos + n)) return;
   const long long at = (long long)page * c.pool_layers + c.layer, src = (at * slots + s) * c.KV + kv;
   const bool key = piece < 6;
   const uint4 w = key ? __ldcs(static_cast<const uint4*>(c.k) + src * 6 + piece)
@@ -159,17 +163,17 @@ cudaError_t launch_window_append(const AppendArgs& a, DevCtl ctl, cudaStream_t s
   return cudaGetLastError();
 }
 
-cudaError_t launch_window_read8(const ServeCache& cache, void* k, void* v, DevCtl ctl,
-                                cudaStream_t stream) {
+cudaError_t launch_window_read8(const ServeCache& cache, void* k, void* v, const int* pos, int* copies,
+                                DevCtl ctl, cudaStream_t stream) {
   const WindowCache& c = cache.c;
   const long long rows = (long long)c.n * (c.window + c.sink) * c.KV;
   const unsigned grid = (unsigned)((rows * 18 + THREADS - 1) / THREADS);
   if (c.type == GLA_BF16)
     read8_kernel<__nv_bfloat16><<<grid, THREADS, 0, stream>>>(
-        cache, static_cast<uint4*>(k), static_cast<uint4*>(v), rows, ctl);
+        cache, static_cast<uint4*>(k), static_cast<uint4*>(v), rows, pos, copies, ctl);
   else
     read8_kernel<__half><<<grid, THREADS, 0, stream>>>(cache, static_cast<uint4*>(k),
-                                                       static_cast<uint4*>(v), rows, ctl);
+                                                       static_cast<uint4*>(v), rows, pos, copies, ctl);
   return cudaGetLastError();
 }
 

@@ -42,6 +42,23 @@ bool is_short(int n, int n_tokens, int KV, int H) {
   return (long long)n_tokens * (H / KV) <= 32ll * std::min(n, n_tokens);
 }
 
+// Over pages of 8 bits, where sequences have more than two items of 128 rows each, the pages are first written
+// out as 16-bit rows, each once: an item that turns a tile of codes into operands for itself takes 2.8 us
+// for it (four warps do), one over 16 bits 1.2, and the copy costs HBM 864 bytes a slot and key head.  4 x 2,048
+// tokens of 16 heads on 1,024 slots of 4 key heads: 107 us in place of 145; with two items each (96 x 16
+// tokens of 16 heads on 2,052) both take 160.  As long as the copy stays below a GiB.
+struct Copy {
+  size_t v, pages, bytes;  // offsets of the values and of the copies' indexes; a multiple of 256
+};
+bool copies_pages(int n, int n_tokens, int KV, int H, int window, int sink, Copy* copy) {
+  const size_t rows = (size_t)n * (window + (size_t)sink) * KV;
+  if ((long long)n_tokens * (H / KV) <= 256ll * n || rows > (1u << 30) / (2 * (kDK + kDV))) return false;
+  copy->v = (rows * kDK * 2 + 255) / 256 * 256;
+  copy->pages = copy->v + (rows * kDV * 2 + 255) / 256 * 256;
+  copy->bytes = copy->pages + ((size_t)n * 4 + 255) / 256 * 256;
+  return true;
+}
+
 template <class TO>
 cudaError_t join(const ChunkArgs& a, const Plan& plan, cudaStream_t stream) {
   const int rows = plan.per * (a.H / a.cache.c.KV);
@@ -56,15 +73,32 @@ size_t window_chunk_workspace_bytes(int n, int n_tokens, int KV, int H, int wind
   if (codes && is_short(n, n_tokens, KV, H))
     return window_short8_workspace_bytes(n, n_tokens, KV, H, window + sink, n_sm);
   const Plan p = make_plan(n, n_tokens, KV, H, window, sink, n_sm);
-  return p.parts > 1 ? Partials::bytes(p.units, p.parts) : 0;
+  Copy copy;
+  const size_t pages = codes && copies_pages(n, n_tokens, KV, H, window, sink, &copy) ? copy.bytes : 0;
+  return pages + (p.parts > 1 ? Partials::bytes(p.units, p.parts) : 0);
 }
 
-cudaError_t launch_window_chunk(const ChunkArgs& a, int n_sm, DevCtl ctl, cudaStream_t stream) {
-  const WindowCache& c = a.cache.c;
+cudaError_t launch_window_chunk(const ChunkArgs& call, int n_sm, DevCtl ctl, cudaStream_t stream) {
+  ChunkArgs a = call;
+  WindowCache& c = a.cache.c;
   if (a.cache.exps && is_short(c.n, a.tok.n_tokens, c.KV, a.H))
     return launch_window_short8(a, n_sm, ctl, stream);
   const Plan plan = make_plan(c.n, a.tok.n_tokens, c.KV, a.H, c.window, c.sink, n_sm);
   cudaError_t e;
+  Copy copy;
+  if (a.cache.exps && copies_pages(c.n, a.tok.n_tokens, c.KV, a.H, c.window, c.sink, &copy)) {
+    char* const to = static_cast<char*>(a.workspace);
+    int* const pages = reinterpret_cast<int*>(to + copy.pages);
+    if ((e = launch_window_read8(a.cache, to, to + copy.v, a.tok.pos, pages, ctl, stream)) != cudaSuccess) return e;
+    c.k = to;
+    c.v = to + copy.v;
+    c.page = pages;
+    c.n_pages = c.n;
+    c.pool_layers = 1;
+    c.layer = 0;
+    a.cache.exps = nullptr;
+    a.workspace = to + copy.bytes;
+  }
   if (a.cache.exps) e = launch8(a, plan, ctl, stream);
   else if (c.type == GLA_BF16) e = run<__nv_bfloat16, false>(a, plan, ctl, stream);
   else e = run<__half, false>(a, plan, ctl, stream);

@@ -26,9 +26,11 @@ struct AppendArgs {
   const void* v;     // [n_tokens,KV,192]
 };
 cudaError_t launch_window_append(const AppendArgs& a, DevCtl ctl, cudaStream_t stream);
-// The pages of c.page as 16-bit rows: k [n,slots,KV,96], v [n,slots,KV,192] of type c.type.
-cudaError_t launch_window_read8(const ServeCache& cache, void* k, void* v, DevCtl ctl,
-                                cudaStream_t stream);
+// The pages of c.page as 16-bit rows: k [n,slots,KV,96], v [n,slots,KV,192] of type c.type.  pos [n] or null:
+// only slots that hold a token of a sequence of so many; copies [n] or null (written): n, or -1 where the page
+// is out of range.
+cudaError_t launch_window_read8(const ServeCache& cache, void* k, void* v, const int* pos, int* copies,
+                                DevCtl ctl, cudaStream_t stream);
 
 struct Decode8Args {
   ServeCache cache;

@@ -96,8 +96,8 @@ GLA_API gla_status gla_get_device_error(void);
  * kernels and the operators around the mixer (default 2e9).  A wait that runs
  * out records GLA_ERR_TIMEOUT and the kernel finishes early without touching
  * memory outside its tensors.
- * In the windowed attention's forward and gradient, some of whose waits last as long as a tile of
- * queries takes to see all its keys, the limit counts from the last step that the CTA made.
+ * In the windowed attention's forward, gradient and chunks over pages, some of whose waits last as long as
+ * a tile of queries takes to see all its keys, the limit counts from the last step that the CTA made.
  * Applies to calls made after it returns.  ns == 0 restores the default. */
 GLA_API gla_status gla_set_wait_timeout_ns(unsigned long long ns);
 
@@ -111,8 +111,8 @@ GLA_API gla_status gla_wait_probe(cudaStream_t stream);
 
 /* Diagnostic of the give-up paths (no counterpart in the article).  For calls made after it
  * returns (process-wide), the tensor-core issuer of every CTA of the chunked forward, backward
- * and segment-pass kernels, and of the windowed attention's forward and gradient, on reaching
- * chunk step (streamed tile) `step` of its loop, waits on a barrier whose phase completes only
+ * and segment-pass kernels, and of the windowed attention's forward, gradient and chunks over pages,
+ * on reaching chunk step (streamed tile) `step` of its loop, waits on a barrier whose phase completes only
  * after that loop.  The bounded wait gives up after the limit of gla_set_wait_timeout_ns, records
  * GLA_ERR_TIMEOUT and raises the CTA's abort flag; every role then leaves its loop (one path per
  * warp), drains its copies and tensor-core work, frees its tensor memory and exits.  In the gated
@@ -120,7 +120,7 @@ GLA_API gla_status gla_wait_probe(cudaStream_t stream);
  * does so at round `step` of tiles and leaves before it hands on its pair; the others give up
  * waiting for that, and each leaves only when nothing is on its way into its memory any more.
  * The layer norm's rings (rows that they take) give up at their row, or pair of rows, `step`, and
- * drain.  The call's outputs are then undefined; the context stays usable.  step < 0 (the
+ * drain; the step and the short chunks over 8-bit pages at their round of 64 slots.  The call's outputs are then undefined; the context stays usable.  step < 0 (the
  * default) turns it off.  No fault,
  * trap or unbounded wait is involved.  The mbarrier wait instruction suspends the waiting
  * thread until the phase completes (up to a hardware limit), so ordinary waits end before
@@ -756,9 +756,12 @@ GLA_API gla_status gla_window_cache_append(const void* k, const void* v, gla_dty
  *   o            [n_tokens,H,192] out_dtype: in_dtype or GLA_FP32 (written)
  *   workspace    gla_window_attn_chunk_workspace_size() bytes, 256-byte aligned (0: not needed).  The
  *                size depends on the device current at the call
- * Softmax, sums and roundings as in gla_window_attn_fwd; slots that no token has reached and rows of
- * other sequences may hold anything, NaN included.  Results repeat bit for bit.  n == 0 or n_tokens == 0
- * returns GLA_OK without launching.
+ * Pages may repeat here.  Softmax, sums and roundings as in gla_window_attn_fwd, and as there q, k and v of the
+ * sequences' rows must be finite, and what their slots hold; slots that no token has reached and rows of other
+ * sequences may hold anything, NaN included.  Over 8-bit pages codes are multiplied exactly.  Where sequences
+ * have few rows (n_tokens H / KV <= 32 min(n, n_tokens)) a slot's weight rounds to fp16 with the 2^e of its
+ * value: by 2^-11 of itself, or by 2^-25 of the page's largest row, and what is below 2^-78 in a page is lost.
+ * Results repeat bit for bit.  n == 0 or n_tokens == 0 returns GLA_OK without launching.
  */
 GLA_API size_t gla_window_attn_chunk_workspace_size(int n, int n_tokens, int H, int KV, int window,
                                                     int sink);
@@ -773,7 +776,7 @@ GLA_API gla_status gla_window_attn_chunk(const void* pool_k, const void* pool_v,
 
 /* gla_window_attn8_decode_step: gla_window_attn_decode_step (whose rules for page, pos, o and the
  * workspace hold) over pages of 8 bits: q, k, v of in_dtype; the token's key and value go into the page
- * as codes, and o[n] takes them as given. */
+ * as codes, and o[n] takes them as given.  Weights round as in gla_window_attn_chunk over few rows. */
 GLA_API size_t gla_window_attn8_decode_workspace_size(int n_active, int H, int KV, int window,
                                                       int sink);
 GLA_API gla_status gla_window_attn8_decode_step(void* pool_k, void* pool_v, signed char* pool_e,

@@ -5,8 +5,7 @@ What goes into pages is exact on both sides (codes and exponents are whole numbe
 equality.  Attention is bounded as in test_gpu_window_attn.py, with u half a step of the 16-bit type: the
 weights round once for the product with v, the output once, |do| <= u (sum p |v| + |o|), sums and scores
 in fp32 add less than 1024 roundings of 2^-24 of the sums of magnitudes, and below 2^-14 fp16 rounds by
-up to 2^-25 whatever the value (TINY, times |v|; with 8-bit pages the products take c 2^e, exactly).  A
-new token's own weight and value in a step over 8-bit pages are not rounded at all."""
+up to 2^-25 whatever the value (TINY, times |v|; with 8-bit pages the products take c 2^e or c, exactly)."""
 import numpy as np
 import pytest
 
