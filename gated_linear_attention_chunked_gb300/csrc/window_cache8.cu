@@ -38,7 +38,7 @@ __device__ __forceinline__ Target target(const AppendArgs& a, int token, const D
     if (given < 0 || given > count) record_error(ctl, DEV_RANGE);
     count = min(max(given, 0), count);
   }
-  const long long t = (long long)s.pos + i;
+  const int t = s.pos + i;
   if (i >= count || (t >= c.sink && i < count - c.window)) return none;
   return Target{slot_at(t, c.window, c.sink), (long long)s.page * c.pool_layers + c.layer};
 }
@@ -64,8 +64,10 @@ append_kernel(AppendArgs a, long long rows, DevCtl ctl) {
   const uint4* vs = static_cast<const uint4*>(a.v);
   // lane l looks up row l / 4; the values' lanes take theirs from it
   const long long mine = row0 + (lane >> 2);
-  const Target at = mine < rows ? target(a, (int)(mine / KV), ctl) : Target{-1, 0};
-  const int kv = (int)(mine % KV);
+  // (rows below 2^31 have a token by one 32-bit division)
+  const int token = rows >> 31 ? (int)(mine / KV) : (int)((unsigned)mine / (unsigned)KV);
+  const Target at = mine < rows ? target(a, token, ctl) : Target{-1, 0};
+  const int kv = (int)(mine - (long long)token * KV);
   if (!__any_sync(0xffffffffu, at.slot >= 0)) return;
   uint4 x[3][3];
   int slot[3], head[3];
@@ -114,17 +116,18 @@ append_kernel(AppendArgs a, long long rows, DevCtl ctl) {
 
 // One thread per 16 codes.  Rows: [n, slots, KV], of 6 (keys) and 12 (values) such pieces.  pos: only slots
 // that hold a token; copies: where page n went, n or (its own out of range) -1.
-template <class T>
+// I: a type that holds the number of pieces.  (With 64-bit divisions the kernel was bound by instructions.)
+template <class T, class I>
 __global__ void __launch_bounds__(THREADS)
 read8_kernel(ServeCache cache, uint4* __restrict__ k, uint4* __restrict__ v, long long rows,
              const int* __restrict__ pos, int* __restrict__ copies, DevCtl ctl) {
   const WindowCache& c = cache.c;
   const int slots = c.window + c.sink;
-  const long long x = (long long)blockIdx.x * THREADS + threadIdx.x, row = x / 18;
-  if (row >= rows) return;
+  const I x = (I)blockIdx.x * THREADS + threadIdx.x, row = x / 18;
+  if (row >= (I)rows) return;
   const int piece = (int)(x - row * 18);
-  const long long ns = row / c.KV;
-  const int kv = (int)(row - ns * c.KV), n = (int)(ns / slots), s = (int)(ns - (long long)n * slots);
+  const I ns = row / (I)c.KV;
+  const int kv = (int)(row - ns * (I)c.KV), n = (int)(ns / (I)slots), s = (int)(ns - (I)n * (I)slots);
   const int page = __ldg(c.page + n);
   const bool there = page >= 0 && page < c.n_pages;
   if (copies && s == 0 && kv == 0 && piece == 0) copies[n] = there ? n : -1;
@@ -146,7 +149,7 @@ read8_kernel(ServeCache cache, uint4* __restrict__ k, uint4* __restrict__ v, lon
     o[2 * i] = scaled<T>(o[2 * i], sc);
     o[2 * i + 1] = scaled<T>(o[2 * i + 1], sc);
   }
-  uint4* dst = key ? k + row * kCK + 2 * piece : v + row * kCV + 2 * (piece - 6);
+  uint4* dst = key ? k + (size_t)row * kCK + 2 * piece : v + (size_t)row * kCV + 2 * (piece - 6);
   __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
   __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
 }
@@ -168,12 +171,17 @@ cudaError_t launch_window_read8(const ServeCache& cache, void* k, void* v, const
   const WindowCache& c = cache.c;
   const long long rows = (long long)c.n * (c.window + c.sink) * c.KV;
   const unsigned grid = (unsigned)((rows * 18 + THREADS - 1) / THREADS);
-  if (c.type == GLA_BF16)
-    read8_kernel<__nv_bfloat16><<<grid, THREADS, 0, stream>>>(
-        cache, static_cast<uint4*>(k), static_cast<uint4*>(v), rows, pos, copies, ctl);
-  else
-    read8_kernel<__half><<<grid, THREADS, 0, stream>>>(cache, static_cast<uint4*>(k),
-                                                       static_cast<uint4*>(v), rows, pos, copies, ctl);
+  auto run = [&](auto kern) {
+    kern<<<grid, THREADS, 0, stream>>>(cache, static_cast<uint4*>(k), static_cast<uint4*>(v), rows, pos, copies, ctl);
+  };
+  const bool wide = (long long)grid * THREADS >> 32;
+  if (c.type == GLA_BF16) {
+    if (wide) run(read8_kernel<__nv_bfloat16, unsigned long long>);
+    else run(read8_kernel<__nv_bfloat16, unsigned>);
+  } else {
+    if (wide) run(read8_kernel<__half, unsigned long long>);
+    else run(read8_kernel<__half, unsigned>);
+  }
   return cudaGetLastError();
 }
 

@@ -5,8 +5,8 @@
 
 namespace gla {
 
-__device__ __forceinline__ int slot_at(long long t, int window, int sink) {
-  return t < sink ? (int)t : sink + (int)((t - sink) % window);
+__device__ __forceinline__ int slot_at(int t, int window, int sink) {
+  return t < sink ? t : sink + (int)((unsigned)(t - sink) % (unsigned)window);
 }
 
 // The sequence whose tokens hold row i: the last b with start[b] <= i (-1: none; n: rows behind all).
