@@ -5,8 +5,10 @@
 //
 //   z = 2^e (c . q),  o = sum p 2^e c / sum p   with the rows' codes c as fp16 operands, exactly
 //
-// whatever the call's type.  An operand is (c + 128) 2^-24, a value without an exponent: an exclusive or and
-// a byte permute; the 128 comes off by a product with the queries' sum before and the weights' sum after.
+// whatever the call's type.  An operand of the scores is (c + 128) 2^-24, a value without an exponent: an
+// exclusive or and a byte permute; the 128 comes off by a product with the queries' sum before.  The values are
+// c itself, one subtraction more: with 128 in sums of thousands of values that cancel, what the tensor cores cut
+// off would be 1.5e-4 of the result.
 // Queries of bf16 are scaled by a power of two per row into fp16's range; the values' 2^e goes into the
 // weight, relative to a common e_ref within 4 of the largest so far, so that a weight rounds by 2^-11 of
 // itself or by 2^-25 of the weight of the page's largest row.  The new tokens' own keys and values are taken as
@@ -63,7 +65,7 @@ struct Shared {
   alignas(16) uint8_t weights[2][8 * NT * P_ROW];  // of two rounds, [row][slot]
   uint2 q[NT][kDK / 16][32];           // the second operand of the scores' products
   float z0[8 * NT], zs[8 * NT];        // of a row: - q . (code 0), a score's factor
-  float top[WARPS][8 * NT], sum[WARPS][8 * NT], zero[WARPS][8 * NT];
+  float top[WARPS][8 * NT], sum[WARPS][8 * NT];
   int e_top[WARPS];
   int found[4];
   int upto[THREADS + 1], sums[WARPS];  // units before a slice of the sequences
@@ -368,22 +370,20 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     zs[r] = sh.zs[8 * (r >> 1) + t2 + (r & 1)];
   }
   auto at = [&](int r) { return s.pos + row_of(8 * (r >> 1) + t2 + (r & 1)) / G; };  // a row's position
-  float acc[TILES][NT][4], wsum[NT][4];  // wsum: of the warp's own slots, of code 0
+  float acc[TILES][NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      wsum[n][k] = 0.f;
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int j = 0; j < TILES; ++j) acc[j][n][k] = 0.f;
-    }
   float m[NR], l[NR];  // base 2, the same in all warps; l of this thread's slots
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
   }
-  int e_ref = -1000;  // acc is in units of 2^(e_ref - 24); -60 at least: what is below 2^-78 in a page is lost
+  int e_ref = -1000;  // acc is in units of 2^e_ref; -60 at least: what is below 2^-78 in a page is lost
 
   // The rare round in which a score passes a row's maximum by more than 8, or an exponent e_ref by more than 4
   // (weights of up to 2^12 lose nothing in fp16): new ones for all, and the sums in their units.
@@ -409,7 +409,6 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
       const float keep = now == m[r] || m[r] == -INFINITY ? 1.f : ex2(m[r] - now);
       m[r] = now;
       l[r] *= keep;
-      wsum[r >> 1][r & 1] *= keep * f;
 #pragma unroll
       for (int j = 0; j < TILES; ++j) {
         acc[j][r >> 1][r & 1] *= keep * f;
@@ -440,7 +439,8 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     copy_wait<STAGES - 1>();
     __syncwarp();
     float z[SB / 16][NT][4];  // slots 16 h + g, + 8
-    float2 f[SB / 8];         // the factors of the thread's slots, 8 k + g
+    float f[SB / 8];          // the factors of the thread's slots, 8 k + g: of keys,
+    uint32_t fv[SB / 8];      // of values, twice
     int ev = -128;
     float ks = 0.f;
     bool up = false;
@@ -482,13 +482,13 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
       if (!all && !(((seen.bits(s.pos + i0, s0) & there) >> (lane & (SB - 1))) & 1)) ev = -128;
       ks = scale_of((signed char)ex.x);
 #pragma unroll
-      for (int k = 0; k < SB / 8; ++k) f[k].x = __shfl_sync(0xffffffffu, ks, 8 * k + g);
+      for (int k = 0; k < SB / 8; ++k) f[k] = __shfl_sync(0xffffffffu, ks, 8 * k + g);
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int k = 0; k < SB / 8; ++k) {
           float& x = z[k >> 1][r >> 1][2 * (k & 1) + (r & 1)];
-          x = x * zs[r] * f[k].x;
+          x = x * zs[r] * f[k];
         }
       if (!all) {
 #pragma unroll
@@ -520,9 +520,10 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     }
     up |= e_top > e_ref + 4;
     auto weigh = [&] {
-      const float vs = pow2(min(max(ev - e_ref, -126), 8));
+      const __half2 vs = __float2half2_rn(pow2(min(max(ev - e_ref, -126), 8)));
 #pragma unroll
-      for (int k = 0; k < SB / 8; ++k) f[k].y = __shfl_sync(0xffffffffu, vs, 8 * k + g);
+      for (int k = 0; k < SB / 8; ++k)
+        fv[k] = __shfl_sync(0xffffffffu, reinterpret_cast<const uint32_t&>(vs), 8 * k + g);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float base[2];
@@ -534,13 +535,13 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
         uint32_t pf[SB / 8];
 #pragma unroll
         for (int k = 0; k < SB / 8; ++k) {
-          float p[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            p[j] = ex2(z[k >> 1][n][2 * (k & 1) + j] - base[j]);
-            part_sum[2 * n + j] += p[j];
-          }
-          pf[k] = pack2<__half>(p[0] * f[k].y, p[1] * f[k].y);
+          // the sum is of the rounded weights: where one outweighs the others, its rounding cancels
+          pf[k] = pack2<__half>(ex2(z[k >> 1][n][2 * (k & 1)] - base[0]), ex2(z[k >> 1][n][2 * (k & 1) + 1] - base[1]));
+          const float2 p = halves<__half>(pf[k]);
+          part_sum[2 * n] += p.x;
+          part_sum[2 * n + 1] += p.y;
+          const __half2 y = __hmul2(reinterpret_cast<const __half2&>(pf[k]), reinterpret_cast<const __half2&>(fv[k]));
+          pf[k] = reinterpret_cast<const uint32_t&>(y);
         }
         static_assert(SB == 16, "a store of two matrices");
         stsm2t(p_to + (i & 1) * (HB * P_ROW) + n * (8 * P_ROW), pf[0], pf[1]);
@@ -576,45 +577,24 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t x4[4];
-          whole16(x[2 * h], x4[0], x4[1]);
-          whole16(x[2 * h + 1], x4[2], x4[3]);
+          whole_of<__half, true>(x[2 * h], x4[0], x4[1]);
+          whole_of<__half, true>(x[2 * h + 1], x4[2], x4[3]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma16816<__half>(acc[j][n], x4, pf[n][2 * h], pf[n][2 * h + 1]);
-        }
-      }
-      if (y == w >> 1) {
-        const uint32_t zero[4] = {kZero16, kZero16, kZero16, kZero16};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma16816<__half>(wsum[n], zero, w & 1 ? pf[n][2] : pf[n][0], w & 1 ? pf[n][3] : pf[n][1]);
         }
       }
     }
   }
   copy_wait<0>();
   if (tid == 0) mbar_arrive(smem_u32(&sh.behind));
-  // 128 off the codes, and the sums' own units
-  if (g == 0) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      *reinterpret_cast<float2*>(sh.zero[w] + 8 * n + t2) = make_float2(wsum[n][0], wsum[n][1]);
-  }
-  __syncthreads();
   {
     const float unit_of = pow2(min(max(e_ref, -126), 127));
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      float zero = 0.f;
+    for (int j = 0; j < TILES; ++j)
 #pragma unroll
-      for (int k = 0; k < WARPS; ++k) zero += sh.zero[k][8 * (r >> 1) + t2 + (r & 1)];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < TILES; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float& x = acc[j][r >> 1][2 * h + (r & 1)];
-          x = (x - zero) * 16777216.f * unit_of;
-        }
-    }
+        for (int k = 0; k < 4; ++k) acc[j][n][k] *= unit_of;
   }
 
   // ---- the new tokens, 16 a warp
@@ -670,10 +650,12 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
             const float base = m[2 * n + j] == -INFINITY ? 0.f : m[2 * n + j];
             z[n][j] = ex2(z[n][j] - base);
             z[n][2 + j] = ex2(z[n][2 + j] - base);
-            part_sum[2 * n + j] = z[n][j] + z[n][2 + j];
           }
-          stsm2t(buf + (8 * n + (lane & 7)) * P_ROW + (16 * w + ((lane >> 3) & 1) * 8) * 2,
-                 pack2<T>(z[n][0], z[n][1]), pack2<T>(z[n][2], z[n][3]));
+          const uint32_t lo = pack2<T>(z[n][0], z[n][1]), hi = pack2<T>(z[n][2], z[n][3]);
+          const float2 x = halves<T>(lo), y = halves<T>(hi);
+          part_sum[2 * n] = x.x + y.x;
+          part_sum[2 * n + 1] = x.y + y.y;
+          stsm2t(buf + (8 * n + (lane & 7)) * P_ROW + (16 * w + ((lane >> 3) & 1) * 8) * 2, lo, hi);
         }
       };
       if (__syncthreads_or(up)) refer(top, -1000);
