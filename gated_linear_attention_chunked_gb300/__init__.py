@@ -160,6 +160,8 @@ def _layer_calls():
         "window_cache_append": ([_P, _P, _I] + [_P] * 7 + [_I] * 10 + [_P], _I),
         "window_cache8_read": ([_P] * 4 + [_I] * 6 + [_P, _P] + [_I] * 4 + [_P], _I),
         "window_attn_chunk_workspace_size": ([_I] * 6, _S),
+        "window_attn_chunk16_workspace_size": ([_I] * 6, _S),
+        "window_attn_chunk8_workspace_size": ([_I] * 6, _S),
         "window_attn_chunk": ([_P] * 6 + [_I] * 7 + [_P] * 3 + [_I, _P, _I, _P, _S] + [_I] * 4 + [_P],
                               _I),
         "window_attn8_decode_workspace_size": ([_I] * 5, _S),

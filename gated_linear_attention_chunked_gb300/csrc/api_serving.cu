@@ -197,14 +197,24 @@ static size_t chunk_bytes(int n, int n_tokens, int H, int KV, int window, int si
              : gla::window_chunk_workspace_bytes(n, n_tokens, KV, H, window, sink, codes, sm_count());
 }
 
-size_t gla_window_attn_chunk_workspace_size(int n, int n_tokens, int H, int KV, int window,
-                                            int sink) {
+static size_t checked_chunk_bytes(int n, int n_tokens, int H, int KV, int window, int sink, bool codes) {
   if (check_window(GLA_BF16, GLA_BF16, window, sink, H, KV, gla::kDK, gla::kDV) != GLA_OK ||
       check_chunk(n, n_tokens, H, KV, window, sink) != GLA_OK)
     return 0;
-  // enough for pages of either kind
-  return std::max(chunk_bytes(n, n_tokens, H, KV, window, sink, false),
-                  chunk_bytes(n, n_tokens, H, KV, window, sink, true));
+  return chunk_bytes(n, n_tokens, H, KV, window, sink, codes);
+}
+size_t gla_window_attn_chunk16_workspace_size(int n, int n_tokens, int H, int KV, int window,
+                                              int sink) {
+  return checked_chunk_bytes(n, n_tokens, H, KV, window, sink, false);
+}
+size_t gla_window_attn_chunk8_workspace_size(int n, int n_tokens, int H, int KV, int window,
+                                             int sink) {
+  return checked_chunk_bytes(n, n_tokens, H, KV, window, sink, true);
+}
+size_t gla_window_attn_chunk_workspace_size(int n, int n_tokens, int H, int KV, int window,
+                                            int sink) {
+  return std::max(checked_chunk_bytes(n, n_tokens, H, KV, window, sink, false),
+                  checked_chunk_bytes(n, n_tokens, H, KV, window, sink, true));
 }
 
 gla_status gla_window_attn_chunk(const void* pool_k, const void* pool_v,

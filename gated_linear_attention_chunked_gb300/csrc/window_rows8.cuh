@@ -91,7 +91,7 @@ struct Args {
 // CTAs: a unit each for the first `whole` units, `parts` for each of the others.
 struct Plan {
   long long units;   // at most
-  int whole, parts, part_slots, rows;  // rows of a unit: 8 or 16
+  int whole, parts, part_slots, rows;  // rows of a unit: 8, 16 or 32
 };
 struct Maps {
   CUtensorMap k, v;
@@ -782,7 +782,9 @@ rows8_join_kernel(Args a, Plan plan) {
 inline Plan make_plan(long long units, long long likely, int rows, int slots, int n_sm) {
   const int hold = std::max(kHold * n_sm, 1), rest = (int)(likely % hold);
   const int most = std::min((slots + 2 * ROUND - 1) / (2 * ROUND), kMostParts);
-  const int cut = rest ? std::min(hold / rest, most) : 1;
+  // (where many more units may come than are likely, each of those has room for as many parts)
+  const long long room = std::max(4ll * hold / std::max(units - (likely - rest), 1ll), 1ll);
+  const int cut = rest ? (int)std::min<long long>(std::min(hold / rest, most), room) : 1;
   if (cut < 2) return Plan{units, (int)units, 1, 0, rows};
   const int part_slots = ((slots + cut - 1) / cut + ROUND - 1) / ROUND * ROUND;
   const int parts = (slots + part_slots - 1) / part_slots;

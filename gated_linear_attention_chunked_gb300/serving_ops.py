@@ -150,10 +150,14 @@ def window_cache8_read(pool_k, pool_v, page, pool_e, window, sink=0, *, layer=0,
 
 
 # --------------------------------------------------------------------------- attention
-def window_attn_chunk_workspace_size(n, n_tokens, H, KV, window, sink=0) -> int:
+def window_attn_chunk_workspace_size(n, n_tokens, H, KV, window, sink=0, bits=None) -> int:
+    """Bytes of `workspace` of window_attn_chunk over pages of `bits` 16 or 8 (None: enough for either)."""
     if (n | n_tokens | H | KV | window | sink) >> 31:
         _fit(n, n_tokens, H, KV, window, sink)
-    return _ops._library().gla_window_attn_chunk_workspace_size(n, n_tokens, H, KV, window, sink)
+    if bits not in (None, 8, 16):
+        raise ValueError(f"bits must be 8 or 16, got {bits}")
+    size = getattr(_ops._library(), f"gla_window_attn_chunk{bits or ''}_workspace_size")
+    return size(n, n_tokens, H, KV, window, sink)
 
 
 def window_attn_chunk(pool_k, pool_v, page, pos, start, q, k, v, window, sink=0, *, layer=0,
@@ -176,8 +180,9 @@ def window_attn_chunk(pool_k, pool_v, page, pos, start, q, k, v, window, sink=0,
             raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
         kp, vp, ep = _pools(pool_k, pool_v, pool_e, dev, t, P, PL, window + sink, KV, dk, dv)
         lib = _ops._library()
-        wp, wb, hold = _ops._scratch(
-            lib.gla_window_attn_chunk_workspace_size(n, N, H, KV, window, sink), dev, workspace)
+        size = (lib.gla_window_attn_chunk16_workspace_size if pool_e is None else
+                lib.gla_window_attn_chunk8_workspace_size)
+        wp, wb, hold = _ops._scratch(size(n, N, H, KV, window, sink), dev, workspace)
         rc = lib.gla_window_attn_chunk(
             kp, vp, ep, _ptr(page, "page", dev, I32, (n,)), _ptr(pos, "pos", dev, I32, (n,)),
             _ptr(start, "start", dev, I32, (n + 1,)), n, N, P, PL, layer, window, sink,

@@ -754,8 +754,8 @@ GLA_API gla_status gla_window_cache_append(const void* k, const void* v, gla_dty
  *   q            [n_tokens,H,96], k [n_tokens,KV,96], v [n_tokens,KV,192] in_dtype (GLA_BF16 or
  *                GLA_FP16), H / KV <= 128
  *   o            [n_tokens,H,192] out_dtype: in_dtype or GLA_FP32 (written)
- *   workspace    gla_window_attn_chunk_workspace_size() bytes, 256-byte aligned (0: not needed).  The
- *                size depends on the device current at the call
+ *   workspace    gla_window_attn_chunk_workspace_size() bytes, enough for pages of either kind, 256-byte
+ *                aligned (0: not needed).  The size depends on the device current at the call
  * Pages may repeat here.  Softmax, sums and roundings as in gla_window_attn_fwd, and as there q, k and v of the
  * sequences' rows must be finite, and what their slots hold; slots that no token has reached and rows of other
  * sequences may hold anything, NaN included.  Over 8-bit pages codes are multiplied exactly.  Where sequences
@@ -765,6 +765,11 @@ GLA_API gla_status gla_window_cache_append(const void* k, const void* v, gla_dty
  */
 GLA_API size_t gla_window_attn_chunk_workspace_size(int n, int n_tokens, int H, int KV, int window,
                                                     int sink);
+/* The same for pages of 16 or of 8 bits only: long chunks over the latter need a copy of them. */
+GLA_API size_t gla_window_attn_chunk16_workspace_size(int n, int n_tokens, int H, int KV,
+                                                      int window, int sink);
+GLA_API size_t gla_window_attn_chunk8_workspace_size(int n, int n_tokens, int H, int KV, int window,
+                                                     int sink);
 GLA_API gla_status gla_window_attn_chunk(const void* pool_k, const void* pool_v,
                                          const signed char* pool_e, const int* page,
                                          const int* pos, const int* start, int n, int n_tokens,

@@ -212,3 +212,49 @@ def test_rotary_past_32_bits(env):
     want, _ = gla.rotary(tail, None, turns, pos)
     got, _ = gla.rotary(x, None, turns, q_out=x)
     assert torch.equal(got[-1:, -50:], want) and not got[:-1, -50:].any()
+
+
+def test_long_chunks_over_codes_and_a_page_that_is_not_there(env):
+    """Long chunks over 8-bit pages go by a copy of the pages in the workspace: pages that are not full, a
+    workspace full of NaN, a layer of several, and a sequence whose page is out of range."""
+    gla, torch, types = env
+    rng = np.random.default_rng(21)
+    new, pos, H, KV, window, sink = [400, 1, 300], [90, 700, 0], 4, 2, 300, 3
+    pool, values = _pool(torch, rng, 4, window + sink, KV, "fp16", types["fp16"], 8)
+    two = [torch.stack([x[:, 0], torch.full_like(x[:, 0], 127)], 1) for x in pool]  # (layer 1: anything)
+    two[2][0, 0, :, 90:] = 127  # exponents of slots that no token has reached
+    start = np.concatenate([[0], np.cumsum(new)])
+    (q, k, v), dev = _new(torch, rng, int(start[-1]), H, KV, "fp16", types["fp16"])
+    size = gla.window_attn_chunk_workspace_size(3, len(q), H, KV, window, sink, bits=8)
+    assert size >= 3 * (window + sink) * KV * 288 * 2 > 0
+    assert gla.window_attn_chunk_workspace_size(3, len(q), H, KV, window, sink, bits=16) < size
+    assert gla.window_attn_chunk_workspace_size(3, len(q), H, KV, window, sink) == size
+
+    def call(page):
+        o = torch.full((len(q), H, 192), 7.0, device="cuda").half()
+        ws = torch.full((size // 4,), float("nan"), device="cuda")
+        gla.window_attn_chunk(two[0], two[1], _ints(torch, page), _ints(torch, pos), _ints(torch, start.tolist()),
+                              *dev, window, sink, pool_e=two[2], out=o, workspace=ws)
+        return o
+    o = call([0, 3, 1])
+    _close(o, *ref.chunk(*values, [0, 3, 1], pos, start, q, k, v, window, sink), "fp16")
+    assert gla.get_device_error() == 0
+    for bad in (4, -1):
+        b = call([0, 3, bad])
+        assert gla.get_device_error() == 6
+        assert bool((b[401:] == 7).all()) and torch.equal(b[:401], o[:401])
+
+
+def test_a_last_round_of_parts_among_packed_tokens(env):
+    """Whole units and parts of the others, of which more might have come than did."""
+    gla, torch, types = env
+    rng = np.random.default_rng(31)
+    n, H, KV, window, sink = 116, 16, 4, 600, 4
+    pos = [(37 * b) % 1300 for b in range(n)]
+    pool, values = _pool(torch, rng, n, window + sink, KV, "bf16", types["bf16"], 8)
+    (q, k, v), dev = _new(torch, rng, n, H, KV, "bf16", types["bf16"])
+    page = rng.permutation(n)
+    o = gla.window_attn_chunk(*pool[:2], _ints(torch, page.tolist()), _ints(torch, pos),
+                              _ints(torch, list(range(n + 1))), *dev, window, sink, pool_e=pool[2])
+    _close(o, *ref.chunk(*values, page, pos, np.arange(n + 1), q, k, v, window, sink), "bf16")
+    assert gla.get_device_error() == 0
