@@ -39,40 +39,50 @@
 namespace gla {
 namespace rows8 {
 
-constexpr int WARPS = 4, THREADS = 32 * WARPS, SB = 16;
-constexpr int ROUND = WARPS * SB;                  // slots
-constexpr int OFF_KEYS = ROUND * kDV;              // a stage: values, keys
-constexpr int STAGE = OFF_KEYS + ROUND * kDK;      // 18,432 bytes
-constexpr int EXPS = 2 * SB + 16;                  // the exponents of a warp's slots, from a word's start
-constexpr int P_ROW = 2 * ROUND + 16;              // bytes of a row's weights
-constexpr int TILES = kDV / 16 / WARPS;            // a warp's channels, 16 each
+constexpr int WARPS = 4, THREADS = 32 * WARPS;
+constexpr int TILES = kDV / 16 / WARPS;  // a warp's channels, 16 each
+constexpr int kHold = 3;                 // CTAs that an SM holds
 constexpr uint64_t DRAIN_NS = 4000000000ull;
 static_assert(kDV % (16 * WARPS) == 0, "the warps' channels");
 
-// Stages of the ring and CTAs that an SM holds, by the groups of 8 rows: with 5, 4 and 3 CTAs of two stages the
-// decode step of 256 tokens on 1,028 slots of 4 key heads took as long (69 us), but 96 chunks of two and four
-// tokens on 2,052 slots 65 and 74 us in place of 48 and 57; four groups with three stages leave room for two
-// CTAs only (96 chunks of eight tokens: 101 us in place of 94).
+// By the groups of 8 rows.  A round of 128 slots has twice the products in flight for the same waits, but with
+// more than one group no room is left for two of them beside the queries: 64 slots then, in three stages, or in two
+// where the rows take the room of the third.  (Rounds of 64 for one group, 256 tokens on 1,028 slots of 4 key
+// heads: 71 us.  With 5, 4 and 3 CTAs of two stages 69, but 96 chunks of two and four tokens on 2,052 slots
+// took 65 and 74 us in place of 48 and 57; four groups in three stages leave room for two CTAs: 96 chunks of
+// eight tokens 101 us in place of 94.)
 template <int NT>
-constexpr int kStages = NT == 4 ? 2 : 3;
-constexpr int kHold = 3;
+struct Shape {
+  static constexpr int SB = NT == 1 ? 32 : 16;           // slots of a round for each warp
+  static constexpr int STAGES = NT == 2 ? 3 : 2;
+  static constexpr int ROUND = WARPS * SB;
+  static constexpr int KEYS = ROUND * kDV, STAGE = KEYS + ROUND * kDK;  // a stage: values, keys
+  static constexpr int EXPS = 2 * SB + 16;               // the exponents of a warp's slots, from a word's start
+  // A warp's weights take the place of its keys of the round, [row][slot].
+  static constexpr int SLICE = SB * kDK, P_ROW = 2 * SB + 16;
+  static_assert(8 * NT * P_ROW <= SLICE, "weights in place of keys");
+};
 
 // What the warps of a unit of NT groups of 8 rows share.
 template <int NT>
 struct Shared {
-  uint64_t full[kStages<NT>], behind;  // mbarriers: a stage is there; the rounds are over
-  uint8_t exps[WARPS][kStages<NT>][EXPS];
-  alignas(16) uint8_t weights[2][8 * NT * P_ROW];  // of two rounds, [row][slot]
-  uint2 q[NT][kDK / 16][32];           // the second operand of the scores' products
+  using S = Shape<NT>;
+  uint64_t full[S::STAGES], behind;    // mbarriers: a stage is there; the rounds are over
+  uint8_t exps[WARPS][S::STAGES][S::EXPS];
+  union {
+    uint2 q[NT][kDK / 16][32];         // the second operand of the scores' products
+    struct {
+      int upto[THREADS + 1], sums[WARPS];  // before: units before a slice of the sequences
+    } find;
+  };
   float z0[8 * NT], zs[8 * NT];        // of a row: - q . (code 0), a score's factor
   float top[WARPS][8 * NT], sum[WARPS][8 * NT];
   int e_top[WARPS];
   int found[4];
-  int upto[THREADS + 1], sums[WARPS];  // units before a slice of the sequences
 };
 template <int NT>
 constexpr int smem_bytes() {
-  return kStages<NT> * STAGE + (int)sizeof(Shared<NT>) + 1024;
+  return Shape<NT>::STAGES * Shape<NT>::STAGE + (int)sizeof(Shared<NT>) + 512;
 }
 static_assert(kHold * (smem_bytes<1>() + 1024) <= 228 * 1024 && kHold * (smem_bytes<2>() + 1024) <= 228 * 1024 &&
                   kHold * (smem_bytes<4>() + 1024) <= 228 * 1024,
@@ -151,18 +161,26 @@ __device__ __forceinline__ void whole16(uint32_t w, uint32_t& even, uint32_t& od
 }
 constexpr uint32_t kZero16 = 0x00800080u;  // of code 0
 
-// Two 8 x 8 matrices of 16 bits to shared memory, transposed; lanes 0 .. 15 have their rows' addresses.
+// Two or four 8 x 8 matrices of 16 bits to shared memory, transposed; lane l has the address of row l % 8 of the
+// (l / 8)-th.
 __device__ __forceinline__ void stsm2t(uint32_t at, uint32_t x, uint32_t y) {
   asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+}
+
+__device__ __forceinline__ void stsm4t(uint32_t at, const uint32_t (&x)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3])
+               : "memory");
 }
 
 template <class T, class TO, int NT>
 __global__ void __launch_bounds__(THREADS, kHold)
 rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
   constexpr int HB = 8 * NT, NR = 2 * NT;  // rows of a unit, and those of a thread
-  constexpr int STAGES = kStages<NT>;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* const smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  using Sh = Shape<NT>;
+  constexpr int SB = Sh::SB, STAGES = Sh::STAGES, ROUND = Sh::ROUND, STAGE = Sh::STAGE, P_ROW = Sh::P_ROW;
+  extern __shared__ __align__(512) uint8_t smem_raw[];  // (the swizzle counts from multiples of 512)
+  uint8_t* const smem = (uint8_t*)(((uintptr_t)smem_raw + 511) & ~(uintptr_t)511);
   Shared<NT>& sh = *reinterpret_cast<Shared<NT>*>(smem + STAGES * STAGE);
   const uint32_t sm = smem_u32(smem), bar = smem_u32(sh.full);
   const WindowCache& c = a.cache.c;
@@ -211,7 +229,7 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     __syncthreads();
   } else {
     // sums of groups over a slice of the sequences a thread, and a search
-    int *const upto = sh.upto, *const sums = sh.sums;
+    int *const upto = sh.find.upto, *const sums = sh.find.sums;
     const int slice = (c.n + THREADS - 1) / THREADS;
     const int lo = min(tid * slice, c.n), hi = min(lo + slice, c.n);
     int mine = 0;
@@ -280,7 +298,7 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     return s0 + SB <= hi && (s0 + SB <= s_end || (s0 >= a_from && s0 + SB <= a_end) || s0 >= b_from);
   };
 
-  // ---- rounds of 64 slots
+  // ---- rounds
   const int rounds = hi > lo ? (hi - lo + ROUND - 1) / ROUND : 0;
   int sent = 0;             // (thread 0)
   auto fetch = [&](int i) {  // by one thread: slots lo + i ROUND ..
@@ -288,7 +306,7 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     const uint32_t st = sm + i % STAGES * STAGE, full = bar + 8 * (i % STAGES);
     mbar_arrive_expect_tx(full, STAGE);
     tma_load_5d(st, &maps.v, full, 0, 0, kv, lo + i * ROUND, page);
-    tma_load_4d(st + OFF_KEYS, &maps.k, full, 0, kv, lo + i * ROUND, page);
+    tma_load_4d(st + Sh::KEYS, &maps.k, full, 0, kv, lo + i * ROUND, page);
     sent = i + 1;
   };
   if (tid == 0)
@@ -426,9 +444,10 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     const int x = lane * kDV + 16 * (TILES * w + j);
     v_at[j] = sm + (x ^ ((x >> 3) & 48));
   }
-  const uint32_t p_sm = smem_u32(sh.weights[0]);
-  const uint32_t p_to = p_sm + (lane & 7) * P_ROW + (w * SB + ((lane >> 3) & 1) * 8) * 2;  // its row of the stores
-  const uint32_t p_from = p_sm + (lane & 7) * P_ROW + (lane >> 3) * 16;               // and of the loads
+  // a lane's row of the weights: of the stores (in the warp's slice) and of the loads (32 slots)
+  const uint32_t p_to = sm + Sh::KEYS + w * Sh::SLICE + (lane & 7) * P_ROW + (lane >> 3) % (SB / 8) * 16;
+  const uint32_t p_from = sm + Sh::KEYS + (lane & 7) * P_ROW +
+                          (SB == 32 ? (lane >> 3) * 16 : (lane >> 4) * Sh::SLICE + ((lane >> 3) & 1) * 16);
   bool dead = false;  // a wait ran out: no more loads, and nothing of use comes out
 #pragma unroll 1
   for (int i = 0; i < rounds; ++i) {
@@ -445,7 +464,7 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     float ks = 0.f;
     bool up = false;
     if (s0 < hi) {
-      const uint8_t* keys = smem + i % STAGES * STAGE + OFF_KEYS + w * SB * kDK;
+      const uint8_t* keys = smem + i % STAGES * STAGE + Sh::KEYS + w * Sh::SLICE;
 #pragma unroll
       for (int h = 0; h < SB / 16; ++h)
 #pragma unroll
@@ -543,8 +562,9 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
           const __half2 y = __hmul2(reinterpret_cast<const __half2&>(pf[k]), reinterpret_cast<const __half2&>(fv[k]));
           pf[k] = reinterpret_cast<const uint32_t&>(y);
         }
-        static_assert(SB == 16, "a store of two matrices");
-        stsm2t(p_to + (i & 1) * (HB * P_ROW) + n * (8 * P_ROW), pf[0], pf[1]);
+        const uint32_t to = p_to + i % STAGES * STAGE + n * (8 * P_ROW);
+        if constexpr (SB == 32) stsm4t(to, pf);
+        else stsm2t(to, pf[0], pf[1]);
       }
     };
     weigh();
@@ -562,14 +582,14 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
 #pragma unroll
     for (int r = 0; r < NR; ++r) l[r] += part_sum[r];
     // codes of slots 2 t, + 1 (x[0]) and + 8, + 9 (x[1]) of the first 16 of 32, x[2], x[3]: of the others
-    const uint32_t st = i % STAGES * STAGE, p_at = p_from + (i & 1) * (HB * P_ROW);
+    const uint32_t st = i % STAGES * STAGE, p_at = p_from + st;
     const int left = hi - (lo + i * ROUND);
 #pragma unroll
     for (int y = 0; y < ROUND / 32; ++y) {
       if (32 * y >= left) break;
       uint32_t pf[NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) ldsm4(pf[n], p_at + n * (8 * P_ROW) + 64 * y);
+      for (int n = 0; n < NT; ++n) ldsm4(pf[n], p_at + n * (8 * P_ROW) + y * (32 / SB) * Sh::SLICE);
 #pragma unroll
       for (int j = 0; j < TILES; ++j) {
         uint32_t x[4];
@@ -600,10 +620,12 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
   // ---- the new tokens, 16 a warp
   const T* nk = static_cast<const T*>(a.k) + ((long long)s.first * KV + kv) * kDK;
   const T* nv = static_cast<const T*>(a.v) + ((long long)s.first * KV + kv) * kDV;
+  // (their weights where the rounds were, which all warps have left when they have met)
+  constexpr int F_ROW = 32 * WARPS + 16;
   if (part == 0) {
     const int sinks = max(c.sink - s.pos, 0);
 #pragma unroll 1
-    for (int j0 = 0, odd = rounds & 1; j0 <= i1; j0 += 16 * WARPS) {
+    for (int j0 = 0; j0 <= i1; j0 += 16 * WARPS) {
       if (j0 + 16 * WARPS - 1 <= i0 - c.window && j0 >= sinks) continue;
       const int mine = j0 + 16 * w;
       float z[NT][4], top[NR], part_sum[NR];
@@ -641,7 +663,6 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
         top[r] = fmaxf(x, y);
         up |= top[r] > m[r] + 8.f;
       }
-      const uint32_t buf = p_sm + odd * (HB * P_ROW);
       auto weigh = [&] {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -655,7 +676,7 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
           const float2 x = halves<T>(lo), y = halves<T>(hi);
           part_sum[2 * n] = x.x + y.x;
           part_sum[2 * n + 1] = x.y + y.y;
-          stsm2t(buf + (8 * n + (lane & 7)) * P_ROW + (16 * w + ((lane >> 3) & 1) * 8) * 2, lo, hi);
+          stsm2t(sm + (8 * n + (lane & 7)) * F_ROW + (16 * w + ((lane >> 3) & 1) * 8) * 2, lo, hi);
         }
       };
       if (__syncthreads_or(up)) refer(top, -1000);
@@ -679,11 +700,11 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
               x[j][k] = __ldg(reinterpret_cast<const uint32_t*>(val + (long long)d * KV * kDV + 16 * j));
           }
         }
-        const uint8_t* weights = sh.weights[odd] + g * P_ROW + (16 * y + t2) * 2;
+        const uint8_t* weights = smem + g * F_ROW + (16 * y + t2) * 2;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint32_t p0 = *reinterpret_cast<const uint32_t*>(weights + n * (8 * P_ROW));
-          const uint32_t p1 = *reinterpret_cast<const uint32_t*>(weights + n * (8 * P_ROW) + 16);
+          const uint32_t p0 = *reinterpret_cast<const uint32_t*>(weights + n * (8 * F_ROW));
+          const uint32_t p1 = *reinterpret_cast<const uint32_t*>(weights + n * (8 * F_ROW) + 16);
 #pragma unroll
           for (int j = 0; j < TILES; ++j) {
             const uint32_t x4[4] = {__byte_perm(x[j][0], x[j][1], 0x5410), __byte_perm(x[j][0], x[j][1], 0x7632),
@@ -692,7 +713,6 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
           }
         }
       }
-      odd ^= 1;
     }
   }
 
@@ -780,6 +800,8 @@ rows8_join_kernel(Args a, Plan plan) {
 // `units` at most, `likely` so many: as many whole ones as fill the device one or more times, and parts of
 // the others that fill it once more, of at least two rounds; nothing is cut where two do not fit.
 inline Plan make_plan(long long units, long long likely, int rows, int slots, int n_sm) {
+  const int ROUND = rows == 8 ? Shape<1>::ROUND : Shape<2>::ROUND;
+  static_assert(Shape<4>::ROUND == Shape<2>::ROUND, "rounds of more than 8 rows");
   const int hold = std::max(kHold * n_sm, 1), rest = (int)(likely % hold);
   const int most = std::min((slots + 2 * ROUND - 1) / (2 * ROUND), kMostParts);
   // (where many more units may come than are likely, each of those has room for as many parts)
@@ -791,7 +813,9 @@ inline Plan make_plan(long long units, long long likely, int rows, int slots, in
   return Plan{units, (int)(likely - rest), parts, part_slots, rows};
 }
 
-inline bool make_maps(Maps* m, const ServeCache& cache) {
+template <int NT>
+bool make_maps(Maps* m, const ServeCache& cache) {
+  constexpr int ROUND = Shape<NT>::ROUND;
   auto fn = encode_tiled_fn();
   if (!fn) return false;
   const WindowCache& c = cache.c;
@@ -813,7 +837,7 @@ inline bool make_maps(Maps* m, const ServeCache& cache) {
 template <class T, class TO, int NT>
 cudaError_t run(const Args& a, const Plan& plan, DevCtl ctl, cudaStream_t stream) {
   Maps m;
-  if (!make_maps(&m, a.cache)) return cudaErrorInvalidValue;
+  if (!make_maps<NT>(&m, a.cache)) return cudaErrorInvalidValue;
   auto kern = rows8_kernel<T, TO, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NT>());
   if (e != cudaSuccess) return e;
