@@ -377,6 +377,37 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     if (g == 0) *reinterpret_cast<float2*>(sh.z0 + 8 * w + t2) = make_float2(-x[0], -x[1]);
     if (t == 0) sh.zs[8 * w + g] = up;
   }
+  const T* nk = static_cast<const T*>(a.k) + ((long long)s.first * KV + kv) * kDK;
+  const T* nv = static_cast<const T*>(a.v) + ((long long)s.first * KV + kv) * kDV;
+  // One token alone: its score by the last warp, and its values' channels of this thread (16 (TILES w + j) + 2 g, +
+  // 1), ahead of the page.  (Behind it, as those of more are, they took 3,300 of a unit's 48,000 cycles; more than
+  // one group of rows has no registers for it.)
+  const bool one = NT == 1 && part == 0 && i1 == 0;
+  [[maybe_unused]] uint32_t own[TILES];
+  if constexpr (NT == 1) {
+    if (one) {
+#pragma unroll
+      for (int j = 0; j < TILES; ++j)
+        own[j] = __ldg(reinterpret_cast<const uint32_t*>(nv + 16 * (TILES * w + j) + 2 * g));
+      if (w == WARPS - 1) {
+        uint32_t qf[kDK / 16][2];
+        load_q(0, qf);
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < kDK / 16; ++j) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(nk + 32 * (j >> 1) + 8 * t + 4 * (j & 1)));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float2 u = halves<T>(qf[j][h]), v = halves<T>(h ? x.y : x.x);
+            z = fmaf(u.x, v.x, fmaf(u.y, v.y, z));
+          }
+        }
+        z += __shfl_xor_sync(0xffffffffu, z, 1);
+        z += __shfl_xor_sync(0xffffffffu, z, 2);
+        if (t == 0) sh.sum[0][g] = z * kLog2e;
+      }
+    }
+  }
   __syncthreads();
 
   // A thread's scores are of slots g, g + 8, .. of the warp's and rows 8 n + t2, + 1 (NR of them); its sums of
@@ -387,6 +418,7 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     z0[r] = sh.z0[8 * (r >> 1) + t2 + (r & 1)];
     zs[r] = sh.zs[8 * (r >> 1) + t2 + (r & 1)];
   }
+  [[maybe_unused]] const float z_own[2] = {sh.sum[0][t2], sh.sum[0][t2 + 1]};
   auto at = [&](int r) { return s.pos + row_of(8 * (r >> 1) + t2 + (r & 1)) / G; };  // a row's position
   float acc[TILES][NT][4];
 #pragma unroll
@@ -618,11 +650,26 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
   }
 
   // ---- the new tokens, 16 a warp
-  const T* nk = static_cast<const T*>(a.k) + ((long long)s.first * KV + kv) * kDK;
-  const T* nv = static_cast<const T*>(a.v) + ((long long)s.first * KV + kv) * kDV;
   // (their weights where the rounds were, which all warps have left when they have met)
   constexpr int F_ROW = 32 * WARPS + 16;
-  if (part == 0) {
+  if constexpr (NT == 1) {
+    if (one) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float now = z_own[r] > m[r] + 8.f ? z_own[r] : m[r];
+        const float keep = now == m[r] || m[r] == -INFINITY ? 1.f : ex2(m[r] - now), p = ex2(z_own[r] - now);
+        m[r] = now;
+        l[r] = l[r] * keep + (w == 0 && g == 0 ? p : 0.f);
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+          const float2 v = halves<T>(own[j]);
+          acc[j][0][r] = fmaf(p, v.x, acc[j][0][r] * keep);
+          acc[j][0][2 + r] = fmaf(p, v.y, acc[j][0][2 + r] * keep);
+        }
+      }
+    }
+  }
+  if (part == 0 && !one) {
     const int sinks = max(c.sink - s.pos, 0);
 #pragma unroll 1
     for (int j0 = 0; j0 <= i1; j0 += 16 * WARPS) {
