@@ -21,10 +21,10 @@
 // share: they are worked out before it is known whether a score passes it by more than 8, and again in the
 // rare round where one does, so that a round has one barrier.
 //
-// Bound by latency: a CTA's first loads, its tokens' own rows and its last sums are a third of its time, beside
-// which the other two of the SM have to keep HBM busy.  256 tokens on 1,028 slots of 4 key heads, 290 bytes a
-// slot and key head: 64 us, 4.7 TB/s of the 6.7 that a copy reaches (without the loads 48, without the products
-// 57); 96 chunks of four tokens on 2,052 slots 58 us.
+// Bound by latency: a CTA's first loads and its last sums are a fifth of its time, and in its rounds it waits for
+// HBM, whose rate then is what a copy reaches; the three CTAs of an SM begin and end nearly together.  256 tokens
+// on 1,028 slots of 4 key heads, 290 bytes a slot and key head: 65 us, 4.7 TB/s of the 6.7 of a copy (without the
+// loads 51 us, without the products 60, without both 29); 96 chunks of four tokens on 2,052 slots 60 us.
 #pragma once
 #include <cuda_runtime.h>
 
