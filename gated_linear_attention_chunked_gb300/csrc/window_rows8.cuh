@@ -844,19 +844,21 @@ rows8_join_kernel(Args a, Plan plan) {
       static_cast<TO*>(a.o) + ((long long)(u.first + i) * a.H + u.kv * G + R - i * G) * kDV);
 }
 
-// `units` at most, `likely` so many: as many whole ones as fill the device one or more times, and parts of
-// the others that fill it once more, of at least two rounds; nothing is cut where two do not fit.
+// `units` at most, `likely` so many: as many whole ones as fill the device one or more times, and the others in
+// as many parts as fill it once more, of at least one round.  (More parts than that, in two turns: 69 us in place of
+// 58 with 64 chunks of four tokens on 2,052 slots, 256 units on 456 places.)
 inline Plan make_plan(long long units, long long likely, int rows, int slots, int n_sm) {
   const int ROUND = rows == 8 ? Shape<1>::ROUND : Shape<2>::ROUND;
   static_assert(Shape<4>::ROUND == Shape<2>::ROUND, "rounds of more than 8 rows");
   const int hold = std::max(kHold * n_sm, 1), rest = (int)(likely % hold);
-  const int most = std::min((slots + 2 * ROUND - 1) / (2 * ROUND), kMostParts);
+  const int most = std::min((slots - 1) / ROUND + 1, kMostParts);
   // (where many more units may come than are likely, each of those has room for as many parts)
   const long long room = std::max(4ll * hold / std::max(units - (likely - rest), 1ll), 1ll);
   const int cut = rest ? (int)std::min<long long>(std::min(hold / rest, most), room) : 1;
   if (cut < 2) return Plan{units, (int)units, 1, 0, rows};
   const int part_slots = ((slots + cut - 1) / cut + ROUND - 1) / ROUND * ROUND;
   const int parts = (slots + part_slots - 1) / part_slots;
+  if (parts < 2) return Plan{units, (int)units, 1, 0, rows};
   return Plan{units, (int)(likely - rest), parts, part_slots, rows};
 }
 
