@@ -41,20 +41,22 @@ namespace rows8 {
 
 constexpr int WARPS = 4, THREADS = 32 * WARPS;
 constexpr int TILES = kDV / 16 / WARPS;  // a warp's channels, 16 each
-constexpr int kHold = 3;                 // CTAs that an SM holds
 constexpr uint64_t DRAIN_NS = 4000000000ull;
 static_assert(kDV % (16 * WARPS) == 0, "the warps' channels");
 
-// By the groups of 8 rows.  A round of 128 slots has twice the products in flight for the same waits, but with
-// more than one group no room is left for two of them beside the queries: 64 slots then, in three stages, or in two
-// where the rows take the room of the third.  (Rounds of 64 for one group, 256 tokens on 1,028 slots of 4 key
-// heads: 71 us.  With 5, 4 and 3 CTAs of two stages 69, but 96 chunks of two and four tokens on 2,052 slots
-// took 65 and 74 us in place of 48 and 57; four groups in three stages leave room for two CTAs: 96 chunks of
-// eight tokens 101 us in place of 94.)
-template <int NT>
+// By the groups of 8 rows.  A round of 128 slots (WIDE) has twice the products in flight for the same waits, but with
+// more than one group no room is left for three CTAs of an SM with two such rounds beside the queries: two CTAs, or
+// rounds of 64 slots in three stages, or in two where the rows take the room of the third.  make_plan
+// has the rule.  Chunks of 4 and 8 tokens on 2,052 slots, 4 key heads, by 128 and by 64 slots: 64 chunks 44 and 58,
+// 56 and 86 us; 96 76 and 60, 103 and 88; 128 84 and 86, 105 and 131; 200 123 and 115, 156 and 173.  (One group by 64
+// slots: 71 us in place of 68 with 256 tokens on 1,028 slots.  With 5, 4 and 3 CTAs of two stages of 64 slots 69, but
+// 96 chunks of two and four tokens took 65 and 74 us in place of 48 and 57; four groups in three stages leave
+// room for two CTAs: 96 chunks of eight tokens 101 us in place of 94.)
+template <int NT, bool WIDE>
 struct Shape {
-  static constexpr int SB = NT == 1 ? 32 : 16;           // slots of a round for each warp
-  static constexpr int STAGES = NT == 2 ? 3 : 2;
+  static constexpr int HOLD = NT > 1 && WIDE ? 2 : 3;          // CTAs that an SM holds
+  static constexpr int SB = WIDE ? 32 : 16;                    // slots of a round for each warp
+  static constexpr int STAGES = NT == 2 && !WIDE ? 3 : 2;
   static constexpr int ROUND = WARPS * SB;
   static constexpr int KEYS = ROUND * kDV, STAGE = KEYS + ROUND * kDK;  // a stage: values, keys
   static constexpr int EXPS = 2 * SB + 16;               // the exponents of a warp's slots, from a word's start
@@ -64,9 +66,9 @@ struct Shape {
 };
 
 // What the warps of a unit of NT groups of 8 rows share.
-template <int NT>
+template <int NT, bool WIDE>
 struct Shared {
-  using S = Shape<NT>;
+  using S = Shape<NT, WIDE>;
   uint64_t full[S::STAGES], behind;    // mbarriers: a stage is there; the rounds are over
   uint8_t exps[WARPS][S::STAGES][S::EXPS];
   union {
@@ -80,13 +82,13 @@ struct Shared {
   int e_top[WARPS];
   int found[4];
 };
-template <int NT>
+template <int NT, bool WIDE>
 constexpr int smem_bytes() {
-  return Shape<NT>::STAGES * Shape<NT>::STAGE + (int)sizeof(Shared<NT>) + 512;
+  using S = Shape<NT, WIDE>;
+  constexpr int bytes = S::STAGES * S::STAGE + (int)sizeof(Shared<NT, WIDE>) + 512;
+  static_assert(S::HOLD * (bytes + 1024) <= 228 * 1024, "shared memory");
+  return bytes;
 }
-static_assert(kHold * (smem_bytes<1>() + 1024) <= 228 * 1024 && kHold * (smem_bytes<2>() + 1024) <= 228 * 1024 &&
-                  kHold * (smem_bytes<4>() + 1024) <= 228 * 1024,
-              "shared memory");
 
 struct Args {
   ServeCache cache;
@@ -102,6 +104,7 @@ struct Args {
 struct Plan {
   long long units;   // at most
   int whole, parts, part_slots, rows;  // rows of a unit: 8, 16 or 32
+  bool wide;                           // rounds of 128 slots with more than 8
 };
 struct Maps {
   CUtensorMap k, v;
@@ -173,15 +176,15 @@ __device__ __forceinline__ void stsm4t(uint32_t at, const uint32_t (&x)[4]) {
                : "memory");
 }
 
-template <class T, class TO, int NT>
-__global__ void __launch_bounds__(THREADS, kHold)
+template <class T, class TO, int NT, bool WIDE>
+__global__ void __launch_bounds__(THREADS, Shape<NT, WIDE>::HOLD)
 rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
   constexpr int HB = 8 * NT, NR = 2 * NT;  // rows of a unit, and those of a thread
-  using Sh = Shape<NT>;
+  using Sh = Shape<NT, WIDE>;
   constexpr int SB = Sh::SB, STAGES = Sh::STAGES, ROUND = Sh::ROUND, STAGE = Sh::STAGE, P_ROW = Sh::P_ROW;
   extern __shared__ __align__(512) uint8_t smem_raw[];  // (the swizzle counts from multiples of 512)
   uint8_t* const smem = (uint8_t*)(((uintptr_t)smem_raw + 511) & ~(uintptr_t)511);
-  Shared<NT>& sh = *reinterpret_cast<Shared<NT>*>(smem + STAGES * STAGE);
+  Shared<NT, WIDE>& sh = *reinterpret_cast<Shared<NT, WIDE>*>(smem + STAGES * STAGE);
   const uint32_t sm = smem_u32(smem), bar = smem_u32(sh.full);
   const WindowCache& c = a.cache.c;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -848,23 +851,27 @@ rows8_join_kernel(Args a, Plan plan) {
 // as many parts as fill it once more, of at least one round.  (More parts than that, in two turns: 69 us in place of
 // 58 with 64 chunks of four tokens on 2,052 slots, 256 units on 456 places.)
 inline Plan make_plan(long long units, long long likely, int rows, int slots, int n_sm) {
-  const int ROUND = rows == 8 ? Shape<1>::ROUND : Shape<2>::ROUND;
-  static_assert(Shape<4>::ROUND == Shape<2>::ROUND, "rounds of more than 8 rows");
-  const int hold = std::max(kHold * n_sm, 1), rest = (int)(likely % hold);
+  // a unit takes three quarters of the time by rounds of 128 slots (16 rows; two thirds with 32), two to an SM
+  const long long two = (likely + 2 * n_sm - 1) / std::max(2 * n_sm, 1), three = (likely + 3 * n_sm - 1) / std::max(3 * n_sm, 1);
+  const bool wide = rows == 8 || (rows == 16 ? 3 * two <= 4 * three : 2 * two <= 3 * three);
+  const int ROUND = wide ? Shape<1, true>::ROUND : Shape<2, false>::ROUND;
+  static_assert(Shape<1, true>::ROUND == Shape<2, true>::ROUND && Shape<1, true>::ROUND == Shape<4, true>::ROUND &&
+                    Shape<2, false>::ROUND == Shape<4, false>::ROUND,
+                "rounds");
+  const int hold = std::max((rows > 8 && wide ? 2 : 3) * n_sm, 1), rest = (int)(likely % hold);
   const int most = std::min((slots - 1) / ROUND + 1, kMostParts);
   // (where many more units may come than are likely, each of those has room for as many parts)
   const long long room = std::max(4ll * hold / std::max(units - (likely - rest), 1ll), 1ll);
   const int cut = rest ? (int)std::min<long long>(std::min(hold / rest, most), room) : 1;
-  if (cut < 2) return Plan{units, (int)units, 1, 0, rows};
+  if (cut < 2) return Plan{units, (int)units, 1, 0, rows, wide};
   const int part_slots = ((slots + cut - 1) / cut + ROUND - 1) / ROUND * ROUND;
   const int parts = (slots + part_slots - 1) / part_slots;
-  if (parts < 2) return Plan{units, (int)units, 1, 0, rows};
-  return Plan{units, (int)(likely - rest), parts, part_slots, rows};
+  if (parts < 2) return Plan{units, (int)units, 1, 0, rows, wide};
+  return Plan{units, (int)(likely - rest), parts, part_slots, rows, wide};
 }
 
-template <int NT>
+template <int ROUND>
 bool make_maps(Maps* m, const ServeCache& cache) {
-  constexpr int ROUND = Shape<NT>::ROUND;
   auto fn = encode_tiled_fn();
   if (!fn) return false;
   const WindowCache& c = cache.c;
@@ -883,15 +890,15 @@ bool make_maps(Maps* m, const ServeCache& cache) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class T, class TO, int NT>
+template <class T, class TO, int NT, bool WIDE>
 cudaError_t run(const Args& a, const Plan& plan, DevCtl ctl, cudaStream_t stream) {
   Maps m;
-  if (!make_maps<NT>(&m, a.cache)) return cudaErrorInvalidValue;
-  auto kern = rows8_kernel<T, TO, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NT>());
+  if (!make_maps<Shape<NT, WIDE>::ROUND>(&m, a.cache)) return cudaErrorInvalidValue;
+  auto kern = rows8_kernel<T, TO, NT, WIDE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NT, WIDE>());
   if (e != cudaSuccess) return e;
   const long long cut = plan.units - plan.whole;
-  kern<<<(unsigned)(plan.whole + cut * plan.parts), THREADS, smem_bytes<NT>(), stream>>>(m, a, plan, ctl);
+  kern<<<(unsigned)(plan.whole + cut * plan.parts), THREADS, smem_bytes<NT, WIDE>(), stream>>>(m, a, plan, ctl);
   if ((e = cudaGetLastError()) != cudaSuccess || plan.parts == 1) return e;
   PdlLaunch l(dim3((unsigned)(cut * plan.rows)), dim3(JOIN_THREADS), 0, stream, true);
   return cudaLaunchKernelEx(&l.cfg, rows8_join_kernel<TO>, a, plan);
@@ -899,9 +906,10 @@ cudaError_t run(const Args& a, const Plan& plan, DevCtl ctl, cudaStream_t stream
 
 template <class T, class TO>
 cudaError_t run(const Args& a, const Plan& plan, DevCtl ctl, cudaStream_t stream) {
-  return plan.rows == 8    ? run<T, TO, 1>(a, plan, ctl, stream)
-         : plan.rows == 16 ? run<T, TO, 2>(a, plan, ctl, stream)
-                           : run<T, TO, 4>(a, plan, ctl, stream);
+  if (plan.rows == 8) return run<T, TO, 1, true>(a, plan, ctl, stream);
+  if (plan.rows == 32)
+    return plan.wide ? run<T, TO, 4, true>(a, plan, ctl, stream) : run<T, TO, 4, false>(a, plan, ctl, stream);
+  return plan.wide ? run<T, TO, 2, true>(a, plan, ctl, stream) : run<T, TO, 2, false>(a, plan, ctl, stream);
 }
 inline cudaError_t launch(const Args& a, gla_dtype out, const Plan& plan, DevCtl ctl, cudaStream_t stream) {
   const bool wide = out == GLA_FP32;

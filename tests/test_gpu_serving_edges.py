@@ -258,3 +258,22 @@ def test_a_last_round_of_parts_among_packed_tokens(env):
                               _ints(torch, list(range(n + 1))), *dev, window, sink, pool_e=pool[2])
     _close(o, *ref.chunk(*values, page, pos, np.arange(n + 1), q, k, v, window, sink), "bf16")
     assert gla.get_device_error() == 0
+
+
+@pytest.mark.parametrize("new,dt", [(4, "bf16"), (4, "fp16"), (7, "bf16"), (8, "fp16")])
+@pytest.mark.parametrize("n", [20, 80])
+def test_drafts_of_many_sequences(env, n, new, dt):
+    """Units of 16 and 32 rows, fewer than two to an SM of 152 and more, and with some sequences a token short."""
+    gla, torch, types = env
+    rng = np.random.default_rng(n + new)
+    H, KV, window, sink = 16, 4, 150, 2
+    sizes = [new - (b % 5 == 4) for b in range(n)]
+    start = np.concatenate([[0], np.cumsum(sizes)])
+    pos = [(53 * b) % 400 for b in range(n)]
+    pool, values = _pool(torch, rng, n, window + sink, KV, dt, types[dt], 8)
+    (q, k, v), dev = _new(torch, rng, int(start[-1]), H, KV, dt, types[dt])
+    page = rng.permutation(n)
+    o = gla.window_attn_chunk(*pool[:2], _ints(torch, page.tolist()), _ints(torch, pos),
+                              _ints(torch, start.tolist()), *dev, window, sink, pool_e=pool[2])
+    _close(o, *ref.chunk(*values, page, pos, start, q, k, v, window, sink), dt)
+    assert gla.get_device_error() == 0
