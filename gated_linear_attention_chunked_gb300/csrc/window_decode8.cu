@@ -4,9 +4,9 @@
 namespace gla {
 namespace {
 
-// Units have 8, 16 or 32 rows: as many as a sequence has, since each unit of its own turns the page's codes
+// Units have 8, 16, 24 or 32 rows: as many as a sequence has, since each unit of its own turns the page's codes
 // into operands again.
-int unit_rows(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+int unit_rows(long long rows) { return rows >= 25 ? 32 : rows >= 17 ? 24 : rows >= 9 ? 16 : 8; }
 
 rows8::Plan decode_plan(int n, int KV, int H, int slots, int n_sm) {
   const int G = H / KV, rows = unit_rows(G);

@@ -48,7 +48,8 @@ static_assert(kDV % (16 * WARPS) == 0, "the warps' channels");
 // more than one group no room is left for three CTAs of an SM with two such rounds beside the queries: two CTAs, or
 // rounds of 64 slots in three stages, or in two where the rows take the room of the third.  make_plan
 // has the rule.  Chunks of 4 and 8 tokens on 2,052 slots, 4 key heads, by 128 and by 64 slots: 64 chunks 44 and 58,
-// 56 and 86 us; 96 76 and 60, 103 and 88; 128 84 and 86, 105 and 131; 200 123 and 115, 156 and 173.  (One group by 64
+// 56 and 86 us; 96 76 and 60, 103 and 88; 128 84 and 86, 105 and 131; 200 123 and 115, 156 and 173.  Of 6, by units of
+// 24 rows: 48 and 69, 89 and 71, 92 and 104 (by units of 32 96 chunks took 88).  (One group by 64
 // slots: 71 us in place of 68 with 256 tokens on 1,028 slots.  With 5, 4 and 3 CTAs of two stages of 64 slots 69, but
 // 96 chunks of two and four tokens took 65 and 74 us in place of 48 and 57; four groups in three stages leave
 // room for two CTAs: 96 chunks of eight tokens 101 us in place of 94.)
@@ -56,7 +57,7 @@ template <int NT, bool WIDE>
 struct Shape {
   static constexpr int HOLD = NT > 1 && WIDE ? 2 : 3;          // CTAs that an SM holds
   static constexpr int SB = WIDE ? 32 : 16;                    // slots of a round for each warp
-  static constexpr int STAGES = NT == 2 && !WIDE ? 3 : 2;
+  static constexpr int STAGES = NT < 4 && !WIDE ? 3 : 2;
   static constexpr int ROUND = WARPS * SB;
   static constexpr int KEYS = ROUND * kDV, STAGE = KEYS + ROUND * kDK;  // a stage: values, keys
   static constexpr int EXPS = 2 * SB + 16;               // the exponents of a warp's slots, from a word's start
@@ -103,7 +104,7 @@ struct Args {
 // CTAs: a unit each for the first `whole` units, `parts` for each of the others.
 struct Plan {
   long long units;   // at most
-  int whole, parts, part_slots, rows;  // rows of a unit: 8, 16 or 32
+  int whole, parts, part_slots, rows;  // rows of a unit: 8, 16, 24 or 32
   bool wide;                           // rounds of 128 slots with more than 8
 };
 struct Maps {
@@ -851,7 +852,7 @@ rows8_join_kernel(Args a, Plan plan) {
 // as many parts as fill it once more, of at least one round.  (More parts than that, in two turns: 69 us in place of
 // 58 with 64 chunks of four tokens on 2,052 slots, 256 units on 456 places.)
 inline Plan make_plan(long long units, long long likely, int rows, int slots, int n_sm) {
-  // a unit takes three quarters of the time by rounds of 128 slots (16 rows; two thirds with 32), two to an SM
+  // a unit takes three quarters of the time by rounds of 128 slots (16 rows; two thirds with more), two to an SM
   const long long two = (likely + 2 * n_sm - 1) / std::max(2 * n_sm, 1), three = (likely + 3 * n_sm - 1) / std::max(3 * n_sm, 1);
   const bool wide = rows == 8 || (rows == 16 ? 3 * two <= 4 * three : 2 * two <= 3 * three);
   const int ROUND = wide ? Shape<1, true>::ROUND : Shape<2, false>::ROUND;
@@ -907,6 +908,8 @@ cudaError_t run(const Args& a, const Plan& plan, DevCtl ctl, cudaStream_t stream
 template <class T, class TO>
 cudaError_t run(const Args& a, const Plan& plan, DevCtl ctl, cudaStream_t stream) {
   if (plan.rows == 8) return run<T, TO, 1, true>(a, plan, ctl, stream);
+  if (plan.rows == 24)
+    return plan.wide ? run<T, TO, 3, true>(a, plan, ctl, stream) : run<T, TO, 3, false>(a, plan, ctl, stream);
   if (plan.rows == 32)
     return plan.wide ? run<T, TO, 4, true>(a, plan, ctl, stream) : run<T, TO, 4, false>(a, plan, ctl, stream);
   return plan.wide ? run<T, TO, 2, true>(a, plan, ctl, stream) : run<T, TO, 2, false>(a, plan, ctl, stream);

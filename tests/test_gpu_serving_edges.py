@@ -260,10 +260,10 @@ def test_a_last_round_of_parts_among_packed_tokens(env):
     assert gla.get_device_error() == 0
 
 
-@pytest.mark.parametrize("new,dt", [(4, "bf16"), (4, "fp16"), (7, "bf16"), (8, "fp16")])
+@pytest.mark.parametrize("new,dt", [(4, "bf16"), (4, "fp16"), (5, "fp16"), (6, "bf16"), (7, "bf16"), (8, "fp16")])
 @pytest.mark.parametrize("n", [20, 80])
 def test_drafts_of_many_sequences(env, n, new, dt):
-    """Units of 16 and 32 rows, fewer than two to an SM of 152 and more, and with some sequences a token short."""
+    """Units of 16, 24 and 32 rows, fewer than two to an SM of 152 and more, and with some sequences a token short."""
     gla, torch, types = env
     rng = np.random.default_rng(n + new)
     H, KV, window, sink = 16, 4, 150, 2
