@@ -417,25 +417,28 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
   }
   {
     // ------------------------------------------------------------ the CTA's items
-    // Tiles of a thread's slice of the sequences, their sums up to each slice, and a search.
+    // Tiles of a thread's slice of the sequences, their sums up to each slice, and a search.  Sums stop at the
+    // tiles that the plan and its workspace have room for: of sequences that overlap, where `start`
+    // decreases, there may be any number.  (Then a slice's tiles are what is left of it, from its front.)
+    const int room = (int)(plan.units / KV);
     int* const upto = (int*)(base + L::STG);
     int* const warps = upto + THREADS + 1;
     const int slice = (c.n + THREADS - 1) / THREADS;
     const int b0 = min(tid * slice, c.n), b1 = min(b0 + slice, c.n);
     int mine = 0;
     for (int b = b0; b < b1; ++b)
-      mine += (sequence(c, a.tok, b, ctl).tokens + plan.per - 1) / plan.per;
+      mine = min(mine + (sequence(c, a.tok, b, ctl).tokens + plan.per - 1) / plan.per, room);
     int sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += y;
+      if (lane >= d) sum = min(sum + y, room);
     }
     if (lane == 31) warps[warp] = sum;
     __syncthreads();
     int before = 0;
-    for (int w = 0; w < warp; ++w) before += warps[w];
-    upto[tid + 1] = before + sum;
+    for (int w = 0; w < warp; ++w) before = min(before + warps[w], room);
+    upto[tid + 1] = min(before + sum, room);
     if (tid == 0) upto[0] = 0;
     __syncthreads();
     const int tiles = upto[THREADS];

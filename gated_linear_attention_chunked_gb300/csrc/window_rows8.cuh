@@ -232,23 +232,25 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     }
     __syncthreads();
   } else {
-    // sums of groups over a slice of the sequences a thread, and a search
+    // sums of groups over a slice of the sequences a thread, and a search; the sums stop at the groups that the
+    // plan has room for, which sequences that overlap, where `start` decreases, could pass
+    const int room = (int)(plan.units / KV);
     int *const upto = sh.find.upto, *const sums = sh.find.sums;
     const int slice = (c.n + THREADS - 1) / THREADS;
     const int lo = min(tid * slice, c.n), hi = min(lo + slice, c.n);
     int mine = 0;
-    for (int i = lo; i < hi; ++i) mine += (sequence(c, a.tok, i, ctl).tokens * G + HB - 1) / HB;
+    for (int i = lo; i < hi; ++i) mine = min(mine + (sequence(c, a.tok, i, ctl).tokens * G + HB - 1) / HB, room);
     int sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += y;
+      if (lane >= d) sum = min(sum + y, room);
     }
     if (lane == 31) sums[w] = sum;
     __syncthreads();
     int before = 0;
-    for (int i = 0; i < w; ++i) before += sums[i];
-    upto[tid + 1] = before + sum;
+    for (int i = 0; i < w; ++i) before = min(before + sums[i], room);
+    upto[tid + 1] = min(before + sum, room);
     if (tid == 0) upto[0] = 0;
     __syncthreads();
     const long long total = (long long)upto[THREADS] * KV;

@@ -723,6 +723,8 @@ GLA_API gla_status gla_rotary_turns(int R, double base, gla_rotary_scaling scali
  *   page         [n] int32 (device), as in gla_window_cache_fill: distinct
  * A sequence whose page, position (negative, or its last past 2^31 - 2) or rows are out of range is left
  * untouched and sets the device error word to GLA_ERR_RANGE.
+ * Where start decreases the word is set too, and sequences may overlap: what their rows of the output
+ * and their pages' slots then hold is undefined, but nothing else is written.
  *
  * Pages (pool_k, pool_v as in gla_window_cache_fill, slots = sink + window) of 16 bits have in_dtype, and
  * pool_e is NULL.  Of 8 bits, pool_k [n_pages,pool_layers,slots,KV,96] and pool_v [..,192] are signed
