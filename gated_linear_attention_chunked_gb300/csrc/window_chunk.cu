@@ -46,8 +46,8 @@ bool is_short(int n, int n_tokens, int KV, int H) {
 // out as 16-bit rows, each once: an item that turns a tile of codes into operands for itself takes 2.8 us
 // for it (four warps do), one over 16 bits 1.2, and the copy costs HBM 864 bytes a slot and key head.  4 x 2,048
 // tokens of 16 heads on 1,024 slots of 4 key heads: 102 us in place of 145; with two items each 96 x 64 tokens on
-// 2,052 slots 261 in place of 285, 60 tokens on 16,388 37 in place of 34; with one 96 x 32 tokens 219 in place
-// of 159.  As long as the copy stays below a GiB.
+// 2,052 slots 261 in place of 276, 60 tokens on 16,388 37 in place of 36; with one 96 x 32 tokens 219 in place
+// of 152.  As long as the copy stays below a GiB.
 struct Copy {
   size_t v, pages, bytes;  // offsets of the values and of the copies' indexes; a multiple of 256
 };
