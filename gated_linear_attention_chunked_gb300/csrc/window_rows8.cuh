@@ -361,7 +361,9 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
       top = top2<T>(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = top2<T>(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const float2 f = halves<T>(top);
-      const int e = min(max((int)(__float_as_uint(fmaxf(f.x, f.y)) >> 23) - 127, -100), 100);
+      // from 2^-126, since a query loses bits where it stays below fp16's 2^-14, to 2^100, since 2^24 log2(e) 2^e has to
+      // be finite: rows of up to 2^115 stay within fp16
+      const int e = min(max((int)(__float_as_uint(fmaxf(f.x, f.y)) >> 23) - 127, -126), 100);
       const float down = pow2(-e);
       up *= pow2(e);
 #pragma unroll

@@ -763,6 +763,8 @@ GLA_API gla_status gla_window_cache_append(const void* k, const void* v, gla_dty
  * sequences may hold anything, NaN included.  Over 8-bit pages codes are multiplied exactly.  Where sequences
  * have few rows (n_tokens H / KV <= 32 min(n, n_tokens)) a slot's weight rounds to fp16 with the 2^e of its
  * value: by 2^-11 of itself, or by 2^-25 of the page's largest row, and what is below 2^-78 in a page is lost.
+ * There bf16 queries have to be below 2^115, and a score is an fp32 sum with 128 on each code, which comes off
+ * again: it is off by fp32's roundings of sum |q| 256 2^e, e the key's exponent.
  * Results repeat bit for bit.  n == 0 or n_tokens == 0 returns GLA_OK without launching.
  */
 GLA_API size_t gla_window_attn_chunk_workspace_size(int n, int n_tokens, int H, int KV, int window,

@@ -104,13 +104,14 @@ def test_large_values_of_bf16(env, route, e):
     c.check(c.chunk(), route == "few")
 
 
-@pytest.mark.parametrize("route,up", [("few", 80), ("codes", 96), ("codes", 105), ("codes", 112), ("copy", 112)])
+@pytest.mark.parametrize("route,up", [("few", 80), ("few", 100), ("few", 112), ("codes", 96), ("codes", 105), ("codes", 112),
+                                      ("copy", 112)])
 def test_large_keys_of_bf16(env, route, up):
     """Keys of about 2^up and queries as much smaller: the scores of ordinary ones."""
     c = Case(env, "bf16", ROUTES[route], seed=up)
     c.e[..., 0] += up + 7
     c.k = c.k * 2.0 ** (up + 7)
-    c.q = c.q * 2.0 ** -(up + 7)
+    c.q = as_dtype_values(c.q * np.float32(2.0 ** -(up + 7)), "bf16")  # (the smallest are subnormal)
     c.check(c.chunk(), route == "few")
 
 
