@@ -79,7 +79,7 @@ struct Shared {
     } find;
   };
   float z0[8 * NT], zs[8 * NT];        // of a row: - q . (code 0), a score's factor
-  float top[WARPS][8 * NT], sum[WARPS][8 * NT];
+  float top[WARPS][8 * NT], sum[WARPS][8 * NT];  // (top[0] before the rounds: the scores of one token alone)
   int e_top[WARPS];
   int found[4];
 };
@@ -412,7 +412,7 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
         }
         z += __shfl_xor_sync(0xffffffffu, z, 1);
         z += __shfl_xor_sync(0xffffffffu, z, 2);
-        if (t == 0) sh.sum[0][g] = z * kLog2e;
+        if (t == 0) sh.top[0][g] = z * kLog2e;
       }
     }
   }
@@ -426,7 +426,9 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     z0[r] = sh.z0[8 * (r >> 1) + t2 + (r & 1)];
     zs[r] = sh.zs[8 * (r >> 1) + t2 + (r & 1)];
   }
-  [[maybe_unused]] const float z_own[2] = {sh.sum[0][t2], sh.sum[0][t2 + 1]};
+  // (read by all ahead of the first round's barrier, behind which `refer` writes there; without rounds, for one token,
+  // nothing does)
+  [[maybe_unused]] const float z_own[2] = {sh.top[0][t2], sh.top[0][t2 + 1]};
   auto at = [&](int r) { return s.pos + row_of(8 * (r >> 1) + t2 + (r & 1)) / G; };  // a row's position
   float acc[TILES][NT][4];
 #pragma unroll
