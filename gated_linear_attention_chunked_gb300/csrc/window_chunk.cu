@@ -9,8 +9,10 @@ using namespace chunk;
 
 // Items are cut where whole ones leave SMs without work: into the parts whose rounds over the device take
 // least, counting a tile of keys as 1, what an item needs besides its tiles as 2, and a part's results,
-// written and joined, as 2.  How many items there are, and how many tiles each has, only the device knows:
-// the sequences are taken for equally long and their windows for full.
+// written and joined, as 2; and of those within a 32nd of the least into the fewest, since each part takes 776 bytes of
+// workspace a (token, query head), so that a gain below the model's own error costs none.  How many items there are,
+// and how many tiles each has, only the device knows: the sequences are taken for equally long and their windows for
+// full.
 Plan make_plan(int n, int n_tokens, int KV, int H, int window, int sink, int n_sm) {
   Plan p;
   const int G = H / KV;
@@ -20,18 +22,22 @@ Plan make_plan(int n, int n_tokens, int KV, int H, int window, int sink, int n_s
   const long long tokens = (n_tokens + n - 1) / n;  // of a sequence
   const long long items = std::max(1ll, n_tokens / tokens) * ((tokens + p.per - 1) / p.per) * KV;
   const double tiles = (window + (double)sink + p.per) / BN + 1.5;
-  double best = 1e30;
-  for (int parts = 1; parts <= kMostParts && parts * 2 <= tiles + 1; ++parts) {
+  auto cost = [&](int parts) {
     const double rounds = (double)((items * parts + n_sm - 1) / n_sm);
-    const double cost = rounds * (tiles / parts + 2 + (parts > 1 ? 2 : 0)) + (parts > 1 ? 2 : 0);
-    if (cost < best) {
-      best = cost;
-      p.parts = parts;
-    }
-  }
+    return rounds * (tiles / parts + 2 + (parts > 1 ? 2 : 0)) + (parts > 1 ? 2 : 0);
+  };
+  const int most = std::min(kMostParts, std::max((int)((tiles + 1) / 2), 1));
+  double best = cost(1);
+  for (int parts = 2; parts <= most; ++parts) best = std::min(best, cost(parts));
+  p.parts = 1;
+  while (cost(p.parts) > best * (33.0 / 32)) ++p.parts;
   const long long all = p.units * p.parts;
   // a CTA an SM, and more where its list of items would not hold them
   p.grid = (unsigned)std::max(std::min<long long>(all, n_sm), (all + LIST - 1) / LIST);
+  const size_t rows = (size_t)n_tokens * H * p.parts;
+  p.ml = ((p.units + 1) * 8 + 255) / 256 * 256;
+  p.o = p.ml + (rows * 8 + 255) / 256 * 256;
+  p.bytes = p.parts > 1 ? p.o + rows * kDV * 4 : 0;
   return p;
 }
 
@@ -76,7 +82,7 @@ size_t window_chunk_workspace_bytes(int n, int n_tokens, int KV, int H, int wind
   const Plan p = make_plan(n, n_tokens, KV, H, window, sink, n_sm);
   Copy copy;
   const size_t pages = codes && copies_pages(n, n_tokens, KV, H, window, sink, &copy) ? copy.bytes : 0;
-  return pages + (p.parts > 1 ? Partials::bytes(p.units, p.parts) : 0);
+  return pages + p.bytes;
 }
 
 cudaError_t launch_window_chunk(const ChunkArgs& call, int n_sm, DevCtl ctl, cudaStream_t stream) {

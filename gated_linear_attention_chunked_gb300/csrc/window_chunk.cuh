@@ -87,7 +87,8 @@ struct Layout {
   static constexpr uint32_t TMEM = BAR + NBAR * 8;
   static constexpr uint32_t COUNT = TMEM + 4;              // items, their tiles
   static constexpr uint32_t INFO = COUNT + 8;              // uint32 [4]: tiles for the issuer (TileInfo)
-  static constexpr uint32_t ABORT = INFO + 16;
+  static constexpr uint32_t PLACE = INFO + 16;             // uint32 [LIST]: items' first rows in the workspace
+  static constexpr uint32_t ABORT = PLACE + 4 * LIST;
   static constexpr uint32_t USED = ABORT + 4 * kWaitWords, BYTES = USED + 1024;
   static_assert(BYTES <= 232448, "shared memory budget");
   static_assert(BAR % 8 == 0 && STG % 512 == 0 && RAWS % 128 == 0, "alignment");
@@ -104,21 +105,18 @@ struct Plan {
   int parts;
   long long units;  // (tile, key head) at most
   unsigned grid;
+  // The workspace of cut items: the tiles' rows and tokens, and by part, key head and row (token, query head)
+  // (reference, sum) and o: an item's rows lie together, and take no more room than there are.  Its bytes, and where
+  // ml and o begin:
+  size_t bytes, ml, o;
 };
-// The workspace of cut items: the tiles' rows and tokens, (reference, sum) and o of each unit's parts.
 struct Partials {
   int* tiles;   // [0]: how many; [2 + 2 i], [3 + 2 i]: row0, n_tok
-  float2* ml;   // [units][parts][128]
-  float* o;     // [units][parts][128][192]
-  static __host__ __device__ size_t head(long long units) { return ((units + 1) * 8 + 255) / 256 * 256; }
-  static __host__ __device__ size_t bytes(long long units, int parts) {
-    return head(units) + (size_t)units * parts * BM * (8 + kDV * 4);
-  }
-  __host__ __device__ Partials(void* p, long long units, int parts) {
-    tiles = static_cast<int*>(p);
-    ml = reinterpret_cast<float2*>(static_cast<char*>(p) + head(units));
-    o = reinterpret_cast<float*>(ml + (size_t)units * parts * BM);
-  }
+  float2* ml;   // [parts][KV][n_tokens][G]
+  float* o;     // [parts][KV][n_tokens][G][192]
+  __device__ __forceinline__ Partials(void* p, const Plan& plan)
+      : tiles(static_cast<int*>(p)), ml(reinterpret_cast<float2*>(static_cast<char*>(p) + plan.ml)),
+        o(reinterpret_cast<float*>(static_cast<char*>(p) + plan.o)) {}
 };
 
 __device__ __forceinline__ int ceil_tiles(int n) { return n <= 0 ? 0 : (n - 1) / BN + 1; }
@@ -277,8 +275,8 @@ __device__ __forceinline__ uint4 values_of(uint32_t lo, uint32_t hi, float s) {
   } else {
     // 0x4B000000 | u is 2^23 + u, from which an addition takes 2^23 + 128; the upper half of c s is its bf16 value.
     // All exact.  (One operation, (2^23 + u) s - (2^23 + 128) s, overflows from s = 2^105, which large rows have; four
-    // steps in bf16 arithmetic take a third longer than it.  96 x 32 tokens on 2,052 slots take 152 us, with the one 160;
-    // 37 tokens on 65,552 slots 90, with it 87.)
+    // steps in bf16 arithmetic take a third longer than it.  96 x 32 tokens on 2,052 slots: 152 us, with the one 160; 37
+    // on 65,552 slots: 3 us more than with it, of 90.)
     const float2 s2 = make_float2(s, s), off = make_float2(-8388736.f, -8388736.f);
     const uint32_t m = 0x4B000000u;
     uint32_t* w = &o.x;
@@ -465,8 +463,12 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
         }
         make_item(items[tid], c, s, plan.per, left * plan.per, unit % KV, part, plan.parts);
         atomicAdd((int*)(base + L::COUNT) + 1, items[tid].te - items[tid].tb);
+        // (rows and parts together are below 2^31)
+        if (SPLIT)
+          ((uint32_t*)(base + L::PLACE))[tid] =
+              ((uint32_t)(part * KV + unit % KV) * a.tok.n_tokens + items[tid].row0) * G;
         if (SPLIT && part == 0 && unit % KV == 0) {
-          const Partials ps(a.workspace, plan.units, plan.parts);
+          const Partials ps(a.workspace, plan);
           ps.tiles[2 + 2 * t] = items[tid].row0;
           ps.tiles[3 + 2 * t] = items[tid].n_tok;
         }
@@ -871,9 +873,8 @@ window_chunk_kernel(const __grid_constant__ Maps maps, ChunkArgs a, Plan plan, D
       float inv = SPLIT ? 1.f : 1.f / sum;
       TO* out;
       if constexpr (SPLIT) {
-        const Partials ps(a.workspace, plan.units, plan.parts);
-        // this part's place: the CTA's items are blockIdx.x, + gridDim.x, ..
-        const long long at = (blockIdx.x + (long long)x * gridDim.x) * BM;
+        const Partials ps(a.workspace, plan);
+        const size_t at = ((const uint32_t*)(base + L::PLACE))[x];
         if (row < rows) ps.ml[at + row] = make_float2(ref, sum);
         out = ps.o + at * kDV;
       } else {
@@ -977,16 +978,16 @@ template <class TO>
 __global__ void __launch_bounds__(JOIN_THREADS)
 window_chunk_join_kernel(ChunkArgs a, Plan plan) {
   griddep_wait();
-  const Partials ps(a.workspace, plan.units, plan.parts);
+  const uint32_t all = (uint32_t)a.tok.n_tokens * a.H;  // (times the parts below 2^31)
+  const Partials ps(a.workspace, plan);
   const int KV = a.cache.c.KV, G = a.H / KV;
   const int unit = blockIdx.x, t = unit / KV, kv = unit % KV, row = blockIdx.y;
   if (t >= ps.tiles[0]) return;
   const int row0 = ps.tiles[2 + 2 * t];
   if (row >= ps.tiles[3 + 2 * t] * G) return;
-  const long long at = (long long)unit * plan.parts * BM + row;
+  const uint32_t at = ((uint32_t)kv * a.tok.n_tokens + row0) * G + row;
   join_row(
-      plan.parts, [&](int p) { return ps.ml[at + (long long)p * BM]; },
-      [&](int p) { return ps.o + (at + (long long)p * BM) * kDV; },
+      plan.parts, [&](int p) { return ps.ml[at + p * all]; }, [&](int p) { return ps.o + (size_t)(at + p * all) * kDV; },
       static_cast<TO*>(a.o) + (((long long)row0 + row / G) * a.H + kv * G + row % G) * kDV);
 }
 
