@@ -7,8 +7,10 @@
 // The gradient is the same with the angle negated.
 //
 // The angle is a fraction of a turn in units of 2^-64, so that pos * turns_i modulo a turn is one
-// 64-bit product, off by pos 2^-65 turns, without reductions in fp64.  The nearest quarter turn is
-// split off as whole numbers, and what is left (at most an eighth) goes to sincospi in fp32.
+// 64-bit product, exact for the table that is given, without reductions in fp64.  (A table made in double is off by
+// a few 2^-53 of a pair's turns, which a position multiplies: less than 1e-9 radians a million tokens on.)  The
+// nearest quarter turn is split off as whole numbers, and what is left (at most an eighth) goes to sincospi
+// in fp32.
 //
 // Bound by HBM: each element is read and written once.  A thread has up to eight pairs of one token
 // (two accesses of 16 bytes) and takes them through the heads of q and k, whose angles are the same, so

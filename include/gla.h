@@ -683,7 +683,7 @@ GLA_API gla_status gla_window_attn_decode_step(void* pool_k, void* pool_v, gla_d
  *   turns        [R / 2] (device): turns per position in units of 2^-64 (gla_rotary_turns)
  *   pos          [B,T] int32 (device) or NULL: token t of each sequence is at position t
  *   scale        finite; 1, or what a scaled table asks for
- * Angles are exact to pos 2^-65 turns, their sines and cosines and the sums fp32, one rounding to
+ * pos turns_i modulo a turn is exact, its sine and cosine and the sums fp32, one rounding to
  * out_dtype.  D <= 4096.  B == 0 or T == 0 returns GLA_OK.
  */
 GLA_API gla_status gla_rotary(const void* q, const long long* q_strides, void* q_out, int H,
@@ -701,6 +701,8 @@ GLA_API gla_status gla_rotary(const void* q, const long long* q_strides, void* q
  *                      are, those that turn at most `low` times (0 <= low < high) divided by factor,
  *                      between them mixed in proportion
  * (context, low and high are read by the last one only, factor by all but GLA_ROTARY_PLAIN).
+ * Made in double: an entry is off by up to (4 + ln(base)) 2^-53 of itself and half a unit (GLA_ROTARY_LINEAR
+ * 5 + ln(base), the other two some roundings more), and the angle of position pos by pos times that.
  */
 typedef enum {
   GLA_ROTARY_PLAIN = 0,
