@@ -204,7 +204,7 @@ rows8_kernel(const __grid_constant__ Maps maps, Args a, Plan plan, DevCtl ctl) {
     prefetch_tensormap(&maps.v);
   }
 
-  // ---- the unit: sequence b, key head kv, rows 16 grp .. of its (token, head) rows
+  // ---- the unit: sequence b, key head kv, rows 8 NT grp .. of its (token, head) rows
   Sequence s;
   int b, kv, grp;
   if (!a.tok.start) {

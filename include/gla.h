@@ -120,8 +120,8 @@ GLA_API gla_status gla_wait_probe(cudaStream_t stream);
  * does so at round `step` of tiles and leaves before it hands on its pair; the others give up
  * waiting for that, and each leaves only when nothing is on its way into its memory any more.
  * The layer norm's rings (rows that they take) give up at their row, or pair of rows, `step`, and
- * drain; the step and the short chunks over 8-bit pages at their round of 64 slots.  The call's outputs are then undefined; the context stays usable.  step < 0 (the
- * default) turns it off.  No fault,
+ * drain; the step and the short chunks over 8-bit pages at round `step` of their slots.  The call's
+ * outputs are then undefined; the context stays usable.  step < 0 (the default) turns it off.  No fault,
  * trap or unbounded wait is involved.  The mbarrier wait instruction suspends the waiting
  * thread until the phase completes (up to a hardware limit), so ordinary waits end before
  * any limit of the timer can be checked: a stall like this is what makes a wait run out. */
@@ -735,6 +735,9 @@ GLA_API gla_status gla_rotary_turns(int R, double base, gla_rotary_scaling scali
  * a row x is held as c 2^e with e = floor(log2(max |x|)) - 6, at least -24 (fp16) or -126 (bf16), and c =
  * x 2^-e rounded to even, within +-127: off by at most 2^(e-1), or less than 2^e for fp16 values above
  * 127.5 2^e.  c 2^e is a value of in_dtype.  An infinity is held as 127 times 2^9 (fp16) or 2^121, NaN as 0.
+ * A page does not know its type: the other calls take the in_dtype (out_dtype) that it was written with.  Pages of
+ * fp16 rows may be taken as bf16 too; of bf16 rows as fp16 only with exponents within -24 .. 9, outside which c 2^e is
+ * rounded to 0, an infinity or NaN.
  *
  * gla_window_cache_append: keys and values k [n_tokens,KV,96], v [n_tokens,KV,192] go into their
  * sequences' pages behind the tokens that are there: each slot gets the last token that belongs there,
@@ -762,7 +765,8 @@ GLA_API gla_status gla_window_cache_append(const void* k, const void* v, gla_dty
  *                aligned (0: not needed).  The size depends on the device current at the call
  * Pages may repeat here.  Softmax, sums and roundings as in gla_window_attn_fwd, and as there q, k and v of the
  * sequences' rows must be finite, and what their slots hold; slots that no token has reached and rows of other
- * sequences may hold anything, NaN included.  Over 8-bit pages codes are multiplied exactly.  Where sequences
+ * sequences may hold anything, NaN included.  Weighted values are summed in fp32 ahead of the division by the
+ * weights' sum, the weights up to 2^8 each: sums past 2^128 are infinite.  Over 8-bit pages codes are multiplied exactly.  Where sequences
  * have few rows (n_tokens H / KV <= 32 min(n, n_tokens)) a slot's weight rounds to fp16 with the 2^e of its
  * value: by 2^-11 of itself, or by 2^-25 of the page's largest row, and what is below 2^-78 in a page is lost.
  * There bf16 queries have to be below 2^115, and a score is an fp32 sum with 128 on each code, which comes off
@@ -801,7 +805,7 @@ GLA_API gla_status gla_window_attn8_decode_step(void* pool_k, void* pool_v, sign
 
 /* gla_window_cache8_read: layer `layer` of pages page[0 .. n-1] as rows of 16 bits, by slot: k
  * [n,slots,KV,96], v [n,slots,KV,192] out_dtype (written), the layout of a 16-bit pool's layer.  Slots that
- * no token has reached give what their bytes say.  A page out of range leaves its rows of k and v
+ * no token has reached give what their bytes say; out_dtype as above.  A page out of range leaves its rows of k and v
  * untouched and sets the device error word to GLA_ERR_RANGE; pages may repeat. */
 GLA_API gla_status gla_window_cache8_read(const void* pool_k, const void* pool_v,
                                           const signed char* pool_e, const int* page, int n,
